@@ -1,0 +1,480 @@
+"""The 4-bit paged KV cache and the moving of its pages, as operators to be measured.
+
+Five operators of the library: the append that quantises rows into an INT4 pool, the gather that
+reads rows back, single-token (decode) attention over an INT4 pool, prefill attention over an
+INT4 pool, and the move of physical blocks that a compaction of a pool asks for.
+
+An INT4 pool keeps, per (block of 16 tokens, KV head), one tile of K and one of V of 17 D / 2
+bytes: 16 D codes of 4 bits (n = value + 8, value in -7 .. 7), then a scale byte (E4M3) for each
+token and group of 32 columns.  An element stands for pool_scale * scale * (n - 8).  Where a
+code and a scale lie in a tile:
+
+  K: the token's row is r = (t & 8) | (t & 3) << 1 | (t >> 2) & 1; column d = 32 j + 8 c + i lies
+     in the row's 32-bit word c * (D / 32) + j, at bits 16 (i >> 2) + 4 (i & 3); its scale is
+     byte r * (D / 32) + j of the scales.
+  V: the token's row is t; column d = 32 j + 4 c + i lies in the row's 16-bit word
+     c' * (D / 32) + j at bits 4 i, with c' = c, or c ^ 4 where D is 128 and t & 2 is set; its
+     scale is byte (t & 3) * (D / 8) + 4 j + (t >> 2) of the scales.
+
+`own` False: each operator in elementary torch operations in 32 bits.  `own` True: the library.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+BS = 16                                       # tokens per block
+K_SCALE, V_SCALE = 0.0131, 0.0087             # the pools' scales (about amax / (7 * 448))
+
+
+# ------------------------------------------------------------------------------ cases
+def listed():
+    return [
+        # one conversation of the Llama-3-8B layout, a few hundred tokens in: latency counts
+        dict(name="decode one sequence", op="decode", batch=1, heads=32, kv_heads=8, dim=128, lens="fixed", length=333, step=False, lens_seed=1),
+        # the repository's headline batch
+        dict(name="decode 64 x 2048", op="decode", batch=64, heads=32, kv_heads=8, dim=128, lens="fixed", length=2048, step=False, lens_seed=2),
+        # few long sequences of the Llama-3-70B layout: the split over a long axis
+        dict(name="decode 4 x 32768", op="decode", batch=4, heads=64, kv_heads=8, dim=128, lens="fixed", length=32768, step=False, lens_seed=3),
+        # the ragged serving batch, the largest decode
+        dict(name="decode ragged 256", op="decode", batch=256, heads=32, kv_heads=8, dim=128, lens="uniform", length=4096, step=False, lens_seed=4),
+        # a whole step (append the new token, attend) of a small model with head_dim 64, odd batch
+        dict(name="step head_dim 64", op="decode", batch=37, heads=14, kv_heads=2, dim=64, lens="uniform", length=1900, step=True, lens_seed=5),
+        # one decode step's new rows of 64 sequences written, and read back
+        dict(name="append 64 rows", op="append", tokens=64, kv_heads=8, dim=128, blocks=8192),
+        # a prompt batch's rows (8 x 2048 and some) written, and read back
+        dict(name="append 16411 rows", op="append", tokens=16411, kv_heads=8, dim=128, blocks=1100),
+        # long sequences handed over whole (prefill instance to decode instance)
+        dict(name="gather 131072 rows", op="gather", tokens=131072, kv_heads=8, dim=128, blocks=9000),
+        # three short ragged chunks behind cached context, head_dim 64
+        dict(name="prefill 3 short chunks", op="prefill", batch=3, heads=8, kv_heads=2, dim=64, chunk=40, context=37, ragged=True, lens_seed=6),
+        # the repository's chunked prefill: 16 chunks of 512 behind up to 8192 cached positions
+        dict(name="prefill 16 x 512", op="prefill", batch=16, heads=32, kv_heads=8, dim=128, chunk=512, context=8192, ragged=False, lens_seed=7),
+        # a few blocks moved in a one-layer pool, odd KV heads
+        dict(name="move 11 blocks", op="move", layers=1, blocks=96, moves=11, kv_heads=3, dim=64, batch=5, entries=9),
+        # a pool of the Llama-3-8B layout (8 layers of it) compacted: 400 of 1024 blocks move
+        dict(name="move 400 blocks", op="move", layers=8, blocks=1024, moves=400, kv_heads=8, dim=128, batch=64, entries=40),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["decode", "decode", "append", "gather", "prefill", "move"])
+    kv_heads, group = rng.choice([1, 2, 3, 4, 8]), rng.choice([1, 2, 3, 4, 7, 8, 16])
+    dim, seed = rng.choice([64, 128, 128]), rng.randrange(1 << 30)
+    if op == "decode":
+        batch = _log(rng, 1, 256)
+        most = max(16, min(32768, 500_000 // batch))
+        return dict(op=op, batch=batch, heads=kv_heads * group, kv_heads=kv_heads, dim=dim, lens=rng.choice(["fixed", "uniform", "lognormal"]),
+                    length=_log(rng, 1, most), step=rng.random() < 0.3, lens_seed=seed)
+    if op in ("append", "gather"):
+        tokens = _log(rng, 1, 50_000)
+        return dict(op=op, tokens=tokens, kv_heads=kv_heads, dim=dim, blocks=-(-tokens // BS) + _log(rng, 1, 4000))
+    if op == "prefill":
+        chunk, context = _log(rng, 1, 500), _log(rng, 1, 8000)
+        batch = _log(rng, 1, max(1, min(16, (1 << 31) // (chunk * (chunk + context) * kv_heads * group))))
+        return dict(op=op, batch=batch, heads=kv_heads * group, kv_heads=kv_heads, dim=dim, chunk=chunk,
+                    context=context, ragged=rng.random() < 0.7, lens_seed=seed)
+    blocks = _log(rng, 8, 1000)
+    return dict(op="move", layers=rng.choice([1, 2, 3, 8]), blocks=blocks, moves=rng.randint(1, blocks // 2), kv_heads=kv_heads, dim=dim,
+                batch=_log(rng, 1, 128), entries=rng.randint(1, 64))
+
+
+# ------------------------------------------------------------------------------ sizes of a case
+def _blocks(n):
+    return -(-np.asarray(n) // BS)
+
+
+def _seq_lens(c):
+    r = np.random.Generator(np.random.PCG64(c["lens_seed"]))
+    if c["lens"] == "fixed":
+        return np.full(c["batch"], c["length"], np.int32)
+    if c["lens"] == "uniform":
+        return r.integers(1, c["length"], size=c["batch"], endpoint=True).astype(np.int32)
+    x = np.rint(np.exp(r.normal(math.log(0.35 * c["length"] + 1), 0.6, size=c["batch"])))
+    return np.clip(x, 1, c["length"]).astype(np.int32)
+
+
+def _chunks(c):
+    """Rows of each sequence's chunk, and its positions including them."""
+    r = np.random.Generator(np.random.PCG64(c["lens_seed"]))
+    P = r.integers(1, c["chunk"], size=c["batch"], endpoint=True) if c["ragged"] else np.full(c["batch"], c["chunk"])
+    C = r.integers(0, c["context"], size=c["batch"], endpoint=True)
+    return P.astype(np.int32), (C + P).astype(np.int32)
+
+
+def work(c):
+    row4, row16 = c["kv_heads"] * c["dim"] * 17 // 32, c["kv_heads"] * c["dim"] * 2      # a token's K (or V) row, stored and as bf16
+    if c["op"] == "decode":
+        L = int(_seq_lens(c).astype(np.int64).sum())
+        b = 2 * L * row4 + 2 * c["batch"] * c["heads"] * c["dim"] * 2 + int(_blocks(_seq_lens(c)).sum()) * 4 + c["batch"] * 4
+        if c["step"]:                                          # the new rows in, written, and read back
+            b += 2 * c["batch"] * (2 * row16 + row4)
+        return {"bytes": b, "flops": 4 * L * c["heads"] * c["dim"]}
+    if c["op"] == "append":
+        return {"bytes": c["tokens"] * (4 * row16 + 4 * row4 + 16), "flops": 16 * c["tokens"] * c["kv_heads"] * c["dim"]}
+    if c["op"] == "gather":
+        return {"bytes": c["tokens"] * (2 * row16 + 2 * row4 + 8), "flops": 4 * c["tokens"] * c["kv_heads"] * c["dim"]}
+    if c["op"] == "prefill":
+        P, L = (x.astype(np.int64) for x in _chunks(c))
+        seen = int((P * (L - P) + P * (P + 1) // 2).sum())
+        return {"bytes": 2 * int(L.sum()) * row4 + 2 * int(P.sum()) * c["heads"] * c["dim"] * 2, "flops": 4 * seen * c["heads"] * c["dim"]}
+    block = c["kv_heads"] * BS * c["dim"] * 2
+    return {"bytes": 4 * c["layers"] * c["moves"] * block + 8 * c["batch"] * c["entries"] + 8 * c["moves"], "flops": 0}
+
+
+# ------------------------------------------------------------------------------ the INT4 tile
+def _order(D, is_key, device):
+    """(code, scale): for code x = token * D + d of a tile its nibble's place (2 * byte + high half), and for
+    scale token * (D / 32) + j its byte."""
+    t, d = torch.arange(BS, device=device)[:, None], torch.arange(D, device=device)[None, :]
+    ng, j = D // 32, d // 32
+    g = torch.arange(ng, device=device)[None, :]
+    if is_key:
+        r = (t & 8) | (t & 3) << 1 | (t >> 2) & 1
+        c, i = d % 32 // 8, d % 8
+        nib = (r * (D // 8) + c * ng + j) * 8 + (i >> 2) * 4 + (i & 3)
+        return nib.reshape(-1), (r * ng + g).reshape(-1)
+    c, i = d % 32 // 4, d % 4
+    if D == 128:
+        c = c ^ ((t & 2) << 1)
+    nib = (t * (D // 4) + c * ng + j) * 4 + i
+    return nib.reshape(-1), ((t & 3) * (D // 8) + 4 * g + (t >> 2)).reshape(-1)
+
+
+def _inverse(p):
+    q = torch.empty_like(p)
+    q[p] = torch.arange(p.numel(), device=p.device)
+    return q
+
+
+def _e4m3(x):
+    return x.clamp(max=448.0).to(torch.float8_e4m3fn)
+
+
+def _quantise(x, pool_scale):
+    """Codes (uint8, 0 .. 15) and scales (E4M3) of rows x [..., D] in 32 bits."""
+    y = (x.float() * torch.tensor(1.0 / np.float32(pool_scale), dtype=torch.float32, device=x.device)).unflatten(-1, (-1, 32))
+    s = _e4m3(y.abs().amax(-1) * torch.tensor(np.float32(1) / np.float32(7), device=x.device))
+    sf = s.float()[..., None]
+    n = torch.where(sf > 0, (y * (1.0 / sf)).round().clamp(-7, 7), 0.0) + 8
+    return n.flatten(-2).to(torch.uint8), s
+
+
+def _layout(D, device="cuda"):
+    """The tile's places, which a program keeps: of K, then of V."""
+    return _order(D, True, device), _order(D, False, device)
+
+
+def _pack(codes, scales, order):
+    """Tiles [..., 17 D / 2] from codes [..., 16, D] and scales [..., 16, D / 32]."""
+    nib, sb = (_inverse(p) for p in order)
+    n = codes.flatten(-2)[..., nib].unflatten(-1, (-1, 2))
+    return torch.cat([n[..., 0] | n[..., 1] << 4, scales.view(torch.uint8).flatten(-2)[..., sb]], -1)
+
+
+def _unpack(tiles, order, pool_scale):
+    """Values [..., 16, D] in 32 bits of tiles [..., 17 D / 2]."""
+    D = tiles.shape[-1] * 2 // 17
+    nib, sb = order
+    b = tiles[..., : 8 * D]
+    n = torch.stack([b & 15, b >> 4], -1).flatten(-2)[..., nib].float() - 8
+    s = tiles[..., 8 * D :][..., sb].view(torch.float8_e4m3fn).float()
+    return ((n.unflatten(-1, (-1, 32)) * s[..., None]) * pool_scale).flatten(-2).unflatten(-1, (BS, D))
+
+
+# ------------------------------------------------------------------------------ inputs
+def _randn(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def _gains(g, Hkv, D):
+    """Keys have a few channels much larger than the rest."""
+    x = 1 + 0.2 * torch.rand(Hkv, 1, D, generator=g, device="cuda")
+    return torch.where(torch.rand(Hkv, 1, D, generator=g, device="cuda") < 0.03, 4 * x, x)
+
+
+def _pool_tensors(g, blocks, Hkv, D):
+    """K and V caches of a pool whose every block holds rows that were written."""
+    k, v = [], []
+    gain, order = _gains(g, Hkv, D), _layout(D)
+    per = max(1, (1 << 26) // (Hkv * BS * D))
+    for at in range(0, blocks, per):
+        n = min(per, blocks - at)
+        k.append(_pack(*_quantise(_randn(g, n, Hkv, BS, D).mul_(gain).bfloat16(), K_SCALE), order[0]))
+        v.append(_pack(*_quantise(_randn(g, n, Hkv, BS, D).bfloat16(), V_SCALE), order[1]))
+    return torch.cat(k), torch.cat(v)
+
+
+def _tables(g, seq_lens, blocks):
+    """Block tables over shuffled physical blocks, -1 where a row needs no more."""
+    nb = torch.from_numpy(_blocks(seq_lens)).cuda()
+    col = torch.arange(int(nb.max()), device="cuda")[None, :]
+    used = col < nb[:, None]
+    t = torch.full(used.shape, -1, dtype=torch.int32, device="cuda")
+    t[used] = torch.randperm(blocks, generator=g, device="cuda")[: int(nb.sum())].int()
+    return t
+
+
+def _pool(c, blocks, layers=1, int4=True):
+    import paged_kv_cache_159_gb300 as pkv
+    p = pkv.Pool(blocks, c["kv_heads"], c["dim"], kv_dtype=pkv.KV_INT4 if int4 else pkv.KV_BF16, k_scale=K_SCALE, v_scale=V_SCALE, num_layers=layers)
+    p.attach_device(torch.cuda.current_device())
+    return p
+
+
+def prepare(c, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(int(seed))
+    Hkv, D = c["kv_heads"], c["dim"]
+    s = dict(case=c, order=_layout(D))
+    bf16 = dict(dtype=torch.bfloat16, device="cuda")
+    if c["op"] in ("decode", "prefill"):
+        P, L = (None, _seq_lens(c)) if c["op"] == "decode" else _chunks(c)
+        blocks = int(_blocks(L).sum())
+        s["kc"], s["vc"] = _pool_tensors(g, blocks, Hkv, D)
+        s["tables"], s["lens"] = _tables(g, L, blocks), torch.from_numpy(L).cuda()
+        rows = c["batch"] if P is None else int(P.sum())
+        s["q"] = _randn(g, rows, c["heads"], D).bfloat16()
+        s["scale"] = float(np.float32(1 / math.sqrt(D)))
+        s["out"] = torch.empty(rows, c["heads"], D, **bf16)
+        if c["op"] == "prefill":
+            s["P"], s["cu"] = torch.from_numpy(P).cuda(), np.concatenate([[0], np.cumsum(P)]).astype(np.int32)
+        elif c["step"]:
+            s["k"], s["v"] = _randn(g, rows, Hkv, D).bfloat16(), _randn(g, rows, Hkv, D).bfloat16()
+            last = s["lens"].long() - 1
+            s["slots"] = s["tables"].gather(1, (last // BS)[:, None])[:, 0].long() * BS + last % BS
+            s["k_read"], s["v_read"] = torch.empty(rows, Hkv, D, **bf16), torch.empty(rows, Hkv, D, **bf16)
+        if own:
+            import paged_kv_cache_159_gb300 as pkv
+            s["pool"] = _pool(c, blocks)
+            if c["op"] == "decode":
+                s["ws"] = torch.zeros(pkv.decode_workspace_bytes(s["pool"], rows, c["heads"], s["tables"].shape[1]), dtype=torch.uint8, device="cuda")
+            else:
+                plan, s["grid"] = pkv.prefill_plan(s["pool"], s["cu"], L, c["heads"], s["tables"].shape[1])
+                s["plan"] = torch.from_numpy(plan).cuda()
+    elif c["op"] in ("append", "gather"):
+        T = c["tokens"]
+        s["kc"], s["vc"] = _pool_tensors(g, c["blocks"], Hkv, D)
+        s["slots"] = (torch.randperm(c["blocks"], generator=g, device="cuda")[: -(-T // BS), None] * BS + torch.arange(BS, device="cuda")).flatten()[:T].contiguous()
+        s["k"], s["v"] = (_randn(g, T, Hkv, D) * _gains(g, Hkv, D)[:, 0]).bfloat16(), _randn(g, T, Hkv, D).bfloat16()
+        s["k_read"], s["v_read"] = torch.empty(T, Hkv, D, **bf16), torch.empty(T, Hkv, D, **bf16)
+        if own:
+            s["pool"] = _pool(c, c["blocks"])
+    else:
+        s["kc"], s["vc"] = (_randn(g, c["layers"], c["blocks"], Hkv, BS, D).bfloat16() for _ in range(2))
+        # the moving blocks are the highest live ids, in descending order, into the lowest free ids
+        n = c["moves"]
+        s["dst"] = torch.randperm(c["blocks"] - n, generator=g, device="cuda")[:n].sort().values.int()
+        s["src"] = torch.arange(c["blocks"] - 1, c["blocks"] - 1 - n, -1, device="cuda", dtype=torch.int32)
+        live = torch.ones(c["blocks"], dtype=torch.bool, device="cuda")
+        live[s["dst"].long()] = False
+        live = live.nonzero()[:, 0]
+        t = live[torch.randint(0, live.numel(), (c["batch"], c["entries"]), generator=g, device="cuda")].int()
+        s["tables"] = torch.where(torch.rand(t.shape, generator=g, device="cuda") < 0.1, -1, t).int()
+        if own:
+            s["pool"] = _pool(c, c["blocks"], c["layers"], int4=False)
+    return s
+
+
+# ------------------------------------------------------------------------------ one pass
+def _write(s):
+    """New rows into their slots, in elementary operations."""
+    D = s["k"].shape[-1]
+    blk, t = s["slots"] // BS, s["slots"] % BS
+    for rows, cache, (nib, sb), scale in ((s["k"], s["kc"], s["order"][0], K_SCALE), (s["v"], s["vc"], s["order"][1], V_SCALE)):
+        n, e = _quantise(rows, scale)
+        at, by = nib.view(BS, D).sort(-1)                                      # a token's nibble places in order, and their columns
+        n = n.gather(-1, by[t][:, None, :].expand(n.shape))
+        both = n[..., 0::2] | n[..., 1::2] << 4
+        where = torch.cat([at[:, 0::2] // 2, 8 * D + sb.view(BS, -1)], -1)[t]
+        start = blk[:, None] * cache.stride(0) + torch.arange(cache.shape[1], device=n.device) * cache.stride(1)
+        cache.view(-1)[start[:, :, None] + where[:, None, :]] = torch.cat([both, e.view(torch.uint8)], -1)
+
+
+def _read(s):
+    """Rows of the slots back, rounded to bf16 once."""
+    D, got = s["q"].shape[-1] if "q" in s else s["k"].shape[-1], []
+    blk, t = s["slots"] // BS, s["slots"] % BS
+    for cache, (nib, sb), scale in ((s["kc"], s["order"][0], K_SCALE), (s["vc"], s["order"][1], V_SCALE)):
+        start = (blk[:, None] * cache.stride(0) + torch.arange(cache.shape[1], device=t.device) * cache.stride(1))[:, :, None]
+        at = nib.view(BS, D)[t][:, None, :]
+        n = (cache.view(-1)[start + at // 2] >> (at % 2 * 4).byte() & 15).float() - 8
+        e = cache.view(-1)[start + (8 * D + sb.view(BS, -1)[t])[:, None, :]].view(torch.float8_e4m3fn).float()
+        got.append(((n.unflatten(-1, (-1, 32)) * e[..., None]) * scale).flatten(-2).bfloat16())
+    return tuple(got)
+
+
+def _gathered(s):
+    """K and V [batch, kv_heads, positions, D] in 32 bits through the block tables."""
+    t = s["tables"].clamp(min=0).long()
+    k, v = _unpack(s["kc"][t], s["order"][0], K_SCALE), _unpack(s["vc"][t], s["order"][1], V_SCALE)
+    return k.transpose(1, 2).flatten(2, 3), v.transpose(1, 2).flatten(2, 3)
+
+
+def _attend(q, k, v, seen, scale):
+    """softmax over the seen positions; q [B, Hkv, rows, D], seen [B, 1, rows, positions]."""
+    x = (q @ k.transpose(-1, -2)).mul_(scale).masked_fill_(~seen, -math.inf)
+    x = x.sub_(x.amax(-1, keepdim=True)).exp_()
+    z = x.sum(-1, keepdim=True)
+    return (x @ v) / z
+
+
+def run(s):
+    c = s["case"]
+    if own:
+        import paged_kv_cache_159_gb300 as pkv
+        p = s["pool"]
+        if c["op"] == "decode":
+            if c["step"]:
+                pkv.decode_step(p, s["q"], s["k"], s["v"], s["kc"], s["vc"], s["tables"], s["lens"], s["scale"], s["out"], s["ws"])
+                pkv.kv_gather(p, s["slots"], s["kc"], s["vc"], s["k_read"], s["v_read"])
+                return s["out"], s["k_read"], s["v_read"]
+            pkv.paged_attention_decode(p, s["q"], s["kc"], s["vc"], s["tables"], s["lens"], s["scale"], s["out"], s["ws"])
+            return s["out"]
+        if c["op"] == "prefill":
+            pkv.paged_prefill(p, s["q"], s["kc"], s["vc"], s["tables"], s["scale"], s["plan"], s["grid"], s["out"])
+            return s["out"]
+        if c["op"] == "move":
+            pkv.move_blocks(p, s["kc"], s["vc"], s["src"], s["dst"], s["tables"])
+            return s["kc"], s["vc"], s["tables"]
+        if c["op"] == "append":
+            pkv.kv_append(p, s["k"], s["v"], s["slots"], s["kc"], s["vc"])
+        pkv.kv_gather(p, s["slots"], s["kc"], s["vc"], s["k_read"], s["v_read"])
+        return s["k_read"], s["v_read"]
+    if c["op"] == "decode":
+        if c["step"]:
+            _write(s)
+        k, v = _gathered(s)
+        q = s["q"].float().unflatten(1, (c["kv_heads"], -1))
+        seen = torch.arange(k.shape[2], device=q.device) < s["lens"][:, None, None, None]
+        out = _attend(q, k, v, seen, s["scale"]).flatten(1, 2).bfloat16()
+        return (out, *_read(s)) if c["step"] else out
+    if c["op"] == "prefill":
+        # every sequence's rows padded to the longest chunk
+        k, v = _gathered(s)
+        P, B = int(np.diff(s["cu"]).max()), c["batch"]
+        i = torch.arange(P, device="cuda")
+        real = i < s["P"][:, None]
+        q = torch.zeros(B, P, c["heads"], c["dim"], device="cuda")
+        q[real] = s["q"].float()
+        q = q.unflatten(2, (c["kv_heads"], -1)).permute(0, 2, 3, 1, 4).flatten(2, 3)          # [B, Hkv, g * P, D]
+        pos = ((s["lens"] - s["P"])[:, None] + i).clamp(max=k.shape[2] - 1)                   # row's own position
+        seen = torch.arange(k.shape[2], device="cuda") <= pos[:, :, None]                     # [B, P, positions]
+        seen = seen[:, None, None].expand(-1, 1, c["heads"] // c["kv_heads"], -1, -1).flatten(2, 3)
+        out = _attend(q, k, v, seen, s["scale"]).unflatten(2, (-1, P)).permute(0, 3, 1, 2, 4).flatten(2, 3)
+        return out[real].bfloat16()
+    if c["op"] == "move":
+        src, dst = s["src"].long(), s["dst"].long()
+        s["kc"][:, dst] = s["kc"][:, src]
+        s["vc"][:, dst] = s["vc"][:, src]
+        new = torch.arange(c["blocks"], device="cuda", dtype=torch.int32)
+        new[src] = s["dst"]
+        s["tables"].copy_(torch.where(s["tables"] < 0, s["tables"], new[s["tables"].clamp(min=0).long()]))
+        return s["kc"], s["vc"], s["tables"]
+    if c["op"] == "append":
+        _write(s)
+    return _read(s)
+
+
+# ------------------------------------------------------------------------------ the definition in 64 bits
+def _places(D, is_key):
+    """For (token, d) the byte and the shift of its code, and the byte of its scale, by the format's words."""
+    at, sh, sc = (np.zeros((BS, D), np.int64) for _ in range(3))
+    ng = D // 32
+    for t in range(BS):
+        for d in range(D):
+            j, e = divmod(d, 32)
+            if is_key:
+                r = 8 * (t // 8) + 2 * (t % 4) + t // 4 % 2
+                bit = 32 * (e // 8 * ng + j) + 16 * (e % 8 // 4) + 4 * (e % 4)
+                sc[t, d] = 8 * D + r * ng + j
+            else:
+                r = t
+                word = e // 4
+                if D == 128 and t // 2 % 2:
+                    word = (word + 4) % 8
+                bit = 16 * (word * ng + j) + 4 * (e % 4)
+                sc[t, d] = 8 * D + (t % 4) * 4 * ng + 4 * j + t // 4
+            at[t, d], sh[t, d] = r * D // 2 + bit // 8, bit % 8
+    return at, sh, sc
+
+
+def _e4m3_values():
+    x = []
+    for b in range(256):
+        e, m = b >> 3 & 15, b & 7
+        v = m / 8 * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7)
+        x.append(-v if b > 127 else v)
+    return x
+
+
+def _rows64(tiles, t, is_key, pool_scale):
+    """Rows t [n] of tiles [n, Hkv, bytes] in 64 bits: [n, Hkv, D]."""
+    D = tiles.shape[-1] * 2 // 17
+    at, sh, sc = (torch.from_numpy(x).cuda()[t] for x in _places(D, is_key))
+    grid = (torch.arange(tiles.shape[0], device="cuda")[:, None, None], torch.arange(tiles.shape[1], device="cuda")[None, :, None])
+    code = (tiles[(*grid, at[:, None, :])].int() >> sh[:, None, :].int()) & 15
+    scale = torch.tensor(_e4m3_values(), dtype=torch.float64, device="cuda")[tiles[(*grid, sc[:, None, :])].long()]
+    return (code.double() - 8) * scale * float(pool_scale)
+
+
+def _stored64(x, pool_scale):
+    """What a row x [n, Hkv, D] is after the append, from the format's definition in 64 bits."""
+    table = torch.tensor(_e4m3_values()[:127], dtype=torch.float64, device="cuda")
+    y = (x.double() / float(np.float32(pool_scale))).view(*x.shape[:-1], -1, 32)
+    a = (y.abs().max(-1).values / 7).clamp(max=448)
+    hi = torch.searchsorted(table, a.contiguous()).clamp(max=126)
+    lo = (hi - 1).clamp(min=0)
+    up, dn = table[hi] - a, a - table[lo]
+    k = torch.where((dn < up) | ((dn == up) & (lo % 2 == 0)), lo, hi)
+    s = table[k][..., None]
+    n = torch.where(s > 0, (y / s.clamp(min=1e-30)).round().clamp(-7, 7), 0.0)
+    return (n * s * float(pool_scale)).reshape(x.shape)
+
+
+def _sequence64(s, b, n):
+    """K and V [n, Hkv, D] of sequence b's first n positions in 64 bits."""
+    pos = torch.arange(n, device="cuda")
+    blk = s["tables"][b].long()[pos // BS]
+    return _rows64(s["kc"][blk], pos % BS, True, K_SCALE), _rows64(s["vc"][blk], pos % BS, False, V_SCALE)
+
+
+def exact(c, seed):
+    s = prepare(c, seed)
+    if c["op"] == "move":
+        at = dict(zip(s["src"].tolist(), s["dst"].tolist()))
+        for a, b in at.items():
+            for l in range(c["layers"]):
+                s["kc"][l, b], s["vc"][l, b] = s["kc"][l, a], s["vc"][l, a]
+        tables = torch.tensor([[at.get(x, x) for x in row] for row in s["tables"].tolist()], dtype=torch.int32)
+        return s["kc"].double(), s["vc"].double(), tables
+    if c["op"] == "gather":
+        blk, t = s["slots"] // BS, s["slots"] % BS
+        return _rows64(s["kc"][blk], t, True, K_SCALE), _rows64(s["vc"][blk], t, False, V_SCALE)
+    if c["op"] == "append":
+        return _stored64(s["k"], K_SCALE), _stored64(s["v"], V_SCALE)
+    new = (_stored64(s["k"], K_SCALE), _stored64(s["v"], V_SCALE)) if c.get("step") else None
+    lens, group = s["lens"].tolist(), c["heads"] // c["kv_heads"]
+    cu = s["cu"].tolist() if c["op"] == "prefill" else list(range(c["batch"] + 1))
+    out = []
+    for b, L in enumerate(lens):
+        k, v = _sequence64(s, b, L)
+        if new:
+            k[-1], v[-1] = new[0][b], new[1][b]
+        q = s["q"][cu[b] : cu[b + 1]].double()                                 # [rows, Hq, D]
+        rows = q.shape[0]
+        late = torch.arange(L, device="cuda")[None, :] > torch.arange(L - rows, L, device="cuda")[:, None]
+        o = torch.empty_like(q)
+        for h in range(c["heads"]):
+            w = q[:, h] @ k[:, h // group].T * s["scale"]
+            w = torch.softmax(w.masked_fill(late, -math.inf), -1)
+            o[:, h] = w @ v[:, h // group]
+        out.append(o)
+    out = torch.cat(out)
+    return (out, *new) if new else out
