@@ -62,7 +62,7 @@ typedef enum {
 #define PKV_DEVERR_TIMEOUT  0x8u   /* a pipeline wait exceeded its bound (about 1 s) */
 #define PKV_DEVERR_PLAN     0x10u  /* prefill: the plan does not match the call (nothing ran) */
 
-typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8E4M3 = 1 } pkv_kv_dtype;
+typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8E4M3 = 1, PKV_KV_INT4 = 2 } pkv_kv_dtype;
 
 /* Shape and element type of a paged K/V pool [Layout]: two caller-owned device tensors
  * key_cache and value_cache, each [num_layers, num_blocks, num_kv_heads, block_size,
@@ -74,7 +74,22 @@ typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8E4M3 = 1 } pkv_kv_dtype;
  * base of layer 0 and cover all layers in one launch.  num_layers 0 means 1; at most 4096,
  * with num_layers * num_blocks * num_kv_heads < 2^31.  FP8 pools store OCP E4M3 codes of
  * x / scale with one scale per tensor [Quant]; k_scale and v_scale must be positive and
- * finite (ignored for bf16). */
+ * finite (ignored for bf16).
+ *
+ * INT4 pools [Quant] keep each (block, KV head) tile of K or V in 17 * head_dim / 2 bytes, so
+ * that key_cache and value_cache are [num_layers, num_blocks, num_kv_heads, 17 * head_dim / 2]
+ * bytes: 4-bit codes n in 8 * head_dim bytes, then a scale byte (E4M3) per token and group of
+ * 32 columns.  An element stands for pool scale * scale * (n - 8), n - 8 in -7 .. 7 (a code
+ * 0 is never written and stands for -8).  With D = head_dim, the tile of token t and column d:
+ *   K: row r = (t & 8) | (t & 3) << 1 | (t >> 2 & 1) of D / 2 bytes; d = 32 j + 8 c + i lies in
+ *      the row's (little-endian) 32-bit word c * (D / 32) + j at bits 4 i; its scale is byte
+ *      8 D + r * (D / 32) + j;
+ *   V: row t of D / 2 bytes; d = 32 j + 4 c + i lies in the row's 16-bit word
+ *      c' * (D / 32) + j at bits 4 i, c' = c ^ 4 where D = 128 and t & 2 is set, else c; its
+ *      scale is byte 8 D + (t & 3) * (D / 8) + 4 j + (t >> 2).
+ * The pool scales bring the scale bytes into E4M3's range: a group's scale is its largest
+ * magnitude / (7 * pool scale), 448 at most; amax / (7 * 448) of the tensor fits every group,
+ * and 1 fits groups whose largest magnitude lies between about 0.11 and 3136. */
 typedef struct {
     int32_t num_blocks;
     int32_t block_size;
@@ -100,10 +115,14 @@ int pkv_pool_destroy(pkv_pool *pool);
 /* Copy the pool's descriptor to *out (num_layers >= 1). */
 int pkv_pool_get_desc(const pkv_pool *pool, pkv_pool_desc *out);
 
-/* Bytes of one layer of one cache tensor: num_blocks * num_kv_heads * block_size *
- * head_dim * element-bytes [Layout][Bytes].  Each of key_cache and value_cache holds
+/* Bytes of one layer of one cache tensor: num_blocks * num_kv_heads * pkv_pool_tile_bytes()
+ * [Layout][Bytes].  Each of key_cache and value_cache holds
  * num_layers times this.  0 for a NULL pool. */
 size_t pkv_pool_layer_bytes(const pkv_pool *pool);
+
+/* Bytes of one (block, KV head) tile of one cache tensor: block_size * head_dim *
+ * element-bytes, or 17 * head_dim / 2 for INT4 pools.  0 for a NULL pool. */
+size_t pkv_pool_tile_bytes(const pkv_pool *pool);
 
 /* Number of blocks currently free. */
 int pkv_pool_num_free(const pkv_pool *pool, int32_t *out);
@@ -228,7 +247,9 @@ int pkv_pool_attach_device(pkv_pool *pool, int device);
 /* Append K/V rows into their slots [Slot][Decode]: for each token t and KV head h with
  * slot = slot_mapping[t] >= 0, key_cache[slot/16][h][slot%16][:] = k[t][h][:] (bf16 bit
  * copy; FP8 pools store E4M3(fl32(k * fl32(1/k_scale))), round-to-nearest-even, saturated
- * to +-448), likewise V.  Device pointers: k, v bf16 [num_tokens, Hkv, D]; slot_mapping
+ * to +-448; INT4 pools quantise each group of 32 columns: with y = fl32(k * fl32(1/k_scale)),
+ * scale = E4M3(fl32(max|y| * fl32(1/7))) and n = clamp(rint(fl32(y * fl32(1/scale))), -7, 7) + 8,
+ * n = 8 where the scale is 0 or y is NaN), likewise V.  Device pointers: k, v bf16 [num_tokens, Hkv, D]; slot_mapping
  * int64 [num_tokens] (negative = padding, skipped); caches as in pkv_pool_desc.  A slot
  * beyond the pool sets PKV_DEVERR_SLOT and its row is skipped.  Slots must be distinct. */
 int pkv_kv_append(pkv_pool *pool, const void *k, const void *v, const int64_t *slot_mapping,
@@ -242,11 +263,27 @@ int pkv_kv_append_layers(pkv_pool *pool, const void *k, const void *v,
                          const int64_t *slot_mapping, int32_t num_tokens, void *key_cache,
                          void *value_cache, void *stream);
 
+/* Read K/V rows back [Slot]: for each token t with slot = slot_mapping[t] >= 0, k[t][h][:] and
+ * v[t][h][:] (device bf16 [num_tokens, Hkv, D], 16-byte aligned) receive what the pool holds at
+ * that slot: the stored bits of a bf16 pool; bf16(fl32(k_scale * element)) of FP8 and INT4
+ * pools, round-to-nearest-even (an INT4 element is scale * (n - 8), exact).  Rows of a negative
+ * slot (padding) stay as they were, and so do those of a slot beyond the pool, which sets
+ * PKV_DEVERR_SLOT.  Slots may repeat.  k and v must not overlap the caches. */
+int pkv_kv_gather(pkv_pool *pool, const int64_t *slot_mapping, int32_t num_tokens, const void *key_cache,
+                  const void *value_cache, void *k, void *v, void *stream);
+
+/* pkv_kv_gather for every layer of the pool in one launch: k, v are [num_layers, num_tokens,
+ * Hkv, D], key_cache and value_cache the whole stacked tensors. */
+int pkv_kv_gather_layers(pkv_pool *pool, const int64_t *slot_mapping, int32_t num_tokens,
+                         const void *key_cache, const void *value_cache, void *k, void *v, void *stream);
+
 /* Tuning knobs for pkv_paged_attention_decode_ex; zero fields mean "choose". */
 typedef struct {
     int32_t grid_ctas;        /* CTAs of the persistent grid (0 = SM count x CTAs per SM) */
     int32_t variant;          /* 0 = auto (3); 1 = CUDA-core dot products; 2 = tensor-core mma with
-                                 the heads as rows; 3 = tensor-core mma with the tokens as rows */
+                                 the heads as rows; 3 = tensor-core mma with the tokens as rows.
+                                 INT4 pools have one variant of their own (0), without
+                                 heads_per_copy and shared_prefix_blocks */
     int32_t warps_per_cta;    /* 0 = auto (4); 4 or 8 */
     int32_t stages;           /* 0 = auto (16 KiB of tiles per warp: 2 bf16 / 4 FP8 at D 128); 2..4 */
     int32_t heads_per_copy;   /* variant 3: KV heads loaded by one copy (the block's tiles of
@@ -295,7 +332,8 @@ size_t pkv_decode_workspace_bytes(const pkv_pool *pool, int32_t batch, int32_t n
  * so any physical placement of the blocks gives bit-identical output.  Requires
  * 1 <= batch <= 4096, num_q_heads a multiple of Hkv with group <= 16, an attached pool,
  * max_blocks >= 1, batch * max_blocks * Hkv < 2^31.  FP8 pools compute q.K with q rounded
- * to fp16 (|q| must stay below 65504).  An invalid seq_len sets PKV_DEVERR_SEQ_LEN and
+ * to fp16 (|q| must stay below 65504).  INT4 pools take q to fp16 with a power of two per
+ * (sequence, KV head) that keeps its largest element in range.  An invalid seq_len sets PKV_DEVERR_SEQ_LEN and
  * zeroes that sequence's output. */
 int pkv_paged_attention_decode(pkv_pool *pool, const void *q, const void *key_cache,
                                const void *value_cache, const int32_t *block_tables,

@@ -1,0 +1,145 @@
+"""The INT4 pool format and attention over it, restated plainly in numpy: codes and scales by
+the format's definition (fp32 where it says fp32), attention in 64 bits.  Shares no code with
+the library; places are computed one (token, column) at a time."""
+from __future__ import annotations
+
+import functools
+
+import numpy as np
+
+BS = 16
+GROUP = 32
+
+
+def tile_bytes(D: int) -> int:
+    return 8 * D + D // 2
+
+
+@functools.lru_cache(None)
+def e4m3_values():
+    """Value of each E4M3 byte (bias 7; 0x7F and 0xFF are NaN)."""
+    out = np.zeros(256)
+    for b in range(256):
+        e, m = (b >> 3) & 15, b & 7
+        v = m / 8 * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7)
+        if e == 15 and m == 7:
+            v = float("nan")
+        out[b] = -v if b & 128 else v
+    return out
+
+
+def e4m3_encode(x) -> np.ndarray:
+    """Bytes of non-negative fp32 values, nearest (ties to the even byte), saturating at 448."""
+    table = e4m3_values()[:127]
+    a = np.minimum(np.asarray(x, np.float64), 448.0)
+    hi = np.clip(np.searchsorted(table, a), 0, 126)
+    lo = np.maximum(hi - 1, 0)
+    up, dn = table[hi] - a, a - table[lo]
+    return np.where((dn < up) | ((dn == up) & (lo % 2 == 0)), lo, hi).astype(np.uint8)
+
+
+@functools.lru_cache(None)
+def places(D: int, is_key: bool):
+    """(byte, shift, scale byte) of every (token, column) of a tile, each [16, D]."""
+    at, sh, sc = (np.zeros((BS, D), np.int64) for _ in range(3))
+    ng = D // GROUP
+    for t in range(BS):
+        for d in range(D):
+            j, e = divmod(d, GROUP)
+            if is_key:
+                r = (t & 8) | (t & 3) << 1 | (t >> 2) & 1
+                c, i = divmod(e, 8)
+                bit = 32 * (c * ng + j) + 4 * i
+                sc[t, d] = 8 * D + r * ng + j
+            else:
+                r = t
+                c, i = divmod(e, 4)
+                if D == 128 and t & 2:
+                    c ^= 4
+                bit = 16 * (c * ng + j) + 4 * i
+                sc[t, d] = 8 * D + (t & 3) * (D // 8) + 4 * j + (t >> 2)
+            at[t, d], sh[t, d] = r * (D // 2) + bit // 8, bit % 8
+    return at, sh, sc
+
+
+def bf16_values(bits) -> np.ndarray:
+    return (np.asarray(bits, np.uint16).astype(np.uint32) << 16).view(np.float32)
+
+
+def quantise(bits, pool_scale: float):
+    """Codes [..., D] and scale bytes [..., D / 32] of bf16 rows, in the format's fp32 steps."""
+    x = bf16_values(bits)
+    with np.errstate(all="ignore"):
+        inv = np.float32(1) / np.float32(pool_scale)
+        y = (x * inv).reshape(*x.shape[:-1], -1, GROUP)
+        a = np.fmax.reduce(np.abs(y), axis=-1, initial=np.float32(0))
+        sb = e4m3_encode(a * (np.float32(1) / np.float32(7)))
+        s = e4m3_values()[sb].astype(np.float32)[..., None]
+        n = np.rint(y * (np.float32(1) / s))
+        n = np.where((s > 0) & ~np.isnan(y), np.clip(n, -7, 7), 0) + 8
+    return n.reshape(x.shape).astype(np.uint8), sb
+
+
+def append(k_bits, v_bits, slots, key_cache, value_cache, k_scale: float, v_scale: float):
+    """Write rows [T, Hkv, D] into their slots of caches uint8 [NB, Hkv, tile bytes], in place."""
+    D = k_bits.shape[-1]
+    for bits, cache, is_key, scale in ((k_bits, key_cache, True, k_scale), (v_bits, value_cache, False, v_scale)):
+        n, sb = quantise(bits, scale)
+        at, sh, sc = places(D, is_key)
+        for i, slot in enumerate(np.asarray(slots)):
+            if slot < 0:
+                continue
+            t = int(slot) % BS
+            tile = cache[int(slot) // BS]                       # [Hkv, bytes]
+            for x in (0, 4):                                    # low and high nibbles never share a byte
+                sel = sh[t] == x
+                tile[:, at[t, sel]] = (tile[:, at[t, sel]] & (0xF0 >> x)) | (n[i][:, sel] << x)
+            tile[:, sc[t, ::GROUP]] = sb[i]
+
+
+def rows(cache, slots, is_key: bool, pool_scale: float) -> np.ndarray:
+    """The elements [T, Hkv, D] that the slots hold, in 64 bits."""
+    D = cache.shape[-1] * 2 // 17
+    at, sh, sc = places(D, is_key)
+    slots = np.asarray(slots)
+    tiles, t = cache[slots // BS], slots % BS                   # [T, Hkv, bytes]
+    code = np.take_along_axis(tiles, np.broadcast_to(at[t][:, None], tiles.shape[:2] + (D,)), -1) >> sh[t][:, None]
+    sb = np.take_along_axis(tiles, np.broadcast_to(sc[t][:, None], tiles.shape[:2] + (D,)), -1)
+    return ((code & 15).astype(np.float64) - 8) * e4m3_values()[sb] * float(np.float32(pool_scale))
+
+
+def attend(q, k, v, scale: float):
+    """One query head over k, v [L, D]: the output, and sum_t p_t |v_t| (for error bounds)."""
+    s = (k @ q) * float(np.float32(scale))
+    p = np.exp(s - s.max())
+    p /= p.sum()
+    return p @ v, p @ np.abs(v)
+
+
+def sequence(key_cache, value_cache, table_row, L: int, k_scale: float, v_scale: float):
+    pos = np.arange(L)
+    slots = np.asarray(table_row)[pos // BS].astype(np.int64) * BS + pos % BS
+    return rows(key_cache, slots, True, k_scale), rows(value_cache, slots, False, v_scale)
+
+
+def decode(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_scale):
+    """q [B, Hq, D] -> (out, sum p |v|, score error unit), each [B, Hq, D] in 64 bits.  The score
+    error unit of (b, head) is scale * max_t sum_j |k scale_tj| sum_{d in j} |q_d|: a score's
+    absolute error per unit of relative error of its partial sums."""
+    q = bf16_values(q_bits).astype(np.float64)
+    B, Hq, D = q.shape
+    Hkv = key_cache.shape[1]
+    out, mag, unit = np.zeros_like(q), np.zeros_like(q), np.zeros_like(q)
+    sc = places(D, True)[2]
+    for b in range(B):
+        L = int(seq_lens[b])
+        k, v = sequence(key_cache, value_cache, tables[b], L, k_scale, v_scale)
+        pos = np.arange(L)
+        blk = np.asarray(tables[b])[pos // BS]
+        for h in range(Hq):
+            hk = h // (Hq // Hkv)
+            out[b, h], mag[b, h] = attend(q[b, h], k[:, hk], v[:, hk], scale)
+            sb = key_cache[blk[:, None], hk, sc[pos % BS][:, ::GROUP]]
+            ks = e4m3_values()[sb] * float(np.float32(k_scale))
+            unit[b, h] = scale * (ks @ np.abs(q[b, h]).reshape(-1, GROUP).sum(-1)).max()
+    return out, mag, unit

@@ -39,7 +39,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libpkv.so")
 OK, ERR_INVALID, ERR_OOM, ERR_DEVICE, ERR_TIMEOUT, ERR_CUDA = range(6)
 TEST_EXPIRE_NONE, TEST_EXPIRE_DECODE, TEST_EXPIRE_PREFILL = range(3)
 DEVERR_SLOT, DEVERR_BLOCK_ID, DEVERR_SEQ_LEN, DEVERR_TIMEOUT, DEVERR_PLAN = 0x1, 0x2, 0x4, 0x8, 0x10
-KV_BF16, KV_FP8E4M3 = 0, 1
+KV_BF16, KV_FP8E4M3, KV_INT4 = 0, 1, 2
 BLOCK_SIZE = 16
 
 EXPORTED = (
@@ -54,7 +54,7 @@ EXPORTED = (
     "pkv_decode_workspace_bytes", "pkv_paged_attention_decode",
     "pkv_paged_attention_decode_ex", "pkv_decode_step", "pkv_paged_attention_decode_noalloc",
     "pkv_get_device_error", "pkv_test_expire_waits", "pkv_probe_copy",
-    "pkv_device_sm_count", "pkv_status_string",
+    "pkv_device_sm_count", "pkv_status_string", "pkv_pool_tile_bytes", "pkv_kv_gather", "pkv_kv_gather_layers",
 )
 
 
@@ -118,6 +118,9 @@ def lib():
             "pkv_kv_append": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P]),
             "pkv_kv_append_layers": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P]),
             "pkv_pool_layer_bytes": (ctypes.c_size_t, [_P]),
+            "pkv_pool_tile_bytes": (ctypes.c_size_t, [_P]),
+            "pkv_kv_gather": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _P, _P]),
+            "pkv_kv_gather_layers": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _P, _P]),
             "pkv_cow_prepare": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _P, _P, ctypes.POINTER(_I32)]),
             "pkv_copy_blocks": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P]),
             "pkv_block_hashes": (ctypes.c_int, [_P, _I32, _I32, ctypes.c_uint64, _P]),
@@ -240,6 +243,10 @@ class Pool:
     def layer_bytes(self) -> int:
         """Bytes of one layer of one cache tensor (pkv_pool_layer_bytes)."""
         return int(lib().pkv_pool_layer_bytes(self._h))
+
+    def tile_bytes(self) -> int:
+        """Bytes of one (block, KV head) tile of one cache tensor (pkv_pool_tile_bytes)."""
+        return int(lib().pkv_pool_tile_bytes(self._h))
 
     def num_free(self) -> int:
         n = _I32()
@@ -414,6 +421,21 @@ def kv_append_layers(pool: Pool, k, v, slots, key_cache, value_cache, stream=Non
                                       _dev_ptr(key_cache, "key_cache"),
                                       _dev_ptr(value_cache, "value_cache"), _stream_ptr(stream)),
            "kv_append_layers")
+
+
+def kv_gather(pool: Pool, slots, key_cache, value_cache, k, v, stream=None):
+    """Read the rows of slots (int64 CUDA [T]) back into k, v (bf16 CUDA [T, Hkv, D])."""
+    _check(lib().pkv_kv_gather(pool.handle, _dev_ptr(slots, "slot_mapping"), int(slots.numel()),
+                               _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
+                               _dev_ptr(k, "k"), _dev_ptr(v, "v"), _stream_ptr(stream)), "kv_gather")
+
+
+def kv_gather_layers(pool: Pool, slots, key_cache, value_cache, k, v, stream=None):
+    """The same in every layer: k, v bf16 CUDA [layers, T, Hkv, D]; caches the stacked tensors."""
+    _check(lib().pkv_kv_gather_layers(pool.handle, _dev_ptr(slots, "slot_mapping"), int(slots.numel()),
+                                      _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
+                                      _dev_ptr(k, "k"), _dev_ptr(v, "v"), _stream_ptr(stream)),
+           "kv_gather_layers")
 
 
 def copy_blocks(pool: Pool, key_cache, value_cache, src, dst, stream=None):

@@ -70,7 +70,7 @@ extern "C" int pkv_copy_blocks(pkv_pool *pool, void *key_cache, void *value_cach
     const pkv_pool_desc &d = pool->desc;
     const int layers = d.num_layers;
     if ((int64_t)num_pairs * layers >= (int64_t)1 << 31) return PKV_ERR_INVALID;
-    const int64_t block_words = (int64_t)d.num_kv_heads * d.block_size * d.head_dim * pkv::elem_bytes(d) / 16;
+    const int64_t block_words = (int64_t)d.num_kv_heads * pkv::tile_bytes(d) / 16;
     pkv::copy_blocks_kernel<<<(unsigned)(num_pairs * layers), pkv::CB_THREADS, 0,
                               static_cast<cudaStream_t>(stream)>>>(
         src, dst, layers, d.num_blocks, block_words, static_cast<uint4 *>(key_cache),

@@ -1,0 +1,5 @@
+// decode_inst_d128_int4.cu -- decode kernels over INT4 pools for head_dim 128.
+#include "decode_int4.cuh"
+
+template cudaError_t pkv::decode::dispatch_int4<128>(const pkv::decode::Plan &, int, bool, int *, cudaStream_t,
+                                                      const pkv::decode::LaunchArgs *);

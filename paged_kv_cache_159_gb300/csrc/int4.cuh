@@ -1,0 +1,130 @@
+// int4.cuh -- the INT4 pool format: layout of a tile, quantisation of a row.
+//
+// "KV Cache 与推理优化" (note.yj-dis.top), section "KV 量化": K/V stored in few bits with
+// scales, the arithmetic in higher precision.  A tile (16 tokens of one KV head, K or V) is
+// 8 D bytes of codes followed by D / 2 bytes of scales.  Each token's row has a scale (E4M3)
+// per group of 32 columns and a 4-bit code n per column: the element is
+//     pool scale * scale * (n - 8),   n - 8 in -7 .. 7.
+//
+// The places follow from how the decode kernel's tensor-core products read them, so that a
+// lane fetches whole words and unpacks without moving bits between lanes:
+//   * K is the row operand of S^T = K Q^T (rows: tokens; k: columns).  Lane (gid, tid) needs
+//     the columns 32 j + 8 tid .. + 7 of mma rows gid and gid + 8 for every group j: they
+//     are consecutive 32-bit words, word tid * (D / 32) + j of a row.  Mma row r holds token
+//     t(r) with r = (t & 8) | (t & 3) << 1 | (t >> 2 & 1), and rows are stored in that order.
+//   * V is the row operand of O^T = V^T P^T (rows: columns d; k: tokens).  Lane (gid, tid)
+//     needs the columns 32 j + 4 gid .. + 3 of tokens tid, tid + 4, tid + 8, tid + 12: 16-bit
+//     words gid * (D / 32) + j of those rows, pairs of which interleave into f16 pairs (t,
+//     t + 4).  At D 128 the rows are 64 bytes, so four of them would share banks: rows
+//     with t & 2 set are stored with their halves swapped (gid ^ 4).
+//   * A lane's scales are consecutive as well: K byte r * (D / 32) + j; V byte
+//     (t & 3) * (D / 8) + 4 j + (t >> 2), four tokens of one group to a word.
+// Every byte belongs to one token, so tokens are written independently of each other.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+namespace int4 {
+
+constexpr int GROUP = 32;                     // columns per scale
+
+__host__ __device__ constexpr int tile_bytes(int D) { return 8 * D + D / 2; }
+
+// Byte offsets within a tile of token t's octet o (columns 8 o .. 8 o + 7): the 32-bit word
+// of K; the two 16-bit words of V (columns 8 o .. + 3 at the first, + 4 .. + 7 VSTEP bytes
+// on); the scale of group o / 4.
+template <int D>
+struct Place {
+    static constexpr int NG = D / GROUP;
+    static constexpr int VSTEP = 2 * NG;
+    __device__ static int k_row(int t) { return (t & 8) | ((t & 3) << 1) | ((t >> 2) & 1); }
+    __device__ static int k_word(int t, int o) { return k_row(t) * (D / 2) + ((o & 3) * NG + (o >> 2)) * 4; }
+    __device__ static int k_scale(int t, int o) { return 8 * D + k_row(t) * NG + (o >> 2); }
+    __device__ static int v_word(int t, int o)
+    {
+        const int c = 2 * (o & 3);
+        return t * (D / 2) + ((D == 128 ? c ^ ((t & 2) << 1) : c) * NG + (o >> 2)) * 2;
+    }
+    __device__ static int v_scale(int t, int o) { return 8 * D + (t & 3) * (4 * NG) + 4 * (o >> 2) + (t >> 2); }
+};
+
+// The value of a scale byte (E4M3, exact in fp32).
+__device__ __forceinline__ float scale_value(uint32_t byte)
+{
+    const uint32_t h = dev::e4m3x2_to_f16x2((uint16_t)byte);
+    return __low2float(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// Quantise an octet of a row (8 bf16; the 4 consecutive lanes of a group call it together):
+// the 8 codes, column 8 o + i at bits 4 i, and the group's scale byte.
+//   y = fl32(x * fl32(1 / pool scale)),  a = max |y| over the group (NaN ignored),
+//   scale = E4M3(fl32(a * fl32(1 / 7))) rounded to nearest even, saturating,
+//   n = clamp(rint(fl32(y * fl32(1 / scale))), -7, 7) + 8   (8 where the scale is 0 or y NaN).
+// Rounding the scale to nearest moves a by at most 1/16, so |y| / scale < 7.5 and the clamp
+// costs no more than half a step.
+__device__ __forceinline__ uint32_t quantise_octet(uint4 x, float inv_pool, uint32_t &scale_byte)
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float y[8], a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[2 * i] = dev::bf16_lo(w[i]) * inv_pool;
+        y[2 * i + 1] = dev::bf16_hi(w[i]) * inv_pool;
+        a = fmaxf(a, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+    }
+    a = fmaxf(a, __shfl_xor_sync(dev::FULL, a, 1));
+    a = fmaxf(a, __shfl_xor_sync(dev::FULL, a, 2));
+    scale_byte = dev::e4m3x2_satfinite(a * (1.0f / 7.0f), 0.f) & 0xffu;
+    const float s = scale_value(scale_byte), r = __frcp_rn(s);
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int n = s > 0.f ? max(-7, min(7, __float2int_rn(y[i] * r))) : 0;
+        codes |= (uint32_t)(n + 8) << (4 * i);
+    }
+    return codes;
+}
+
+// Token t's octet o of a K or V tile.
+template <int D>
+__device__ __forceinline__ void store_k(uint8_t *tile, int t, int o, uint32_t codes, uint32_t scale_byte)
+{
+    using P = Place<D>;
+    *reinterpret_cast<uint32_t *>(tile + P::k_word(t, o)) = codes;
+    if ((o & 3) == 0) tile[P::k_scale(t, o)] = (uint8_t)scale_byte;
+}
+
+template <int D>
+__device__ __forceinline__ void store_v(uint8_t *tile, int t, int o, uint32_t codes, uint32_t scale_byte)
+{
+    using P = Place<D>;
+    uint8_t *w = tile + P::v_word(t, o);
+    *reinterpret_cast<uint16_t *>(w) = (uint16_t)codes;
+    *reinterpret_cast<uint16_t *>(w + P::VSTEP) = (uint16_t)(codes >> 16);
+    if ((o & 3) == 0) tile[P::v_scale(t, o)] = (uint8_t)scale_byte;
+}
+
+// One warp writes token t's K and V rows (bf16, 16-byte aligned) into their tiles: lanes 0 ..
+// D / 8 - 1 take K's octets, lanes 16 .. 16 + D / 8 - 1 V's.
+template <int D>
+__device__ __forceinline__ void write_row_pair(const uint16_t *k, const uint16_t *v, float inv_k, float inv_v, int t,
+                                               uint8_t *ktile, uint8_t *vtile, int lane)
+{
+    const int o = lane & 15;
+    const bool isv = lane >= 16, mine = o < D / 8;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (mine) x = *reinterpret_cast<const uint4 *>((isv ? v : k) + 8 * o);
+    uint32_t sb;
+    const uint32_t codes = quantise_octet(x, isv ? inv_v : inv_k, sb);
+    if (!mine) return;
+    if (isv) store_v<D>(vtile, t, o, codes, sb);
+    else store_k<D>(ktile, t, o, codes, sb);
+}
+
+}  // namespace int4
+}  // namespace pkv

@@ -23,7 +23,16 @@ extern template cudaError_t pkv::decode::dispatch_nw_ns<64, true>(const pkv::dec
 
 namespace pkv {
 namespace decode {
+
+// decode_int4.cuh, compiled by decode_inst_*_int4.cu
+template <int D>
+cudaError_t dispatch_int4(const Plan &pl, int group, bool launch, int *per_sm, cudaStream_t s, const LaunchArgs *a);
+extern template cudaError_t dispatch_int4<64>(const Plan &, int, bool, int *, cudaStream_t, const LaunchArgs *);
+extern template cudaError_t dispatch_int4<128>(const Plan &, int, bool, int *, cudaStream_t, const LaunchArgs *);
+
 namespace {
+
+constexpr int INT4_WARPS = 4;
 
 int sm_count_cached()
 {
@@ -43,6 +52,9 @@ int sm_count_cached()
 cudaError_t dispatch(const pkv_pool_desc &d, const Plan &pl, int group, bool launch, int *per_sm,
                      cudaStream_t s, const LaunchArgs *p)
 {
+    if (d.kv_dtype == PKV_KV_INT4)
+        return d.head_dim == 128 ? dispatch_int4<128>(pl, group, launch, per_sm, s, p)
+                                 : dispatch_int4<64>(pl, group, launch, per_sm, s, p);
     const bool fp8 = d.kv_dtype == PKV_KV_FP8E4M3;
     if (d.head_dim == 128)
         return fp8 ? dispatch_nw_ns<128, true>(pl, group, launch, per_sm, s, p)
@@ -62,10 +74,13 @@ int make_plan(const pkv_pool_desc &d, int B, int Hq, int MB, const pkv_decode_op
     if ((long long)d.num_layers * B * d.num_kv_heads >= (1LL << 31)) return PKV_ERR_INVALID;
     pkv_decode_opts z{};
     if (!o) o = &z;
-    pl.variant = o->variant ? o->variant : 3;
-    if (pl.variant < 1 || pl.variant > 3) return PKV_ERR_INVALID;
+    // an INT4 pool has one variant of its own (plan variant 0), without the options of variant 3
+    const bool i4 = d.kv_dtype == PKV_KV_INT4;
+    if (i4 && (o->variant != 0 || o->heads_per_copy > 1)) return PKV_ERR_INVALID;
+    pl.variant = o->variant || i4 ? o->variant : 3;
+    if (pl.variant < 0 || pl.variant > 3) return PKV_ERR_INVALID;
     if (pl.variant == 1 && group > 8) return PKV_ERR_INVALID;
-    pl.nw = o->warps_per_cta ? o->warps_per_cta : 4;
+    pl.nw = o->warps_per_cta ? o->warps_per_cta : i4 ? INT4_WARPS : 4;
     if (pl.variant == 3) {
         if (o->heads_per_copy) {
             pl.hp = o->heads_per_copy;
@@ -79,14 +94,13 @@ int make_plan(const pkv_pool_desc &d, int B, int Hq, int MB, const pkv_decode_op
         pl.hp = 1;
     }
     // default ring: 16 KiB of tiles per warp (2 bf16 or 4 FP8 stages at head_dim 128)
-    pl.ns = o->stages ? o->stages : (elem_bytes(d) == 1 && pl.variant >= 2 ? 4 : 2);
+    pl.ns = o->stages ? o->stages : i4 ? 32 / pl.nw : (elem_bytes(d) == 1 && pl.variant >= 2 ? 4 : 2);
     if (o->grid_ctas < 0 || o->shared_prefix_blocks < 0) return PKV_ERR_INVALID;
     pl.sp = o->shared_prefix_blocks;
     if (pl.sp > 0 && (pl.variant != 3 || pl.hp != 1)) return PKV_ERR_INVALID;
     if (o->unit_cost < -1 || o->unit_cost > 4096) return PKV_ERR_INVALID;
     pl.uc = o->unit_cost == 0 ? 16 : (o->unit_cost < 0 ? 0 : o->unit_cost);
-    const int tile = BS * d.head_dim * elem_bytes(d);
-    pl.smem = Layout(pl.nw, pl.ns, tile, d.head_dim, group, B, pl.hp).total + 1024;   // + alignment slack
+    pl.smem = Layout(pl.nw, pl.ns, tile_bytes(d), d.head_dim, group, B, pl.hp).total + 1024;   // + alignment slack
     if (pl.smem > 227 * 1024) return PKV_ERR_INVALID;
     if (o->grid_ctas) {
         pl.grid = o->grid_ctas;

@@ -44,7 +44,12 @@ int test_expire();
 
 // Validation shared by the CUDA entry points.
 int check_attached(const pkv_pool *pool);
-inline int elem_bytes(const pkv_pool_desc &d) { return d.kv_dtype == PKV_KV_FP8E4M3 ? 1 : 2; }
+inline int elem_bytes(const pkv_pool_desc &d) { return d.kv_dtype == PKV_KV_FP8E4M3 ? 1 : 2; }    // bf16, FP8 pools
+// Bytes of one (block, KV head) tile of K or V (INT4: 4-bit codes and a scale byte per 32 columns).
+inline int tile_bytes(const pkv_pool_desc &d)
+{
+    return d.kv_dtype == PKV_KV_INT4 ? 8 * d.head_dim + d.head_dim / 2 : d.block_size * d.head_dim * elem_bytes(d);
+}
 
 namespace decode {
 // Every host-side check of pkv_paged_attention_decode with batch >= 1 (arguments, alignment,

@@ -27,8 +27,8 @@ bool valid_desc(const pkv_pool_desc *d)
     if (!d) return false;
     if (d->num_blocks < 1 || d->block_size != 16 || d->num_kv_heads < 1) return false;
     if (d->head_dim != 64 && d->head_dim != 128) return false;
-    if (d->kv_dtype != PKV_KV_BF16 && d->kv_dtype != PKV_KV_FP8E4M3) return false;
-    if (d->kv_dtype == PKV_KV_FP8E4M3) {
+    if (d->kv_dtype != PKV_KV_BF16 && d->kv_dtype != PKV_KV_FP8E4M3 && d->kv_dtype != PKV_KV_INT4) return false;
+    if (d->kv_dtype != PKV_KV_BF16) {
         if (!(d->k_scale > 0.0f) || !std::isfinite(d->k_scale)) return false;
         if (!(d->v_scale > 0.0f) || !std::isfinite(d->v_scale)) return false;
     }
@@ -114,7 +114,7 @@ int pkv_pool_create(const pkv_pool_desc *desc, const int32_t *free_order, pkv_po
     } else {
         for (int32_t i = 0; i < nb; ++i) p->free_list.push_back(i);
     }
-    if (desc->kv_dtype == PKV_KV_FP8E4M3) {
+    if (desc->kv_dtype != PKV_KV_BF16) {
         p->inv_k_scale = 1.0f / desc->k_scale;
         p->inv_v_scale = 1.0f / desc->v_scale;
     } else {
@@ -152,8 +152,10 @@ size_t pkv_pool_layer_bytes(const pkv_pool *pool)
 {
     if (!pool) return 0;
     const pkv_pool_desc &d = pool->desc;
-    return (size_t)d.num_blocks * d.num_kv_heads * d.block_size * d.head_dim * pkv::elem_bytes(d);
+    return (size_t)d.num_blocks * d.num_kv_heads * pkv::tile_bytes(d);
 }
+
+size_t pkv_pool_tile_bytes(const pkv_pool *pool) { return pool ? (size_t)pkv::tile_bytes(pool->desc) : 0; }
 
 int pkv_pool_num_free(const pkv_pool *pool, int32_t *out)
 {

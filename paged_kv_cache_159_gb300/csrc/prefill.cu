@@ -876,6 +876,7 @@ extern "C" int pkv_paged_prefill(pkv_pool *pool, const void *q, const void *key_
     int st = pkv::check_attached(pool);
     if (st != PKV_OK) return st;
     const pkv_pool_desc &d = pool->desc;
+    if (d.kv_dtype == PKV_KV_INT4) return PKV_ERR_INVALID;
     if (batch < 1 || num_q_heads < 1 || max_blocks < 1 || total_q < 0 || grid < 1 || !std::isfinite(scale))
         return PKV_ERR_INVALID;
     if (total_q == 0) return PKV_OK;
