@@ -258,6 +258,7 @@ def prepare(c, seed):
             else:
                 plan, s["grid"] = pkv.prefill_plan(s["pool"], s["cu"], L, c["heads"], s["tables"].shape[1])
                 s["plan"] = torch.from_numpy(plan).cuda()
+                s["ws"] = torch.empty(pkv.prefill_workspace_bytes(s["pool"], s["cu"], L, s["tables"].shape[1]), dtype=torch.uint8, device="cuda")
     elif c["op"] in ("append", "gather"):
         T = c["tokens"]
         s["kc"], s["vc"] = _pool_tensors(g, c["blocks"], Hkv, D)
@@ -338,7 +339,7 @@ def run(s):
             pkv.paged_attention_decode(p, s["q"], s["kc"], s["vc"], s["tables"], s["lens"], s["scale"], s["out"], s["ws"])
             return s["out"]
         if c["op"] == "prefill":
-            pkv.paged_prefill(p, s["q"], s["kc"], s["vc"], s["tables"], s["scale"], s["plan"], s["grid"], s["out"])
+            pkv.paged_prefill(p, s["q"], s["kc"], s["vc"], s["tables"], s["scale"], s["plan"], s["grid"], s["out"], workspace=s["ws"])
             return s["out"]
         if c["op"] == "move":
             pkv.move_blocks(p, s["kc"], s["vc"], s["src"], s["dst"], s["tables"])
