@@ -175,6 +175,47 @@ int pkv_cow_prepare(pkv_pool *pool, int32_t *tables, const int32_t *seq_lens, in
 int pkv_copy_blocks(pkv_pool *pool, void *key_cache, void *value_cache, const int32_t *src,
                     const int32_t *dst, int32_t num_pairs, void *stream);
 
+/* Fork a sequence [Paged][Life]: num_forks rows of tables_out (host int32 [num_forks,
+ * max_blocks]) continue the sequence of seq_len positions whose row is table_row (host,
+ * ceil(seq_len / block_size) entries or more).  Its full blocks are shared, one more reference
+ * for each fork; a partly filled last block gets a fresh copy for each fork, from the front of
+ * the free list: src_out[i], dst_out[i] (host int32, room for num_forks entries each), and
+ * *num_copies of them -- run pkv_copy_blocks on the pairs before the forks append.  Unused
+ * entries are -1.  The sequence itself keeps its blocks and may append without a copy of its
+ * last block.  INVALID (nothing changed) if seq_len < 1 or needs more than max_blocks entries,
+ * or an entry is not an allocated block; OOM (nothing changed) if the free list is too short.
+ * tables_out must not overlap table_row. */
+int pkv_fork_tables(pkv_pool *pool, const int32_t *table_row, int32_t seq_len, int32_t num_forks,
+                    int32_t max_blocks, int32_t *tables_out, int32_t *src_out, int32_t *dst_out,
+                    int32_t *num_copies);
+
+/* Compact the pool [Life]: at most max_moves times, the allocated block with the highest id
+ * moves to the free id that is lowest, while that is lower.  Move i is src_out[i] (strictly
+ * descending) to dst_out[i] (ascending), host int32 with room for max_moves entries each;
+ * *num_moves receives their count.  Without a limit (max_moves >= num_blocks / 2) the
+ * allocated blocks end up as ids 0 .. n-1.  References and the prefix cache's entries follow
+ * the blocks; the remaining free ids keep their order, then come the vacated ones in the
+ * order of the moves.  The content and the block tables are not touched here: run
+ * pkv_move_blocks (content and device tables) and pkv_remap_tables (host tables) before the
+ * pool is used or allocates again.  OOM (nothing changed) if host memory runs out. */
+int pkv_pool_compact(pkv_pool *pool, int32_t max_moves, int32_t *src_out, int32_t *dst_out, int32_t *num_moves);
+
+/* Replace every entry of tables (host, num_entries) that equals a src[i] with dst[i].  INVALID
+ * (nothing changed) if src is not strictly descending. */
+int pkv_remap_tables(int32_t *tables, int64_t num_entries, const int32_t *src, const int32_t *dst,
+                     int32_t num_moves);
+
+/* The moves of a compaction on the device, in one launch [Life][Layout]: for every move i and
+ * every layer the K and V content of block src[i] is copied to block dst[i], and every entry of
+ * block_tables (device int32, num_entries of them; NULL with 0) that equals a src[i] becomes
+ * dst[i].  src, dst: device int32, num_moves entries, src strictly descending (else entries of
+ * the tables may stay as they are); the dst ids distinct and none of them a src, as
+ * pkv_pool_compact gives them.  caches: the whole stacked tensors.  A move with an id outside
+ * [0, num_blocks) sets PKV_DEVERR_BLOCK_ID and is skipped. */
+int pkv_move_blocks(pkv_pool *pool, void *key_cache, void *value_cache, const int32_t *src,
+                    const int32_t *dst, int32_t num_moves, int32_t *block_tables, int64_t num_entries,
+                    void *stream);
+
 /* Slot of each sequence's newest token, at position seq_lens[b]-1 [Slot]:
  * slot = tables[b][(L-1) / block_size] * block_size + (L-1) % block_size.  Host arrays:
  * tables int32 [batch, max_blocks], seq_lens int32 [batch], slots_out int64 [batch].
@@ -417,6 +458,21 @@ int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const int32_t *s
 int pkv_paged_prefill(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
                       const int32_t *block_tables, int32_t batch, int32_t num_q_heads, int32_t max_blocks,
                       int32_t total_q, float scale, const void *plan, int32_t grid, void *out, void *stream);
+
+/* The same with a workspace, which INT4 pools need (pkv_paged_prefill refuses them; other
+ * pools ignore it): the blocks that the batch's sequences with rows use are expanded to bf16
+ * there by one more launch, exactly, and attended over as a bf16 pool's.  workspace: device
+ * memory, 256-byte aligned, of at least pkv_prefill_workspace_bytes() bytes for the cu_q,
+ * seq_lens and max_blocks that the plan was made with (host arrays; 0 for other pools and for
+ * invalid shapes); its content before and after is unspecified, and calls sharing it must not
+ * overlap on the GPU.  A workspace too small for the plan sets PKV_DEVERR_PLAN and computes
+ * nothing; one too small for a single block is INVALID. */
+size_t pkv_prefill_workspace_bytes(const pkv_pool *pool, const int32_t *cu_q, const int32_t *seq_lens,
+                                   int32_t batch, int32_t max_blocks);
+int pkv_paged_prefill_ex(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
+                         const int32_t *block_tables, int32_t batch, int32_t num_q_heads, int32_t max_blocks,
+                         int32_t total_q, float scale, const void *plan, int32_t grid, void *out,
+                         void *workspace, size_t workspace_bytes, void *stream);
 
 /* Host side of one decode step, for pkv_decode_step_host: host memory, page-locked (pinned)
  * for the copies to be asynchronous.  block_tables and seq_lens may be NULL when the device

@@ -143,3 +143,24 @@ def decode(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_s
             ks = e4m3_values()[sb] * float(np.float32(k_scale))
             unit[b, h] = scale * (ks @ np.abs(q[b, h]).reshape(-1, GROUP).sum(-1)).max()
     return out, mag, unit
+
+
+def prefill(q_bits, key_cache, value_cache, tables, seq_lens, cu_q, scale, k_scale, v_scale):
+    """q [T, Hq, D]: row cu_q[b] + i attends over positions 0 .. L_b - P_b + i of sequence b; (out,
+    sum p |v|) in 64 bits."""
+    q = bf16_values(q_bits).astype(np.float64)
+    Hq, Hkv = q.shape[1], key_cache.shape[1]
+    out, mag = np.zeros_like(q), np.zeros_like(q)
+    for b, L in enumerate(np.asarray(seq_lens).tolist()):
+        r0, r1 = int(cu_q[b]), int(cu_q[b + 1])
+        if r1 == r0:
+            continue
+        k, v = sequence(key_cache, value_cache, tables[b], L, k_scale, v_scale)
+        for h in range(Hq):
+            hk = h // (Hq // Hkv)
+            s = q[r0:r1, h] @ k[:, hk].T * float(np.float32(scale))
+            s[np.arange(L)[None, :] > np.arange(L - (r1 - r0), L)[:, None]] = -np.inf
+            p = np.exp(s - s.max(-1, keepdims=True))
+            p /= p.sum(-1, keepdims=True)
+            out[r0:r1, h], mag[r0:r1, h] = p @ v[:, hk], p @ np.abs(v[:, hk])
+    return out, mag

@@ -66,6 +66,7 @@
 #include <queue>
 #include <vector>
 
+#include "int4.cuh"
 #include "pkv_internal.h"
 #include "tc_device.cuh"
 
@@ -82,13 +83,112 @@ constexpr float TAU = 8.0f;        // raise the running max only beyond 2^8
 constexpr uint32_t PLAN_MAGIC = 0x504b5650u;   // "PVKP"
 constexpr uint32_t TMEM_COLS = 512;            // S (and P over it): 2 buffers x 2 q-tiles x 64, O: 2 x D
 
-// A plan: header, per-CTA unit ranges, units.
-struct PlanHeader { uint32_t magic; int32_t num_units, grid, group, tp, hq, hkv, pad; };
+// A plan: header, per-CTA unit ranges, units; for INT4 pools (batch > 0) the expanded blocks
+// before each sequence as well (batch + 1 entries).
+struct PlanHeader { uint32_t magic; int32_t num_units, grid, group, tp, hq, hkv, batch; };
 struct Unit { int32_t b, h, row0, pos0, npos, nkv, kmax, pad; };
 
 __host__ __device__ inline size_t plan_units_offset(int grid)
 {
     return (sizeof(PlanHeader) + sizeof(int32_t) * (size_t)(grid + 1) + 31) / 32 * 32;
+}
+
+__host__ __device__ inline size_t plan_expand_offset(int grid, size_t units)
+{
+    return plan_units_offset(grid) + units * sizeof(Unit);
+}
+
+// ------------------------------------------------------------------------------------
+// INT4 pools.  Every query tile of 256 rows reads all keys before it, so a chunk of P positions
+// would unpack each K/V element P g / 256 times; converting inside the attention kernel also
+// competes with its softmax (the E4M3 path runs at 0.68 of the bf16 one).  Instead one kernel
+// expands the blocks that the batch's sequences use into bf16 tiles in the workspace, once --
+// exactly: scale * (n - 8) has 4 + 3 significant bits -- with block tables of its own, and the
+// bf16 attention kernel runs over those; the pool's scales go where a bf16 pool's 1 goes.  It
+// moves 17/32 bytes in and 2 out per element, bound by DRAM.
+//
+// Workspace: int32 tables [batch][max_blocks], then K and V [blocks][Hkv][16][D] bf16.
+// ------------------------------------------------------------------------------------
+struct ExpandParams {
+    const uint8_t *plan;
+    const int32_t *tables;
+    const uint8_t *key_cache, *value_cache;
+    int32_t *ws_tables;
+    uint16_t *ws_k, *ws_v;
+    uint32_t *err;
+    int B, MB, Hkv, num_blocks, capacity, grid;       // capacity: blocks that the workspace holds
+};
+
+constexpr int EXPAND_THREADS = 256;
+
+// (n - 8) * scale of the codes at bits 0-3 of each half of w, as bf16 pairs: 128 + n by an
+// and-or, then exact arithmetic.
+__device__ __forceinline__ uint32_t expand_pair(uint32_t w, __nv_bfloat162 scale)
+{
+    const uint32_t x = (w & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), __float2bfloat162_rn(136.f)), scale);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Octet of codes (column i at bits 4 i) to 8 bf16.
+__device__ __forceinline__ uint4 expand_octet(uint32_t codes, uint32_t scale_byte)
+{
+    const __nv_bfloat162 s = __float2bfloat162_rn(int4::scale_value(scale_byte));
+    // halves hold columns 0-3 and 4-7: pairs (0, 4), (1, 5), (2, 6), (3, 7)
+    const uint32_t a = expand_pair(codes, s), b = expand_pair(codes >> 4, s), c = expand_pair(codes >> 8, s),
+                   d = expand_pair(codes >> 12, s);
+    return make_uint4(__byte_perm(a, b, 0x5410u), __byte_perm(c, d, 0x5410u), __byte_perm(a, b, 0x7632u),
+                      __byte_perm(c, d, 0x7632u));
+}
+
+// A CTA per expanded block (a grid stride apart), a warp per KV head.
+template <int D>
+__global__ void __launch_bounds__(EXPAND_THREADS) prefill_expand_kernel(const ExpandParams p)
+{
+    using P = int4::Place<D>;
+    constexpr int OCTETS = D / 8, TPP = 32 / OCTETS;             // octets of a row, tokens per pass
+    const PlanHeader *hdr = reinterpret_cast<const PlanHeader *>(p.plan);
+    if (hdr->magic != PLAN_MAGIC || hdr->grid != p.grid || hdr->batch != p.B) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_PLAN);
+        return;
+    }
+    const int32_t *off = reinterpret_cast<const int32_t *>(p.plan + plan_expand_offset(hdr->grid, (size_t)hdr->num_units));
+    const int total = off[p.B];
+    if (total > p.capacity) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_PLAN);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, o = lane % OCTETS, t0 = lane / OCTETS;
+    for (int x = blockIdx.x; x < total; x += gridDim.x) {
+        int lo = 0, hi = p.B;                                    // off[lo] <= x < off[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(off + mid) <= x) lo = mid;
+            else hi = mid;
+        }
+        const int j = x - __ldg(off + lo);
+        const int id = __ldg(p.tables + (size_t)lo * p.MB + j);
+        const bool ok = id >= 0 && id < p.num_blocks;
+        if (threadIdx.x == 0) {
+            if (!ok) dev::flag_error(p.err, PKV_DEVERR_BLOCK_ID);
+            p.ws_tables[(size_t)lo * p.MB + j] = ok ? x : -1;
+        }
+        if (!ok) continue;
+        for (int h = warp; h < p.Hkv; h += EXPAND_THREADS / 32) {
+            const size_t tile = ((size_t)id * p.Hkv + h) * int4::tile_bytes(D), out = ((size_t)x * p.Hkv + h) * (16 * D);
+            const uint8_t *kt = p.key_cache + tile, *vt = p.value_cache + tile;
+            uint4 *ko = reinterpret_cast<uint4 *>(p.ws_k + out), *vo = reinterpret_cast<uint4 *>(p.ws_v + out);
+#pragma unroll
+            for (int t = t0; t < 16; t += TPP) {
+                const uint8_t *w = vt + P::v_word(t, o);
+                const uint32_t kc = __ldg(reinterpret_cast<const uint32_t *>(kt + P::k_word(t, o)));
+                const uint32_t vc = __ldg(reinterpret_cast<const uint16_t *>(w)) |
+                                    ((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(w + P::VSTEP)) << 16);
+                ko[t * OCTETS + o] = expand_octet(kc, __ldg(kt + P::k_scale(t, o)));
+                vo[t * OCTETS + o] = expand_octet(vc, __ldg(vt + P::v_scale(t, o)));
+            }
+        }
+    }
 }
 
 struct Params {
@@ -100,6 +200,7 @@ struct Params {
     float score_scale;           // scale * k_scale * log2(e)
     float out_scale;             // v_scale (1 for bf16 pools)
     int test_stall;              // failure-path test: the Q loader waits on a barrier nothing completes
+    int expanded;                // sequences of an INT4 call (tables and caches are the workspace's), or 0
 };
 
 template <int D, bool FP8>
@@ -167,7 +268,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const int32_t *cta_off = reinterpret_cast<const int32_t *>(p.plan + sizeof(PlanHeader));
     const Unit *units = reinterpret_cast<const Unit *>(p.plan + plan_units_offset(p.grid));
     if (hdr->magic != PLAN_MAGIC || hdr->grid != p.grid || hdr->group != p.group || hdr->hq != p.Hq ||
-        hdr->hkv != p.Hkv || hdr->tp != p.TP) {
+        hdr->hkv != p.Hkv || hdr->tp != p.TP || hdr->batch != p.expanded ||
+        (p.expanded > 0 && reinterpret_cast<const int32_t *>(p.plan + plan_expand_offset(hdr->grid, (size_t)hdr->num_units))[p.expanded] > p.num_blocks)) {
         if (tid == 0 && blockIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_PLAN);
         return;
     }
@@ -714,6 +816,50 @@ cudaError_t launch(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorM
 
 int tile_positions(int group) { return 2 * BM / group; }
 
+// Workspace of an INT4 call: the expanded tables, then K and V of `blocks` blocks.
+size_t ws_tables_bytes(int batch, int max_blocks) { return ((size_t)batch * max_blocks * 4 + 255) / 256 * 256; }
+size_t ws_block_bytes(const pkv_pool_desc &d) { return (size_t)d.num_kv_heads * BS * d.head_dim * 2; }
+
+// Expand the batch's blocks (see ExpandParams); the caches and tables that the attention kernel
+// then reads replace key_cache, value_cache and tables.
+int expand(const pkv_pool *pool, const void *&key_cache, const void *&value_cache, const int32_t *&tables, int batch,
+           int max_blocks, const void *plan, int grid, void *workspace, size_t workspace_bytes, int &num_blocks, cudaStream_t s)
+{
+    const pkv_pool_desc &d = pool->desc;
+    const size_t head = ws_tables_bytes(batch, max_blocks), block = ws_block_bytes(d);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < head + 2 * block) return PKV_ERR_INVALID;
+    // the attention kernel's (block, head) tile index is a 32-bit number
+    const size_t most = (((size_t)1 << 31) - 1) / (size_t)d.num_kv_heads;
+    const size_t capacity = std::min((workspace_bytes - head) / (2 * block), most);
+    const int sms = sm_count();
+    if (sms < 1) return PKV_ERR_CUDA;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    ExpandParams p;
+    p.plan = static_cast<const uint8_t *>(plan);
+    p.tables = tables;
+    p.key_cache = static_cast<const uint8_t *>(key_cache);
+    p.value_cache = static_cast<const uint8_t *>(value_cache);
+    p.ws_tables = reinterpret_cast<int32_t *>(ws);
+    p.ws_k = reinterpret_cast<uint16_t *>(ws + head);
+    p.ws_v = reinterpret_cast<uint16_t *>(ws + head + capacity * block);
+    p.err = pool->d_err;
+    p.B = batch;
+    p.MB = max_blocks;
+    p.Hkv = d.num_kv_heads;
+    p.num_blocks = d.num_blocks;
+    p.capacity = (int)capacity;
+    p.grid = grid;
+    const unsigned ctas = (unsigned)std::min<int64_t>((int64_t)sms * 8, (int64_t)batch * max_blocks);
+    if (d.head_dim == 128) prefill_expand_kernel<128><<<ctas, EXPAND_THREADS, 0, s>>>(p);
+    else prefill_expand_kernel<64><<<ctas, EXPAND_THREADS, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+    key_cache = p.ws_k;
+    value_cache = p.ws_v;
+    tables = p.ws_tables;
+    num_blocks = p.capacity;
+    return PKV_OK;
+}
+
 }  // namespace prefill
 }  // namespace pkv
 
@@ -727,7 +873,24 @@ extern "C" size_t pkv_prefill_plan_bytes(const pkv_pool *pool, int32_t batch, in
     const int tp = tile_positions(g);
     const size_t units = (size_t)pool->desc.num_kv_heads * ((size_t)total_q / tp + batch);
     const int grid = std::max(1, sm_count());
-    return plan_units_offset(grid) + units * sizeof(Unit);
+    const size_t more = pool->desc.kv_dtype == PKV_KV_INT4 ? ((size_t)batch + 1) * sizeof(int32_t) : 0;
+    return plan_expand_offset(grid, units) + more;
+}
+
+extern "C" size_t pkv_prefill_workspace_bytes(const pkv_pool *pool, const int32_t *cu_q, const int32_t *seq_lens,
+                                              int32_t batch, int32_t max_blocks)
+{
+    using namespace pkv::prefill;
+    if (!pool || !cu_q || !seq_lens || batch < 1 || max_blocks < 1 || pool->desc.kv_dtype != PKV_KV_INT4) return 0;
+    size_t blocks = 0;
+    for (int b = 0; b < batch; ++b) {
+        const int64_t P = (int64_t)cu_q[b + 1] - cu_q[b], L = seq_lens[b];
+        if (P < 0 || L < P || L < 1 || (L + BS - 1) / BS > max_blocks) return 0;
+        if (P > 0) blocks += (size_t)((L + BS - 1) / BS);
+    }
+    if (blocks == 0) blocks = 1;
+    if (blocks >= ((size_t)1 << 31) / (size_t)pool->desc.num_kv_heads) return 0;
+    return ws_tables_bytes(batch, max_blocks) + 2 * blocks * ws_block_bytes(pool->desc);
 }
 
 extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const int32_t *seq_lens,
@@ -766,7 +929,8 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
     const int sms = sm_count();
     if (sms < 1) return PKV_ERR_CUDA;
     const int grid = std::max(1, std::min<int>(sms, (int)units.size()));
-    const size_t need = plan_units_offset(grid) + units.size() * sizeof(Unit);
+    const bool i4 = pool->desc.kv_dtype == PKV_KV_INT4;
+    const size_t need = plan_expand_offset(grid, units.size()) + (i4 ? ((size_t)batch + 1) * sizeof(int32_t) : 0);
     if (need > plan_bytes) return PKV_ERR_INVALID;
     // A unit costs its K/V tiles plus about three tile-times of its own: waiting for its Q
     // rows, the S -> softmax -> P.V chain filling and draining, and writing its output
@@ -853,7 +1017,7 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
     for (auto &v : per)
         std::sort(v.begin(), v.end(), [&](int a, int b) { return rank[(size_t)a] < rank[(size_t)b]; });
     uint8_t *out = static_cast<uint8_t *>(plan_out);
-    PlanHeader hdr{PLAN_MAGIC, (int32_t)units.size(), grid, g, tp, num_q_heads, Hkv, 0};
+    PlanHeader hdr{PLAN_MAGIC, (int32_t)units.size(), grid, g, tp, num_q_heads, Hkv, i4 ? batch : 0};
     std::memcpy(out, &hdr, sizeof(hdr));
     int32_t *off = reinterpret_cast<int32_t *>(out + sizeof(PlanHeader));
     Unit *dst = reinterpret_cast<Unit *>(out + plan_units_offset(grid));
@@ -863,6 +1027,14 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
         for (int i : per[(size_t)c]) dst[n++] = units[(size_t)i];
     }
     off[grid] = n;
+    if (i4) {
+        int32_t *ex = reinterpret_cast<int32_t *>(out + plan_expand_offset(grid, units.size())), at = 0;
+        for (int b = 0; b < batch; ++b) {
+            ex[b] = at;
+            if (cu_q[b + 1] > cu_q[b]) at += (seq_lens[b] - 1) / BS + 1;
+        }
+        ex[batch] = at;
+    }
     *grid_out = grid;
     return PKV_OK;
 }
@@ -872,11 +1044,19 @@ extern "C" int pkv_paged_prefill(pkv_pool *pool, const void *q, const void *key_
                                  int32_t max_blocks, int32_t total_q, float scale, const void *plan,
                                  int32_t grid, void *out, void *stream)
 {
+    return pkv_paged_prefill_ex(pool, q, key_cache, value_cache, block_tables, batch, num_q_heads, max_blocks, total_q,
+                                scale, plan, grid, out, nullptr, 0, stream);
+}
+
+extern "C" int pkv_paged_prefill_ex(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
+                                    const int32_t *block_tables, int32_t batch, int32_t num_q_heads,
+                                    int32_t max_blocks, int32_t total_q, float scale, const void *plan,
+                                    int32_t grid, void *out, void *workspace, size_t workspace_bytes, void *stream)
+{
     using namespace pkv::prefill;
     int st = pkv::check_attached(pool);
     if (st != PKV_OK) return st;
     const pkv_pool_desc &d = pool->desc;
-    if (d.kv_dtype == PKV_KV_INT4) return PKV_ERR_INVALID;
     if (batch < 1 || num_q_heads < 1 || max_blocks < 1 || total_q < 0 || grid < 1 || !std::isfinite(scale))
         return PKV_ERR_INVALID;
     if (total_q == 0) return PKV_OK;
@@ -891,8 +1071,15 @@ extern "C" int pkv_paged_prefill(pkv_pool *pool, const void *q, const void *key_
     const int tp = tile_positions(g);
     const int D = d.head_dim;
     const bool fp8 = d.kv_dtype == PKV_KV_FP8E4M3;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     CUtensorMap qm, km, vm;
-    const uint64_t rows = (uint64_t)d.num_blocks * d.num_kv_heads;
+    int num_blocks = d.num_blocks;
+    if (d.kv_dtype == PKV_KV_INT4) {
+        st = expand(pool, key_cache, value_cache, block_tables, batch, max_blocks, plan, grid, workspace, workspace_bytes,
+                    num_blocks, s);
+        if (st != PKV_OK) return st;
+    }
+    const uint64_t rows = (uint64_t)num_blocks * d.num_kv_heads;
     if (!encode_3d(&qm, q, D, num_q_heads, total_q, (uint64_t)D * 2, (uint64_t)num_q_heads * D * 2, 64, g, tp))
         return PKV_ERR_CUDA;
     if (fp8) {
@@ -918,13 +1105,13 @@ extern "C" int pkv_paged_prefill(pkv_pool *pool, const void *q, const void *key_
     p.Hkv = d.num_kv_heads;
     p.group = g;
     p.TP = tp;
-    p.num_blocks = d.num_blocks;
+    p.num_blocks = num_blocks;
     p.grid = grid;
     // (E4M3 pools: q enters the products as q * 2^-8)
     p.score_scale = scale * d.k_scale * LOG2E * (fp8 ? 1.0f / FP8_Q_SCALE : 1.0f);
     p.out_scale = d.v_scale;
     p.test_stall = pkv::test_expire() == PKV_TEST_EXPIRE_PREFILL;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    p.expanded = d.kv_dtype == PKV_KV_INT4 ? batch : 0;
     const cudaError_t e = D == 128 ? (fp8 ? launch<128, true>(qm, km, vm, p, s) : launch<128, false>(qm, km, vm, p, s))
                                    : (fp8 ? launch<64, true>(qm, km, vm, p, s) : launch<64, false>(qm, km, vm, p, s));
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
