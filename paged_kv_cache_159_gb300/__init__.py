@@ -55,6 +55,8 @@ EXPORTED = (
     "pkv_paged_attention_decode_ex", "pkv_decode_step", "pkv_paged_attention_decode_noalloc",
     "pkv_get_device_error", "pkv_test_expire_waits", "pkv_probe_copy",
     "pkv_device_sm_count", "pkv_status_string", "pkv_pool_tile_bytes", "pkv_kv_gather", "pkv_kv_gather_layers",
+    "pkv_fork_tables", "pkv_pool_compact", "pkv_remap_tables", "pkv_move_blocks",
+    "pkv_prefill_workspace_bytes", "pkv_paged_prefill_ex",
 )
 
 
@@ -118,6 +120,10 @@ def lib():
             "pkv_kv_append": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P]),
             "pkv_kv_append_layers": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P]),
             "pkv_pool_layer_bytes": (ctypes.c_size_t, [_P]),
+            "pkv_fork_tables": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _P, _P, _P, ctypes.POINTER(_I32)]),
+            "pkv_pool_compact": (ctypes.c_int, [_P, _I32, _P, _P, ctypes.POINTER(_I32)]),
+            "pkv_remap_tables": (ctypes.c_int, [_P, ctypes.c_int64, _P, _P, _I32]),
+            "pkv_move_blocks": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, ctypes.c_int64, _P]),
             "pkv_pool_tile_bytes": (ctypes.c_size_t, [_P]),
             "pkv_kv_gather": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _P, _P]),
             "pkv_kv_gather_layers": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _P, _P]),
@@ -134,6 +140,9 @@ def lib():
             "pkv_prefill_plan_bytes": (ctypes.c_size_t, [_P, _I32, _I32, _I32]),
             "pkv_prefill_plan": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _P, ctypes.c_size_t,
                                                 ctypes.POINTER(_I32)]),
+            "pkv_prefill_workspace_bytes": (ctypes.c_size_t, [_P, _P, _P, _I32, _I32]),
+            "pkv_paged_prefill_ex": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, ctypes.c_float, _P,
+                                                    _I32, _P, _P, ctypes.c_size_t, _P]),
             "pkv_paged_prefill": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32,
                                                  ctypes.c_float, _P, _I32, _P, _P]),
             "pkv_decode_step_host": (ctypes.c_int, [_P, ctypes.POINTER(host_step), ctypes.POINTER(device_step),
@@ -293,6 +302,28 @@ class Pool:
                "cow_prepare")
         return tables, np.stack([src[:n.value], dst[:n.value]], axis=1)
 
+    def fork(self, table_row, seq_len: int, num_forks: int):
+        """Fork a sequence (pkv_fork_tables): returns (tables int32 [num_forks, MB], int32 [n, 2]
+        (partly filled, fresh) pairs for copy_blocks); MB is table_row's length."""
+        row = np.ascontiguousarray(table_row, dtype=np.int32)
+        tables = np.empty((int(num_forks), row.size), dtype=np.int32)
+        src = np.empty(max(1, int(num_forks)), dtype=np.int32)
+        dst = np.empty_like(src)
+        n = _I32()
+        _check(lib().pkv_fork_tables(self._h, _np_ptr(row), int(seq_len), int(num_forks), row.size, _np_ptr(tables),
+                                     _np_ptr(src), _np_ptr(dst), ctypes.byref(n)), "fork_tables")
+        return tables, np.stack([src[:n.value], dst[:n.value]], axis=1)
+
+    def compact(self, max_moves=None) -> np.ndarray:
+        """Compact the pool's bookkeeping (pkv_pool_compact): int32 [n, 2] (old, new) ids.  Run
+        move_blocks and remap_tables on them before the pool is used or allocates again."""
+        room = self.desc.num_blocks // 2 if max_moves is None else int(max_moves)
+        src = np.empty(max(1, room), dtype=np.int32)
+        dst = np.empty_like(src)
+        n = _I32()
+        _check(lib().pkv_pool_compact(self._h, room, _np_ptr(src), _np_ptr(dst), ctypes.byref(n)), "pool_compact")
+        return np.stack([src[:n.value], dst[:n.value]], axis=1)
+
     # ---- automatic prefix caching (host)
     def prefix_lookup(self, tokens, salt: int = 0) -> np.ndarray:
         """Physical blocks of the longest cached prefix of ``tokens`` (pkv_prefix_lookup)."""
@@ -356,6 +387,16 @@ def slot_mapping_all(tables, seq_lens, block_size: int = BLOCK_SIZE) -> np.ndarr
     return out
 
 
+def remap_tables(tables, moves) -> np.ndarray:
+    """Host block tables after a compaction's moves (pkv_remap_tables); the input is not modified."""
+    tables = np.array(tables, dtype=np.int32, copy=True, order="C")
+    moves = np.asarray(moves, dtype=np.int32).reshape(-1, 2)
+    src, dst = np.ascontiguousarray(moves[:, 0]), np.ascontiguousarray(moves[:, 1])
+    _check(lib().pkv_remap_tables(_np_ptr(tables), tables.size, _np_ptr(src), _np_ptr(dst), src.size),
+           "remap_tables")
+    return tables
+
+
 def block_hashes(tokens, salt: int = 0, block_size: int = BLOCK_SIZE) -> np.ndarray:
     """Chained 64-bit hash of every full block of ``tokens`` (pkv_block_hashes)."""
     tokens = np.ascontiguousarray(tokens, dtype=np.int32)
@@ -393,16 +434,27 @@ def prefill_plan(pool: Pool, cu_q, seq_lens, num_q_heads: int, max_blocks: int):
     return buf, grid.value
 
 
+def prefill_workspace_bytes(pool: Pool, cu_q, seq_lens, max_blocks: int) -> int:
+    """Device workspace bytes of an INT4 pool's prefill (pkv_prefill_workspace_bytes); 0 for other pools."""
+    cu_q = np.ascontiguousarray(cu_q, dtype=np.int32)
+    seq_lens = np.ascontiguousarray(seq_lens, dtype=np.int32)
+    return int(lib().pkv_prefill_workspace_bytes(pool.handle, _np_ptr(cu_q), _np_ptr(seq_lens), seq_lens.size,
+                                                 int(max_blocks)))
+
+
 def paged_prefill(pool: Pool, q, key_cache, value_cache, block_tables, scale: float, plan, grid: int,
-                  out, stream=None):
+                  out, stream=None, workspace=None):
     """q/out: bf16 CUDA [T, Hq, D]; block_tables int32 CUDA [B, MB]; plan: the device copy
-    (uint8 CUDA tensor) of prefill_plan's bytes, grid its grid."""
+    (uint8 CUDA tensor) of prefill_plan's bytes, grid its grid; workspace (INT4 pools): CUDA
+    uint8 tensor of >= prefill_workspace_bytes() bytes."""
     T, Hq, _ = q.shape
-    _check(lib().pkv_paged_prefill(pool.handle, _dev_ptr(q, "q"), _dev_ptr(key_cache, "key_cache"),
-                                   _dev_ptr(value_cache, "value_cache"), _dev_ptr(block_tables, "block_tables"),
-                                   int(block_tables.shape[0]), int(Hq), int(block_tables.shape[1]), int(T),
-                                   float(scale), _dev_ptr(plan, "plan"), int(grid), _dev_ptr(out, "out"),
-                                   _stream_ptr(stream)), "paged_prefill")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().pkv_paged_prefill_ex(pool.handle, _dev_ptr(q, "q"), _dev_ptr(key_cache, "key_cache"),
+                                      _dev_ptr(value_cache, "value_cache"), _dev_ptr(block_tables, "block_tables"),
+                                      int(block_tables.shape[0]), int(Hq), int(block_tables.shape[1]), int(T),
+                                      float(scale), _dev_ptr(plan, "plan"), int(grid), _dev_ptr(out, "out"),
+                                      _dev_ptr(workspace, "workspace"), int(ws_bytes), _stream_ptr(stream)),
+           "paged_prefill")
 
 
 def kv_append(pool: Pool, k, v, slots, key_cache, value_cache, stream=None):
@@ -444,6 +496,15 @@ def copy_blocks(pool: Pool, key_cache, value_cache, src, dst, stream=None):
                                  _dev_ptr(value_cache, "value_cache"), _dev_ptr(src, "src"),
                                  _dev_ptr(dst, "dst"), int(src.numel()), _stream_ptr(stream)),
            "copy_blocks")
+
+
+def move_blocks(pool: Pool, key_cache, value_cache, src, dst, block_tables=None, stream=None):
+    """Move blocks src[i] -> dst[i] (int32 CUDA tensors, src descending: Pool.compact's moves) in
+    every layer, K and V, and point block_tables (int32 CUDA, in place) at the new ids."""
+    entries = 0 if block_tables is None else int(block_tables.numel())
+    _check(lib().pkv_move_blocks(pool.handle, _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
+                                 _dev_ptr(src, "src"), _dev_ptr(dst, "dst"), int(src.numel()),
+                                 _dev_ptr(block_tables, "block_tables"), entries, _stream_ptr(stream)), "move_blocks")
 
 
 def _opts(opts):

@@ -28,6 +28,10 @@ namespace pkv {
 // Free the pool's prefix cache, if any (its block references are not released).
 void destroy_prefix_cache(pkv_pool *pool);
 
+// Blocks changed places: cached block id b is now to[b] where that is not negative.  Allocates
+// nothing.
+void rename_prefix_blocks(pkv_pool *pool, const std::vector<int32_t> &to);
+
 // A tiled tensor map (TMA descriptor) of rank 3 or 4 over `ptr`: dims innermost first,
 // strides in bytes of dims 1 .. rank-1, box in elements.  false if the driver's encoder is
 // unavailable or refuses.

@@ -12,9 +12,11 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime_api.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <functional>
 #include <mutex>
 #include <new>
 
@@ -308,6 +310,98 @@ int pkv_cow_prepare(pkv_pool *pool, int32_t *tables, const int32_t *seq_lens, in
         ++n;
     }
     *num_copies = n;
+    return PKV_OK;
+}
+
+// Fork ("KV Cache 与推理优化", PagedAttention section: requests that share a prefix reference the
+// same blocks and part where they diverge): the full blocks are shared, the partly filled last
+// block, which both sides are about to write, is copied at once.
+int pkv_fork_tables(pkv_pool *pool, const int32_t *table_row, int32_t seq_len, int32_t num_forks,
+                    int32_t max_blocks, int32_t *tables_out, int32_t *src_out, int32_t *dst_out,
+                    int32_t *num_copies)
+{
+    if (!pool || num_forks < 0 || max_blocks < 1 || !num_copies || !table_row) return PKV_ERR_INVALID;
+    if (num_forks > 0 && (!tables_out || !src_out || !dst_out)) return PKV_ERR_INVALID;
+    const int32_t bs = pool->desc.block_size;
+    const int64_t nblk = ((int64_t)seq_len + bs - 1) / bs;
+    if (seq_len < 1 || nblk > max_blocks) return PKV_ERR_INVALID;
+    for (int64_t j = 0; j < nblk; ++j)
+        if (table_row[j] < 0 || table_row[j] >= pool->desc.num_blocks || pool->refcount[(size_t)table_row[j]] < 1)
+            return PKV_ERR_INVALID;
+    const int64_t full = seq_len / bs;
+    const bool partial = full < nblk;
+    if (partial && (size_t)num_forks > pool->free_list.size()) return PKV_ERR_OOM;
+    for (int32_t f = 0; f < num_forks; ++f) {
+        int32_t *row = tables_out + (int64_t)f * max_blocks;
+        for (int64_t j = 0; j < full; ++j) {
+            row[j] = table_row[j];
+            pool->refcount[(size_t)row[j]] += 1;
+        }
+        if (partial) {
+            const int32_t fresh = pool->free_list.front();
+            pool->free_list.pop_front();
+            pool->refcount[(size_t)fresh] = 1;
+            row[full] = fresh;
+            src_out[f] = table_row[full];
+            dst_out[f] = fresh;
+        }
+        for (int64_t j = nblk; j < max_blocks; ++j) row[j] = -1;
+    }
+    *num_copies = partial ? num_forks : 0;
+    return PKV_OK;
+}
+
+// Compaction ("理解 KV Cache" §3.5: blocks come from and return to a free pool, in any order, so
+// the live ones scatter): the live block with the highest id takes the free place with the lowest
+// id, as long as that is lower.
+int pkv_pool_compact(pkv_pool *pool, int32_t max_moves, int32_t *src_out, int32_t *dst_out, int32_t *num_moves)
+{
+    if (!pool || max_moves < 0 || !num_moves || (max_moves > 0 && (!src_out || !dst_out))) return PKV_ERR_INVALID;
+    const int32_t nb = pool->desc.num_blocks;
+    int32_t n = 0;
+    for (int32_t lo = 0, hi = nb - 1; n < max_moves; ++n, ++lo, --hi) {
+        while (lo < hi && pool->refcount[(size_t)lo] > 0) ++lo;
+        while (lo < hi && pool->refcount[(size_t)hi] == 0) --hi;
+        if (lo >= hi) break;
+        src_out[n] = hi;
+        dst_out[n] = lo;
+    }
+    *num_moves = 0;
+    if (n == 0) return PKV_OK;
+    try {                                     // whatever allocates, before anything changes
+        std::vector<int32_t> to((size_t)nb, -1);
+        std::vector<char> taken((size_t)nb, 0);
+        for (int32_t i = 0; i < n; ++i) {
+            to[(size_t)src_out[i]] = dst_out[i];
+            taken[(size_t)dst_out[i]] = 1;
+        }
+        std::deque<int32_t> free_list;
+        for (int32_t id : pool->free_list)
+            if (!taken[(size_t)id]) free_list.push_back(id);
+        for (int32_t i = 0; i < n; ++i) free_list.push_back(src_out[i]);
+        pool->free_list.swap(free_list);
+        for (int32_t i = 0; i < n; ++i) {
+            pool->refcount[(size_t)dst_out[i]] = pool->refcount[(size_t)src_out[i]];
+            pool->refcount[(size_t)src_out[i]] = 0;
+        }
+        pkv::rename_prefix_blocks(pool, to);
+    } catch (const std::bad_alloc &) {
+        return PKV_ERR_OOM;
+    }
+    *num_moves = n;
+    return PKV_OK;
+}
+
+int pkv_remap_tables(int32_t *tables, int64_t num_entries, const int32_t *src, const int32_t *dst, int32_t num_moves)
+{
+    if (num_entries < 0 || num_moves < 0 || (num_entries > 0 && !tables) || (num_moves > 0 && (!src || !dst)))
+        return PKV_ERR_INVALID;
+    for (int32_t i = 1; i < num_moves; ++i)
+        if (src[i] >= src[i - 1]) return PKV_ERR_INVALID;
+    for (int64_t e = 0; e < num_entries; ++e) {
+        const int32_t *at = std::lower_bound(src, src + num_moves, tables[e], std::greater<int32_t>());
+        if (at != src + num_moves && *at == tables[e]) tables[e] = dst[at - src];
+    }
     return PKV_OK;
 }
 

@@ -78,6 +78,28 @@ struct pkv_prefix_cache {
         return nullptr;
     }
 
+    // Entries of moved blocks under their new ids (nodes are re-keyed in place).
+    void rename(const std::vector<int32_t> &to)
+    {
+        auto moved = [&](int32_t b) { return b >= 0 && to[(size_t)b] >= 0 ? to[(size_t)b] : b; };
+        for (auto &h : by_hash) h.second = moved(h.second);
+        for (size_t b = to.size(); b-- > 0;) {
+            if (to[b] < 0) continue;
+            auto node = by_block.extract((int32_t)b);
+            if (node.empty()) continue;
+            pkv_prefix_entry &e = node.mapped();
+            auto leaf = leaves.extract({e.stamp, e.block});
+            e.block = to[b];
+            node.key() = e.block;
+            by_block.insert(std::move(node));
+            if (!leaf.empty()) {
+                leaf.value().second = to[b];
+                leaves.insert(std::move(leaf));
+            }
+        }
+        for (auto &kv : by_block) kv.second.parent = moved(kv.second.parent);
+    }
+
     // Remove an entry and release the cache's reference on its block.
     void drop(pkv_pool *pool, int32_t block)
     {
@@ -99,6 +121,11 @@ struct pkv_prefix_cache {
 };
 
 namespace pkv {
+
+void rename_prefix_blocks(pkv_pool *pool, const std::vector<int32_t> &to)
+{
+    if (pool->prefix) pool->prefix->rename(to);
+}
 
 void destroy_prefix_cache(pkv_pool *pool)
 {
