@@ -531,7 +531,8 @@ int pkv_decode_step_host(pkv_pool *pool, const pkv_host_step *host, const pkv_de
  * pools again and do not call this entry point across a reset.  Every argument check is
  * made before anything is queued; a call that passes them clears the array's counters with
  * an asynchronous memset on `stream`, then runs the same kernel with the same launch plan
- * as pkv_paged_attention_decode, so the two give bit-identical outputs.  All calls on a
+ * as pkv_paged_attention_decode, so the two give bit-identical outputs (INT4 pools: the grid is
+ * halved until its partials fit the array, which changes the order of the sums).  All calls on a
  * device share the array, so calls that overlap on the GPU race and must not be issued.
  * The pool must be attached beforehand (pkv_pool_attach_device allocates its 4-byte error
  * word once). */
@@ -554,7 +555,8 @@ int pkv_get_device_error(pkv_pool *pool, void *stream, uint32_t *bits_out);
  * PKV_DEVERR_TIMEOUT, and the roles that depend on the stalled one give up in turn (each
  * after its normal bound of about 1 s at most); copies already in flight are waited for
  * (bounded) before a CTA leaves, so the context stays usable and pkv_get_device_error()
- * returns PKV_ERR_TIMEOUT.  Outputs of such a launch are unspecified.  Decode workspace
+ * returns PKV_ERR_TIMEOUT.  (The decode of INT4 pools has no such waits and is not affected.)
+ * Outputs of such a launch are unspecified.  Decode workspace
  * counters still return to zero.  PKV_TEST_EXPIRE_NONE (the default) turns it off.  The
  * setting is process-wide and read when a call launches; INVALID for any other value. */
 #define PKV_TEST_EXPIRE_NONE 0

@@ -1,28 +1,34 @@
-// decode_int4.cuh -- single-query attention over an INT4 pool: the compute of the persistent
-// stream-K decode kernel (decode_kernels.cuh) for tiles of 4-bit codes.
+// decode_int4.cuh -- single-query attention over an INT4 pool.
 //
 // With k = scale_kj (n - 8) per group j of 32 columns (the pool's k_scale goes into the score
 // scale), and likewise v:
-//   S_t   = sum_j scale_tj (sum_{d in j} q_d n_td - 8 sum_{d in j} q_d)
+//   S_t   = sum_j scale_tj sum_{d in j} q_d (n_td - 8)
 //   O_d   = sum_t (p_t scale_tj(d)) (n_td - 8)
 // Both products run on the f16 tensor cores (m16n8k16, fp32 accumulation) with tokens (S^T = K
 // Q^T) or columns (O^T = V^T P^T) as the 16 rows and the group's query heads as the 8 columns,
 // so each code is unpacked once per step whatever the group.
-//   * K codes become 64 + n by one and-or on the packed word (nibble at mantissa bits 4-7 of
-//     an f16 with exponent 2^6); the excess 72 sum q of every group is a constant of the unit
-//     and enters as the accumulators' start value, so S needs no subtraction per element.  The
-//     fp32 sums then carry 72 / 8 times the magnitude, 2^-20 of the largest partial sum.
+//   * Codes become 1024 + n or 64 + n by one and-or on the packed word (a nibble at mantissa bits
+//     0-3 of an f16 with exponent 2^10, or 4-7 with 2^6; one shift by 8 brings the other two
+//     nibbles there), then n - 8 by an exact subtraction on the fp16 pipe: the integer pipe
+//     issues at half rate and would otherwise set the pace.
 //   * Group j's partial sums (two k-steps) are multiplied with scale_tj in fp32 as they join S.
 //   * p scale is formed per group in f16: p <= 2^7 (the running max is raised past that) and
 //     scale <= 448, below f16's largest value; p and p scale each round to 11 bits, and the
 //     scales are exact.
-//   * V codes become n - 8 exactly (1024 + n or 64 + n, minus a constant, in f16): here an
-//     excess in the accumulators would be large against outputs that average out.
 //   * q is taken to f16 with a power of two per unit that brings its largest magnitude to
 //     [128, 256): exact for every bf16 element above 2^-25 of the largest.
-// What bounds it: instruction issue.  At HBM speed an SM receives 42 elements a clock and can
-// issue 128 lane instructions, 3 an element; unpacking, the products, scales and softmax of
-// a 16-token block take about 2.
+//
+// Schedule.  A 16-token block of one head is 2 x 17 D / 2 bytes, little work to hand between
+// warps, so nothing is: a warp copies its own tiles (cp.async into a ring of its own, NST - 1
+// tiles ahead), computes, and writes its result from registers; it waits for no other warp,
+// and the CTA meets only to scan seq_lens.  Teams of HG warps, one per KV head, take the same
+// blocks at about the same time, since the heads' tiles of a block lie together in memory.  The
+// blocks of all (layer, sequence, head group) units are laid end to end and cut evenly over
+// the teams of a one-wave grid.  A team that holds a whole unit writes its output; a cut unit
+// leaves a partial (max, sum, unnormalised output) per team, and a second launch merges them,
+// a warp per output row, in team order: placement of the blocks changes no bit.  Both launches
+// may start while the one before them drains (programmatic dependent launch) and wait for it
+// before they read.
 #pragma once
 
 #include "decode_kernels.cuh"
@@ -30,11 +36,19 @@
 namespace pkv {
 namespace decode {
 
+constexpr int I4_NW = 8;                            // warps per CTA
+constexpr int I4_NT = I4_NW * 32;
+
+// KV heads of a team: all of them up to 8, else the largest divisor up to 8.
+__host__ __device__ constexpr int int4_team(int Hkv)
+{
+    int h = Hkv < 8 ? Hkv : 8;
+    while (Hkv % h) --h;
+    return h;
+}
+
 template <int D, int NH>
 struct Int4Compute {
-    static constexpr bool SWIZZLED = false;         // tiles hold their own bank-conflict-free order
-    static constexpr bool IDENTITY_SLOTS = true;    // merge-area column d at d
-    static constexpr int FORMAT = PKV_KV_INT4;
     static constexpr int TILE = int4::tile_bytes(D);
     static constexpr int NG = D / 32;               // column groups
     static constexpr int ROWB = D / 2;              // bytes of a row's codes
@@ -43,15 +57,10 @@ struct Int4Compute {
     static constexpr uint32_t F16_64 = 0x54005400u, F16_1024 = 0x64006400u;      // {64, 64}, {1024, 1024}
 
     uint32_t qb[NG][2][NH][2];    // Q^T fragments: group, k-step, heads, word
-    float c0[NG][NH][2];          // -72 sum_{d in j} q_d of this lane's columns
     float acc[2 * NG][NH][4];
     float m[NH][2], l[NH][2];
     float base_sc = 0.f;          // scale * k_scale * log2(e)
     float sc = 0.f;               // the unit's score scale (with the queries' power of two)
-
-    // Output column of O^T row r (0..15) of m-tile mt: codes 2 (mt & 1) + (r >> 3) of word r & 7.
-    __device__ static int dcol(int mt, int r) { return 32 * (mt >> 1) + 4 * (r & 7) + 2 * (mt & 1) + (r >> 3); }
-    __device__ static int slot_of_d(int d) { return d; }
 
     __device__ void start(const uint16_t *qs, int group, int lane)
     {
@@ -82,7 +91,7 @@ struct Int4Compute {
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 const uint32_t w[4] = {raw[j][h].x, raw[j][h].y, raw[j][h].z, raw[j][h].w};
-                float x[8], sum = 0.f;               // columns 32 j + 8 tid + i of head 8 h + gid
+                float x[8];                          // columns 32 j + 8 tid + i of head 8 h + gid
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     x[2 * i] = dev::bf16_lo(w[i]) * up;
@@ -91,17 +100,8 @@ struct Int4Compute {
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {    // pair 2 s + b of a word: codes 2 s + b and + 4
-                        const uint32_t f = dev::pack_f16x2(x[2 * s + b], x[2 * s + b + 4]);
-                        qb[j][s][h][b] = f;
-                        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f));
-                        sum += v.x + v.y;
-                    }
-                sum += __shfl_xor_sync(dev::FULL, sum, 1);
-                sum += __shfl_xor_sync(dev::FULL, sum, 2);
-                // head 8 h + n's sum lies in lanes 4 n .. 4 n + 3; this lane's columns are 2 tid, + 1
-                c0[j][h][0] = -72.f * __shfl_sync(dev::FULL, sum, 8 * tid);
-                c0[j][h][1] = -72.f * __shfl_sync(dev::FULL, sum, 8 * tid + 4);
+                    for (int b = 0; b < 2; ++b)      // pair 2 s + b of a word: codes 2 s + b and + 4
+                        qb[j][s][h][b] = dev::pack_f16x2(x[2 * s + b], x[2 * s + b + 4]);
             }
 #pragma unroll
         for (int mt = 0; mt < 2 * NG; ++mt)
@@ -126,10 +126,9 @@ struct Int4Compute {
         const __half2 d = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&d);
     }
-    // 64 + n of the nibbles at bits 4-7 of each half
-    __device__ static __forceinline__ uint32_t up64(uint32_t w) { return (w & 0x00F000F0u) | F16_64; }
-    // 1024 + n of the nibbles at bits 0-3 of each half
-    __device__ static __forceinline__ uint32_t up1024(uint32_t w) { return (w & 0x000F000Fu) | F16_1024; }
+    // n - 8 of the nibbles at bits 0-3, and at bits 4-7, of each half, as f16 pairs
+    __device__ static __forceinline__ uint32_t low(uint32_t w) { return hsub((w & 0x000F000Fu) | F16_1024, 0x64086408u); }
+    __device__ static __forceinline__ uint32_t high(uint32_t w) { return hsub((w & 0x00F000F0u) | F16_64, 0x54805480u); }
 
     // NG consecutive 32-bit words.
     __device__ static __forceinline__ void load_words(const uint8_t *src, uint32_t (&w)[NG])
@@ -177,11 +176,12 @@ struct Int4Compute {
         float s[NH][4];
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            const uint32_t a0[4] = {up64(k0[j] << 4), up64(k1[j] << 4), up64(k0[j]), up64(k1[j])};
-            const uint32_t a1[4] = {up64(k0[j] >> 4), up64(k1[j] >> 4), up64(k0[j] >> 8), up64(k1[j] >> 8)};
+            const uint32_t x = k0[j], y = k1[j], x8 = x >> 8, y8 = y >> 8;
+            const uint32_t a0[4] = {low(x), low(y), high(x), high(y)};
+            const uint32_t a1[4] = {low(x8), low(y8), high(x8), high(y8)};
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                float d[4] = {c0[j][h][0], c0[j][h][1], c0[j][h][0], c0[j][h][1]};
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
                 dev::mma_f16_16816(d, a0, qb[j][0][h][0], qb[j][0][h][1]);
                 dev::mma_f16_16816(d, a1, qb[j][1][h][0], qb[j][1][h][1]);
 #pragma unroll
@@ -265,9 +265,8 @@ struct Int4Compute {
             const uint32_t x = __byte_perm(w[0][j >> 1], w[1][j >> 1], sel);      // tokens tid, tid + 4
             const uint32_t y = __byte_perm(w[2][j >> 1], w[3][j >> 1], sel);      // tokens tid + 8, tid + 12
             const uint32_t x8 = x >> 8, y8 = y >> 8;
-            constexpr uint32_t C1032 = 0x64086408u, C72 = 0x54805480u;
-            const uint32_t a0[4] = {hsub(up1024(x), C1032), hsub(up64(x), C72), hsub(up1024(y), C1032), hsub(up64(y), C72)};
-            const uint32_t a1[4] = {hsub(up1024(x8), C1032), hsub(up64(x8), C72), hsub(up1024(y8), C1032), hsub(up64(y8), C72)};
+            const uint32_t a0[4] = {low(x), high(x), low(y), high(y)};
+            const uint32_t a1[4] = {low(x8), high(x8), low(y8), high(y8)};
             const uint32_t s0 = dev::e4m3x2_to_f16x2((uint16_t)vs[j]), s1 = dev::e4m3x2_to_f16x2((uint16_t)(vs[j] >> 16));
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
@@ -278,16 +277,18 @@ struct Int4Compute {
         }
     }
 
-    __device__ void block(const uint8_t *kt, const uint8_t *vt, int ntok, float /*score_scale*/, int lane)
+    __device__ __forceinline__ void block(const uint8_t *kt, const uint8_t *vt, int ntok, int lane)
     {
         if (ntok == BS) block_impl<false>(kt, vt, BS, lane);
         else block_impl<true>(kt, vt, ntok, lane);
     }
 
-    // Write this warp's (max, sum) rows and accumulators into the merge area ([head][d]).
-    __device__ void dump(float *ml, float *accs, int group, int lane)
+    // The state's rows (query heads 0 .. group - 1): f(row, max, sum, group j, four consecutive
+    // columns from 32 j + 4 gid).
+    template <class F>
+    __device__ __forceinline__ void rows(int group, int lane, F f)
     {
-        const int gid = lane >> 2, tid = lane & 3;
+        const int tid = lane & 3;
 #pragma unroll
         for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -296,50 +297,322 @@ struct Int4Compute {
                 x += __shfl_xor_sync(dev::FULL, x, 4);
                 x += __shfl_xor_sync(dev::FULL, x, 8);
                 x += __shfl_xor_sync(dev::FULL, x, 16);
-                const int head = 8 * h + 2 * tid + r;
-                if (head < group) {
-                    if (gid == 0) {
-                        ml[head * 2] = m[h][r];
-                        ml[head * 2 + 1] = x;
-                    }
-                    float *row = accs + head * (D + ACC_PAD);
+                const int row = 8 * h + 2 * tid + r;
+                if (row < group) {
 #pragma unroll
-                    for (int mt = 0; mt < 2 * NG; ++mt) {
-                        row[dcol(mt, gid)] = acc[mt][h][r];
-                        row[dcol(mt, gid + 8)] = acc[mt][h][r + 2];
-                    }
+                    for (int j = 0; j < NG; ++j)
+                        f(row, m[h][r], x, j, make_float4(acc[2 * j][h][r], acc[2 * j][h][r + 2], acc[2 * j + 1][h][r],
+                                                          acc[2 * j + 1][h][r + 2]));
                 }
             }
     }
 };
 
-template <int D, int NW, int NS, int NH>
-__global__ void __launch_bounds__((NW + 2) * 32, 8 / NW) decode_int4_kernel(const DecodeParams p)
+// Shared memory of a CTA: the warps' rings, then prefix [B + 1], lens [B] and the scan's sums.
+template <int D, int NST>
+constexpr size_t int4_ring_bytes() { return (size_t)I4_NW * NST * 2 * int4::tile_bytes(D); }
+
+// The even split of W tasks over T teams.
+__host__ __device__ __forceinline__ long long int4_start(long long W, int T, int t) { return W * t / T; }
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
 {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// p.part_o [teams][2][HG][group][D], p.part_ml [teams][2][HG][group][2], p.prefix_n [B + 2]: the
+// tasks before each sequence within a layer, then the number of teams.
+template <int D, int NST, int NH>
+__global__ void __launch_bounds__(I4_NT, NH == 2 ? 1 : 2) decode_int4_kernel(const DecodeParams p)
+{
+    constexpr int TILE = int4::tile_bytes(D);
+    constexpr int CH = TILE / 16;                  // 16-byte pieces of a tile
+    extern __shared__ __align__(128) uint8_t smem[];
+    int32_t *prefix = reinterpret_cast<int32_t *>(smem + int4_ring_bytes<D, NST>()), *lens = prefix + p.B + 1;
+    int32_t *wsum = lens + p.B;                    // [I4_NW]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int Hkv = p.Hkv, group = p.group, HG = int4_team(Hkv), HGN = Hkv / HG;
+    pdl_launch();
+    pdl_wait();
+
+    // ---- tasks per sequence (head groups x blocks; 0 for an invalid length), scanned
+    {
+        const int per = (p.B + I4_NT - 1) / I4_NT;
+        const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+        int run = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int L = __ldg(p.seq_lens + b);
+            const bool ok = L >= 1 && L <= p.MB * BS;
+            lens[b] = L;
+            if (!ok && blockIdx.x == 0) {
+                dev::flag_error(p.err, PKV_DEVERR_SEQ_LEN);
+                for (int l = 0; l < p.layers; ++l)
+                    for (int e = 0; e < p.Hq * D; ++e) p.out[((size_t)l * p.B + b) * p.Hq * D + e] = 0;
+            }
+            prefix[b] = run;
+            run += ok ? HGN * ((L + BS - 1) / BS) : 0;
+        }
+        int incl = run;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(dev::FULL, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+        int base = incl - run, total = 0;
+#pragma unroll
+        for (int w = 0; w < I4_NW; ++w) {
+            if (w < warp) base += wsum[w];
+            total += wsum[w];
+        }
+        for (int b = b0; b < b1; ++b) prefix[b] += base;
+        if (tid == 0) prefix[p.B] = total;
+        __syncthreads();
+    }
+    const int W1 = prefix[p.B];
+    const long long W = (long long)W1 * p.layers;
+    const int teams = (int)min(W, (long long)((int)gridDim.x * I4_NW / HG));
+    if (blockIdx.x == 0) {                         // for the merge
+        for (int b = tid; b <= p.B; b += I4_NT) p.prefix_n[b] = prefix[b];
+        if (tid == 0) p.prefix_n[p.B + 1] = teams;
+    }
+    const int gw = blockIdx.x * I4_NW + warp, team = gw / HG, hh = gw - team * HG;
+    if (team >= teams) return;
+    const long long s = int4_start(W, teams, team), e = int4_start(W, teams, team + 1);
+    const int n = (int)(e - s);
+
+    struct U { int l, b, h, L, nb; long long U0; };
+    auto unit_of = [&](long long r) {
+        U u;
+        u.l = p.layers > 1 ? (int)div_nonneg(r, W1) : 0;
+        const int rl = (int)(r - (long long)u.l * W1);
+        u.b = find_seq(prefix, p.B, rl);
+        u.L = lens[u.b];
+        u.nb = (u.L + BS - 1) / BS;
+        const int hg = (rl - prefix[u.b]) / u.nb;
+        u.h = hg * HG + hh;
+        u.U0 = (long long)u.l * W1 + prefix[u.b] + (long long)hg * u.nb;
+        return u;
+    };
+    // Tile of task s + i (((layer * blocks) + block) * Hkv + head, -1 for a bad entry), for a chunk
+    // of 32 tasks, lane x holding task 32 chunk + x; app: (layer * B + b) * 16 + offset of a new
+    // token that goes into the task's block, or -1.  fetch() starts the table loads a chunk
+    // ahead, finish() checks the entries.
+    struct Pending { int id, base, app; };
+    auto fetch = [&](int chunk) {
+        Pending q{-1, -1, -1};
+        const int i = chunk * 32 + lane;
+        if (i < n) {
+            const U u = unit_of(s + i);
+            const int blk = (int)(s + i - u.U0);
+            q.id = __ldg(p.block_tables + (size_t)u.b * p.MB + blk);
+            q.base = u.l * p.num_blocks * Hkv + u.h;
+            if (p.k_new && blk == u.nb - 1) q.app = (u.l * p.B + u.b) * BS + (u.L - 1) % BS;
+        }
+        return q;
+    };
+    auto finish = [&](const Pending &q, int &app) {
+        app = -1;
+        if (q.base < 0) return -1;
+        if (q.id < 0 || q.id >= p.num_blocks) {
+            dev::flag_error(p.err, PKV_DEVERR_BLOCK_ID);
+            return -1;
+        }
+        app = q.app;
+        return q.base + q.id * Hkv;
+    };
+    const uint32_t ring0 = dev::smem_u32(smem) + warp * (NST * 2 * TILE);
+    const uint8_t *ring = smem + warp * (NST * 2 * TILE);
+    Pending pend = fetch(0);
+    int acur, tcur = finish(pend, acur);
+    pend = fetch(1);
+    int ii = 0, ist = 0;                           // next task to copy, its stage
+    unsigned good = 0;                             // stages that hold a tile
+    auto issue = [&]() {
+        if (ii < n) {
+            if ((ii & 31) == 0 && ii > 0) {
+                tcur = finish(pend, acur);
+                pend = fetch((ii >> 5) + 1);
+            }
+            const int t = __shfl_sync(dev::FULL, tcur, ii & 31);
+            if (p.k_new) {                         // the new token's row goes in before its block is read
+                const int a = __shfl_sync(dev::FULL, acur, ii & 31);
+                if (a >= 0) {
+                    const int lb = a / BS;
+                    const size_t src = ((size_t)lb * Hkv + t % Hkv) * D;
+                    int4::write_row_pair<D>(p.k_new + src, p.v_new + src, p.inv_k_scale, p.inv_v_scale, a % BS,
+                                            const_cast<uint8_t *>(p.key_cache) + (size_t)t * TILE,
+                                            const_cast<uint8_t *>(p.value_cache) + (size_t)t * TILE, lane);
+                    __threadfence();
+                    __syncwarp();
+                }
+            }
+            if (t >= 0) {
+                good |= 1u << ist;
+                const uint8_t *k = p.key_cache + (size_t)t * TILE + lane * 16, *v = p.value_cache + (size_t)t * TILE + lane * 16;
+                const uint32_t dst = ring0 + ist * (2 * TILE) + lane * 16;
+#pragma unroll
+                for (int c = 0; c < 2 * CH; c += 32) {
+                    // pieces c + lane: of K below CH, of V from there on
+                    const bool isk = c + 32 <= CH || (c < CH && c + lane < CH);
+                    if (c + 32 <= 2 * CH || c + lane < 2 * CH)
+                        cp16(dst + c * 16, isk ? k + c * 16 : v + (c - CH) * 16);
+                }
+            } else {
+                good &= ~(1u << ist);
+            }
+            ++ii;
+            ist = ist + 1 == NST ? 0 : ist + 1;
+        }
+        cp_commit();                               // a group per step, empty past the end
+    };
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) issue();
+
     Int4Compute<D, NH> cmp;
     cmp.base_sc = p.score_scale;
-    decode_body<D, NW, NS, 1>(p, cmp, nullptr, nullptr);
+    int st = 0;                                    // stage of the next task to compute
+    for (long long lo = s; lo < e;) {
+        const U u = unit_of(lo);
+        const long long U1 = u.U0 + u.nb, hi = min(e, U1);
+        const size_t lb = (size_t)u.l * p.B + u.b;
+        cmp.start(p.q + (lb * p.Hq + (size_t)u.h * group) * D, group, lane);
+        int left = u.L - (int)(lo - u.U0) * BS;    // positions from this block on
+        for (long long r = lo; r < hi; ++r, left -= BS) {
+            cp_wait<NST - 2>();                    // this task's tile has landed (this lane's pieces)
+            __syncwarp();                          // every lane's; and the stage before it is read
+            issue();
+            const uint8_t *kt = ring + st * (2 * TILE);
+            if ((good >> st) & 1u) cmp.block(kt, kt + TILE, min(BS, left), lane);
+            st = st + 1 == NST ? 0 : st + 1;
+        }
+        const int gid = lane >> 2;
+        if (lo == u.U0 && hi == U1) {
+            uint16_t *out = p.out + (lb * p.Hq + (size_t)u.h * group) * D + 4 * gid;
+            cmp.rows(group, lane, [&](int row, float, float sum, int j, float4 v) {
+                const float inv = sum > 0.f ? p.out_scale / sum : 0.f;
+                *reinterpret_cast<uint2 *>(out + row * D + 32 * j) =
+                    make_uint2(dev::pack_bf16x2(v.x * inv, v.y * inv), dev::pack_bf16x2(v.z * inv, v.w * inv));
+            });
+        } else {
+            const size_t prow = (((size_t)team * 2 + (lo == s ? 0 : 1)) * HG + hh) * group;
+            cmp.rows(group, lane, [&](int row, float m, float sum, int j, float4 v) {
+                *reinterpret_cast<float4 *>(p.part_o + (prow + row) * D + 32 * j + 4 * gid) = v;
+                if (j == 0 && gid == 0) *reinterpret_cast<float2 *>(p.part_ml + (prow + row) * 2) = make_float2(m, sum);
+            });
+        }
+        lo = hi;
+    }
+    cp_wait<0>();
 }
+
+// Merge the partials of cut units, a warp per output row, MB_ partials in flight at a time.
+template <int D>
+__global__ void __launch_bounds__(I4_NT) decode_int4_merge_kernel(const DecodeParams p)
+{
+    constexpr int DPL = D / 32, BATCH = 8;
+    const int lane = threadIdx.x & 31, HG = int4_team(p.Hkv);
+    const long long row = (long long)blockIdx.x * I4_NW + (threadIdx.x >> 5);
+    if (row >= (long long)p.layers * p.B * p.Hq) return;
+    const int lb = (int)(row / p.Hq), hq = (int)(row - (long long)lb * p.Hq), l = lb / p.B, b = lb - l * p.B;
+    const int h = hq / p.group, hg = h / HG, hh = h - hg * HG;
+    pdl_launch();
+    pdl_wait();
+    const int P0 = __ldcg(p.prefix_n + b), P1 = __ldcg(p.prefix_n + b + 1), W1 = __ldcg(p.prefix_n + p.B), T = __ldcg(p.prefix_n + p.B + 1);
+    const int nb = (P1 - P0) / (p.Hkv / HG);
+    if (nb == 0) return;                                     // an invalid length
+    const long long W = (long long)W1 * p.layers, U0 = (long long)l * W1 + P0 + (long long)hg * nb, U1 = U0 + nb;
+    // team of task r: the last t with W t / T <= r
+    auto owner = [&](long long r) { return (int)(((r + 1) * T - 1) / W); };
+    const int c0 = owner(U0), c1 = owner(U1 - 1);
+    if (c0 == c1) return;                                    // a whole unit
+    const int first_slot = int4_start(W, T, c0) < U0 ? 1 : 0;
+    float M = -INFINITY, den = 0.f, num[DPL];
+#pragma unroll
+    for (int x = 0; x < DPL; ++x) num[x] = 0.f;
+    for (int c = c0; c <= c1; c += BATCH) {
+        float2 ml[BATCH];
+        float o[BATCH][DPL];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int x = 0; x < DPL; ++x) o[i][x] = 0.f;
+            if (c + i <= c1) {
+                const size_t pr = (((size_t)(c + i) * 2 + (c + i == c0 ? first_slot : 0)) * HG + hh) * p.group + (hq - h * p.group);
+                ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + pr);
+                if constexpr (DPL == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + pr * D) + lane);
+                    o[i][0] = v.x; o[i][1] = v.y; o[i][2] = v.z; o[i][3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.part_o + pr * D) + lane);
+                    o[i][0] = v.x; o[i][1] = v.y;
+                }
+            }
+        }
+        float Mn = M;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) Mn = fmaxf(Mn, ml[i].x);
+        if (Mn == -INFINITY) continue;                       // nothing valid so far (bad table entries)
+        const float a = dev::fast_exp2(M - Mn);
+        den *= a;
+#pragma unroll
+        for (int x = 0; x < DPL; ++x) num[x] *= a;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const float w = dev::fast_exp2(ml[i].x - Mn);
+            den = fmaf(ml[i].y, w, den);
+#pragma unroll
+            for (int x = 0; x < DPL; ++x) num[x] = fmaf(o[i][x], w, num[x]);
+        }
+        M = Mn;
+    }
+    const float inv = den > 0.f ? p.out_scale / den : 0.f;
+    uint16_t *dst = p.out + row * D + lane * DPL;
+    if constexpr (DPL == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(dev::pack_bf16x2(num[0] * inv, num[1] * inv), dev::pack_bf16x2(num[2] * inv, num[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = dev::pack_bf16x2(num[0] * inv, num[1] * inv);
+}
+
+constexpr int I4_NST = 4;                           // stages of a warp's ring
 
 // Either report CTAs per SM (launch == false) or launch.
 template <int D>
 cudaError_t dispatch_int4(const Plan &pl, int group, bool launch, int *per_sm, cudaStream_t s, const LaunchArgs *a)
 {
-    auto go = [&](auto kernel) -> cudaError_t {
-        const int threads = (pl.nw + 2) * 32;
-        cudaError_t e = prepare(kernel, pl.smem, threads, launch ? nullptr : per_sm);
-        if (e != cudaSuccess || !launch) return e;
-        kernel<<<pl.grid, threads, pl.smem, s>>>(a->p);
-        return cudaGetLastError();
-    };
-    auto by_ring = [&](auto nh) -> cudaError_t {
-        constexpr int NH = decltype(nh)::value;
-        if (pl.nw == 4 && pl.ns == 4) return go(decode_int4_kernel<D, 4, 4, NH>);
-        if (pl.nw == 4 && pl.ns == 8) return go(decode_int4_kernel<D, 4, 8, NH>);
-        if (pl.nw == 8 && pl.ns == 4) return go(decode_int4_kernel<D, 8, 4, NH>);
-        return cudaErrorInvalidConfiguration;
-    };
-    return group > 8 ? by_ring(std::integral_constant<int, 2>{}) : by_ring(std::integral_constant<int, 1>{});
+    auto kernel = group > 8 ? decode_int4_kernel<D, I4_NST, 2> : decode_int4_kernel<D, I4_NST, 1>;
+    cudaError_t e = prepare(kernel, pl.smem, I4_NT, launch ? nullptr : per_sm);
+    if (e != cudaSuccess || !launch) return e;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)pl.grid);
+    cfg.blockDim = dim3(I4_NT);
+    cfg.dynamicSmemBytes = pl.smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a->p);
+    if (e != cudaSuccess || a->p.MB == 1) return e;           // one block: no unit is cut
+    const long long rows = (long long)a->p.layers * a->p.B * a->p.Hq;
+    cfg.gridDim = dim3((unsigned)((rows + I4_NW - 1) / I4_NW));
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, decode_int4_merge_kernel<D>, a->p);
+}
+
+template <int D>
+size_t int4_smem(int B)
+{
+    return int4_ring_bytes<D, I4_NST>() + ((size_t)2 * B + 1 + I4_NW) * 4;
 }
 
 }  // namespace decode

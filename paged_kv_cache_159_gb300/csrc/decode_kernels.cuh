@@ -1408,11 +1408,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p, Compute &cmp,
             const size_t src = ((size_t)lb * Hkv + h) * D;
             const size_t dst = ((size_t)t * BS + off) * D;               // element index
             constexpr int EPL = D / 32;
-            if constexpr (Compute::FORMAT == PKV_KV_INT4) {
-                int4::write_row_pair<D>(p.k_new + src, p.v_new + src, p.inv_k_scale, p.inv_v_scale, off,
-                                        const_cast<uint8_t *>(p.key_cache) + (size_t)t * TILE,
-                                        const_cast<uint8_t *>(p.value_cache) + (size_t)t * TILE, lane);
-            } else if constexpr (Compute::FORMAT == PKV_KV_FP8E4M3) {
+            if constexpr (Compute::FORMAT == PKV_KV_FP8E4M3) {
                 const uint16_t *ks = p.k_new + src + lane * EPL;
                 const uint16_t *vs = p.v_new + src + lane * EPL;
                 uint32_t kc = 0, vc = 0;

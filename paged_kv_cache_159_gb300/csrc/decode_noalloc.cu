@@ -59,7 +59,18 @@ extern "C" int pkv_paged_attention_decode_noalloc(pkv_pool *pool, const void *q,
     if (st != PKV_OK) return st;
     if (batch < 0) return PKV_ERR_INVALID;
     if (batch == 0) return PKV_OK;
-    const size_t need = pkv_decode_workspace_bytes(pool, batch, num_q_heads, max_blocks, nullptr);
+    size_t need = pkv_decode_workspace_bytes(pool, batch, num_q_heads, max_blocks, nullptr);
+    // An INT4 pool's partials are per warp and grow with the grid: the largest halving of the grid
+    // whose partials fit.
+    pkv_decode_opts opts{};
+    if (pool->desc.kv_dtype == PKV_KV_INT4 && need > (size_t)PKV_NOALLOC_SCRATCH_BYTES) {
+        int32_t sms = 0;
+        if (pkv_device_sm_count(pool->device, &sms) != PKV_OK) return PKV_ERR_CUDA;
+        for (opts.grid_ctas = 2 * sms; need > (size_t)PKV_NOALLOC_SCRATCH_BYTES && opts.grid_ctas > 1;) {
+            opts.grid_ctas /= 2;
+            need = pkv_decode_workspace_bytes(pool, batch, num_q_heads, max_blocks, &opts);
+        }
+    }
     if (need == 0 || need > (size_t)PKV_NOALLOC_SCRATCH_BYTES) return PKV_ERR_INVALID;
     void *scratch = nullptr;
     st = scratch_address(pool->device, &scratch);       // first call on a device: symbol lookup
@@ -67,7 +78,7 @@ extern "C" int pkv_paged_attention_decode_noalloc(pkv_pool *pool, const void *q,
     // every check the decode makes, before anything is queued on the shared array
     st = pkv::decode::check_decode_call(pool, q, key_cache, value_cache, block_tables, seq_lens, batch,
                                         num_q_heads, max_blocks, scale, out, scratch,
-                                        (size_t)PKV_NOALLOC_SCRATCH_BYTES);
+                                        (size_t)PKV_NOALLOC_SCRATCH_BYTES, &opts);
     if (st != PKV_OK) return st;
     // the per-(sequence, KV head) counters lead the scratch and must start at zero
     const size_t counters = ((size_t)batch * pool->desc.num_kv_heads * 4 + 255) / 256 * 256;
@@ -75,5 +86,5 @@ extern "C" int pkv_paged_attention_decode_noalloc(pkv_pool *pool, const void *q,
         return PKV_ERR_CUDA;
     return pkv_paged_attention_decode_ex(pool, q, key_cache, value_cache, block_tables, seq_lens, batch,
                                          num_q_heads, max_blocks, scale, out, scratch,
-                                         (size_t)PKV_NOALLOC_SCRATCH_BYTES, nullptr, stream);
+                                         (size_t)PKV_NOALLOC_SCRATCH_BYTES, &opts, stream);
 }

@@ -27,12 +27,16 @@ namespace decode {
 // decode_int4.cuh, compiled by decode_inst_*_int4.cu
 template <int D>
 cudaError_t dispatch_int4(const Plan &pl, int group, bool launch, int *per_sm, cudaStream_t s, const LaunchArgs *a);
+template <int D>
+size_t int4_smem(int B);
+extern template size_t int4_smem<64>(int);
+extern template size_t int4_smem<128>(int);
 extern template cudaError_t dispatch_int4<64>(const Plan &, int, bool, int *, cudaStream_t, const LaunchArgs *);
 extern template cudaError_t dispatch_int4<128>(const Plan &, int, bool, int *, cudaStream_t, const LaunchArgs *);
 
 namespace {
 
-constexpr int INT4_WARPS = 4;
+constexpr int INT4_WARPS = 8;               // warps per CTA of the INT4 kernel
 
 int sm_count_cached()
 {
@@ -63,6 +67,33 @@ cudaError_t dispatch(const pkv_pool_desc &d, const Plan &pl, int group, bool lau
                : dispatch_nw_ns<64, false>(pl, group, launch, per_sm, s, p);
 }
 
+// The plan of an INT4 pool: one kernel shape, the grid one wave of CTAs; the workspace keeps the
+// counters' area of the other pools (untouched, so it stays zero), then the scanned lengths and
+// the partial states that the merge reads.
+int make_plan_int4(const pkv_pool_desc &d, int B, int group, const pkv_decode_opts &o, Plan &pl)
+{
+    if (o.variant || o.warps_per_cta || o.stages || o.heads_per_copy || o.shared_prefix_blocks || o.unit_cost || o.grid_ctas < 0)
+        return PKV_ERR_INVALID;
+    pl.variant = pl.nw = pl.ns = pl.hp = pl.sp = pl.uc = 0;
+    pl.smem = d.head_dim == 128 ? int4_smem<128>(B) : int4_smem<64>(B);
+    if (o.grid_ctas) {
+        pl.grid = o.grid_ctas;
+    } else {
+        int per_sm = 0;
+        if (dispatch(d, pl, group, false, &per_sm, nullptr, nullptr) != cudaSuccess || per_sm < 1) return PKV_ERR_CUDA;
+        pl.grid = sm_count_cached() * per_sm;
+    }
+    // rows of partials: 2 segments of every team's HG warps, the warps of the grid at most
+    const size_t rows = (size_t)pl.grid * INT4_WARPS * 2 * group;
+    pl.ws_counters = 0;
+    pl.ws_pre_n = ((size_t)d.num_layers * B * d.num_kv_heads * 4 + 255) / 256 * 256;
+    pl.ws_o = pl.ws_pre_n + (((size_t)B + 2) * 4 + 255) / 256 * 256;
+    pl.ws_ml = pl.ws_o + (rows * d.head_dim * 4 + 255) / 256 * 256;
+    pl.ws_bytes = pl.ws_ml + (rows * 2 * 4 + 255) / 256 * 256;
+    pl.ws_pre_o = pl.ws_pre_ml = 0;
+    return PKV_OK;
+}
+
 // Choose variant, CTA shape and grid; size the workspace.  Queries the device (occupancy)
 // unless opts fixes the grid.
 int make_plan(const pkv_pool_desc &d, int B, int Hq, int MB, const pkv_decode_opts *o, Plan &pl)
@@ -74,13 +105,11 @@ int make_plan(const pkv_pool_desc &d, int B, int Hq, int MB, const pkv_decode_op
     if ((long long)d.num_layers * B * d.num_kv_heads >= (1LL << 31)) return PKV_ERR_INVALID;
     pkv_decode_opts z{};
     if (!o) o = &z;
-    // an INT4 pool has one variant of its own (plan variant 0), without the options of variant 3
-    const bool i4 = d.kv_dtype == PKV_KV_INT4;
-    if (i4 && (o->variant != 0 || o->heads_per_copy > 1)) return PKV_ERR_INVALID;
-    pl.variant = o->variant || i4 ? o->variant : 3;
-    if (pl.variant < 0 || pl.variant > 3) return PKV_ERR_INVALID;
+    if (d.kv_dtype == PKV_KV_INT4) return make_plan_int4(d, B, group, *o, pl);
+    pl.variant = o->variant ? o->variant : 3;
+    if (pl.variant < 1 || pl.variant > 3) return PKV_ERR_INVALID;
     if (pl.variant == 1 && group > 8) return PKV_ERR_INVALID;
-    pl.nw = o->warps_per_cta ? o->warps_per_cta : i4 ? INT4_WARPS : 4;
+    pl.nw = o->warps_per_cta ? o->warps_per_cta : 4;
     if (pl.variant == 3) {
         if (o->heads_per_copy) {
             pl.hp = o->heads_per_copy;
@@ -94,7 +123,7 @@ int make_plan(const pkv_pool_desc &d, int B, int Hq, int MB, const pkv_decode_op
         pl.hp = 1;
     }
     // default ring: 16 KiB of tiles per warp (2 bf16 or 4 FP8 stages at head_dim 128)
-    pl.ns = o->stages ? o->stages : i4 ? 32 / pl.nw : (elem_bytes(d) == 1 && pl.variant >= 2 ? 4 : 2);
+    pl.ns = o->stages ? o->stages : (elem_bytes(d) == 1 && pl.variant >= 2 ? 4 : 2);
     if (o->grid_ctas < 0 || o->shared_prefix_blocks < 0) return PKV_ERR_INVALID;
     pl.sp = o->shared_prefix_blocks;
     if (pl.sp > 0 && (pl.variant != 3 || pl.hp != 1)) return PKV_ERR_INVALID;
@@ -231,7 +260,7 @@ int decode_impl(pkv_pool *pool, int layers, const void *q, const void *k_new, co
     p.test_stall = test_expire() == PKV_TEST_EXPIRE_DECODE;
     p.shared_prefix = pl.sp;
     p.unit_cost = pl.uc;
-    p.prefix_n = pl.sp ? reinterpret_cast<int32_t *>(ws + pl.ws_pre_n) : nullptr;
+    p.prefix_n = pl.ws_pre_n ? reinterpret_cast<int32_t *>(ws + pl.ws_pre_n) : nullptr;
     p.pref_o = pl.sp ? reinterpret_cast<float *>(ws + pl.ws_pre_o) : nullptr;
     p.pref_ml = pl.sp ? reinterpret_cast<float *>(ws + pl.ws_pre_ml) : nullptr;
     p.B = batch;
@@ -262,11 +291,11 @@ int decode_impl(pkv_pool *pool, int layers, const void *q, const void *k_new, co
 int check_decode_call(const pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
                       const int32_t *block_tables, const int32_t *seq_lens, int32_t batch, int32_t num_q_heads,
                       int32_t max_blocks, float scale, const void *out, const void *workspace,
-                      size_t workspace_bytes)
+                      size_t workspace_bytes, const pkv_decode_opts *opts)
 {
     Plan pl;
     return check_call(pool, q, nullptr, nullptr, key_cache, value_cache, block_tables, seq_lens, batch,
-                      num_q_heads, max_blocks, scale, out, workspace, workspace_bytes, nullptr, pl);
+                      num_q_heads, max_blocks, scale, out, workspace, workspace_bytes, opts, pl);
 }
 
 }  // namespace decode

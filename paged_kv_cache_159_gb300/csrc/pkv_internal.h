@@ -62,7 +62,7 @@ namespace decode {
 int check_decode_call(const pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
                       const int32_t *block_tables, const int32_t *seq_lens, int32_t batch, int32_t num_q_heads,
                       int32_t max_blocks, float scale, const void *out, const void *workspace,
-                      size_t workspace_bytes);
+                      size_t workspace_bytes, const pkv_decode_opts *opts);
 }  // namespace decode
 
 }  // namespace pkv
