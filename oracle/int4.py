@@ -123,13 +123,18 @@ def sequence(key_cache, value_cache, table_row, L: int, k_scale: float, v_scale:
 
 
 def decode(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_scale):
-    """q [B, Hq, D] -> (out, sum p |v|, score error unit), each [B, Hq, D] in 64 bits.  The score
-    error unit of (b, head) is scale * max_t sum_j |k scale_tj| sum_{d in j} |q_d|: a score's
-    absolute error per unit of relative error of its partial sums."""
+    """q [B, Hq, D] -> (out, sum p |v|, score error), each [B, Hq, D] in 64 bits.  The score error of
+    (b, head) bounds how far a score may be off that is formed from f16 products of q with the codes
+    and fp32 sums: with ks_tj = k scale * scale of token t and group j,
+      scale * max_t sum_j ks_tj (7 * 32 * 2^-24 max|q| + 2^-16 sum_{d in j} |q_d|):
+    an element of q is off by at most 2^-24 of the largest, times |n - 8| <= 7 for 32 columns; a
+    group's sum starts at -8 sum q and takes two products of codes up to 15, each off by at most
+    2^-21 of the largest of these, at most 15 sum |q|, and its joining the score rounds four times
+    by 2^-24: in all below 2^-16 of sum |q|."""
     q = bf16_values(q_bits).astype(np.float64)
     B, Hq, D = q.shape
     Hkv = key_cache.shape[1]
-    out, mag, unit = np.zeros_like(q), np.zeros_like(q), np.zeros_like(q)
+    out, mag, ds = np.zeros_like(q), np.zeros_like(q), np.zeros_like(q)
     sc = places(D, True)[2]
     for b in range(B):
         L = int(seq_lens[b])
@@ -141,8 +146,9 @@ def decode(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_s
             out[b, h], mag[b, h] = attend(q[b, h], k[:, hk], v[:, hk], scale)
             sb = key_cache[blk[:, None], hk, sc[pos % BS][:, ::GROUP]]
             ks = e4m3_values()[sb] * float(np.float32(k_scale))
-            unit[b, h] = scale * (ks @ np.abs(q[b, h]).reshape(-1, GROUP).sum(-1)).max()
-    return out, mag, unit
+            aq = np.abs(q[b, h])
+            ds[b, h] = scale * (ks @ (224 * 2.0 ** -24 * aq.max() + 2.0 ** -16 * aq.reshape(-1, GROUP).sum(-1))).max()
+    return out, mag, ds
 
 
 def prefill(q_bits, key_cache, value_cache, tables, seq_lens, cu_q, scale, k_scale, v_scale):

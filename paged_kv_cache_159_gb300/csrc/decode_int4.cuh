@@ -4,19 +4,21 @@
 // scale), and likewise v:
 //   S_t   = sum_j scale_tj sum_{d in j} q_d (n_td - 8)
 //   O_d   = sum_t (p_t scale_tj(d)) (n_td - 8)
-// Both products run on the f16 tensor cores (m16n8k16, fp32 accumulation) with tokens (S^T = K
-// Q^T) or columns (O^T = V^T P^T) as the 16 rows and the group's query heads as the 8 columns,
-// so each code is unpacked once per step whatever the group.
-//   * Codes become 1024 + n or 64 + n by one and-or on the packed word (a nibble at mantissa bits
-//     0-3 of an f16 with exponent 2^10, or 4-7 with 2^6; one shift by 8 brings the other two
-//     nibbles there), then n - 8 by an exact subtraction on the fp16 pipe: the integer pipe
-//     issues at half rate and would otherwise set the pace.
-//   * Group j's partial sums (two k-steps) are multiplied with scale_tj in fp32 as they join S.
-//   * p scale is formed per group in f16: p <= 2^7 (the running max is raised past that) and
-//     scale <= 448, below f16's largest value; p and p scale each round to 11 bits, and the
-//     scales are exact.
-//   * q is taken to f16 with a power of two per unit that brings its largest magnitude to
-//     [128, 256): exact for every bf16 element above 2^-25 of the largest.
+// with tokens (S^T = K Q^T) or columns (O^T = V^T P^T) as the 16 rows of a tensor-core product
+// and the group's query heads as its 8 columns, so each code is unpacked once per step whatever
+// the group.  Unpacking sets the pace (the integer pipe issues at half rate), so codes go to
+// the f16 tensor cores as they are: a nibble n at the low bits of an f16 is the subnormal n 2^-24,
+// one nibble up it is n 2^-20, so one and makes an operand register of two codes (after one shift
+// by 8 for the other half of a word).
+//   * K: q is scaled by a power of two per unit (exact) to a largest magnitude in [2^14, 2^15), and
+//     the columns at the upper nibbles by 2^-4 of that, which evens out the two factors: exact
+//     for every bf16 element of at least 2^-24 of the largest.  The -8 of every code is the
+//     accumulators' start value, -8 2^-24 sum_{d in j} q_d.
+//   * Group j's partial sums are multiplied with scale_tj in fp32 as they join S.
+//   * V: a second product with the constant -8 2^-24 (-8 2^-20) takes the offset out step by step,
+//     so that the accumulators stay as small as the sums they stand for.
+//   * p scale is formed per group in f16: p 2^8 <= 2^15 (the running max is raised past 2^7) and
+//     scale 2^-8 (the scale byte moved to f16's fields) <= 1.75; both products round to 11 bits.
 //
 // Schedule.  A 16-token block of one head is 2 x 17 D / 2 bytes, little work to hand between
 // warps, so nothing is: a warp copies its own tiles (cp.async into a ring of its own, NST - 1
@@ -53,10 +55,12 @@ struct Int4Compute {
     static constexpr int NG = D / 32;               // column groups
     static constexpr int ROWB = D / 2;              // bytes of a row's codes
     static constexpr int SCALES = 8 * D;            // byte offset of a tile's scales
+    static constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;     // nibbles 0 and 1 of each half
+    static constexpr float OFF = 8.0f;              // m is kept 8 below the max: p is held as p 2^8
     static constexpr float TAU = 7.0f;              // raise the running max beyond 2^7
-    static constexpr uint32_t F16_64 = 0x54005400u, F16_1024 = 0x64006400u;      // {64, 64}, {1024, 1024}
 
-    uint32_t qb[NG][2][NH][2];    // Q^T fragments: group, k-step, heads, word
+    uint32_t qb[NG][NH][4];       // Q^T fragments of group j: 2 words of each k-step
+    float c0[NG][NH][4];          // -8 2^-24 sum_{d in j} q_d of this lane's columns, for both rows
     float acc[2 * NG][NH][4];
     float m[NH][2], l[NH][2];
     float base_sc = 0.f;          // scale * k_scale * log2(e)
@@ -81,27 +85,39 @@ struct Int4Compute {
             }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(dev::FULL, amax, o));
-        int e = 0;                                   // amax * 2^e in [128, 256)
-        if (amax > 0.f) e = 7 - (((int)(__float_as_uint(amax) >> 23) & 0xff) - 127);
+        int e = 0;                                   // amax * 2^e in [2^14, 2^15)
+        if (amax > 0.f) e = 14 - (((int)(__float_as_uint(amax) >> 23) & 0xff) - 127);
         e = max(-126, min(126, e));
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        sc = base_sc * __uint_as_float((uint32_t)(127 - e) << 23);
+        sc = base_sc * 0x1p24f * __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int j = 0; j < NG; ++j)
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 const uint32_t w[4] = {raw[j][h].x, raw[j][h].y, raw[j][h].z, raw[j][h].w};
-                float x[8];                          // columns 32 j + 8 tid + i of head 8 h + gid
+                float x[8], sum = 0.f;               // columns 32 j + 8 tid + i of head 8 h + gid
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     x[2 * i] = dev::bf16_lo(w[i]) * up;
                     x[2 * i + 1] = dev::bf16_hi(w[i]) * up;
                 }
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                for (int i = 0; i < 4; ++i) {        // pair i of a word: codes i and i + 4, at the upper nibbles for odd i
+                    const float f = (i & 1) ? 0x1p-4f : 1.f;
+                    const uint32_t v = dev::pack_f16x2(x[i] * f, x[i + 4] * f);
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+                    sum += (y.x + y.y) * ((i & 1) ? 16.f : 1.f);
+                    qb[j][h][i] = v;
+                }
+                sum += __shfl_xor_sync(dev::FULL, sum, 1);
+                sum += __shfl_xor_sync(dev::FULL, sum, 2);
+                // head 8 h + n's sum lies in lanes 4 n .. 4 n + 3; this lane's columns are 2 tid, + 1
+                sum *= -8.f * 0x1p-24f;
+                c0[j][h][0] = c0[j][h][2] = __shfl_sync(dev::FULL, sum, 8 * tid);
+                c0[j][h][1] = c0[j][h][3] = __shfl_sync(dev::FULL, sum, 8 * tid + 4);
+                // kept as they are: the compiler would otherwise form them anew for every block
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)      // pair 2 s + b of a word: codes 2 s + b and + 4
-                        qb[j][s][h][b] = dev::pack_f16x2(x[2 * s + b], x[2 * s + b + 4]);
+                for (int i = 0; i < 4; ++i) asm volatile("" : "+r"(qb[j][h][i]), "+f"(c0[j][h][i]));
             }
 #pragma unroll
         for (int mt = 0; mt < 2 * NG; ++mt)
@@ -116,19 +132,19 @@ struct Int4Compute {
         }
     }
 
-    __device__ static __forceinline__ uint32_t hsub(uint32_t a, uint32_t b)
-    {
-        const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-        return *reinterpret_cast<const uint32_t *>(&d);
-    }
     __device__ static __forceinline__ uint32_t hmul(uint32_t a, uint32_t b)
     {
         const __half2 d = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&d);
     }
-    // n - 8 of the nibbles at bits 0-3, and at bits 4-7, of each half, as f16 pairs
-    __device__ static __forceinline__ uint32_t low(uint32_t w) { return hsub((w & 0x000F000Fu) | F16_1024, 0x64086408u); }
-    __device__ static __forceinline__ uint32_t high(uint32_t w) { return hsub((w & 0x00F000F0u) | F16_64, 0x54805480u); }
+    // D = A B + C with a C that stays
+    __device__ static __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4])
+    {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+    }
 
     // NG consecutive 32-bit words.
     __device__ static __forceinline__ void load_words(const uint8_t *src, uint32_t (&w)[NG])
@@ -177,13 +193,12 @@ struct Int4Compute {
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             const uint32_t x = k0[j], y = k1[j], x8 = x >> 8, y8 = y >> 8;
-            const uint32_t a0[4] = {low(x), low(y), high(x), high(y)};
-            const uint32_t a1[4] = {low(x8), low(y8), high(x8), high(y8)};
+            const uint32_t a0[4] = {x & LO, y & LO, x & HI, y & HI}, a1[4] = {x8 & LO, y8 & LO, x8 & HI, y8 & HI};
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                dev::mma_f16_16816(d, a0, qb[j][0][h][0], qb[j][0][h][1]);
-                dev::mma_f16_16816(d, a1, qb[j][1][h][0], qb[j][1][h][1]);
+                float d[4];
+                mma_f16(d, a0, qb[j][h][0], qb[j][h][1], c0[j][h]);
+                dev::mma_f16_16816(d, a1, qb[j][h][2], qb[j][h][3]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const float f = c < 2 ? ks0[j] : ks1[j];
@@ -200,8 +215,8 @@ struct Int4Compute {
                 const float x = s[h][c] * sc;
                 s[h][c] = (!PARTIAL || t0 + 8 * (c >> 1) < ntok) ? x : -INFINITY;
             }
-            need |= fmaxf(s[h][0], s[h][2]) > m[h][0] + TAU;
-            need |= fmaxf(s[h][1], s[h][3]) > m[h][1] + TAU;
+            need |= fmaxf(s[h][0], s[h][2]) > m[h][0] + (OFF + TAU);
+            need |= fmaxf(s[h][1], s[h][3]) > m[h][1] + (OFF + TAU);
         }
         if (__any_sync(dev::FULL, need)) {
 #pragma unroll
@@ -212,7 +227,7 @@ struct Int4Compute {
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 16));
-                    const float mn = fmaxf(m[h][r], mx);
+                    const float mn = fmaxf(m[h][r], mx - OFF);
                     const float alpha = dev::fast_exp2(m[h][r] - mn);
                     m[h][r] = mn;
                     l[h][r] *= alpha;
@@ -223,7 +238,7 @@ struct Int4Compute {
                     }
                 }
         }
-        // ---- P = exp2(S - m), transposed: tokens tid, tid + 4 of head gid in word 0, tid + 8,
+        // ---- P 2^8 = exp2(S - m), transposed: tokens tid, tid + 4 of head gid in word 0, tid + 8,
         //      tid + 12 in word 1
         uint32_t pb[NH][2];
 #pragma unroll
@@ -265,12 +280,15 @@ struct Int4Compute {
             const uint32_t x = __byte_perm(w[0][j >> 1], w[1][j >> 1], sel);      // tokens tid, tid + 4
             const uint32_t y = __byte_perm(w[2][j >> 1], w[3][j >> 1], sel);      // tokens tid + 8, tid + 12
             const uint32_t x8 = x >> 8, y8 = y >> 8;
-            const uint32_t a0[4] = {low(x), high(x), low(y), high(y)};
-            const uint32_t a1[4] = {low(x8), high(x8), low(y8), high(y8)};
-            const uint32_t s0 = dev::e4m3x2_to_f16x2((uint16_t)vs[j]), s1 = dev::e4m3x2_to_f16x2((uint16_t)(vs[j] >> 16));
+            const uint32_t a0[4] = {x & LO, x & HI, y & LO, y & HI}, a1[4] = {x8 & LO, x8 & HI, y8 & LO, y8 & HI};
+            constexpr uint32_t EIGHT[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};     // -8 2^-24, -8 2^-20
+            // scale 2^-8: the scale bytes at bits 7-14 of each half
+            const uint32_t s0 = __byte_perm(vs[j], 0u, 0x4140u) * 128u, s1 = __byte_perm(vs[j], 0u, 0x4342u) * 128u;
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 const uint32_t b0 = hmul(pb[h][0], s0), b1 = hmul(pb[h][1], s1);
+                dev::mma_f16_16816(acc[2 * j][h], EIGHT, b0, b1);
+                dev::mma_f16_16816(acc[2 * j + 1][h], EIGHT, b0, b1);
                 dev::mma_f16_16816(acc[2 * j][h], a0, b0, b1);
                 dev::mma_f16_16816(acc[2 * j + 1][h], a1, b0, b1);
             }
@@ -301,8 +319,9 @@ struct Int4Compute {
                 if (row < group) {
 #pragma unroll
                     for (int j = 0; j < NG; ++j)
-                        f(row, m[h][r], x, j, make_float4(acc[2 * j][h][r], acc[2 * j][h][r + 2], acc[2 * j + 1][h][r],
-                                                          acc[2 * j + 1][h][r + 2]));
+                        // back from n 2^-24 (n 2^-20), and scale 2^-8 (p 2^8 is in the sum as well)
+                        f(row, m[h][r], x, j, make_float4(acc[2 * j][h][r] * 0x1p32f, acc[2 * j][h][r + 2] * 0x1p28f,
+                                                          acc[2 * j + 1][h][r] * 0x1p32f, acc[2 * j + 1][h][r + 2] * 0x1p28f));
                 }
             }
     }

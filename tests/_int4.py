@@ -72,27 +72,24 @@ class Case:
         return out
 
     def check(self, out, kh=None, vh=None):
-        ref, mag, unit = O.decode(bits(self.q), self.kh if kh is None else kh, self.vh if vh is None else vh,
+        ref, mag, ds = O.decode(bits(self.q), self.kh if kh is None else kh, self.vh if vh is None else vh,
                                   self.tables, self.lens, self.scale, self.k_scale, self.v_scale)
-        within(out, ref, mag, unit, self.lens[:, None, None], self.v_scale)
+        within(out, ref, mag, ds, self.lens[:, None, None], self.v_scale)
 
 
-def within(out, ref, mag, unit, L, v_scale):
+def within(out, ref, mag, ds, L, v_scale):
     """|out - ref| against the arithmetic's bound:
       output rounding             2^-8 |ref|
       p and p * scale in f16      2 * 2^-11 of sum p |v|
-      scores                      a group's partial sum starts at -72 sum |q| and takes two
-                                  products of at most 79 sum |q|: three fp32 roundings (2^-22
-                                  each, truncating) of at most 151 sum |q|, 453 * 2^-22 < 2^-13
-                                  of the score unit; it enters p and the normaliser
+      scores                      off by ds (oracle/int4.py), which enters p and the normaliser
       exp2, sums                  2^-16
-      f16 underflow               p and p * scale each off by 2^-25 for every position, p's with
-                                  |v| <= 7 * 448 * v_scale and the other's with 7 * v_scale; the
-                                  largest p is at least 1
+      f16 underflow               p 2^8 and p * scale each off by 2^-25 for every position, which
+                                  is at most 7 * 448 * v_scale and 2^8 * 7 * v_scale of the
+                                  largest p 2^8 >= 2^8
     """
     got = out.float().cpu().double().numpy()
     assert np.isfinite(got).all()
-    tol = 2.0 ** -8 * np.abs(ref) + mag * (2.0 ** -10 + 2 * unit * 2.0 ** -13 + 2.0 ** -16)
+    tol = 2.0 ** -8 * np.abs(ref) + mag * (2.0 ** -10 + 2 * ds + 2.0 ** -16)
     tol = tol + L * 2.0 ** -25 * (7 * 448 + 7) * v_scale
     bad = np.abs(got - ref) > tol
     assert not bad.any(), "%d of %d outside; worst %.3g times its bound" % (

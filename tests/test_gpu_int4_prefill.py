@@ -77,8 +77,8 @@ def test_prefill_row_agrees_with_decode():
     c = Chunks([50, 3], [100, 400], 8, 2, 128, seed=4)
     out = c.prefill()
     c.q = c.rows[torch.from_numpy(c.cu[1:].astype(np.int64) - 1)]
-    ref, mag, unit = O.decode(I.bits(c.q), c.kh, c.vh, c.tables, c.lens, c.scale, c.k_scale, c.v_scale)
-    I.within(c.decode(), ref, mag, unit, c.lens[:, None, None], c.v_scale)
+    ref, mag, ds = O.decode(I.bits(c.q), c.kh, c.vh, c.tables, c.lens, c.scale, c.k_scale, c.v_scale)
+    I.within(c.decode(), ref, mag, ds, c.lens[:, None, None], c.v_scale)
     last = out[torch.from_numpy(c.cu[1:].astype(np.int64) - 1).cuda()].float().cpu().double().numpy()
     assert (np.abs(last - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -10) * mag).all()
 
