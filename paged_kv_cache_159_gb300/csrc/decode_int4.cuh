@@ -22,7 +22,7 @@
 //
 // Schedule.  A 16-token block of one head is 2 x 17 D / 2 bytes, little work to hand between
 // warps, so nothing is: a warp copies its own tiles (cp.async into a ring of its own, NST - 1
-// tiles ahead), computes, and writes its result from registers; it waits for no other warp,
+// pairs of tiles ahead), computes a pair at a time, and writes its result from registers; it waits for no other warp,
 // and the CTA meets only to scan seq_lens.  Teams of HG warps, one per KV head, take the same
 // blocks at about the same time, since the heads' tiles of a block lie together in memory.  The
 // blocks of all (layer, sequence, head group) units are laid end to end and cut evenly over
@@ -65,6 +65,35 @@ struct Int4Compute {
     float m[NH][2], l[NH][2];
     float base_sc = 0.f;          // scale * k_scale * log2(e)
     float sc = 0.f;               // the unit's score scale (with the queries' power of two)
+    uint32_t ok, oks, ov, ovs;    // byte offsets in a tile of this lane's K words, K scales, V words, V scales
+
+    __device__ __forceinline__ void setup(int lane)
+    {
+        const int gid = lane >> 2, tid = lane & 3;
+        ok = lane * (4 * NG);                        // row gid (8 NG bytes to four lanes), word tid NG
+        oks = SCALES + gid * NG;
+        ov = TILE + tid * ROWB + (D == 128 ? gid ^ ((tid & 2) << 1) : gid) * (2 * NG);
+        ovs = TILE + SCALES + tid * (4 * NG);
+        asm volatile("" : "+r"(ok), "+r"(oks), "+r"(ov), "+r"(ovs));      // (not formed anew for every block)
+    }
+
+    // Shared-memory loads at a 32-bit address.
+    template <int N>
+    __device__ static __forceinline__ void lds(uint32_t a, uint32_t (&w)[N])
+    {
+        if constexpr (N == 4)
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+        else if constexpr (N == 2)
+            asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+        else
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(a));
+    }
+    __device__ static __forceinline__ uint32_t lds16(uint32_t a)
+    {
+        uint16_t x;
+        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(a));
+        return x;
+    }
 
     __device__ void start(const uint16_t *qs, int group, int lane)
     {
@@ -146,50 +175,32 @@ struct Int4Compute {
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
     }
 
-    // NG consecutive 32-bit words.
-    __device__ static __forceinline__ void load_words(const uint8_t *src, uint32_t (&w)[NG])
+    // S^T of one tile: stored rows gid, gid + 8 (tokens t0, t0 + 8); columns 8 h + 2 tid, + 1.
+    __device__ __forceinline__ void scores(uint32_t tiles, float (&s)[NH][4])
     {
+        uint32_t k0[NG], k1[NG], b0, b1;
+        lds(tiles + ok, k0);
+        lds(tiles + ok + 8 * ROWB, k1);
         if constexpr (NG == 4) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(src);
-            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+            uint32_t t[1];
+            lds(tiles + oks, t);
+            b0 = t[0];
+            lds(tiles + oks + 8 * NG, t);
+            b1 = t[0];
         } else {
-            const uint2 x = *reinterpret_cast<const uint2 *>(src);
-            w[0] = x.x; w[1] = x.y;
+            b0 = lds16(tiles + oks);
+            b1 = lds16(tiles + oks + 8 * NG);
         }
-    }
-
-    // One 16-token block; PARTIAL: only tokens < ntok are valid (the rest masked by select).
-    template <bool PARTIAL>
-    __device__ __forceinline__ void block_impl(const uint8_t *kt, const uint8_t *vt, int ntok, int lane)
-    {
-        const int gid = lane >> 2, tid = lane & 3;
-        // ---- S^T = K Q^T: stored rows gid, gid + 8 (tokens t0, t0 + 8); columns 8 h + 2 tid, + 1
-        const int t0 = (gid >> 1) + 4 * (gid & 1);
-        uint32_t k0[NG], k1[NG];
-        load_words(kt + gid * ROWB + tid * (4 * NG), k0);
-        load_words(kt + (gid + 8) * ROWB + tid * (4 * NG), k1);
         float ks0[NG], ks1[NG];
-        {
-            const uint8_t *src = kt + SCALES + gid * NG;
-            uint32_t b0, b1;
-            if constexpr (NG == 4) {
-                b0 = *reinterpret_cast<const uint32_t *>(src);
-                b1 = *reinterpret_cast<const uint32_t *>(src + 8 * NG);
-            } else {
-                b0 = *reinterpret_cast<const uint16_t *>(src);
-                b1 = *reinterpret_cast<const uint16_t *>(src + 8 * NG);
-            }
 #pragma unroll
-            for (int j = 0; j < NG; j += 2) {
-                const uint32_t x = dev::e4m3x2_to_f16x2((uint16_t)(b0 >> (8 * j)));
-                const uint32_t y = dev::e4m3x2_to_f16x2((uint16_t)(b1 >> (8 * j)));
-                const float2 fx = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-                const float2 fy = __half22float2(*reinterpret_cast<const __half2 *>(&y));
-                ks0[j] = fx.x; ks0[j + 1] = fx.y;
-                ks1[j] = fy.x; ks1[j + 1] = fy.y;
-            }
+        for (int j = 0; j < NG; j += 2) {
+            const uint32_t x = dev::e4m3x2_to_f16x2((uint16_t)(b0 >> (8 * j)));
+            const uint32_t y = dev::e4m3x2_to_f16x2((uint16_t)(b1 >> (8 * j)));
+            const float2 fx = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+            const float2 fy = __half22float2(*reinterpret_cast<const __half2 *>(&y));
+            ks0[j] = fx.x; ks0[j + 1] = fx.y;
+            ks1[j] = fy.x; ks1[j + 1] = fy.y;
         }
-        float s[NH][4];
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             const uint32_t x = k0[j], y = k1[j], x8 = x >> 8, y8 = y >> 8;
@@ -206,54 +217,16 @@ struct Int4Compute {
                 }
             }
         }
-        // ---- scale, mask, lazy running max
-        bool need = false;
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float x = s[h][c] * sc;
-                s[h][c] = (!PARTIAL || t0 + 8 * (c >> 1) < ntok) ? x : -INFINITY;
-            }
-            need |= fmaxf(s[h][0], s[h][2]) > m[h][0] + (OFF + TAU);
-            need |= fmaxf(s[h][1], s[h][3]) > m[h][1] + (OFF + TAU);
-        }
-        if (__any_sync(dev::FULL, need)) {
-#pragma unroll
-            for (int h = 0; h < NH; ++h)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float mx = fmaxf(s[h][r], s[h][r + 2]);
-                    mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 16));
-                    const float mn = fmaxf(m[h][r], mx - OFF);
-                    const float alpha = dev::fast_exp2(m[h][r] - mn);
-                    m[h][r] = mn;
-                    l[h][r] *= alpha;
-#pragma unroll
-                    for (int mt = 0; mt < 2 * NG; ++mt) {
-                        acc[mt][h][r] *= alpha;
-                        acc[mt][h][r + 2] *= alpha;
-                    }
-                }
-        }
-        // ---- P 2^8 = exp2(S - m), transposed: tokens tid, tid + 4 of head gid in word 0, tid + 8,
-        //      tid + 12 in word 1
-        uint32_t pb[NH][2];
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-            const float p0 = dev::fast_exp2(s[h][0] - m[h][0]), p1 = dev::fast_exp2(s[h][1] - m[h][1]);
-            const float p2 = dev::fast_exp2(s[h][2] - m[h][0]), p3 = dev::fast_exp2(s[h][3] - m[h][1]);
-            l[h][0] += p0 + p2;
-            l[h][1] += p1 + p3;
-            pb[h][0] = dev::movmatrix_trans(dev::pack_f16x2(p0, p1));
-            pb[h][1] = dev::movmatrix_trans(dev::pack_f16x2(p2, p3));
-        }
-        // ---- O^T += V^T (P scale)^T
+    }
+
+    // O^T += V^T (P scale)^T of one tile; pb: tokens tid, tid + 4 of head gid in word 0, tid + 8,
+    // tid + 12 in word 1.  MASK: tokens from ntok on count nothing, whatever they hold.
+    template <bool MASK>
+    __device__ __forceinline__ void outputs(uint32_t tiles, int ntok, int tid, const uint32_t (&pb)[NH][2])
+    {
         uint32_t vs[NG];                             // scales of group j: tokens tid, + 4, + 8, + 12
-        load_words(vt + SCALES + tid * (4 * NG), vs);
-        if constexpr (PARTIAL) {                     // a NaN scale past the end would survive p = 0
+        lds(tiles + ovs, vs);
+        if constexpr (MASK) {
             uint32_t mask = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) mask |= tid + 4 * i < ntok ? 0xffu << (8 * i) : 0u;
@@ -261,19 +234,8 @@ struct Int4Compute {
             for (int j = 0; j < NG; ++j) vs[j] &= mask;
         }
         uint32_t w[4][NG / 2];                       // tokens tid + 4 i: 16-bit word of group j in half j & 1
-        {
-            const int c = D == 128 ? gid ^ ((tid & 2) << 1) : gid;
-            const uint8_t *src = vt + tid * ROWB + c * (2 * NG);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (NG == 4) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(src + 4 * i * ROWB);
-                    w[i][0] = x.x; w[i][1] = x.y;
-                } else {
-                    w[i][0] = *reinterpret_cast<const uint32_t *>(src + 4 * i * ROWB);
-                }
-            }
-        }
+        for (int i = 0; i < 4; ++i) lds(tiles + ov + 4 * i * ROWB, w[i]);
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
@@ -295,10 +257,66 @@ struct Int4Compute {
         }
     }
 
-    __device__ __forceinline__ void block(const uint8_t *kt, const uint8_t *vt, int ntok, int lane)
+    // Two blocks (32 positions), K, V, K, V tiles at the shared-memory address given; FULL: all of them valid, else the first n0 of the first
+    // tile and the first n1 of the second (n0 + n1 > 0), the rest masked by select.
+    template <bool FULL>
+    __device__ __forceinline__ void pair(uint32_t tiles, int n0, int n1, int lane)
     {
-        if (ntok == BS) block_impl<false>(kt, vt, BS, lane);
-        else block_impl<true>(kt, vt, ntok, lane);
+        const int gid = lane >> 2, tid = lane & 3;           // (of masked pairs only)
+        float s[2][NH][4];
+        scores(tiles, s[0]);
+        scores(tiles + 2 * TILE, s[1]);
+        // ---- scale, mask, lazy running max
+        const int t0 = (gid >> 1) + 4 * (gid & 1);
+        bool need = false;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float v = s[x][h][c] * sc;
+                    s[x][h][c] = (FULL || t0 + 8 * (c >> 1) < (x ? n1 : n0)) ? v : -INFINITY;
+                }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                need |= fmaxf(fmaxf(s[0][h][r], s[0][h][r + 2]), fmaxf(s[1][h][r], s[1][h][r + 2])) > m[h][r] + (OFF + TAU);
+        }
+        if (__any_sync(dev::FULL, need)) {
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float mx = fmaxf(fmaxf(s[0][h][r], s[0][h][r + 2]), fmaxf(s[1][h][r], s[1][h][r + 2]));
+                    mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 16));
+                    const float mn = fmaxf(m[h][r], mx - OFF);
+                    const float alpha = dev::fast_exp2(m[h][r] - mn);
+                    m[h][r] = mn;
+                    l[h][r] *= alpha;
+#pragma unroll
+                    for (int mt = 0; mt < 2 * NG; ++mt) {
+                        acc[mt][h][r] *= alpha;
+                        acc[mt][h][r + 2] *= alpha;
+                    }
+                }
+        }
+        // ---- P 2^8 = exp2(S - m), transposed
+        uint32_t pb[2][NH][2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                const float p0 = dev::fast_exp2(s[x][h][0] - m[h][0]), p1 = dev::fast_exp2(s[x][h][1] - m[h][1]);
+                const float p2 = dev::fast_exp2(s[x][h][2] - m[h][0]), p3 = dev::fast_exp2(s[x][h][3] - m[h][1]);
+                l[h][0] += p0 + p2;
+                l[h][1] += p1 + p3;
+                pb[x][h][0] = dev::movmatrix_trans(dev::pack_f16x2(p0, p1));
+                pb[x][h][1] = dev::movmatrix_trans(dev::pack_f16x2(p2, p3));
+            }
+        outputs<!FULL>(tiles, n0, tid, pb[0]);
+        outputs<!FULL>(tiles + 2 * TILE, n1, tid, pb[1]);
     }
 
     // The state's rows (query heads 0 .. group - 1): f(row, max, sum, group j, four consecutive
@@ -329,7 +347,26 @@ struct Int4Compute {
 
 // Shared memory of a CTA: the warps' rings, then prefix [B + 1], lens [B] and the scan's sums.
 template <int D, int NST>
-constexpr size_t int4_ring_bytes() { return (size_t)I4_NW * NST * 2 * int4::tile_bytes(D); }
+constexpr size_t int4_ring_bytes() { return (size_t)I4_NW * NST * 4 * int4::tile_bytes(D); }
+
+// A unit (layer l, sequence b, KV head h): its length and blocks, the task it starts at.
+struct Int4Unit { int l, b, h, L, nb; long long U0; };
+
+// Not inlined: once per unit and 32 tasks, so that the streaming loop stays small.
+static __device__ __noinline__ Int4Unit int4_unit_at(long long r, const int32_t *prefix, const int32_t *lens, int B, int layers, int HG, int hh)
+{
+    Int4Unit u;
+    const int W1 = prefix[B];
+    u.l = layers > 1 ? (int)div_nonneg(r, W1) : 0;
+    const int rl = (int)(r - (long long)u.l * W1);
+    u.b = find_seq(prefix, B, rl);
+    u.L = lens[u.b];
+    u.nb = (u.L + BS - 1) / BS;
+    const int hg = (rl - prefix[u.b]) / u.nb;
+    u.h = hg * HG + hh;
+    u.U0 = (long long)u.l * W1 + prefix[u.b] + (long long)hg * u.nb;
+    return u;
+}
 
 // The even split of W tasks over T teams.
 __host__ __device__ __forceinline__ long long int4_start(long long W, int T, int t) { return W * t / T; }
@@ -340,6 +377,10 @@ __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.laun
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16_if(uint32_t dst, const void *src, int yes)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src), "r"(yes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -355,7 +396,8 @@ __global__ void __launch_bounds__(I4_NT, NH == 2 ? 1 : 2) decode_int4_kernel(con
     extern __shared__ __align__(128) uint8_t smem[];
     int32_t *prefix = reinterpret_cast<int32_t *>(smem + int4_ring_bytes<D, NST>()), *lens = prefix + p.B + 1;
     int32_t *wsum = lens + p.B;                    // [I4_NW]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(dev::FULL, tid >> 5, 0);         // (known to be the same in every lane)
     const int Hkv = p.Hkv, group = p.group, HG = int4_team(Hkv), HGN = Hkv / HG;
     pdl_launch();
     pdl_wait();
@@ -407,110 +449,123 @@ __global__ void __launch_bounds__(I4_NT, NH == 2 ? 1 : 2) decode_int4_kernel(con
     const long long s = int4_start(W, teams, team), e = int4_start(W, teams, team + 1);
     const int n = (int)(e - s);
 
-    struct U { int l, b, h, L, nb; long long U0; };
-    auto unit_of = [&](long long r) {
-        U u;
-        u.l = p.layers > 1 ? (int)div_nonneg(r, W1) : 0;
-        const int rl = (int)(r - (long long)u.l * W1);
-        u.b = find_seq(prefix, p.B, rl);
-        u.L = lens[u.b];
-        u.nb = (u.L + BS - 1) / BS;
-        const int hg = (rl - prefix[u.b]) / u.nb;
-        u.h = hg * HG + hh;
-        u.U0 = (long long)u.l * W1 + prefix[u.b] + (long long)hg * u.nb;
-        return u;
-    };
-    // Tile of task s + i (((layer * blocks) + block) * Hkv + head, -1 for a bad entry), for a chunk
-    // of 32 tasks, lane x holding task 32 chunk + x; app: (layer * B + b) * 16 + offset of a new
-    // token that goes into the task's block, or -1.  fetch() starts the table loads a chunk
-    // ahead, finish() checks the entries.
-    struct Pending { int id, base, app; };
+    using U = Int4Unit;
+    auto unit_of = [&](long long r) { return int4_unit_at(r, prefix, lens, p.B, p.layers, HG, hh); };
+    // Tile of task s + i ((layer * blocks + block) * Hkv + head, -1 for a bad entry), for a chunk of
+    // 32 tasks, lane x holding task 32 chunk + x.  fetch() starts the table loads two chunks ahead
+    // of their use, finish() checks the entries.
+    struct Pending { int id, base; };
     auto fetch = [&](int chunk) {
-        Pending q{-1, -1, -1};
+        Pending q{-1, -1};
         const int i = chunk * 32 + lane;
         if (i < n) {
             const U u = unit_of(s + i);
-            const int blk = (int)(s + i - u.U0);
-            q.id = __ldg(p.block_tables + (size_t)u.b * p.MB + blk);
+            q.id = __ldg(p.block_tables + (size_t)u.b * p.MB + (int)(s + i - u.U0));
             q.base = u.l * p.num_blocks * Hkv + u.h;
-            if (p.k_new && blk == u.nb - 1) q.app = (u.l * p.B + u.b) * BS + (u.L - 1) % BS;
         }
         return q;
     };
-    auto finish = [&](const Pending &q, int &app) {
-        app = -1;
+    auto finish = [&](const Pending &q) {
         if (q.base < 0) return -1;
         if (q.id < 0 || q.id >= p.num_blocks) {
             dev::flag_error(p.err, PKV_DEVERR_BLOCK_ID);
             return -1;
         }
-        app = q.app;
         return q.base + q.id * Hkv;
     };
-    const uint32_t ring0 = dev::smem_u32(smem) + warp * (NST * 2 * TILE);
-    const uint8_t *ring = smem + warp * (NST * 2 * TILE);
-    Pending pend = fetch(0);
-    int acur, tcur = finish(pend, acur);
-    pend = fetch(1);
-    int ii = 0, ist = 0;                           // next task to copy, its stage
-    unsigned good = 0;                             // stages that hold a tile
-    auto issue = [&]() {
-        if (ii < n) {
-            if ((ii & 31) == 0 && ii > 0) {
-                tcur = finish(pend, acur);
-                pend = fetch((ii >> 5) + 1);
-            }
-            const int t = __shfl_sync(dev::FULL, tcur, ii & 31);
-            if (p.k_new) {                         // the new token's row goes in before its block is read
-                const int a = __shfl_sync(dev::FULL, acur, ii & 31);
-                if (a >= 0) {
-                    const int lb = a / BS;
-                    const size_t src = ((size_t)lb * Hkv + t % Hkv) * D;
-                    int4::write_row_pair<D>(p.k_new + src, p.v_new + src, p.inv_k_scale, p.inv_v_scale, a % BS,
-                                            const_cast<uint8_t *>(p.key_cache) + (size_t)t * TILE,
-                                            const_cast<uint8_t *>(p.value_cache) + (size_t)t * TILE, lane);
-                    __threadfence();
-                    __syncwarp();
-                }
-            }
-            if (t >= 0) {
-                good |= 1u << ist;
-                const uint8_t *k = p.key_cache + (size_t)t * TILE + lane * 16, *v = p.value_cache + (size_t)t * TILE + lane * 16;
-                const uint32_t dst = ring0 + ist * (2 * TILE) + lane * 16;
+    Pending f0 = fetch(0), f1 = fetch(1), pend = fetch(2);
+    int cur = finish(f0), nxt = finish(f1), at = 32;  // tiles of tasks at - 32 .. at - 1, at .. at + 31
+    // The ring holds NST pairs of tasks: consecutive blocks of a unit, the second one absent at the
+    // end of a run of odd length.  The copy cursor: task s + ii, in a unit whose tasks here end
+    // before s + ihi and in all before s + iend.  Bad entries copy tile 0 and count as absent.
+    constexpr uint32_t STAGE = 4 * TILE, RING = NST * STAGE;
+    const uint32_t ring = dev::smem_u32(smem) + warp * RING;
+    const uint8_t *kbase = p.key_cache + lane * 16, *vbase = p.value_cache + lane * 16;
+    int ii = 0;
+    U iu = unit_of(s);
+    int iend = __shfl_sync(dev::FULL, (int)min((long long)INT_MAX, iu.U0 + iu.nb - s), 0), ihi = min(n, iend);
+    uint32_t io = 0;                               // its stage's offset
+    unsigned good = 0;                             // a bit per tile, the pair copied last at bits 0 and 1
+    const int rest = lane < CH % 32;               // this lane takes part in a tile's last, partial piece
+    auto copy_tile = [&](int t, uint32_t dst) {
+        const uint8_t *k = kbase + (size_t)(unsigned)t * TILE, *v = vbase + (size_t)(unsigned)t * TILE;
 #pragma unroll
-                for (int c = 0; c < 2 * CH; c += 32) {
-                    // pieces c + lane: of K below CH, of V from there on
-                    const bool isk = c + 32 <= CH || (c < CH && c + lane < CH);
-                    if (c + 32 <= 2 * CH || c + lane < 2 * CH)
-                        cp16(dst + c * 16, isk ? k + c * 16 : v + (c - CH) * 16);
-                }
+        for (int c = 0; c < CH; c += 32) {
+            if (c + 32 <= CH) {
+                cp16(dst + c * 16, k + c * 16);
+                cp16(dst + TILE + c * 16, v + c * 16);
             } else {
-                good &= ~(1u << ist);
+                cp16_if(dst + c * 16, k + c * 16, rest);
+                cp16_if(dst + TILE + c * 16, v + c * 16, rest);
             }
+        }
+    };
+    auto issue = [&]() {
+        good <<= 2;
+        if (ii < n) {
+            if (ii >= at) {                        // cur is used up
+                cur = nxt;
+                nxt = finish(pend);
+                pend = fetch((at >> 5) + 2);
+                at += 32;
+            }
+            const int t0 = __shfl_sync(dev::FULL, cur, ii & 31);
+            const uint32_t dst = ring + io + lane * 16;
+            int last = t0;
             ++ii;
-            ist = ist + 1 == NST ? 0 : ist + 1;
+            int t1 = -1;
+            const bool two = ii < ihi;
+            if (two) {
+                t1 = __shfl_sync(dev::FULL, ii < at ? cur : nxt, ii & 31);
+                last = t1;
+                ++ii;
+            }
+            if (p.k_new && ii == iend && last >= 0) {   // the new token's row goes in before its block is read
+                const size_t src = (((size_t)iu.l * p.B + iu.b) * Hkv + iu.h) * D;
+                int4::write_row_pair<D>(p.k_new + src, p.v_new + src, p.inv_k_scale, p.inv_v_scale, (iu.L - 1) % BS,
+                                        const_cast<uint8_t *>(p.key_cache) + (size_t)last * TILE,
+                                        const_cast<uint8_t *>(p.value_cache) + (size_t)last * TILE, lane);
+                __threadfence();
+                __syncwarp();
+            }
+            copy_tile(max(t0, 0), dst);
+            if (two) copy_tile(max(t1, 0), dst + 2 * TILE);
+            good |= (t0 >= 0 ? 1u : 0u) | (t1 >= 0 ? 2u : 0u);
+            if (ii == ihi && ii < n) {
+                iu = unit_of(s + ii);
+                iend = __shfl_sync(dev::FULL, (int)min((long long)INT_MAX, iu.U0 + iu.nb - s), 0);
+                ihi = min(n, iend);
+            }
+            io = io + STAGE == RING ? 0u : io + STAGE;
         }
         cp_commit();                               // a group per step, empty past the end
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < NST - 1; ++i) issue();
 
     Int4Compute<D, NH> cmp;
     cmp.base_sc = p.score_scale;
-    int st = 0;                                    // stage of the next task to compute
+    cmp.setup(lane);
+    uint32_t co = ring;                            // address of the next pair to compute
     for (long long lo = s; lo < e;) {
         const U u = unit_of(lo);
         const long long U1 = u.U0 + u.nb, hi = min(e, U1);
         const size_t lb = (size_t)u.l * p.B + u.b;
         cmp.start(p.q + (lb * p.Hq + (size_t)u.h * group) * D, group, lane);
-        int left = u.L - (int)(lo - u.U0) * BS;    // positions from this block on
-        for (long long r = lo; r < hi; ++r, left -= BS) {
-            cp_wait<NST - 2>();                    // this task's tile has landed (this lane's pieces)
+        int left = u.L - (int)(lo - u.U0) * BS;    // positions from this pair on, up to the run's end
+        left = __shfl_sync(dev::FULL, min(left, (int)(hi - lo) * BS), 0);
+        for (; left > 0; left -= 2 * BS) {
+            cp_wait<NST - 2>();                    // this pair has landed (this lane's pieces)
             __syncwarp();                          // every lane's; and the stage before it is read
             issue();
-            const uint8_t *kt = ring + st * (2 * TILE);
-            if ((good >> st) & 1u) cmp.block(kt, kt + TILE, min(BS, left), lane);
-            st = st + 1 == NST ? 0 : st + 1;
+            const unsigned g = (good >> (2 * (NST - 1))) & 3u;
+            if (left >= 2 * BS && g == 3u) {
+                cmp.template pair<true>(co, BS, BS, lane);
+            } else {
+                const int n0 = (g & 1u) ? min(left, BS) : 0, n1 = (g & 2u) ? max(0, min(left - BS, BS)) : 0;
+                if (n0 + n1 > 0) cmp.template pair<false>(co, n0, n1, lane);
+            }
+            co = co + STAGE == ring + RING ? ring : co + STAGE;
         }
         const int gid = lane >> 2;
         if (lo == u.U0 && hi == U1) {
@@ -532,67 +587,97 @@ __global__ void __launch_bounds__(I4_NT, NH == 2 ? 1 : 2) decode_int4_kernel(con
     cp_wait<0>();
 }
 
-// Merge the partials of cut units, a warp per output row, MB_ partials in flight at a time.
-template <int D>
+// Merge the partials of cut units: S warps of a CTA per output row, each taking every S-th partial,
+// up to 8 of them in flight at a time; the row's first warp combines the S results.
+template <int D, int S>
 __global__ void __launch_bounds__(I4_NT) decode_int4_merge_kernel(const DecodeParams p)
 {
     constexpr int DPL = D / 32, BATCH = 8;
-    const int lane = threadIdx.x & 31, HG = int4_team(p.Hkv);
-    const long long row = (long long)blockIdx.x * I4_NW + (threadIdx.x >> 5);
-    if (row >= (long long)p.layers * p.B * p.Hq) return;
-    const int lb = (int)(row / p.Hq), hq = (int)(row - (long long)lb * p.Hq), l = lb / p.B, b = lb - l * p.B;
-    const int h = hq / p.group, hg = h / HG, hh = h - hg * HG;
+    __shared__ float part[S > 1 ? I4_NW : 1][D + 2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, HG = int4_team(p.Hkv), sub = warp % S;
+    const long long row = (long long)blockIdx.x * (I4_NW / S) + warp / S;
     pdl_launch();
     pdl_wait();
-    const int P0 = __ldcg(p.prefix_n + b), P1 = __ldcg(p.prefix_n + b + 1), W1 = __ldcg(p.prefix_n + p.B), T = __ldcg(p.prefix_n + p.B + 1);
-    const int nb = (P1 - P0) / (p.Hkv / HG);
-    if (nb == 0) return;                                     // an invalid length
-    const long long W = (long long)W1 * p.layers, U0 = (long long)l * W1 + P0 + (long long)hg * nb, U1 = U0 + nb;
-    // team of task r: the last t with W t / T <= r
-    auto owner = [&](long long r) { return (int)(((r + 1) * T - 1) / W); };
-    const int c0 = owner(U0), c1 = owner(U1 - 1);
-    if (c0 == c1) return;                                    // a whole unit
-    const int first_slot = int4_start(W, T, c0) < U0 ? 1 : 0;
+    bool cut = false;
     float M = -INFINITY, den = 0.f, num[DPL];
 #pragma unroll
     for (int x = 0; x < DPL; ++x) num[x] = 0.f;
-    for (int c = c0; c <= c1; c += BATCH) {
-        float2 ml[BATCH];
-        float o[BATCH][DPL];
+    if (row < (long long)p.layers * p.B * p.Hq) {
+        const int lb = (int)(row / p.Hq), hq = (int)(row - (long long)lb * p.Hq), l = lb / p.B, b = lb - l * p.B;
+        const int h = hq / p.group, hg = h / HG, hh = h - hg * HG;
+        const int P0 = __ldcg(p.prefix_n + b), P1 = __ldcg(p.prefix_n + b + 1), W1 = __ldcg(p.prefix_n + p.B), T = __ldcg(p.prefix_n + p.B + 1);
+        const int nb = (P1 - P0) / (p.Hkv / HG);
+        const long long W = (long long)W1 * p.layers, U0 = (long long)l * W1 + P0 + (long long)hg * nb;
+        // team of task r: the last t with W t / T <= r
+        auto owner = [&](long long r) { return (int)div_nonneg((r + 1) * T - 1, W); };
+        const int c0 = nb ? owner(U0) : 0, c1 = nb ? owner(U0 + nb - 1) : 0;
+        cut = c0 < c1;                                       // (not an invalid length, nor a whole unit)
+        const int first_slot = cut && int4_start(W, T, c0) < U0 ? 1 : 0;
+        for (int c = c0 + sub; cut && c <= c1; c += BATCH * S) {
+            float2 ml[BATCH];
+            float o[BATCH][DPL];
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            ml[i] = make_float2(-INFINITY, 0.f);
+            for (int i = 0; i < BATCH; ++i) {
+                const int cc = c + i * S;
+                ml[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int x = 0; x < DPL; ++x) o[i][x] = 0.f;
-            if (c + i <= c1) {
-                const size_t pr = (((size_t)(c + i) * 2 + (c + i == c0 ? first_slot : 0)) * HG + hh) * p.group + (hq - h * p.group);
-                ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + pr);
-                if constexpr (DPL == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + pr * D) + lane);
-                    o[i][0] = v.x; o[i][1] = v.y; o[i][2] = v.z; o[i][3] = v.w;
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.part_o + pr * D) + lane);
-                    o[i][0] = v.x; o[i][1] = v.y;
+                for (int x = 0; x < DPL; ++x) o[i][x] = 0.f;
+                if (cc <= c1) {
+                    const size_t pr = (((size_t)cc * 2 + (cc == c0 ? first_slot : 0)) * HG + hh) * p.group + (hq - h * p.group);
+                    ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + pr);
+                    if constexpr (DPL == 4) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + pr * D) + lane);
+                        o[i][0] = v.x; o[i][1] = v.y; o[i][2] = v.z; o[i][3] = v.w;
+                    } else {
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.part_o + pr * D) + lane);
+                        o[i][0] = v.x; o[i][1] = v.y;
+                    }
                 }
             }
+            float Mn = M;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) Mn = fmaxf(Mn, ml[i].x);
+            if (Mn == -INFINITY) continue;                   // nothing valid so far (bad table entries)
+            const float a = dev::fast_exp2(M - Mn);
+            den *= a;
+#pragma unroll
+            for (int x = 0; x < DPL; ++x) num[x] *= a;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const float w = dev::fast_exp2(ml[i].x - Mn);
+                den = fmaf(ml[i].y, w, den);
+#pragma unroll
+                for (int x = 0; x < DPL; ++x) num[x] = fmaf(o[i][x], w, num[x]);
+            }
+            M = Mn;
         }
-        float Mn = M;
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) Mn = fmaxf(Mn, ml[i].x);
-        if (Mn == -INFINITY) continue;                       // nothing valid so far (bad table entries)
-        const float a = dev::fast_exp2(M - Mn);
-        den *= a;
-#pragma unroll
-        for (int x = 0; x < DPL; ++x) num[x] *= a;
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const float w = dev::fast_exp2(ml[i].x - Mn);
-            den = fmaf(ml[i].y, w, den);
-#pragma unroll
-            for (int x = 0; x < DPL; ++x) num[x] = fmaf(o[i][x], w, num[x]);
-        }
-        M = Mn;
     }
+    if constexpr (S > 1) {
+#pragma unroll
+        for (int x = 0; x < DPL; ++x) part[warp][lane * DPL + x] = num[x];
+        if (lane == 0) {
+            part[warp][D] = M;
+            part[warp][D + 1] = den;
+        }
+        __syncthreads();
+        if (sub == 0) {
+            float Mn = M;
+#pragma unroll
+            for (int i = 1; i < S; ++i) Mn = fmaxf(Mn, part[warp + i][D]);
+            const float a = Mn == -INFINITY ? 0.f : dev::fast_exp2(M - Mn);
+            den *= a;
+#pragma unroll
+            for (int x = 0; x < DPL; ++x) num[x] *= a;
+#pragma unroll
+            for (int i = 1; i < S; ++i) {
+                const float w = Mn == -INFINITY ? 0.f : dev::fast_exp2(part[warp + i][D] - Mn);
+                den = fmaf(part[warp + i][D + 1], w, den);
+#pragma unroll
+                for (int x = 0; x < DPL; ++x) num[x] = fmaf(part[warp + i][lane * DPL + x], w, num[x]);
+            }
+        }
+    }
+    if (!cut || sub) return;
     const float inv = den > 0.f ? p.out_scale / den : 0.f;
     uint16_t *dst = p.out + row * D + lane * DPL;
     if constexpr (DPL == 4)
@@ -601,7 +686,7 @@ __global__ void __launch_bounds__(I4_NT) decode_int4_merge_kernel(const DecodePa
         *reinterpret_cast<uint32_t *>(dst) = dev::pack_bf16x2(num[0] * inv, num[1] * inv);
 }
 
-constexpr int I4_NST = 4;                           // stages of a warp's ring
+constexpr int I4_NST = 3;                           // pairs of tiles in a warp's ring
 
 // Either report CTAs per SM (launch == false) or launch.
 template <int D>
@@ -622,10 +707,19 @@ cudaError_t dispatch_int4(const Plan &pl, int group, bool launch, int *per_sm, c
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kernel, a->p);
     if (e != cudaSuccess || a->p.MB == 1) return e;           // one block: no unit is cut
-    const long long rows = (long long)a->p.layers * a->p.B * a->p.Hq;
-    cfg.gridDim = dim3((unsigned)((rows + I4_NW - 1) / I4_NW));
+    // the merge: as many warps to a row as leave each about a batch of its partials (on average a
+    // unit's share of the teams)
+    const long long rows = (long long)a->p.layers * a->p.B * a->p.Hq, units = (long long)a->p.layers * a->p.B * (a->p.Hkv / int4_team(a->p.Hkv));
+    const long long parts = (long long)pl.grid * I4_NW / int4_team(a->p.Hkv) / units;
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, decode_int4_merge_kernel<D>, a->p);
+    auto merge = [&](auto s_) {
+        constexpr int S = decltype(s_)::value;
+        cfg.gridDim = dim3((unsigned)((rows + I4_NW / S - 1) / (I4_NW / S)));
+        return cudaLaunchKernelEx(&cfg, decode_int4_merge_kernel<D, S>, a->p);
+    };
+    if (parts > 32) return merge(std::integral_constant<int, 8>{});
+    if (parts > 8) return merge(std::integral_constant<int, 4>{});
+    return merge(std::integral_constant<int, 1>{});
 }
 
 template <int D>
