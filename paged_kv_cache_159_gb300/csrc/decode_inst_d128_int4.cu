@@ -3,4 +3,4 @@
 
 template cudaError_t pkv::decode::dispatch_int4<128>(const pkv::decode::Plan &, int, bool, int *, cudaStream_t,
                                                       const pkv::decode::LaunchArgs *);
-template size_t pkv::decode::int4_smem<128>(int);
+template void pkv::decode::int4_shape<128>(int, int, int *, size_t *);

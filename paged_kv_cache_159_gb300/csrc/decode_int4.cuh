@@ -38,8 +38,13 @@
 namespace pkv {
 namespace decode {
 
-constexpr int I4_NW = 8;                            // warps per CTA
-constexpr int I4_NT = I4_NW * 32;
+// Warps of a CTA, one CTA per SM, by the registers that a warp's state needs (168 a thread at 12 warps,
+// 128 at 16; 16 columns hold twice the state).  At D 128 twelve warps run as fast as sixteen, which
+// spill: the integer pipe is what they share.
+template <int D, int NH>
+constexpr int int4_warps() { return D == 128 ? (NH == 1 ? 12 : 8) : (NH == 1 ? 16 : 12); }
+constexpr int I4_NST = 3;                           // pairs of blocks in a warp's ring
+constexpr int I4_MERGE_WARPS = 8;
 
 // KV heads of a team: all of them up to 8, else the largest divisor up to 8.
 __host__ __device__ constexpr int int4_team(int Hkv)
@@ -346,8 +351,8 @@ struct Int4Compute {
 };
 
 // Shared memory of a CTA: the warps' rings, then prefix [B + 1], lens [B] and the scan's sums.
-template <int D, int NST>
-constexpr size_t int4_ring_bytes() { return (size_t)I4_NW * NST * 4 * int4::tile_bytes(D); }
+template <int D, int NH>
+__host__ __device__ constexpr size_t int4_ring_bytes() { return (size_t)int4_warps<D, NH>() * I4_NST * 4 * int4::tile_bytes(D); }
 
 // A unit (layer l, sequence b, KV head h): its length and blocks, the task it starts at.
 struct Int4Unit { int l, b, h, L, nb; long long U0; };
@@ -388,13 +393,15 @@ __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0
 
 // p.part_o [teams][2][HG][group][D], p.part_ml [teams][2][HG][group][2], p.prefix_n [B + 2]: the
 // tasks before each sequence within a layer, then the number of teams.
-template <int D, int NST, int NH>
-__global__ void __launch_bounds__(I4_NT, NH == 2 ? 1 : 2) decode_int4_kernel(const DecodeParams p)
+// APPEND: the new tokens' rows are written first.
+template <int D, int NH, bool APPEND>
+__global__ void __launch_bounds__(int4_warps<D, NH>() * 32, 1) decode_int4_kernel(const DecodeParams p)
 {
+    constexpr int NST = I4_NST, NW = int4_warps<D, NH>(), NT = NW * 32;
     constexpr int TILE = int4::tile_bytes(D);
     constexpr int CH = TILE / 16;                  // 16-byte pieces of a tile
     extern __shared__ __align__(128) uint8_t smem[];
-    int32_t *prefix = reinterpret_cast<int32_t *>(smem + int4_ring_bytes<D, NST>()), *lens = prefix + p.B + 1;
+    int32_t *prefix = reinterpret_cast<int32_t *>(smem + int4_ring_bytes<D, NH>()), *lens = prefix + p.B + 1;
     int32_t *wsum = lens + p.B;                    // [I4_NW]
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(dev::FULL, tid >> 5, 0);         // (known to be the same in every lane)
@@ -404,7 +411,7 @@ __global__ void __launch_bounds__(I4_NT, NH == 2 ? 1 : 2) decode_int4_kernel(con
 
     // ---- tasks per sequence (head groups x blocks; 0 for an invalid length), scanned
     {
-        const int per = (p.B + I4_NT - 1) / I4_NT;
+        const int per = (p.B + NT - 1) / NT;
         const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
         int run = 0;
         for (int b = b0; b < b1; ++b) {
@@ -429,7 +436,7 @@ __global__ void __launch_bounds__(I4_NT, NH == 2 ? 1 : 2) decode_int4_kernel(con
         __syncthreads();
         int base = incl - run, total = 0;
 #pragma unroll
-        for (int w = 0; w < I4_NW; ++w) {
+        for (int w = 0; w < NW; ++w) {
             if (w < warp) base += wsum[w];
             total += wsum[w];
         }
@@ -439,12 +446,12 @@ __global__ void __launch_bounds__(I4_NT, NH == 2 ? 1 : 2) decode_int4_kernel(con
     }
     const int W1 = prefix[p.B];
     const long long W = (long long)W1 * p.layers;
-    const int teams = (int)min(W, (long long)((int)gridDim.x * I4_NW / HG));
+    const int teams = (int)min(W, (long long)((int)gridDim.x * NW / HG));
     if (blockIdx.x == 0) {                         // for the merge
-        for (int b = tid; b <= p.B; b += I4_NT) p.prefix_n[b] = prefix[b];
+        for (int b = tid; b <= p.B; b += NT) p.prefix_n[b] = prefix[b];
         if (tid == 0) p.prefix_n[p.B + 1] = teams;
     }
-    const int gw = blockIdx.x * I4_NW + warp, team = gw / HG, hh = gw - team * HG;
+    const int gw = blockIdx.x * NW + warp, team = gw / HG, hh = gw - team * HG;
     if (team >= teams) return;
     const long long s = int4_start(W, teams, team), e = int4_start(W, teams, team + 1);
     const int n = (int)(e - s);
@@ -520,7 +527,7 @@ __global__ void __launch_bounds__(I4_NT, NH == 2 ? 1 : 2) decode_int4_kernel(con
                 last = t1;
                 ++ii;
             }
-            if (p.k_new && ii == iend && last >= 0) {   // the new token's row goes in before its block is read
+            if (APPEND && ii == iend && last >= 0) {   // the new token's row goes in before its block is read
                 const size_t src = (((size_t)iu.l * p.B + iu.b) * Hkv + iu.h) * D;
                 int4::write_row_pair<D>(p.k_new + src, p.v_new + src, p.inv_k_scale, p.inv_v_scale, (iu.L - 1) % BS,
                                         const_cast<uint8_t *>(p.key_cache) + (size_t)last * TILE,
@@ -590,12 +597,12 @@ __global__ void __launch_bounds__(I4_NT, NH == 2 ? 1 : 2) decode_int4_kernel(con
 // Merge the partials of cut units: S warps of a CTA per output row, each taking every S-th partial,
 // up to 8 of them in flight at a time; the row's first warp combines the S results.
 template <int D, int S>
-__global__ void __launch_bounds__(I4_NT) decode_int4_merge_kernel(const DecodeParams p)
+__global__ void __launch_bounds__(I4_MERGE_WARPS * 32) decode_int4_merge_kernel(const DecodeParams p)
 {
     constexpr int DPL = D / 32, BATCH = 8;
-    __shared__ float part[S > 1 ? I4_NW : 1][D + 2];
+    __shared__ float part[S > 1 ? I4_MERGE_WARPS : 1][D + 2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, HG = int4_team(p.Hkv), sub = warp % S;
-    const long long row = (long long)blockIdx.x * (I4_NW / S) + warp / S;
+    const long long row = (long long)blockIdx.x * (I4_MERGE_WARPS / S) + warp / S;
     pdl_launch();
     pdl_wait();
     bool cut = false;
@@ -686,21 +693,22 @@ __global__ void __launch_bounds__(I4_NT) decode_int4_merge_kernel(const DecodePa
         *reinterpret_cast<uint32_t *>(dst) = dev::pack_bf16x2(num[0] * inv, num[1] * inv);
 }
 
-constexpr int I4_NST = 3;                           // pairs of tiles in a warp's ring
-
 // Either report CTAs per SM (launch == false) or launch.
 template <int D>
 cudaError_t dispatch_int4(const Plan &pl, int group, bool launch, int *per_sm, cudaStream_t s, const LaunchArgs *a)
 {
-    auto kernel = group > 8 ? decode_int4_kernel<D, I4_NST, 2> : decode_int4_kernel<D, I4_NST, 1>;
-    cudaError_t e = prepare(kernel, pl.smem, I4_NT, launch ? nullptr : per_sm);
+    const bool wide = group > 8, append = launch && a->p.k_new;
+    auto kernel = wide ? (append ? decode_int4_kernel<D, 2, true> : decode_int4_kernel<D, 2, false>)
+                       : (append ? decode_int4_kernel<D, 1, true> : decode_int4_kernel<D, 1, false>);
+    const int threads = pl.nw * 32;
+    cudaError_t e = prepare(kernel, pl.smem, threads, launch ? nullptr : per_sm);
     if (e != cudaSuccess || !launch) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)pl.grid);
-    cfg.blockDim = dim3(I4_NT);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = s;
     cfg.attrs = &attr;
@@ -709,12 +717,14 @@ cudaError_t dispatch_int4(const Plan &pl, int group, bool launch, int *per_sm, c
     if (e != cudaSuccess || a->p.MB == 1) return e;           // one block: no unit is cut
     // the merge: as many warps to a row as leave each about a batch of its partials (on average a
     // unit's share of the teams)
-    const long long rows = (long long)a->p.layers * a->p.B * a->p.Hq, units = (long long)a->p.layers * a->p.B * (a->p.Hkv / int4_team(a->p.Hkv));
-    const long long parts = (long long)pl.grid * I4_NW / int4_team(a->p.Hkv) / units;
+    const int HG = int4_team(a->p.Hkv);
+    const long long rows = (long long)a->p.layers * a->p.B * a->p.Hq, units = (long long)a->p.layers * a->p.B * (a->p.Hkv / HG);
+    const long long parts = (long long)pl.grid * pl.nw / HG / units;
+    cfg.blockDim = dim3(I4_MERGE_WARPS * 32);
     cfg.dynamicSmemBytes = 0;
     auto merge = [&](auto s_) {
         constexpr int S = decltype(s_)::value;
-        cfg.gridDim = dim3((unsigned)((rows + I4_NW / S - 1) / (I4_NW / S)));
+        cfg.gridDim = dim3((unsigned)((rows + I4_MERGE_WARPS / S - 1) / (I4_MERGE_WARPS / S)));
         return cudaLaunchKernelEx(&cfg, decode_int4_merge_kernel<D, S>, a->p);
     };
     if (parts > 32) return merge(std::integral_constant<int, 8>{});
@@ -722,10 +732,13 @@ cudaError_t dispatch_int4(const Plan &pl, int group, bool launch, int *per_sm, c
     return merge(std::integral_constant<int, 1>{});
 }
 
+// Warps of a CTA for a group size, and a CTA's shared memory for a batch.
 template <int D>
-size_t int4_smem(int B)
+void int4_shape(int group, int B, int *warps, size_t *smem)
 {
-    return int4_ring_bytes<D, I4_NST>() + ((size_t)2 * B + 1 + I4_NW) * 4;
+    const bool wide = group > 8;
+    *warps = wide ? int4_warps<D, 2>() : int4_warps<D, 1>();
+    *smem = (wide ? int4_ring_bytes<D, 2>() : int4_ring_bytes<D, 1>()) + ((size_t)2 * B + 1 + *warps) * 4;
 }
 
 }  // namespace decode

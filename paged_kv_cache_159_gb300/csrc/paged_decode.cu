@@ -28,15 +28,13 @@ namespace decode {
 template <int D>
 cudaError_t dispatch_int4(const Plan &pl, int group, bool launch, int *per_sm, cudaStream_t s, const LaunchArgs *a);
 template <int D>
-size_t int4_smem(int B);
-extern template size_t int4_smem<64>(int);
-extern template size_t int4_smem<128>(int);
+void int4_shape(int group, int B, int *warps, size_t *smem);
+extern template void int4_shape<64>(int, int, int *, size_t *);
+extern template void int4_shape<128>(int, int, int *, size_t *);
 extern template cudaError_t dispatch_int4<64>(const Plan &, int, bool, int *, cudaStream_t, const LaunchArgs *);
 extern template cudaError_t dispatch_int4<128>(const Plan &, int, bool, int *, cudaStream_t, const LaunchArgs *);
 
 namespace {
-
-constexpr int INT4_WARPS = 8;               // warps per CTA of the INT4 kernel
 
 int sm_count_cached()
 {
@@ -74,8 +72,9 @@ int make_plan_int4(const pkv_pool_desc &d, int B, int group, const pkv_decode_op
 {
     if (o.variant || o.warps_per_cta || o.stages || o.heads_per_copy || o.shared_prefix_blocks || o.unit_cost || o.grid_ctas < 0)
         return PKV_ERR_INVALID;
-    pl.variant = pl.nw = pl.ns = pl.hp = pl.sp = pl.uc = 0;
-    pl.smem = d.head_dim == 128 ? int4_smem<128>(B) : int4_smem<64>(B);
+    pl.variant = pl.ns = pl.hp = pl.sp = pl.uc = 0;
+    if (d.head_dim == 128) int4_shape<128>(group, B, &pl.nw, &pl.smem);
+    else int4_shape<64>(group, B, &pl.nw, &pl.smem);
     if (o.grid_ctas) {
         pl.grid = o.grid_ctas;
     } else {
@@ -84,7 +83,7 @@ int make_plan_int4(const pkv_pool_desc &d, int B, int group, const pkv_decode_op
         pl.grid = sm_count_cached() * per_sm;
     }
     // rows of partials: 2 segments of every team's HG warps, the warps of the grid at most
-    const size_t rows = (size_t)pl.grid * INT4_WARPS * 2 * group;
+    const size_t rows = (size_t)pl.grid * pl.nw * 2 * group;
     pl.ws_counters = 0;
     pl.ws_pre_n = ((size_t)d.num_layers * B * d.num_kv_heads * 4 + 255) / 256 * 256;
     pl.ws_o = pl.ws_pre_n + (((size_t)B + 2) * 4 + 255) / 256 * 256;
