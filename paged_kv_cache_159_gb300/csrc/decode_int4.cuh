@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(int4_warps<D, NH>() * 32, 1) decode_int4_kerne
     }
     const int W1 = prefix[p.B];
     const long long W = (long long)W1 * p.layers;
-    const int teams = (int)min(W, (long long)((int)gridDim.x * NW / HG));
+    const int teams = (int)min((W + 1) / 2, (long long)((int)gridDim.x * NW / HG));
     if (blockIdx.x == 0) {                         // for the merge
         for (int b = tid; b <= p.B; b += NT) p.prefix_n[b] = prefix[b];
         if (tid == 0) p.prefix_n[p.B + 1] = teams;

@@ -109,6 +109,23 @@ __device__ __forceinline__ void store_v(uint8_t *tile, int t, int o, uint32_t co
     if ((o & 3) == 0) tile[P::v_scale(t, o)] = (uint8_t)scale_byte;
 }
 
+// The (layer, token, head) row of octet i of [layers, tokens, heads, D / 8], and the octet: with 32-bit
+// arithmetic wherever the whole range fits (a 64-bit division is some seventy instructions, more
+// than the rest of an octet's work).
+template <int D, class I>
+struct Row {
+    int o, h;
+    int64_t layer, t;
+    __device__ __forceinline__ Row(I i, I num_tokens, I num_kv_heads)
+    {
+        const I row = i / (D / 8), lt = row / num_kv_heads, l = lt / num_tokens;
+        o = (int)(i - row * (D / 8));
+        h = (int)(row - lt * num_kv_heads);
+        layer = (int64_t)l;
+        t = (int64_t)(lt - l * num_tokens);
+    }
+};
+
 // One warp writes token t's K and V rows (bf16, 16-byte aligned) into their tiles: lanes 0 ..
 // D / 8 - 1 take K's octets, lanes 16 .. 16 + D / 8 - 1 V's.
 template <int D>

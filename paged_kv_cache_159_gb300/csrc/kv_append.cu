@@ -14,6 +14,8 @@
 // writes every layer: a token has the same slot in each, since a block spans all layers.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "int4.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -92,35 +94,63 @@ __global__ void __launch_bounds__(256) kv_append_fp8_kernel(
 // INT4 pool: a thread per octet (8 columns, 16 bytes of bf16), so that the four lanes of a
 // 32-column group share its maximum by two shuffles, K and V handled by the same thread: one
 // 32-bit word of K codes, two 16-bit words of V codes and, by the group's first lane, the scale
-// bytes (places and arithmetic: int4.cuh).
-template <int D>
+// bytes (places and arithmetic: int4.cuh).  A thread takes UNROLL octets a block's width apart, their
+// loads in flight together.  I: the index type, 32 bits where the octets' count allows.
+template <int D, int UNROLL, class I>
 __global__ void __launch_bounds__(256) kv_append_int4_kernel(
     const uint4 *__restrict__ k, const uint4 *__restrict__ v, const int64_t *__restrict__ slots,
-    int64_t num_tokens, int layers, int num_kv_heads, int64_t num_slots, float inv_k, float inv_v,
+    I num_tokens, I total, I num_kv_heads, int64_t num_slots, float inv_k, float inv_v,
     uint8_t *__restrict__ key_cache, uint8_t *__restrict__ value_cache, uint32_t *err)
 {
-    constexpr int OCTETS = D / 8, TILE = int4::tile_bytes(D);
-    const int64_t total = layers * num_tokens * num_kv_heads * OCTETS;
-    // whole warps take part in every pass (the shuffles)
-    for (int64_t i0 = blockIdx.x * (int64_t)blockDim.x + (threadIdx.x & ~31); i0 < total;
-         i0 += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t i = i0 + (threadIdx.x & 31);
-        const bool in = i < total;
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        const uint4 kx = in ? __ldg(k + i) : zero, vx = in ? __ldg(v + i) : zero;
-        uint32_t ks, vs;
-        const uint32_t kc = int4::quantise_octet(kx, inv_k, ks), vc = int4::quantise_octet(vx, inv_v, vs);
-        if (!in) continue;
-        const int64_t row = i / OCTETS, lt = row / num_kv_heads;       // (layer, token, head); (layer, token)
-        const int o = (int)(i - row * OCTETS), h = (int)(row - lt * num_kv_heads);
-        const int64_t layer = lt / num_tokens, t = lt - layer * num_tokens;
-        const int64_t slot = __ldg(slots + t);
-        if (slot >= num_slots) flag_error(err, PKV_DEVERR_SLOT);
-        if (slot < 0 || slot >= num_slots) continue;
-        const int64_t tile = ((layer * (num_slots >> 4) + (slot >> 4)) * num_kv_heads + h) * TILE;
-        int4::store_k<D>(key_cache + tile, (int)(slot & 15), o, kc, ks);
-        int4::store_v<D>(value_cache + tile, (int)(slot & 15), o, vc, vs);
+    constexpr int TILE = int4::tile_bytes(D);
+    const I i0 = (I)blockIdx.x * (I)(256 * UNROLL) + threadIdx.x;
+    uint4 kx[UNROLL], vx[UNROLL];
+    int64_t tile[UNROLL];
+    int off[UNROLL], oct[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        const I i = i0 + (I)(256 * u);
+        kx[u] = vx[u] = make_uint4(0u, 0u, 0u, 0u);
+        tile[u] = -1;
+        if (i < total) {
+            kx[u] = __ldcs(k + i);
+            vx[u] = __ldcs(v + i);
+            const int4::Row<D, I> r(i, num_tokens, num_kv_heads);
+            const int64_t slot = __ldg(slots + r.t);
+            if (slot >= num_slots) flag_error(err, PKV_DEVERR_SLOT);
+            else if (slot >= 0) tile[u] = ((r.layer * (num_slots >> 4) + (slot >> 4)) * (int64_t)num_kv_heads + r.h) * TILE;
+            off[u] = (int)(slot & 15);
+            oct[u] = r.o;
+        }
     }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {                 // (whole warps: the shuffles)
+        uint32_t ks, vs;
+        const uint32_t kc = int4::quantise_octet(kx[u], inv_k, ks), vc = int4::quantise_octet(vx[u], inv_v, vs);
+        if (tile[u] < 0) continue;
+        int4::store_k<D>(key_cache + tile[u], off[u], oct[u], kc, ks);
+        int4::store_v<D>(value_cache + tile[u], off[u], oct[u], vc, vs);
+    }
+}
+
+template <int D>
+void append_int4(const pkv_pool *pool, int layers, const void *k, const void *v, const int64_t *slots, int32_t num_tokens,
+                 void *key_cache, void *value_cache, cudaStream_t s)
+{
+    const pkv_pool_desc &d = pool->desc;
+    const int64_t total = (int64_t)layers * num_tokens * d.num_kv_heads * (D / 8);
+    auto run = [&](auto unroll, auto index) {
+        constexpr int U = decltype(unroll)::value;
+        using I = decltype(index);
+        kv_append_int4_kernel<D, U, I><<<(unsigned)((total + 256 * U - 1) / (256 * U)), 256, 0, s>>>(
+            static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), slots, (I)num_tokens, (I)total, (I)d.num_kv_heads,
+            (int64_t)d.num_blocks * d.block_size, pool->inv_k_scale, pool->inv_v_scale, static_cast<uint8_t *>(key_cache),
+            static_cast<uint8_t *>(value_cache), pool->d_err);
+    };
+    // few octets: one a thread, to spread them over the SMs; many: four in flight
+    if (total < (int64_t)1 << 18) run(std::integral_constant<int, 1>{}, uint32_t{});
+    else if (total < (int64_t)1 << 31) run(std::integral_constant<int, 4>{}, uint32_t{});
+    else run(std::integral_constant<int, 4>{}, uint64_t{});
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -151,14 +181,8 @@ int append_impl(pkv_pool *pool, int layers, const void *k, const void *v,
             num_tokens, layers, d.num_kv_heads, chunks, num_slots, static_cast<uint4 *>(key_cache),
             static_cast<uint4 *>(value_cache), pool->d_err);
     } else if (d.kv_dtype == PKV_KV_INT4) {
-        auto run = [&](auto kernel) {
-            kernel<<<(unsigned)blocks, threads, 0, s>>>(
-                static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), slot_mapping, num_tokens, layers,
-                d.num_kv_heads, num_slots, pool->inv_k_scale, pool->inv_v_scale, static_cast<uint8_t *>(key_cache),
-                static_cast<uint8_t *>(value_cache), pool->d_err);
-        };
-        if (d.head_dim == 128) run(kv_append_int4_kernel<128>);
-        else run(kv_append_int4_kernel<64>);
+        if (d.head_dim == 128) append_int4<128>(pool, layers, k, v, slot_mapping, num_tokens, key_cache, value_cache, s);
+        else append_int4<64>(pool, layers, k, v, slot_mapping, num_tokens, key_cache, value_cache, s);
     } else {
         kv_append_fp8_kernel<<<(unsigned)blocks, threads, 0, s>>>(
             static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), slot_mapping,

@@ -12,6 +12,8 @@
 // Bound by DRAM: a row's reads are 17 D / 32 bytes (INT4), D (FP8) or 2 D, its writes 2 D.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "int4.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -27,63 +29,93 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
                       dev::pack_bf16x2(x[6], x[7]));
 }
 
-// Octet o of token t of a tile.
+// Octet o of token t of a tile: its stored words (load), and its 8 bf16 (expand).
 template <int FORMAT, int D, bool IS_K>
-__device__ __forceinline__ uint4 read_octet(const uint8_t *tile, int t, int o, float scale)
-{
-    if constexpr (FORMAT == PKV_KV_BF16) {
-        return __ldg(reinterpret_cast<const uint4 *>(tile + t * (2 * D)) + o);
-    } else if constexpr (FORMAT == PKV_KV_FP8E4M3) {
-        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(tile + t * D) + o);
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t h = dev::e4m3x2_to_f16x2((uint16_t)((i < 2 ? c.x : c.y) >> (16 * (i & 1))));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            x[2 * i] = f.x * scale;
-            x[2 * i + 1] = f.y * scale;
-        }
-        return pack8(x);
-    } else {
-        using P = int4::Place<D>;
-        uint32_t codes, sb;
-        if constexpr (IS_K) {
-            codes = __ldg(reinterpret_cast<const uint32_t *>(tile + P::k_word(t, o)));
-            sb = __ldg(tile + P::k_scale(t, o));
+struct Octet {
+    uint4 w;                              // bf16: the octet; FP8: codes in x, y; INT4: codes in x, the scale byte in y
+    __device__ __forceinline__ void load(const uint8_t *tile, int t, int o)
+    {
+        if constexpr (FORMAT == PKV_KV_BF16) {
+            w = __ldg(reinterpret_cast<const uint4 *>(tile + t * (2 * D)) + o);
+        } else if constexpr (FORMAT == PKV_KV_FP8E4M3) {
+            const uint2 c = __ldg(reinterpret_cast<const uint2 *>(tile + t * D) + o);
+            w.x = c.x;
+            w.y = c.y;
         } else {
-            const uint8_t *w = tile + P::v_word(t, o);
-            codes = __ldg(reinterpret_cast<const uint16_t *>(w)) |
-                    ((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(w + P::VSTEP)) << 16);
-            sb = __ldg(tile + P::v_scale(t, o));
+            using P = int4::Place<D>;
+            if constexpr (IS_K) {
+                w.x = __ldg(reinterpret_cast<const uint32_t *>(tile + P::k_word(t, o)));
+                w.y = __ldg(tile + P::k_scale(t, o));
+            } else {
+                const uint8_t *s = tile + P::v_word(t, o);
+                w.x = __ldg(reinterpret_cast<const uint16_t *>(s));
+                w.z = __ldg(reinterpret_cast<const uint16_t *>(s + P::VSTEP));
+                w.y = __ldg(tile + P::v_scale(t, o));
+            }
         }
-        const float s = int4::scale_value(sb);
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = ((float)((int)((codes >> (4 * i)) & 15u) - 8) * s) * scale;
-        return pack8(x);
     }
-}
+    __device__ __forceinline__ uint4 expand(float scale) const
+    {
+        if constexpr (FORMAT == PKV_KV_BF16) {
+            return w;
+        } else if constexpr (FORMAT == PKV_KV_FP8E4M3) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t h = dev::e4m3x2_to_f16x2((uint16_t)((i < 2 ? w.x : w.y) >> (16 * (i & 1))));
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                x[2 * i] = f.x * scale;
+                x[2 * i + 1] = f.y * scale;
+            }
+            return pack8(x);
+        } else {
+            const uint32_t codes = IS_K ? w.x : (w.x | (w.z << 16));
+            const float s = int4::scale_value(w.y);
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // 2^23 + n, less 2^23 + 8: the code's value, exactly
+                const float n = __uint_as_float(((codes >> (4 * i)) & 15u) | 0x4B000000u) - 8388616.f;
+                x[i] = (n * s) * scale;
+            }
+            return pack8(x);
+        }
+    }
+};
 
-template <int FORMAT, int D>
+// A thread takes UNROLL octets a block's width apart, their loads in flight together.  I: the index
+// type, 32 bits where the octets' count allows.
+template <int FORMAT, int D, int UNROLL, class I>
 __global__ void __launch_bounds__(THREADS) kv_gather_kernel(
-    const int64_t *__restrict__ slots, int64_t num_tokens, int layers, int num_kv_heads, int64_t num_slots,
+    const int64_t *__restrict__ slots, I num_tokens, I total, I num_kv_heads, int64_t num_slots,
     float k_scale, float v_scale, const uint8_t *__restrict__ key_cache, const uint8_t *__restrict__ value_cache,
     uint4 *__restrict__ k, uint4 *__restrict__ v, uint32_t *err)
 {
-    constexpr int OCTETS = D / 8;
     constexpr int64_t TILE = FORMAT == PKV_KV_INT4 ? int4::tile_bytes(D) : 16 * D * (FORMAT == PKV_KV_BF16 ? 2 : 1);
-    const int64_t total = layers * num_tokens * num_kv_heads * OCTETS;
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t row = i / OCTETS, lt = row / num_kv_heads;       // (layer, token, head); (layer, token)
-        const int o = (int)(i - row * OCTETS), h = (int)(row - lt * num_kv_heads);
-        const int64_t layer = lt / num_tokens, t = lt - layer * num_tokens;
-        const int64_t slot = __ldg(slots + t);
+    const I i0 = (I)blockIdx.x * (I)(THREADS * UNROLL) + threadIdx.x;
+    Octet<FORMAT, D, true> ko[UNROLL];
+    Octet<FORMAT, D, false> vo[UNROLL];
+    bool in[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        // (no branches, so that the loads go out together: skipped rows read slot 0)
+        const I i = i0 + (I)(THREADS * u);
+        const int4::Row<D, I> r(i < total ? i : total - 1, num_tokens, num_kv_heads);
+        const int64_t slot = __ldg(slots + r.t);
+        const bool valid = slot >= 0 && slot < num_slots;
+        in[u] = valid && i < total;
         if (slot >= num_slots) dev::flag_error(err, PKV_DEVERR_SLOT);
-        if (slot < 0 || slot >= num_slots) continue;
-        const int64_t tile = ((layer * (num_slots >> 4) + (slot >> 4)) * num_kv_heads + h) * TILE;
-        const int off = (int)(slot & 15);
-        k[i] = read_octet<FORMAT, D, true>(key_cache + tile, off, o, k_scale);
-        v[i] = read_octet<FORMAT, D, false>(value_cache + tile, off, o, v_scale);
+        const int64_t at = valid ? slot : 0;
+        const int64_t tile = ((r.layer * (num_slots >> 4) + (at >> 4)) * (int64_t)num_kv_heads + r.h) * TILE;
+        ko[u].load(key_cache + tile, (int)(at & 15), r.o);
+        vo[u].load(value_cache + tile, (int)(at & 15), r.o);
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        if (!in[u]) continue;
+        const I i = i0 + (I)(THREADS * u);
+        __stcs(k + i, ko[u].expand(k_scale));
+        __stcs(v + i, vo[u].expand(v_scale));
     }
 }
 
@@ -102,25 +134,28 @@ int gather_impl(pkv_pool *pool, int layers, const int64_t *slot_mapping, int32_t
         return PKV_ERR_INVALID;
     const pkv_pool_desc &d = pool->desc;
     const int64_t total = (int64_t)layers * num_tokens * d.num_kv_heads * (d.head_dim / 8);
-    int64_t blocks = (total + THREADS - 1) / THREADS;
-    if (blocks > 65535LL * 32) blocks = 65535LL * 32;
-    auto run = [&](auto kernel) {
-        kernel<<<(unsigned)blocks, THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
-            slot_mapping, num_tokens, layers, d.num_kv_heads, (int64_t)d.num_blocks * d.block_size, d.k_scale,
-            d.v_scale, static_cast<const uint8_t *>(key_cache), static_cast<const uint8_t *>(value_cache),
-            static_cast<uint4 *>(k), static_cast<uint4 *>(v), pool->d_err);
+    auto launch = [&](auto format, auto dim, auto unroll, auto index) {
+        constexpr int U = decltype(unroll)::value;
+        using I = decltype(index);
+        kv_gather_kernel<decltype(format)::value, decltype(dim)::value, U, I>
+            <<<(unsigned)((total + THREADS * U - 1) / (THREADS * U)), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
+                slot_mapping, (I)num_tokens, (I)total, (I)d.num_kv_heads, (int64_t)d.num_blocks * d.block_size, d.k_scale,
+                d.v_scale, static_cast<const uint8_t *>(key_cache), static_cast<const uint8_t *>(value_cache),
+                static_cast<uint4 *>(k), static_cast<uint4 *>(v), pool->d_err);
     };
-    const bool wide = d.head_dim == 128;
-    if (d.kv_dtype == PKV_KV_BF16) {
-        if (wide) run(kv_gather_kernel<PKV_KV_BF16, 128>);
-        else run(kv_gather_kernel<PKV_KV_BF16, 64>);
-    } else if (d.kv_dtype == PKV_KV_FP8E4M3) {
-        if (wide) run(kv_gather_kernel<PKV_KV_FP8E4M3, 128>);
-        else run(kv_gather_kernel<PKV_KV_FP8E4M3, 64>);
-    } else {
-        if (wide) run(kv_gather_kernel<PKV_KV_INT4, 128>);
-        else run(kv_gather_kernel<PKV_KV_INT4, 64>);
-    }
+    auto run = [&](auto format, auto dim) {
+        // few octets: one a thread, to spread them over the SMs; many: four in flight
+        if (total < (int64_t)1 << 18) launch(format, dim, std::integral_constant<int, 1>{}, uint32_t{});
+        else if (total < (int64_t)1 << 31) launch(format, dim, std::integral_constant<int, 4>{}, uint32_t{});
+        else launch(format, dim, std::integral_constant<int, 4>{}, uint64_t{});
+    };
+    auto by_dim = [&](auto format) {
+        if (d.head_dim == 128) run(format, std::integral_constant<int, 128>{});
+        else run(format, std::integral_constant<int, 64>{});
+    };
+    if (d.kv_dtype == PKV_KV_BF16) by_dim(std::integral_constant<int, PKV_KV_BF16>{});
+    else if (d.kv_dtype == PKV_KV_FP8E4M3) by_dim(std::integral_constant<int, PKV_KV_FP8E4M3>{});
+    else by_dim(std::integral_constant<int, PKV_KV_INT4>{});
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
