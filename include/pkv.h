@@ -306,8 +306,8 @@ int pkv_kv_append_layers(pkv_pool *pool, const void *k, const void *v,
 
 /* Read K/V rows back [Slot]: for each token t with slot = slot_mapping[t] >= 0, k[t][h][:] and
  * v[t][h][:] (device bf16 [num_tokens, Hkv, D], 16-byte aligned) receive what the pool holds at
- * that slot: the stored bits of a bf16 pool; bf16(fl32(k_scale * element)) of FP8 and INT4
- * pools, round-to-nearest-even (an INT4 element is scale * (n - 8), exact).  Rows of a negative
+ * that slot: the stored bits of a bf16 pool; bf16(fl32(k_scale * element)) of an FP8 pool;
+ * bf16(fl32((n - 8) * fl32(scale * k_scale))) of an INT4 pool; all round-to-nearest-even.  Rows of a negative
  * slot (padding) stay as they were, and so do those of a slot beyond the pool, which sets
  * PKV_DEVERR_SLOT.  Slots may repeat.  k and v must not overlap the caches. */
 int pkv_kv_gather(pkv_pool *pool, const int64_t *slot_mapping, int32_t num_tokens, const void *key_cache,

@@ -97,15 +97,21 @@ def append(k_bits, v_bits, slots, key_cache, value_cache, k_scale: float, v_scal
             tile[:, sc[t, ::GROUP]] = sb[i]
 
 
-def rows(cache, slots, is_key: bool, pool_scale: float) -> np.ndarray:
-    """The elements [T, Hkv, D] that the slots hold, in 64 bits."""
+def codes(cache, slots, is_key: bool):
+    """What the slots hold: n - 8 and the scales' values, each [T, Hkv, D]."""
     D = cache.shape[-1] * 2 // 17
     at, sh, sc = places(D, is_key)
     slots = np.asarray(slots)
     tiles, t = cache[slots // BS], slots % BS                   # [T, Hkv, bytes]
     code = np.take_along_axis(tiles, np.broadcast_to(at[t][:, None], tiles.shape[:2] + (D,)), -1) >> sh[t][:, None]
     sb = np.take_along_axis(tiles, np.broadcast_to(sc[t][:, None], tiles.shape[:2] + (D,)), -1)
-    return ((code & 15).astype(np.float64) - 8) * e4m3_values()[sb] * float(np.float32(pool_scale))
+    return (code & 15).astype(np.int64) - 8, e4m3_values()[sb]
+
+
+def rows(cache, slots, is_key: bool, pool_scale: float) -> np.ndarray:
+    """The elements [T, Hkv, D] that the slots hold, in 64 bits."""
+    n, s = codes(cache, slots, is_key)
+    return n * s * float(np.float32(pool_scale))
 
 
 def attend(q, k, v, scale: float):

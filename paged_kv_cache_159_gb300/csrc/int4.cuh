@@ -27,6 +27,7 @@
 #include <cstdint>
 
 #include "pkv_device.cuh"
+#include "tc_device.cuh"
 
 namespace pkv {
 namespace int4 {
@@ -60,32 +61,61 @@ __device__ __forceinline__ float scale_value(uint32_t byte)
     return __low2float(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// Quantise an octet of a row (8 bf16; the 4 consecutive lanes of a group call it together):
-// the 8 codes, column 8 o + i at bits 4 i, and the group's scale byte.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// Quantise an octet of a row (8 bf16; whole warps call it, the 4 consecutive lanes of a group
+// share their maximum): the 8 codes, column 8 o + i at bits 4 i, and the group's scale byte.
 //   y = fl32(x * fl32(1 / pool scale)),  a = max |y| over the group (NaN ignored),
 //   scale = E4M3(fl32(a * fl32(1 / 7))) rounded to nearest even, saturating,
 //   n = clamp(rint(fl32(y * fl32(1 / scale))), -7, 7) + 8   (8 where the scale is 0 or y NaN).
 // Rounding the scale to nearest moves a by at most 1/16, so |y| / scale < 7.5 and the clamp
-// costs no more than half a step.
+// costs no more than half a step; where the scale is neither saturated nor subnormal it
+// changes nothing.  Bound by instruction issue, so the common case does without the clamp and
+// NaN: the maximum is taken on the bits of x, two at a time (multiplying is monotonic), and the
+// rest in packed fp32 pairs.  Adding 1.5 2^23 rounds to the nearest integer (ties to even); four
+// codes join as one exact integer below 2^16.
 __device__ __forceinline__ uint32_t quantise_octet(uint4 x, float inv_pool, uint32_t &scale_byte)
 {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float y[8], a = 0.f;
+    constexpr uint32_t ABS = 0x7fff7fffu;
+    const uint32_t m2 = __vmaxu2(__vmaxu2(w[0] & ABS, w[1] & ABS), __vmaxu2(w[2] & ABS, w[3] & ABS));
+    uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+    top = max(top, __shfl_xor_sync(dev::FULL, top, 1));
+    top = max(top, __shfl_xor_sync(dev::FULL, top, 2));
+    float a = __uint_as_float(top << 16) * inv_pool;
+    const bool nan = top > 0x7f80u;
+    if (__any_sync(dev::FULL, nan)) {                  // the maximum without them
+        float b = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        y[2 * i] = dev::bf16_lo(w[i]) * inv_pool;
-        y[2 * i + 1] = dev::bf16_hi(w[i]) * inv_pool;
-        a = fmaxf(a, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+        for (int i = 0; i < 4; ++i) b = fmaxf(b, fmaxf(fabsf(dev::bf16_lo(w[i]) * inv_pool), fabsf(dev::bf16_hi(w[i]) * inv_pool)));
+        b = fmaxf(b, __shfl_xor_sync(dev::FULL, b, 1));
+        a = fmaxf(b, __shfl_xor_sync(dev::FULL, b, 2));
     }
-    a = fmaxf(a, __shfl_xor_sync(dev::FULL, a, 1));
-    a = fmaxf(a, __shfl_xor_sync(dev::FULL, a, 2));
     scale_byte = dev::e4m3x2_satfinite(a * (1.0f / 7.0f), 0.f) & 0xffu;
-    const float s = scale_value(scale_byte), r = __frcp_rn(s);
+    const float s = scale_value(scale_byte), r = s > 0.f ? __frcp_rn(s) : 0.f;
+    const bool plain = a * r < 7.5f && !nan;
     uint32_t codes = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int n = s > 0.f ? max(-7, min(7, __float2int_rn(y[i] * r))) : 0;
-        codes |= (uint32_t)(n + 8) << (4 * i);
+    for (int q = 0; q < 2; ++q) {
+        float2 n[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t b = w[2 * q + i];
+            float2 v = mul2(mul2(make_float2(dev::bf16_lo(b), dev::bf16_hi(b)), make_float2(inv_pool, inv_pool)), make_float2(r, r));
+            if (!plain) {
+                v.x = v.x == v.x ? fminf(fmaxf(v.x, -7.f), 7.f) : 0.f;
+                v.y = v.y == v.y ? fminf(fmaxf(v.y, -7.f), 7.f) : 0.f;
+            }
+            n[i] = tc::fadd2(tc::fadd2(v, make_float2(12582912.f, 12582912.f)), make_float2(-12582904.f, -12582904.f));      // n + 8
+        }
+        const float2 t = tc::ffma2(n[1], make_float2(256.f, 256.f), n[0]);
+        codes |= (__float_as_uint(fmaf(t.y, 16.f, t.x) + 8388608.f) & 0xffffu) << (16 * q);
     }
     return codes;
 }
@@ -118,7 +148,7 @@ struct Row {
     int64_t layer, t;
     __device__ __forceinline__ Row(I i, I num_tokens, I num_kv_heads)
     {
-        const I row = i / (D / 8), lt = row / num_kv_heads, l = lt / num_tokens;
+        const I row = i / (D / 8), lt = row / num_kv_heads, l = lt < num_tokens ? (I)0 : lt / num_tokens;
         o = (int)(i - row * (D / 8));
         h = (int)(row - lt * num_kv_heads);
         layer = (int64_t)l;

@@ -6,9 +6,9 @@
 // a decode instance, or moved into a pool of another type, whatever the pool stores them in.
 //
 // A thread per octet (8 columns of a row), K and V by the same thread, so that every output
-// row is written in 16-byte pieces by consecutive lanes.  FP8 and INT4 elements become
-// bf16(fl32(pool scale * value)): E4M3 values, and scale * (n - 8) of INT4, are exact in fp32,
-// so each element is rounded twice, and only once where the pool scale is a power of two.
+// row is written in 16-byte pieces by consecutive lanes.  An FP8 element becomes bf16(fl32(pool scale *
+// value)), an INT4 one bf16(fl32((n - 8) * fl32(scale * pool scale))): at most two fp32 roundings before
+// the one to bf16, none where the pool scale is a power of two.
 // Bound by DRAM: a row's reads are 17 D / 32 bytes (INT4), D (FP8) or 2 D, its writes 2 D.
 #include <cuda_runtime.h>
 
@@ -70,13 +70,15 @@ struct Octet {
             return pack8(x);
         } else {
             const uint32_t codes = IS_K ? w.x : (w.x | (w.z << 16));
-            const float s = int4::scale_value(w.y);
+            // the nibble at bits 4 i joins 2^23's mantissa in place; less 2^23 + 8 16^i it is (n - 8) 16^i,
+            // exactly, and the multiplier's 16^-i brings it back
+            const float s = int4::scale_value(w.y) * scale;
+            const float m[4] = {s, s * 0x1p-4f, s * 0x1p-8f, s * 0x1p-12f};
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                // 2^23 + n, less 2^23 + 8: the code's value, exactly
-                const float n = __uint_as_float(((codes >> (4 * i)) & 15u) | 0x4B000000u) - 8388616.f;
-                x[i] = (n * s) * scale;
+                const uint32_t bits = ((i < 4 ? codes : codes >> 16) & (15u << (4 * (i & 3)))) | 0x4B000000u;
+                x[i] = (__uint_as_float(bits) - (8388608.f + (float)(8 << (4 * (i & 3))))) * m[i & 3];
             }
             return pack8(x);
         }

@@ -49,8 +49,9 @@ def test_append_and_gather_bit_for_bit(T, Hkv, D):
     for out, cache, is_key, s in ((ko, kh, True, 0.0131), (vo, vh, False, 0.0087)):
         ref = torch.full((T, Hkv, D), -5.0, dtype=torch.bfloat16)
         w = slots >= 0
-        # scale * (n - 8) is exact in fp32; times the pool scale in fp32, then bf16
-        x = O.rows(cache, slots[w], is_key, 1.0).astype(np.float32) * np.float32(s)
+        # (n - 8) times the fp32 product of the scales, in fp32, then bf16
+        n, e = O.codes(cache, slots[w], is_key)
+        x = n.astype(np.float32) * (e.astype(np.float32) * np.float32(s))
         ref[torch.from_numpy(w)] = torch.from_numpy(x).bfloat16()
         assert np.array_equal(I.bits(out), I.bits(ref))
 
