@@ -99,23 +99,31 @@ __device__ __forceinline__ uint32_t quantise_octet(uint4 x, float inv_pool, uint
     }
     scale_byte = dev::e4m3x2_satfinite(a * (1.0f / 7.0f), 0.f) & 0xffu;
     const float s = scale_value(scale_byte), r = s > 0.f ? __frcp_rn(s) : 0.f;
-    const bool plain = a * r < 7.5f && !nan;
+    const float2 inv2 = make_float2(inv_pool, inv_pool);
     uint32_t codes = 0;
+    if (a * r < 7.5f && !nan) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        float2 n[2];
+        for (int q = 0; q < 2; ++q) {
+            float2 n[2];                               // n + 8
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t b = w[2 * q + i];
-            float2 v = mul2(mul2(make_float2(dev::bf16_lo(b), dev::bf16_hi(b)), make_float2(inv_pool, inv_pool)), make_float2(r, r));
-            if (!plain) {
-                v.x = v.x == v.x ? fminf(fmaxf(v.x, -7.f), 7.f) : 0.f;
-                v.y = v.y == v.y ? fminf(fmaxf(v.y, -7.f), 7.f) : 0.f;
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t b = w[2 * q + i];
+                const float2 y = mul2(make_float2(dev::bf16_lo(b), dev::bf16_hi(b)), inv2);
+                // (a packed product would be fused with the packed sum, although both say .rn)
+                const float2 v = make_float2(__fmul_rn(y.x, r), __fmul_rn(y.y, r));
+                n[i] = tc::fadd2(tc::fadd2(v, make_float2(12582912.f, 12582912.f)), make_float2(-12582904.f, -12582904.f));
             }
-            n[i] = tc::fadd2(tc::fadd2(v, make_float2(12582912.f, 12582912.f)), make_float2(-12582904.f, -12582904.f));      // n + 8
+            const float2 t = tc::ffma2(n[1], make_float2(256.f, 256.f), n[0]);
+            codes |= (__float_as_uint(fmaf(t.y, 16.f, t.x) + 8388608.f) & 0xffffu) << (16 * q);
         }
-        const float2 t = tc::ffma2(n[1], make_float2(256.f, 256.f), n[0]);
-        codes |= (__float_as_uint(fmaf(t.y, 16.f, t.x) + 8388608.f) & 0xffffu) << (16 * q);
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t b = i < 2 ? w[0] : i < 4 ? w[1] : i < 6 ? w[2] : w[3];
+            float v = __fmul_rn(__fmul_rn((i & 1) ? dev::bf16_hi(b) : dev::bf16_lo(b), inv_pool), r);
+            v = v == v ? fminf(fmaxf(v, -7.f), 7.f) : 0.f;
+            codes |= (uint32_t)(__float2int_rn(v) + 8) << (4 * i);
+        }
     }
     return codes;
 }
