@@ -141,12 +141,26 @@ __device__ __forceinline__ uint4 expand_octet(uint32_t codes, uint32_t scale_byt
                       __byte_perm(c, d, 0x7632u));
 }
 
-// A CTA per expanded block (a grid stride apart), a warp per KV head.
+// NG consecutive words.
+template <int NG>
+__device__ __forceinline__ void load_words(const uint8_t *src, uint32_t (&w)[NG])
+{
+    if constexpr (NG == 4) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src));
+        w[0] = x.x; w[1] = x.y;
+    }
+}
+
+// A CTA per expanded block (a grid stride apart), a warp per KV head.  Lane (r, c) of a pass takes
+// stored row r of eight and one octet of every group in it: 4 NG consecutive bytes of K (the words of
+// octet c), 4 NG of V (the 16-bit words of two neighbouring columns' quads), and the row's scales.
 template <int D>
 __global__ void __launch_bounds__(EXPAND_THREADS) prefill_expand_kernel(const ExpandParams p)
 {
-    using P = int4::Place<D>;
-    constexpr int OCTETS = D / 8, TPP = 32 / OCTETS;             // octets of a row, tokens per pass
+    constexpr int NG = D / 32, OCTETS = D / 8;
     const PlanHeader *hdr = reinterpret_cast<const PlanHeader *>(p.plan);
     if (hdr->magic != PLAN_MAGIC || hdr->grid != p.grid || hdr->batch != p.B) {
         if (blockIdx.x == 0 && threadIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_PLAN);
@@ -158,7 +172,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS) prefill_expand_kernel(const Ex
         if (blockIdx.x == 0 && threadIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_PLAN);
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, o = lane % OCTETS, t0 = lane / OCTETS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3;
     for (int x = blockIdx.x; x < total; x += gridDim.x) {
         int lo = 0, hi = p.B;                                    // off[lo] <= x < off[hi]
         while (hi - lo > 1) {
@@ -178,14 +192,28 @@ __global__ void __launch_bounds__(EXPAND_THREADS) prefill_expand_kernel(const Ex
             const size_t tile = ((size_t)id * p.Hkv + h) * int4::tile_bytes(D), out = ((size_t)x * p.Hkv + h) * (16 * D);
             const uint8_t *kt = p.key_cache + tile, *vt = p.value_cache + tile;
             uint4 *ko = reinterpret_cast<uint4 *>(p.ws_k + out), *vo = reinterpret_cast<uint4 *>(p.ws_v + out);
+            uint32_t kw[2][NG], vw[2][NG], vs[2][NG], ks[2];
 #pragma unroll
-            for (int t = t0; t < 16; t += TPP) {
-                const uint8_t *w = vt + P::v_word(t, o);
-                const uint32_t kc = __ldg(reinterpret_cast<const uint32_t *>(kt + P::k_word(t, o)));
-                const uint32_t vc = __ldg(reinterpret_cast<const uint16_t *>(w)) |
-                                    ((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(w + P::VSTEP)) << 16);
-                ko[t * OCTETS + o] = expand_octet(kc, __ldg(kt + P::k_scale(t, o)));
-                vo[t * OCTETS + o] = expand_octet(vc, __ldg(vt + P::v_scale(t, o)));
+            for (int x = 0; x < 2; ++x) {
+                const int r = 8 * x + (lane >> 2);
+                load_words(kt + r * (D / 2) + c * (4 * NG), kw[x]);
+                load_words(vt + r * (D / 2) + c * (4 * NG), vw[x]);
+                load_words(vt + 8 * D + (r & 3) * (4 * NG), vs[x]);
+                if constexpr (NG == 4) ks[x] = __ldg(reinterpret_cast<const uint32_t *>(kt + 8 * D + r * NG));
+                else ks[x] = __ldg(reinterpret_cast<const uint16_t *>(kt + 8 * D + r * NG));
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = 8 * x + (lane >> 2);
+                // K: stored row r holds token (r & 8) | (r >> 1 & 3) | (r & 1) << 2; V: token r, whose quads
+                // 2 c, 2 c + 1 are octet c, or c ^ 2 where the halves are swapped
+                const int t = (r & 8) | ((r >> 1) & 3) | ((r & 1) << 2), oc = D == 128 ? c ^ (r & 2) : c;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    ko[t * OCTETS + 4 * j + c] = expand_octet(kw[x][j], (ks[x] >> (8 * j)) & 0xffu);
+                    const uint32_t codes = __byte_perm(vw[x][j >> 1], vw[x][NG / 2 + (j >> 1)], (j & 1) ? 0x7632u : 0x5410u);
+                    vo[r * OCTETS + 4 * j + oc] = expand_octet(codes, (vs[x][j] >> (8 * (r >> 2))) & 0xffu);
+                }
             }
         }
     }
