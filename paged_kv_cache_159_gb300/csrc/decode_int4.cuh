@@ -594,23 +594,30 @@ __global__ void __launch_bounds__(int4_warps<D, NH>() * 32, 1) decode_int4_kerne
     cp_wait<0>();
 }
 
-// Merge the partials of cut units: S warps of a CTA per output row, each taking every S-th partial,
-// up to 8 of them in flight at a time; the row's first warp combines the S results.
-template <int D, int S>
+// Merge the partials of cut units.  S warps of a CTA per output row, each taking every S-th partial;
+// the row's first warp combines the S results.  Or (S = 1) R rows of one KV head to a warp.  Either way
+// 8 partials are in flight at a time.
+template <int D, int S, int R>
 __global__ void __launch_bounds__(I4_MERGE_WARPS * 32) decode_int4_merge_kernel(const DecodeParams p)
 {
-    constexpr int DPL = D / 32, BATCH = 8;
+    static_assert(S == 1 || R == 1, "one way or the other");
+    constexpr int DPL = D / 32, BATCH = 8 / R;
     __shared__ float part[S > 1 ? I4_MERGE_WARPS : 1][D + 2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, HG = int4_team(p.Hkv), sub = warp % S;
-    const long long row = (long long)blockIdx.x * (I4_MERGE_WARPS / S) + warp / S;
+    const long long row = ((long long)blockIdx.x * (I4_MERGE_WARPS / S) + warp / S) * R;
     pdl_launch();
     pdl_wait();
     bool cut = false;
-    float M = -INFINITY, den = 0.f, num[DPL];
+    float M[R], den[R], num[R][DPL];
 #pragma unroll
-    for (int x = 0; x < DPL; ++x) num[x] = 0.f;
+    for (int q = 0; q < R; ++q) {
+        M[q] = -INFINITY;
+        den[q] = 0.f;
+#pragma unroll
+        for (int x = 0; x < DPL; ++x) num[q][x] = 0.f;
+    }
     if (row < (long long)p.layers * p.B * p.Hq) {
-        const int lb = (int)(row / p.Hq), hq = (int)(row - (long long)lb * p.Hq), l = lb / p.B, b = lb - l * p.B;
+        const int lb = (int)div_nonneg(row, p.Hq), hq = (int)(row - (long long)lb * p.Hq), l = lb / p.B, b = lb - l * p.B;
         const int h = hq / p.group, hg = h / HG, hh = h - hg * HG;
         const int P0 = __ldcg(p.prefix_n + b), P1 = __ldcg(p.prefix_n + b + 1), W1 = __ldcg(p.prefix_n + p.B), T = __ldcg(p.prefix_n + p.B + 1);
         const int nb = (P1 - P0) / (p.Hkv / HG);
@@ -621,76 +628,85 @@ __global__ void __launch_bounds__(I4_MERGE_WARPS * 32) decode_int4_merge_kernel(
         cut = c0 < c1;                                       // (not an invalid length, nor a whole unit)
         const int first_slot = cut && int4_start(W, T, c0) < U0 ? 1 : 0;
         for (int c = c0 + sub; cut && c <= c1; c += BATCH * S) {
-            float2 ml[BATCH];
-            float o[BATCH][DPL];
+            float2 ml[R][BATCH];
+            float o[R][BATCH][DPL];
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                const int cc = c + i * S;
-                ml[i] = make_float2(-INFINITY, 0.f);
+            for (int i = 0; i < BATCH; ++i)
 #pragma unroll
-                for (int x = 0; x < DPL; ++x) o[i][x] = 0.f;
-                if (cc <= c1) {
-                    const size_t pr = (((size_t)cc * 2 + (cc == c0 ? first_slot : 0)) * HG + hh) * p.group + (hq - h * p.group);
-                    ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + pr);
-                    if constexpr (DPL == 4) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + pr * D) + lane);
-                        o[i][0] = v.x; o[i][1] = v.y; o[i][2] = v.z; o[i][3] = v.w;
-                    } else {
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.part_o + pr * D) + lane);
-                        o[i][0] = v.x; o[i][1] = v.y;
+                for (int q = 0; q < R; ++q) {
+                    const int cc = c + i * S;
+                    ml[q][i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                    for (int x = 0; x < DPL; ++x) o[q][i][x] = 0.f;
+                    if (cc <= c1) {
+                        const size_t pr = (((size_t)cc * 2 + (cc == c0 ? first_slot : 0)) * HG + hh) * p.group + (hq - h * p.group) + q;
+                        ml[q][i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + pr);
+                        if constexpr (DPL == 4) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + pr * D) + lane);
+                            o[q][i][0] = v.x; o[q][i][1] = v.y; o[q][i][2] = v.z; o[q][i][3] = v.w;
+                        } else {
+                            const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.part_o + pr * D) + lane);
+                            o[q][i][0] = v.x; o[q][i][1] = v.y;
+                        }
                     }
                 }
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                float Mn = M[q];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) Mn = fmaxf(Mn, ml[q][i].x);
+                if (Mn == -INFINITY) continue;               // nothing valid so far (bad table entries)
+                const float a = dev::fast_exp2(M[q] - Mn);
+                den[q] *= a;
+#pragma unroll
+                for (int x = 0; x < DPL; ++x) num[q][x] *= a;
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const float w = dev::fast_exp2(ml[q][i].x - Mn);
+                    den[q] = fmaf(ml[q][i].y, w, den[q]);
+#pragma unroll
+                    for (int x = 0; x < DPL; ++x) num[q][x] = fmaf(o[q][i][x], w, num[q][x]);
+                }
+                M[q] = Mn;
             }
-            float Mn = M;
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) Mn = fmaxf(Mn, ml[i].x);
-            if (Mn == -INFINITY) continue;                   // nothing valid so far (bad table entries)
-            const float a = dev::fast_exp2(M - Mn);
-            den *= a;
-#pragma unroll
-            for (int x = 0; x < DPL; ++x) num[x] *= a;
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                const float w = dev::fast_exp2(ml[i].x - Mn);
-                den = fmaf(ml[i].y, w, den);
-#pragma unroll
-                for (int x = 0; x < DPL; ++x) num[x] = fmaf(o[i][x], w, num[x]);
-            }
-            M = Mn;
         }
     }
     if constexpr (S > 1) {
 #pragma unroll
-        for (int x = 0; x < DPL; ++x) part[warp][lane * DPL + x] = num[x];
+        for (int x = 0; x < DPL; ++x) part[warp][lane * DPL + x] = num[0][x];
         if (lane == 0) {
-            part[warp][D] = M;
-            part[warp][D + 1] = den;
+            part[warp][D] = M[0];
+            part[warp][D + 1] = den[0];
         }
         __syncthreads();
         if (sub == 0) {
-            float Mn = M;
+            float Mn = M[0];
 #pragma unroll
             for (int i = 1; i < S; ++i) Mn = fmaxf(Mn, part[warp + i][D]);
-            const float a = Mn == -INFINITY ? 0.f : dev::fast_exp2(M - Mn);
-            den *= a;
+            const float a = Mn == -INFINITY ? 0.f : dev::fast_exp2(M[0] - Mn);
+            den[0] *= a;
 #pragma unroll
-            for (int x = 0; x < DPL; ++x) num[x] *= a;
+            for (int x = 0; x < DPL; ++x) num[0][x] *= a;
 #pragma unroll
             for (int i = 1; i < S; ++i) {
                 const float w = Mn == -INFINITY ? 0.f : dev::fast_exp2(part[warp + i][D] - Mn);
-                den = fmaf(part[warp + i][D + 1], w, den);
+                den[0] = fmaf(part[warp + i][D + 1], w, den[0]);
 #pragma unroll
-                for (int x = 0; x < DPL; ++x) num[x] = fmaf(part[warp + i][lane * DPL + x], w, num[x]);
+                for (int x = 0; x < DPL; ++x) num[0][x] = fmaf(part[warp + i][lane * DPL + x], w, num[0][x]);
             }
         }
     }
     if (!cut || sub) return;
-    const float inv = den > 0.f ? p.out_scale / den : 0.f;
-    uint16_t *dst = p.out + row * D + lane * DPL;
-    if constexpr (DPL == 4)
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(dev::pack_bf16x2(num[0] * inv, num[1] * inv), dev::pack_bf16x2(num[2] * inv, num[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(dst) = dev::pack_bf16x2(num[0] * inv, num[1] * inv);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        const float inv = den[q] > 0.f ? p.out_scale / den[q] : 0.f;
+        uint16_t *dst = p.out + (row + q) * D + lane * DPL;
+        if constexpr (DPL == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(dev::pack_bf16x2(num[q][0] * inv, num[q][1] * inv),
+                                                         dev::pack_bf16x2(num[q][2] * inv, num[q][3] * inv));
+        else
+            *reinterpret_cast<uint32_t *>(dst) = dev::pack_bf16x2(num[q][0] * inv, num[q][1] * inv);
+    }
 }
 
 // Either report CTAs per SM (launch == false) or launch.
@@ -715,21 +731,24 @@ cudaError_t dispatch_int4(const Plan &pl, int group, bool launch, int *per_sm, c
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kernel, a->p);
     if (e != cudaSuccess || a->p.MB == 1) return e;           // one block: no unit is cut
-    // the merge: as many warps to a row as leave each about a batch of its partials (on average a
-    // unit's share of the teams)
+    // the merge: by a unit's average share of the teams, as many warps to a row as leave each about a
+    // batch of its partials, or four rows to a warp where most units are whole or cut once (8192 rows
+    // of the ragged batch: 3.7 us a launch less than a warp each)
     const int HG = int4_team(a->p.Hkv);
     const long long rows = (long long)a->p.layers * a->p.B * a->p.Hq, units = (long long)a->p.layers * a->p.B * (a->p.Hkv / HG);
     const long long parts = (long long)pl.grid * pl.nw / HG / units;
     cfg.blockDim = dim3(I4_MERGE_WARPS * 32);
     cfg.dynamicSmemBytes = 0;
-    auto merge = [&](auto s_) {
-        constexpr int S = decltype(s_)::value;
-        cfg.gridDim = dim3((unsigned)((rows + I4_MERGE_WARPS / S - 1) / (I4_MERGE_WARPS / S)));
-        return cudaLaunchKernelEx(&cfg, decode_int4_merge_kernel<D, S>, a->p);
+    auto merge = [&](auto s_, auto r_) {
+        constexpr int S = decltype(s_)::value, R = decltype(r_)::value, PER = I4_MERGE_WARPS / S * R;
+        cfg.gridDim = dim3((unsigned)((rows + PER - 1) / PER));
+        return cudaLaunchKernelEx(&cfg, decode_int4_merge_kernel<D, S, R>, a->p);
     };
-    if (parts > 32) return merge(std::integral_constant<int, 8>{});
-    if (parts > 8) return merge(std::integral_constant<int, 4>{});
-    return merge(std::integral_constant<int, 1>{});
+    using One = std::integral_constant<int, 1>;
+    if (parts > 32) return merge(std::integral_constant<int, 8>{}, One{});
+    if (parts > 8) return merge(std::integral_constant<int, 4>{}, One{});
+    if (parts <= 1 && group % 4 == 0) return merge(One{}, std::integral_constant<int, 4>{});
+    return merge(One{}, One{});
 }
 
 // Warps of a CTA for a group size, and a CTA's shared memory for a batch.

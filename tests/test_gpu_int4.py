@@ -140,6 +140,9 @@ SHAPES = [  # lens, Hq, Hkv, D
     ([64, 1000, 3], 16, 1, 128),
     ([300] * 12, 12, 3, 128),
     ([2500], 32, 8, 128),
+    ([70, 33, 1], 24, 12, 64),             # more KV heads than a team: 6 of 12
+    ([40, 130], 22, 11, 128),              # 11 teams of one
+    ([90, 17], 32, 16, 64),
 ]
 
 
@@ -173,6 +176,39 @@ def test_physical_placement_and_repeats_do_not_change_a_bit():
         c = I.Case(lens, 16, 4, 128, seed=5, order_seed=order)
         outs += [c.decode({"grid_ctas": 61}), c.decode({"grid_ctas": 61})]
     assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D", [(700, 4, 2, 64), (4096, 1, 1, 128)])
+def test_large_batches_of_short_sequences(B, Hq, Hkv, D):
+    lens = np.random.default_rng(B).integers(1, 40, B)
+    lens[5] = 300
+    c = I.Case(lens.tolist(), Hq, Hkv, D, seed=B)
+    c.check(c.decode())
+
+
+def test_offsets_past_32_bits():
+    """The same rows at the far end of a pool of 4.5 GB a cache: same codes, rows and outputs."""
+    c = I.Case([40, 1000], 16, 8, 128, seed=21)
+    NB, shift = 520_000, 520_000 - c.NB
+    pool = pkv.Pool(NB, 8, 128, pkv.KV_INT4, c.k_scale, c.v_scale)
+    pool.attach_device(0)
+    kc, vc = (torch.zeros(NB, 8, 1088, dtype=torch.uint8, device="cuda") for _ in range(2))
+    slots = I.dev(c.slots + 16 * shift)
+    pkv.kv_append(pool, c.k.cuda(), c.v.cuda(), slots, kc, vc)
+    ko, vo, kr, vr = (torch.zeros_like(c.k, device="cuda") for _ in range(4))
+    pkv.kv_gather(pool, slots, kc, vc, ko, vo)
+    pkv.kv_gather(c.pool, I.dev(c.slots), c.kc, c.vc, kr, vr)
+    assert torch.equal(ko, kr) and torch.equal(vo, vr) and int(kr.count_nonzero()) > 0
+    bt = torch.where(c.bt >= 0, c.bt + shift, c.bt)
+    out = torch.zeros_like(c.q, device="cuda")
+    pkv.paged_attention_decode(pool, c.q.cuda(), kc, vc, bt, c.sl, c.scale, out, c.workspace())
+    assert pool.get_device_error() == (pkv.OK, 0) and torch.equal(out, c.decode())
+    m = torch.arange(NB - 1, NB - 4, -1, dtype=torch.int32, device="cuda")
+    want = [x[m.long()] for x in (kc, vc)]
+    pkv.move_blocks(pool, kc, vc, m, torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"), bt)
+    assert torch.equal(kc[:3], want[0]) and torch.equal(vc[:3], want[1])
+    pkv.paged_attention_decode(pool, c.q.cuda(), kc, vc, bt, c.sl, c.scale, out, c.workspace())
+    assert torch.equal(out, c.decode())
 
 
 def test_long_sequence_over_many_ctas():
