@@ -193,21 +193,32 @@ def _np_ptr(a: np.ndarray):
 
 
 def _dev_ptr(t, what: str):
-    """Device address of a contiguous CUDA tensor (or None)."""
+    """Device address of a contiguous CUDA tensor (or None).  A plain int: the argument types make
+    the pointer of it, and the smallest calls take no longer on the device than here."""
     if t is None:
         return None
     if not getattr(t, "is_cuda", False):
         raise ValueError("%s must be a CUDA tensor" % what)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+_current_raw_stream = None
 
 
 def _stream_ptr(stream):
     if stream is None:
-        import torch
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
+        global _current_raw_stream
+        if _current_raw_stream is None:
+            import torch
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # without building a Stream object
+            if raw is None:
+                _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+            else:
+                _current_raw_stream = lambda: raw(torch.cuda.current_device())  # noqa: E731
+        return _current_raw_stream()
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 class Pool:
@@ -592,7 +603,7 @@ def decode_step_host(pool: Pool, host: dict, dev: dict, key_cache, value_cache, 
     h = host_step(_host_ptr(host["q"], "q"), _host_ptr(host.get("k_new"), "k_new"), _host_ptr(host.get("v_new"), "v_new"),
                   _host_ptr(host.get("block_tables"), "block_tables"), _host_ptr(host.get("seq_lens"), "seq_lens"),
                   _host_ptr(host["out"], "out"), int(bool(host.get("contiguous", False))))
-    d = device_step(*[(_dev_ptr(dev.get(k), k).value if dev.get(k) is not None else None)
+    d = device_step(*[_dev_ptr(dev.get(k), k)
                       for k in ("q", "k_new", "v_new", "block_tables", "seq_lens", "out")])
     o = _opts(opts)
     _check(lib().pkv_decode_step_host(pool.handle, ctypes.byref(h), ctypes.byref(d), _dev_ptr(key_cache, "key_cache"),
@@ -618,7 +629,7 @@ class DecodeStepHost:
                             _host_ptr(host.get("block_tables"), "block_tables"),
                             _host_ptr(host.get("seq_lens"), "seq_lens"), _host_ptr(host["out"], "out"),
                             int(bool(host.get("contiguous", False))))
-        self._d = device_step(*[(_dev_ptr(dev.get(k), k).value if dev.get(k) is not None else None)
+        self._d = device_step(*[_dev_ptr(dev.get(k), k)
                                 for k in ("q", "k_new", "v_new", "block_tables", "seq_lens", "out")])
         self._o = _opts(opts)
         self._fn = lib().pkv_decode_step_host
