@@ -69,63 +69,84 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return d;
 }
 
-// Quantise an octet of a row (8 bf16; whole warps call it, the 4 consecutive lanes of a group
-// share their maximum): the 8 codes, column 8 o + i at bits 4 i, and the group's scale byte.
+// Quantise octets of rows (8 bf16 each; whole warps call it, the 4 consecutive lanes of a group
+// share its maximum): the 8 codes, column 8 o + i at bits 4 i, and the group's scale byte.
 //   y = fl32(x * fl32(1 / pool scale)),  a = max |y| over the group (NaN ignored),
 //   scale = E4M3(fl32(a * fl32(1 / 7))) rounded to nearest even, saturating,
 //   n = clamp(rint(fl32(y * fl32(1 / scale))), -7, 7) + 8   (8 where the scale is 0 or y NaN).
 // Rounding the scale to nearest moves a by at most 1/16, so |y| / scale < 7.5 and the clamp
 // costs no more than half a step; where the scale is neither saturated nor subnormal it
 // changes nothing.  Bound by instruction issue, so the common case does without the clamp and
-// NaN: the maximum is taken on the bits of x, two at a time (multiplying is monotonic), and the
-// rest in packed fp32 pairs.  Adding 1.5 2^23 rounds to the nearest integer (ties to even); four
-// codes join as one exact integer below 2^16.
-__device__ __forceinline__ uint32_t quantise_octet(uint4 x, float inv_pool, uint32_t &scale_byte)
+// NaN, and a warp that holds either takes the plain steps below: the maximum is taken on the bits
+// of x, two at a time (multiplying is monotonic), and the rest in packed fp32 pairs.  Adding 1.5 2^23
+// rounds to the nearest integer (ties to even); four codes join as one exact integer below 2^16.
+static __device__ __noinline__ uint32_t quantise_plain(uint4 x, float inv_pool, uint32_t *scale_byte)
 {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    constexpr uint32_t ABS = 0x7fff7fffu;
-    const uint32_t m2 = __vmaxu2(__vmaxu2(w[0] & ABS, w[1] & ABS), __vmaxu2(w[2] & ABS, w[3] & ABS));
-    uint32_t top = max(m2 & 0xffffu, m2 >> 16);
-    top = max(top, __shfl_xor_sync(dev::FULL, top, 1));
-    top = max(top, __shfl_xor_sync(dev::FULL, top, 2));
-    float a = __uint_as_float(top << 16) * inv_pool;
-    const bool nan = top > 0x7f80u;
-    if (__any_sync(dev::FULL, nan)) {                  // the maximum without them
-        float b = 0.f;
+    float y[8], a = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b = fmaxf(b, fmaxf(fabsf(dev::bf16_lo(w[i]) * inv_pool), fabsf(dev::bf16_hi(w[i]) * inv_pool)));
-        b = fmaxf(b, __shfl_xor_sync(dev::FULL, b, 1));
-        a = fmaxf(b, __shfl_xor_sync(dev::FULL, b, 2));
+    for (int i = 0; i < 8; ++i) {
+        y[i] = __fmul_rn((i & 1) ? dev::bf16_hi(w[i >> 1]) : dev::bf16_lo(w[i >> 1]), inv_pool);
+        a = fmaxf(a, fabsf(y[i]));
     }
-    scale_byte = dev::e4m3x2_satfinite(a * (1.0f / 7.0f), 0.f) & 0xffu;
-    const float s = scale_value(scale_byte), r = s > 0.f ? __frcp_rn(s) : 0.f;
-    const float2 inv2 = make_float2(inv_pool, inv_pool);
+    a = fmaxf(a, __shfl_xor_sync(dev::FULL, a, 1));
+    a = fmaxf(a, __shfl_xor_sync(dev::FULL, a, 2));
+    *scale_byte = dev::e4m3x2_satfinite(a * (1.0f / 7.0f), 0.f) & 0xffu;
+    const float s = scale_value(*scale_byte), r = s > 0.f ? __frcp_rn(s) : 0.f;
     uint32_t codes = 0;
-    if (a * r < 7.5f && !nan) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+    for (int i = 0; i < 8; ++i) {
+        float v = __fmul_rn(y[i], r);
+        v = v == v ? fminf(fmaxf(v, -7.f), 7.f) : 0.f;
+        codes |= (uint32_t)(__float2int_rn(v) + 8) << (4 * i);
+    }
+    return codes;
+}
+
+template <int N>
+__device__ __forceinline__ void quantise(const uint4 (&x)[N], const float (&inv_pool)[N], uint32_t (&codes)[N],
+                                         uint32_t (&scale_byte)[N])
+{
+    float r[N];
+    bool rare = false;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        constexpr uint32_t ABS = 0x7fff7fffu;
+        const uint32_t m2 = __vmaxu2(__vmaxu2(x[k].x & ABS, x[k].y & ABS), __vmaxu2(x[k].z & ABS, x[k].w & ABS));
+        uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+        top = max(top, __shfl_xor_sync(dev::FULL, top, 1));
+        top = max(top, __shfl_xor_sync(dev::FULL, top, 2));
+        const float a = __uint_as_float(top << 16) * inv_pool[k];
+        scale_byte[k] = dev::e4m3x2_satfinite(a * (1.0f / 7.0f), 0.f) & 0xffu;
+        const float s = scale_value(scale_byte[k]);
+        r[k] = s > 0.f ? __frcp_rn(s) : 0.f;
+        rare |= !(a * r[k] < 7.5f);                    // (NaN among them)
+    }
+    if (__any_sync(dev::FULL, rare)) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) codes[k] = quantise_plain(x[k], inv_pool[k], &scale_byte[k]);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        float q[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
             float2 n[2];                               // n + 8
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t b = w[2 * q + i];
-                const float2 y = mul2(make_float2(dev::bf16_lo(b), dev::bf16_hi(b)), inv2);
+                const uint32_t b = w[2 * h + i];
+                const float2 y = mul2(make_float2(dev::bf16_lo(b), dev::bf16_hi(b)), make_float2(inv_pool[k], inv_pool[k]));
                 // (a packed product would be fused with the packed sum, although both say .rn)
-                const float2 v = make_float2(__fmul_rn(y.x, r), __fmul_rn(y.y, r));
+                const float2 v = make_float2(__fmul_rn(y.x, r[k]), __fmul_rn(y.y, r[k]));
                 n[i] = tc::fadd2(tc::fadd2(v, make_float2(12582912.f, 12582912.f)), make_float2(-12582904.f, -12582904.f));
             }
             const float2 t = tc::ffma2(n[1], make_float2(256.f, 256.f), n[0]);
-            codes |= (__float_as_uint(fmaf(t.y, 16.f, t.x) + 8388608.f) & 0xffffu) << (16 * q);
+            q[h] = fmaf(t.y, 16.f, t.x) + 8388608.f;
         }
-    } else {
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t b = i < 2 ? w[0] : i < 4 ? w[1] : i < 6 ? w[2] : w[3];
-            float v = __fmul_rn(__fmul_rn((i & 1) ? dev::bf16_hi(b) : dev::bf16_lo(b), inv_pool), r);
-            v = v == v ? fminf(fmaxf(v, -7.f), 7.f) : 0.f;
-            codes |= (uint32_t)(__float2int_rn(v) + 8) << (4 * i);
-        }
+        codes[k] = __byte_perm(__float_as_uint(q[0]), __float_as_uint(q[1]), 0x5410u);
     }
-    return codes;
 }
 
 // Token t's octet o of a K or V tile.
@@ -172,13 +193,14 @@ __device__ __forceinline__ void write_row_pair(const uint16_t *k, const uint16_t
 {
     const int o = lane & 15;
     const bool isv = lane >= 16, mine = o < D / 8;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (mine) x = *reinterpret_cast<const uint4 *>((isv ? v : k) + 8 * o);
-    uint32_t sb;
-    const uint32_t codes = quantise_octet(x, isv ? inv_v : inv_k, sb);
+    uint4 x[1] = {make_uint4(0u, 0u, 0u, 0u)};
+    if (mine) x[0] = *reinterpret_cast<const uint4 *>((isv ? v : k) + 8 * o);
+    const float inv[1] = {isv ? inv_v : inv_k};
+    uint32_t codes[1], sb[1];
+    quantise(x, inv, codes, sb);
     if (!mine) return;
-    if (isv) store_v<D>(vtile, t, o, codes, sb);
-    else store_k<D>(ktile, t, o, codes, sb);
+    if (isv) store_v<D>(vtile, t, o, codes[0], sb[0]);
+    else store_k<D>(ktile, t, o, codes[0], sb[0]);
 }
 
 }  // namespace int4

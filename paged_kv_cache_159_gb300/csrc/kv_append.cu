@@ -104,32 +104,31 @@ __global__ void __launch_bounds__(256) kv_append_int4_kernel(
 {
     constexpr int TILE = int4::tile_bytes(D);
     const I i0 = (I)blockIdx.x * (I)(256 * UNROLL) + threadIdx.x;
-    uint4 kx[UNROLL], vx[UNROLL];
+    uint4 x[UNROLL][2];
     int64_t tile[UNROLL];
-    int off[UNROLL], oct[UNROLL];
+    int off[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-        const I i = i0 + (I)(256 * u);
-        kx[u] = vx[u] = make_uint4(0u, 0u, 0u, 0u);
-        tile[u] = -1;
-        if (i < total) {
-            kx[u] = __ldcs(k + i);
-            vx[u] = __ldcs(v + i);
-            const int4::Row<D, I> r(i, num_tokens, num_kv_heads);
-            const int64_t slot = __ldg(slots + r.t);
-            if (slot >= num_slots) flag_error(err, PKV_DEVERR_SLOT);
-            else if (slot >= 0) tile[u] = ((r.layer * (num_slots >> 4) + (slot >> 4)) * (int64_t)num_kv_heads + r.h) * TILE;
-            off[u] = (int)(slot & 15);
-            oct[u] = r.o;
-        }
+        // (no branches, so that the loads go out together: past the end the last octet again)
+        const I i = i0 + (I)(256 * u), j = i < total ? i : total - 1;
+        x[u][0] = __ldcs(k + j);
+        x[u][1] = __ldcs(v + j);
+        const int4::Row<D, I> r(j, num_tokens, num_kv_heads);
+        const int64_t slot = __ldg(slots + r.t);
+        if (slot >= num_slots) flag_error(err, PKV_DEVERR_SLOT);
+        const bool in = i < total && slot >= 0 && slot < num_slots;
+        tile[u] = in ? ((r.layer * (num_slots >> 4) + (slot >> 4)) * (int64_t)num_kv_heads + r.h) * TILE : -1;
+        off[u] = (int)(slot & 15);
     }
+    const float inv[2] = {inv_k, inv_v};
+    const int o = (int)(threadIdx.x % (D / 8));        // (a block's width is whole rows)
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {                 // (whole warps: the shuffles)
-        uint32_t ks, vs;
-        const uint32_t kc = int4::quantise_octet(kx[u], inv_k, ks), vc = int4::quantise_octet(vx[u], inv_v, vs);
+        uint32_t codes[2], sb[2];
+        int4::quantise(x[u], inv, codes, sb);
         if (tile[u] < 0) continue;
-        int4::store_k<D>(key_cache + tile[u], off[u], oct[u], kc, ks);
-        int4::store_v<D>(value_cache + tile[u], off[u], oct[u], vc, vs);
+        int4::store_k<D>(key_cache + tile[u], off[u], o, codes[0], sb[0]);
+        int4::store_v<D>(value_cache + tile[u], off[u], o, codes[1], sb[1]);
     }
 }
 
