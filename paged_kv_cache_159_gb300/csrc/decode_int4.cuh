@@ -493,18 +493,19 @@ __global__ void __launch_bounds__(int4_warps<D, NH>() * 32, 1) decode_int4_kerne
     int iend = __shfl_sync(dev::FULL, (int)min((long long)INT_MAX, iu.U0 + iu.nb - s), 0), ihi = min(n, iend);
     uint32_t io = 0;                               // its stage's offset
     unsigned good = 0;                             // a bit per tile, the pair copied last at bits 0 and 1
-    const int rest = lane < CH % 32;               // this lane takes part in a tile's last, partial piece
+    // the last CH % 32 pieces of a tile: lanes 0 .. 4 REST - 1 take those of the pair's four tiles at once
+    constexpr int REST = CH % 32;
+    static_assert(4 * REST <= 32, "one copy for the rests");
+    const int rt = lane / REST;                    // tile of the pair (K, V, K, V)
+    const uint8_t *rbase = ((rt & 1) ? p.value_cache : p.key_cache) + (CH / 32 * 32 + lane % REST) * 16;
+    const uint32_t rdst = ring + rt * TILE + (CH / 32 * 32 + lane % REST) * 16;
+    const int rest = lane < 4 * REST;
     auto copy_tile = [&](int t, uint32_t dst) {
         const uint8_t *k = kbase + (size_t)(unsigned)t * TILE, *v = vbase + (size_t)(unsigned)t * TILE;
 #pragma unroll
-        for (int c = 0; c < CH; c += 32) {
-            if (c + 32 <= CH) {
-                cp16(dst + c * 16, k + c * 16);
-                cp16(dst + TILE + c * 16, v + c * 16);
-            } else {
-                cp16_if(dst + c * 16, k + c * 16, rest);
-                cp16_if(dst + TILE + c * 16, v + c * 16, rest);
-            }
+        for (int c = 0; c + 32 <= CH; c += 32) {
+            cp16(dst + c * 16, k + c * 16);
+            cp16(dst + TILE + c * 16, v + c * 16);
         }
     };
     auto issue = [&]() {
@@ -537,6 +538,7 @@ __global__ void __launch_bounds__(int4_warps<D, NH>() * 32, 1) decode_int4_kerne
             }
             copy_tile(max(t0, 0), dst);
             if (two) copy_tile(max(t1, 0), dst + 2 * TILE);
+            cp16_if(rdst + io, rbase + (size_t)(unsigned)max((rt & 2) ? t1 : t0, 0) * TILE, rest);
             good |= (t0 >= 0 ? 1u : 0u) | (t1 >= 0 ? 2u : 0u);
             if (ii == ihi && ii < n) {
                 iu = unit_of(s + ii);
