@@ -132,7 +132,7 @@ def decode(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_s
     """q [B, Hq, D] -> (out, sum p |v|, score error), each [B, Hq, D] in 64 bits.  The score error of
     (b, head) bounds how far a score may be off that is formed from f16 products of q with the codes
     and fp32 sums: with ks_tj = k scale * scale of token t and group j,
-      scale * max_t sum_j ks_tj (7 * 32 * 2^-24 max|q| + 2^-16 sum_{d in j} |q_d|):
+      |scale| * max_t sum_j ks_tj (7 * 32 * 2^-24 max|q| + 2^-16 sum_{d in j} |q_d|):
     an element of q is off by at most 2^-24 of the largest, times |n - 8| <= 7 for 32 columns; a
     group's sum starts at -8 sum q and takes two products of codes up to 15, each off by at most
     2^-21 of the largest of these, at most 15 sum |q|, and its joining the score rounds four times
@@ -153,7 +153,7 @@ def decode(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_s
             sb = key_cache[blk[:, None], hk, sc[pos % BS][:, ::GROUP]]
             ks = e4m3_values()[sb] * float(np.float32(k_scale))
             aq = np.abs(q[b, h])
-            ds[b, h] = scale * (ks @ (224 * 2.0 ** -24 * aq.max() + 2.0 ** -16 * aq.reshape(-1, GROUP).sum(-1))).max()
+            ds[b, h] = abs(scale) * (ks @ (224 * 2.0 ** -24 * aq.max() + 2.0 ** -16 * aq.reshape(-1, GROUP).sum(-1))).max()
     return out, mag, ds
 
 

@@ -69,7 +69,8 @@ struct Int4Compute {
     float acc[2 * NG][NH][4];
     float m[NH][2], l[NH][2];
     float base_sc = 0.f;          // scale * k_scale * log2(e)
-    float sc = 0.f;               // the unit's score scale (with the queries' power of two)
+    float sc = 0.f, rsc = 0.f;    // the unit's score scale (with the queries' power of two), positive, and 1 / it
+    float thr[NH][2];             // the running max is raised where a score (times sc) passes this (times sc)
     uint32_t ok, oks, ov, ovs;    // byte offsets in a tile of this lane's K words, K scales, V words, V scales
 
     __device__ __forceinline__ void setup(int lane)
@@ -122,8 +123,10 @@ struct Int4Compute {
         int e = 0;                                   // amax * 2^e in [2^14, 2^15)
         if (amax > 0.f) e = 14 - (((int)(__float_as_uint(amax) >> 23) & 0xff) - 127);
         e = max(-126, min(126, e));
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        sc = base_sc * 0x1p24f * __uint_as_float((uint32_t)(127 - e) << 23);
+        const float up = copysignf(__uint_as_float((uint32_t)(127 + e) << 23), base_sc);     // (q takes a negative scale's sign)
+        // (at a scale of zero a masked score still has to come out as -infinity)
+        sc = fmaxf(fabsf(base_sc) * 0x1p24f * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
+        rsc = 1.f / sc;
 #pragma unroll
         for (int j = 0; j < NG; ++j)
 #pragma unroll
@@ -163,6 +166,7 @@ struct Int4Compute {
         for (int h = 0; h < NH; ++h) {
             m[h][0] = m[h][1] = -INFINITY;
             l[h][0] = l[h][1] = 0.f;
+            thr[h][0] = thr[h][1] = -INFINITY;
         }
     }
 
@@ -280,12 +284,11 @@ struct Int4Compute {
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float v = s[x][h][c] * sc;
-                    s[x][h][c] = (FULL || t0 + 8 * (c >> 1) < (x ? n1 : n0)) ? v : -INFINITY;
+                    if (!FULL && !(t0 + 8 * (c >> 1) < (x ? n1 : n0))) s[x][h][c] = -INFINITY;
                 }
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                need |= fmaxf(fmaxf(s[0][h][r], s[0][h][r + 2]), fmaxf(s[1][h][r], s[1][h][r + 2])) > m[h][r] + (OFF + TAU);
+                need |= fmaxf(fmaxf(s[0][h][r], s[0][h][r + 2]), fmaxf(s[1][h][r], s[1][h][r + 2])) > thr[h][r];
         }
         if (__any_sync(dev::FULL, need)) {
 #pragma unroll
@@ -296,7 +299,8 @@ struct Int4Compute {
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 16));
-                    const float mn = fmaxf(m[h][r], mx - OFF);
+                    const float mn = fmaxf(m[h][r], mx * sc - OFF);
+                    thr[h][r] = (mn + (OFF + TAU)) * rsc;
                     const float alpha = dev::fast_exp2(m[h][r] - mn);
                     m[h][r] = mn;
                     l[h][r] *= alpha;
@@ -313,8 +317,8 @@ struct Int4Compute {
         for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                const float p0 = dev::fast_exp2(s[x][h][0] - m[h][0]), p1 = dev::fast_exp2(s[x][h][1] - m[h][1]);
-                const float p2 = dev::fast_exp2(s[x][h][2] - m[h][0]), p3 = dev::fast_exp2(s[x][h][3] - m[h][1]);
+                const float p0 = dev::fast_exp2(fmaf(s[x][h][0], sc, -m[h][0])), p1 = dev::fast_exp2(fmaf(s[x][h][1], sc, -m[h][1]));
+                const float p2 = dev::fast_exp2(fmaf(s[x][h][2], sc, -m[h][0])), p3 = dev::fast_exp2(fmaf(s[x][h][3], sc, -m[h][1]));
                 l[h][0] += p0 + p2;
                 l[h][1] += p1 + p3;
                 pb[x][h][0] = dev::movmatrix_trans(dev::pack_f16x2(p0, p1));

@@ -162,6 +162,13 @@ def test_decode_over_magnitudes(q_gain, v_gain, ks, vs, D):
     c.check(c.decode())
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.25, 2.0])
+def test_any_finite_scale(scale):
+    c = I.Case([100, 7, 33], 8, 2, 128, seed=8)
+    c.scale = scale
+    c.check(c.decode())
+
+
 def test_one_position_returns_its_value():
     c = I.Case([1, 1], 4, 2, 128, v_scale=0.25)
     ref = O.rows(c.vh, c.slots, False, 0.25)
