@@ -34,6 +34,7 @@
 #pragma once
 
 #include "decode_kernels.cuh"
+#include "int4.cuh"
 
 namespace pkv {
 namespace decode {

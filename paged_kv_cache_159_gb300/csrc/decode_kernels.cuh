@@ -59,7 +59,6 @@
 #include <mutex>
 #include <type_traits>
 
-#include "int4.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "tc_device.cuh"
@@ -237,8 +236,6 @@ struct MmaCompute {
     static constexpr bool SWIZZLED = false;    // linear tiles (1-D bulk copies)
     static constexpr bool IDENTITY_SLOTS = false;   // merge-area columns in fragment order
     static constexpr int ELEM = FP8 ? 1 : 2;
-    static constexpr int TILE = BS * D * ELEM;       // bytes of one (block, KV head) tile
-    static constexpr int FORMAT = FP8 ? PKV_KV_FP8E4M3 : PKV_KV_BF16;
     static constexpr int ROW = D * ELEM;
     static constexpr int KS = D / 16;                   // k-steps of S = Q.K^T
     static constexpr int EK = 16 / ELEM;                // elements in a 16-byte piece
@@ -453,8 +450,6 @@ struct SimtCompute {
     static constexpr bool SWIZZLED = false;    // linear tiles (1-D bulk copies)
     static constexpr bool IDENTITY_SLOTS = true;    // merge-area column d at d
     static constexpr int ELEM = FP8 ? 1 : 2;
-    static constexpr int TILE = BS * D * ELEM;       // bytes of one (block, KV head) tile
-    static constexpr int FORMAT = FP8 ? PKV_KV_FP8E4M3 : PKV_KV_BF16;
     static constexpr int ROW = D * ELEM;
     static constexpr int EPL = D / 32;
     static constexpr int HALF = 8;                       // tokens per softmax step
@@ -602,8 +597,6 @@ struct TokCompute {
     static constexpr bool SWIZZLED = true;
     static constexpr bool IDENTITY_SLOTS = true;    // merge-area column d at d
     static constexpr int ELEM = FP8 ? 1 : 2;
-    static constexpr int TILE = BS * D * ELEM;       // bytes of one (block, KV head) tile
-    static constexpr int FORMAT = FP8 ? PKV_KV_FP8E4M3 : PKV_KV_BF16;
     static constexpr int ROWB = D * ELEM;                 // bytes of one token row
     static constexpr int SEG = ROWB < 128 ? ROWB : 128;   // bytes of one swizzled row segment
     static constexpr int SEGBYTES = BS * SEG;             // one [16 tokens][SEG] segment of a tile
@@ -897,11 +890,12 @@ struct TokCompute {
 // ------------------------------------------------------------------------------------
 // The decode kernel body: NW streaming warps and one epilogue warp.
 // ------------------------------------------------------------------------------------
-template <int D, int NW, int NS, int HP, class Compute>
+template <int D, bool FP8, int NW, int NS, int HP, class Compute>
 __device__ __forceinline__ void decode_body(const DecodeParams &p, Compute &cmp, const CUtensorMap *kmap,
                                             const CUtensorMap *vmap)
 {
-    constexpr int TILE = Compute::TILE;           // one (block, KV head) tile of K or V
+    constexpr int ELEM = FP8 ? 1 : 2;
+    constexpr int TILE = BS * D * ELEM;           // one (block, KV head) tile of K or V
     constexpr int NWARP = NW + 2;                 // NW consumers, the epilogue warp, the producer
     constexpr int NTHR = NWARP * 32;
     // A task is one block of HP consecutive KV heads, loaded by one copy of HP tiles for K and
@@ -910,8 +904,9 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p, Compute &cmp,
     constexpr int NSTAGE = NSTREAM * NS;          // CTA-wide ring; task i: stage i % NSTAGE, stream i % NSTREAM
     constexpr int STAGE = 2 * HP * TILE;          // K tiles, then V tiles
     static_assert(NW % HP == 0 && NSTAGE <= 32 && 32 % NSTREAM == 0, "ring and step shapes");
-    // swizzled tiles: row segments of at most 128 bytes, [segment][16 tokens][segment bytes]
-    constexpr int NSEG = (TILE / BS + 127) / 128;
+    // swizzled tiles: SEG-byte row segments, [segment][16 tokens][SEG] per tile
+    constexpr int SEG = D * ELEM < 128 ? D * ELEM : 128;
+    constexpr int NSEG = D * ELEM / SEG;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // the stage ring starts 1024-byte aligned (the swizzle pattern repeats every 1024 bytes)
     uint8_t *smem = smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -1408,7 +1403,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p, Compute &cmp,
             const size_t src = ((size_t)lb * Hkv + h) * D;
             const size_t dst = ((size_t)t * BS + off) * D;               // element index
             constexpr int EPL = D / 32;
-            if constexpr (Compute::FORMAT == PKV_KV_FP8E4M3) {
+            if constexpr (FP8) {
                 const uint16_t *ks = p.k_new + src + lane * EPL;
                 const uint16_t *vs = p.v_new + src + lane * EPL;
                 uint32_t kc = 0, vc = 0;
@@ -1585,7 +1580,7 @@ template <int D, bool FP8, int NW, int NS, bool G16>
 __global__ void __launch_bounds__((NW + 2) * 32, 8 / NW) decode_mma_kernel(const DecodeParams p)
 {
     MmaCompute<D, FP8, G16> cmp;
-    decode_body<D, NW, NS, 1>(p, cmp, nullptr, nullptr);
+    decode_body<D, FP8, NW, NS, 1>(p, cmp, nullptr, nullptr);
 }
 
 template <int D, bool FP8, int NW, int NS, int HP, int NH>
@@ -1596,7 +1591,7 @@ decode_tok_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     TokCompute<D, FP8, NH> cmp;
     cmp.setup(threadIdx.x & 31);
     cmp.base_sc = p.score_scale;
-    decode_body<D, NW, NS, HP>(p, cmp, &kmap, &vmap);
+    decode_body<D, FP8, NW, NS, HP>(p, cmp, &kmap, &vmap);
 }
 
 // ------------------------------------------------------------------------------------
@@ -1852,7 +1847,7 @@ __global__ void __launch_bounds__((NW + 2) * 32) decode_simt_kernel(const Decode
 {
     SimtCompute<D, FP8, GP> cmp;
     cmp.sscale = p.score_scale;
-    decode_body<D, NW, NS, 1>(p, cmp, nullptr, nullptr);
+    decode_body<D, FP8, NW, NS, 1>(p, cmp, nullptr, nullptr);
 }
 
 // ------------------------------------------------------------------------------------
