@@ -21,16 +21,25 @@
 //     scale 2^-8 (the scale byte moved to f16's fields) <= 1.75; both products round to 11 bits.
 //
 // Schedule.  A 16-token block of one head is 2 x 17 D / 2 bytes, little work to hand between
-// warps, so nothing is: a warp copies its own tiles (cp.async into a ring of its own, NST - 1
-// pairs of tiles ahead), computes a pair at a time, and writes its result from registers; it waits for no other warp,
-// and the CTA meets only to scan seq_lens.  Teams of HG warps, one per KV head, take the same
-// blocks at about the same time, since the heads' tiles of a block lie together in memory.  The
+// warps, so nothing is: a warp copies its own tiles (cp.async into a ring of its own, two pairs of
+// blocks ahead), computes a pair at a time, and writes its result from registers; it waits for no
+// other warp, and the CTA meets only to scan seq_lens.  Teams of HG warps, one per KV head, take the
+// same blocks at about the same time, since the heads' tiles of a block lie together in memory.  The
 // blocks of all (layer, sequence, head group) units are laid end to end and cut evenly over
 // the teams of a one-wave grid.  A team that holds a whole unit writes its output; a cut unit
-// leaves a partial (max, sum, unnormalised output) per team, and a second launch merges them,
-// a warp per output row, in team order: placement of the blocks changes no bit.  Both launches
-// may start while the one before them drains (programmatic dependent launch) and wait for it
-// before they read.
+// leaves a partial (max, sum, unnormalised output) per team, and a second launch merges them
+// in team order: placement of the blocks changes no bit.  Both launches may start while the one
+// before them drains (programmatic dependent launch) and wait for it before they read.
+//
+// What it measured (GB300; us a pass in a graph over three states, 32 / 8 heads, D 128, K/V of 64 x
+// 2048 positions, 143.7 MB, and of the ragged batch, 592.9 MB; the measured copy peak gives 21.2
+// and 87.3): streaming alone 28.0 and 97.3; the first version, on the other pools' schedule with
+// a producer warp and bulk copies of 1088 bytes, 67 and 228; own copies and the merge launch 44 and
+// 148; subnormal operands and pairs of blocks, 43.7 and 139; twelve warps, 41.0 and 132; now 39.6 and
+// 122.7.  Not kept: E4M3 products for K (emulated by conversions on this GPU, 58 and 181), loads
+// straight to registers (48 and 159: too few bytes in flight), four pairs in the ring (no change),
+// V's codes as whole bytes less their upper nibbles (119, but off by 2^-14 of a step where codes cancel).
+// What bounds it: instruction issue, the integer pipe (two clocks an instruction) first.
 #pragma once
 
 #include "decode_kernels.cuh"
@@ -40,8 +49,8 @@ namespace pkv {
 namespace decode {
 
 // Warps of a CTA, one CTA per SM, by the registers that a warp's state needs (168 a thread at 12 warps,
-// 128 at 16; 16 columns hold twice the state).  At D 128 twelve warps run as fast as sixteen, which
-// spill: the integer pipe is what they share.
+// 128 at 16; 16 columns hold twice the state).  At D 128 sixteen warps spill and are slower (43.7 against
+// 41.0 us for 64 x 2048, 139 against 132 for the ragged batch).
 template <int D, int NH>
 constexpr int int4_warps() { return D == 128 ? (NH == 1 ? 12 : 8) : (NH == 1 ? 16 : 12); }
 constexpr int I4_NST = 3;                           // pairs of blocks in a warp's ring

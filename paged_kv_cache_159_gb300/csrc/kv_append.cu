@@ -95,7 +95,9 @@ __global__ void __launch_bounds__(256) kv_append_fp8_kernel(
 // 32-column group share its maximum by two shuffles, K and V handled by the same thread: one
 // 32-bit word of K codes, two 16-bit words of V codes and, by the group's first lane, the scale
 // bytes (places and arithmetic: int4.cuh).  A thread takes UNROLL octets a block's width apart, their
-// loads in flight together.  I: the index type, 32 bits where the octets' count allows.
+// loads in flight together.  I: the index type, 32 bits where the octets' count allows.  Bound by
+// instruction issue (about 280 an octet of K and of V): 16411 tokens of 8 heads, D 128, 85 MB, take about
+// 23 us of the 39.9 us that append and gather of them take together.
 template <int D, int UNROLL, class I>
 __global__ void __launch_bounds__(256) kv_append_int4_kernel(
     const uint4 *__restrict__ k, const uint4 *__restrict__ v, const int64_t *__restrict__ slots,

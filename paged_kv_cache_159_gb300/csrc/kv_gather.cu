@@ -9,7 +9,9 @@
 // row is written in 16-byte pieces by consecutive lanes.  An FP8 element becomes bf16(fl32(pool scale *
 // value)), an INT4 one bf16(fl32((n - 8) * fl32(scale * pool scale))): at most two fp32 roundings before
 // the one to bf16, none where the pool scale is a power of two.
-// Bound by DRAM: a row's reads are 17 D / 32 bytes (INT4), D (FP8) or 2 D, its writes 2 D.
+// Bound by DRAM (a row's reads are 17 D / 32 bytes for INT4, D for FP8 or 2 D, its writes 2 D) and, for INT4,
+// nearly by instruction issue: 131072 tokens of 8 heads, D 128, 680.5 MB, take 120 us, 5.66 TB/s;
+// 157 us with 64-bit indexing and one octet a thread.
 #include <cuda_runtime.h>
 
 #include <type_traits>
