@@ -323,8 +323,8 @@ typedef struct {
     int32_t grid_ctas;        /* CTAs of the persistent grid (0 = SM count x CTAs per SM) */
     int32_t variant;          /* 0 = auto (3); 1 = CUDA-core dot products; 2 = tensor-core mma with
                                  the heads as rows; 3 = tensor-core mma with the tokens as rows.
-                                 INT4 pools have one variant of their own (0), without
-                                 heads_per_copy and shared_prefix_blocks */
+                                 INT4 pools have a kernel and schedule of their own: of these
+                                 fields they take grid_ctas only, any other is INVALID */
     int32_t warps_per_cta;    /* 0 = auto (4); 4 or 8 */
     int32_t stages;           /* 0 = auto (16 KiB of tiles per warp: 2 bf16 / 4 FP8 at D 128); 2..4 */
     int32_t heads_per_copy;   /* variant 3: KV heads loaded by one copy (the block's tiles of
@@ -368,14 +368,15 @@ size_t pkv_decode_workspace_bytes(const pkv_pool *pool, int32_t batch, int32_t n
  * Calls sharing a workspace must not overlap on the GPU.
  * Positions j >= L_b are never used, whatever they hold.  The work -- every sequence's
  * blocks for every KV head -- is split evenly over a one-wave persistent grid; a
- * (sequence, head) cut by that split is finished by whichever of its CTAs ends last.  All
+ * (sequence, head) cut by that split is finished by whichever of its CTAs ends last (INT4 pools:
+ * split over the grid's warps, and a second launch on the stream merges what the split cut).  All
  * split points and merge orders depend only on seq_lens, the grid and logical positions,
  * so any physical placement of the blocks gives bit-identical output.  Requires
  * 1 <= batch <= 4096, num_q_heads a multiple of Hkv with group <= 16, an attached pool,
  * max_blocks >= 1, batch * max_blocks * Hkv < 2^31.  FP8 pools compute q.K with q rounded
  * to fp16 (|q| must stay below 65504).  INT4 pools take q to fp16 with a power of two per
- * (sequence, KV head) that keeps its largest element in range.  An invalid seq_len sets PKV_DEVERR_SEQ_LEN and
- * zeroes that sequence's output. */
+ * (sequence, KV head) that keeps its largest element in range.  An invalid seq_len sets
+ * PKV_DEVERR_SEQ_LEN and zeroes that sequence's output. */
 int pkv_paged_attention_decode(pkv_pool *pool, const void *q, const void *key_cache,
                                const void *value_cache, const int32_t *block_tables,
                                const int32_t *seq_lens, int32_t batch, int32_t num_q_heads,
@@ -465,8 +466,9 @@ int pkv_paged_prefill(pkv_pool *pool, const void *q, const void *key_cache, cons
  * memory, 256-byte aligned, of at least pkv_prefill_workspace_bytes() bytes for the cu_q,
  * seq_lens and max_blocks that the plan was made with (host arrays; 0 for other pools and for
  * invalid shapes); its content before and after is unspecified, and calls sharing it must not
- * overlap on the GPU.  A workspace too small for the plan sets PKV_DEVERR_PLAN and computes
- * nothing; one too small for a single block is INVALID. */
+ * overlap on the GPU.  A workspace too small for the plan, or a max_blocks other than the
+ * plan's, sets PKV_DEVERR_PLAN and computes nothing; a workspace too small for a single block
+ * is INVALID. */
 size_t pkv_prefill_workspace_bytes(const pkv_pool *pool, const int32_t *cu_q, const int32_t *seq_lens,
                                    int32_t batch, int32_t max_blocks);
 int pkv_paged_prefill_ex(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,

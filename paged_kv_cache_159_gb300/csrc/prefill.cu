@@ -84,7 +84,7 @@ constexpr uint32_t PLAN_MAGIC = 0x504b5650u;   // "PVKP"
 constexpr uint32_t TMEM_COLS = 512;            // S (and P over it): 2 buffers x 2 q-tiles x 64, O: 2 x D
 
 // A plan: header, per-CTA unit ranges, units; for INT4 pools (batch > 0) the expanded blocks
-// before each sequence as well (batch + 1 entries).
+// before each sequence as well (batch + 1 entries), and the width of the tables.
 struct PlanHeader { uint32_t magic; int32_t num_units, grid, group, tp, hq, hkv, batch; };
 struct Unit { int32_t b, h, row0, pos0, npos, nkv, kmax, pad; };
 
@@ -121,6 +121,13 @@ struct ExpandParams {
 };
 
 constexpr int EXPAND_THREADS = 256;
+
+// Whether a call's workspace (capacity blocks) and table width fit the plan's expansion.
+__device__ __forceinline__ bool expanded_ok(const uint8_t *expand, int batch, int capacity, int max_blocks)
+{
+    const int32_t *off = reinterpret_cast<const int32_t *>(expand);
+    return off[batch] <= capacity && off[batch + 1] == max_blocks;
+}
 
 // (n - 8) * scale of the codes at bits 0-3 of each half of w, as bf16 pairs: 128 + n by an
 // and-or, then exact arithmetic.
@@ -169,7 +176,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS) prefill_expand_kernel(const Ex
     }
     const int32_t *off = reinterpret_cast<const int32_t *>(p.plan + plan_expand_offset(hdr->grid, (size_t)hdr->num_units));
     const int total = off[p.B];
-    if (total > p.capacity) {
+    if (!expanded_ok(reinterpret_cast<const uint8_t *>(off), p.B, p.capacity, p.MB)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_PLAN);
         return;
     }
@@ -298,7 +305,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const Unit *units = reinterpret_cast<const Unit *>(p.plan + plan_units_offset(p.grid));
     if (hdr->magic != PLAN_MAGIC || hdr->grid != p.grid || hdr->group != p.group || hdr->hq != p.Hq ||
         hdr->hkv != p.Hkv || hdr->tp != p.TP || hdr->batch != p.expanded ||
-        (p.expanded > 0 && reinterpret_cast<const int32_t *>(p.plan + plan_expand_offset(hdr->grid, (size_t)hdr->num_units))[p.expanded] > p.num_blocks)) {
+        (p.expanded > 0 && !expanded_ok(p.plan + plan_expand_offset(hdr->grid, (size_t)hdr->num_units), p.expanded, p.num_blocks, p.MB))) {
         if (tid == 0 && blockIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_PLAN);
         return;
     }
@@ -902,7 +909,7 @@ extern "C" size_t pkv_prefill_plan_bytes(const pkv_pool *pool, int32_t batch, in
     const int tp = tile_positions(g);
     const size_t units = (size_t)pool->desc.num_kv_heads * ((size_t)total_q / tp + batch);
     const int grid = std::max(1, sm_count());
-    const size_t more = pool->desc.kv_dtype == PKV_KV_INT4 ? ((size_t)batch + 1) * sizeof(int32_t) : 0;
+    const size_t more = pool->desc.kv_dtype == PKV_KV_INT4 ? ((size_t)batch + 2) * sizeof(int32_t) : 0;
     return plan_expand_offset(grid, units) + more;
 }
 
@@ -935,6 +942,8 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
     if (g > 16) return PKV_ERR_INVALID;
     const int tp = tile_positions(g);
     if (cu_q[0] != 0) return PKV_ERR_INVALID;
+    const bool i4 = pool->desc.kv_dtype == PKV_KV_INT4;
+    if (i4 && pkv_prefill_workspace_bytes(pool, cu_q, seq_lens, batch, max_blocks) == 0) return PKV_ERR_INVALID;
     std::vector<Unit> units;
     for (int b = 0; b < batch; ++b) {
         const int64_t P = (int64_t)cu_q[b + 1] - cu_q[b], L = seq_lens[b];
@@ -958,8 +967,7 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
     const int sms = sm_count();
     if (sms < 1) return PKV_ERR_CUDA;
     const int grid = std::max(1, std::min<int>(sms, (int)units.size()));
-    const bool i4 = pool->desc.kv_dtype == PKV_KV_INT4;
-    const size_t need = plan_expand_offset(grid, units.size()) + (i4 ? ((size_t)batch + 1) * sizeof(int32_t) : 0);
+    const size_t need = plan_expand_offset(grid, units.size()) + (i4 ? ((size_t)batch + 2) * sizeof(int32_t) : 0);
     if (need > plan_bytes) return PKV_ERR_INVALID;
     // A unit costs its K/V tiles plus about three tile-times of its own: waiting for its Q
     // rows, the S -> softmax -> P.V chain filling and draining, and writing its output
@@ -1063,6 +1071,7 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
             if (cu_q[b + 1] > cu_q[b]) at += (seq_lens[b] - 1) / BS + 1;
         }
         ex[batch] = at;
+        ex[batch + 1] = max_blocks;
     }
     *grid_out = grid;
     return PKV_OK;

@@ -312,6 +312,43 @@ def test_decode_captured_replayed_and_on_another_stream():
         c.check(out)
 
 
+def test_decodes_captured_behind_copies_and_joined_streams():
+    # the decode's launches may start early: their inputs come from a copy, from another stream's
+    # append and from a decode just before, all within one capture, replayed back to back
+    c = I.Case([65, 1000, 7, 300], 16, 4, 128, seed=8)
+    want = c.decode()
+    c.sl.fill_(1)
+    q, q0, lens = c.q.cuda(), torch.zeros_like(c.q, device="cuda"), torch.from_numpy(c.lens).cuda()
+    outs, ws, side = [torch.zeros_like(want) for _ in range(3)], [c.workspace(), c.workspace()], torch.cuda.Stream()
+    kc, vc = torch.zeros_like(c.kc), torch.zeros_like(c.vc)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        q0.copy_(q)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            kc.copy_(c.kc)
+            pkv.paged_attention_decode(c.pool, q0, c.kc, c.vc, c.bt, lens, c.scale, outs[2], ws[1], stream=side)
+            vc.copy_(c.vc)
+        c.sl.copy_(lens)
+        main.wait_stream(side)
+        pkv.paged_attention_decode(c.pool, q0, kc, vc, c.bt, c.sl, c.scale, outs[0], ws[0])
+        pkv.paged_attention_decode(c.pool, outs[0], kc, vc, c.bt, c.sl, c.scale, outs[1], ws[0])
+        q0.zero_()
+        c.sl.fill_(1)
+        kc.zero_()
+    twice = torch.zeros_like(want)
+    pkv.paged_attention_decode(c.pool, want, c.kc, c.vc, c.bt, lens, c.scale, twice, c.workspace())
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[2], want) and torch.equal(outs[1], twice)
+    assert c.pool.get_device_error() == (pkv.OK, 0)
+
+
 def test_copy_blocks_moves_whole_tiles():
     layers, NB, Hkv, D = 2, 6, 3, 64
     pool = _pool(NB, Hkv, D, layers)

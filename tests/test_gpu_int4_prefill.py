@@ -115,6 +115,17 @@ def test_bad_entries_and_mismatched_plans_are_flagged():
     assert torch.equal(c.prefill(), ref)
 
 
+def test_a_plan_of_other_tables_is_flagged():
+    # a plan made for wider tables than the call's: nothing is read past them or written
+    c = Chunks([20, 30], [0, 40], 4, 2, 64)
+    narrow = c.bt[:, :2].contiguous()
+    out = torch.full_like(c.rows, 7.0, device="cuda")
+    args = [narrow if x is c.bt else x for x in c.args(out, c.ws)]
+    pkv.paged_prefill(*args)
+    assert c.pool.get_device_error() == (pkv.ERR_DEVICE, pkv.DEVERR_PLAN)
+    assert bool((out == 7.0).all())
+
+
 def test_refusals():
     c = Chunks([20], [0], 4, 2, 64)
     out, L, P = torch.zeros_like(c.rows, device="cuda"), pkv.lib(), ctypes.c_void_p
