@@ -16,6 +16,12 @@ Names follow the C ABI without the ``pkv_`` prefix:
 * ``decode_step(...)`` -- append each new token at position L-1 and decode, one launch.
 * ``kv_append_layers``, ``decode_step_layers`` -- the same over every layer of a pool whose
   caches stack ``num_layers`` layers (``Pool(..., num_layers=L)``), one launch each.
+* ``KV_INT4`` pools -- caches are uint8 ``[NB, Hkv, Pool.tile_bytes()]`` (layers stacked in front);
+  every entry point here takes them, ``paged_prefill`` with a workspace
+  (``prefill_workspace_bytes``).
+* ``kv_gather``, ``kv_gather_layers`` -- rows of any pool type back as bf16.
+* ``Pool.fork`` -- sequences that continue one another's blocks; ``Pool.compact`` with
+  ``move_blocks`` (content and device tables) and ``remap_tables`` (host tables).
 * ``Pool.cow_prepare`` and ``copy_blocks`` -- copy-on-write of shared blocks before an append.
 * ``block_hashes``, ``Pool.prefix_lookup / prefix_insert / prefix_evict / prefix_clear`` --
   automatic prefix caching on the host.
