@@ -34,6 +34,11 @@ namespace int4 {
 
 constexpr int GROUP = 32;                     // columns per scale
 
+// Rows (of one head) up to which append and gather take an octet a thread, above it a quarter of a row:
+// append / gather at D 128, us: 2048 rows 1.8 / 1.9 against 2.6 / 2.2, 8192 rows 2.7 / 2.5 against 3.2 / 2.5,
+// 16384 rows 3.9 / 3.3 against 3.9 / 3.2, 65536 rows 11.0 / 8.5 against 8.9 / 6.7.
+constexpr int64_t FEW_ROWS = 8192;
+
 __host__ __device__ constexpr int tile_bytes(int D) { return 8 * D + D / 2; }
 
 // Byte offsets within a tile of token t's octet o (columns 8 o .. 8 o + 7): the 32-bit word
@@ -168,17 +173,37 @@ __device__ __forceinline__ void store_v(uint8_t *tile, int t, int o, uint32_t co
     if ((o & 3) == 0) tile[P::v_scale(t, o)] = (uint8_t)scale_byte;
 }
 
-// The (layer, token, head) row of octet i of [layers, tokens, heads, D / 8], and the octet: with 32-bit
-// arithmetic wherever the whole range fits (a 64-bit division is some seventy instructions, more
-// than the rest of an octet's work).
-template <int D, class I>
+// Lane c of the four that share a row takes octets 4 j + c, one of every group j: 4 NG consecutive
+// bytes of the row in K (octet c's words) as in V (the 16-bit words of quads 2 c and 2 c + 1, which are
+// octet c's, or c ^ 2's where the row's halves are swapped).  So a row moves in a few wide accesses.
+template <int NG>
+__device__ __forceinline__ void load_words(const uint8_t *src, uint32_t (&w)[NG])
+{
+    if constexpr (NG == 4) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src));
+        w[0] = x.x; w[1] = x.y;
+    }
+}
+template <int NG>
+__device__ __forceinline__ void store_words(uint8_t *dst, const uint32_t (&w)[NG])
+{
+    if constexpr (NG == 4) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+}
+
+// The (layer, token, head) row of lane i of [layers, tokens, heads, LANES]: with 32-bit arithmetic wherever
+// the whole range fits (a 64-bit division is some seventy instructions, more than the rest of an
+// octet's work).
+template <int LANES, class I>
 struct Row {
-    int o, h;
+    int h;
     int64_t layer, t;
     __device__ __forceinline__ Row(I i, I num_tokens, I num_kv_heads)
     {
-        const I row = i / (D / 8), lt = row / num_kv_heads, l = lt < num_tokens ? (I)0 : lt / num_tokens;
-        o = (int)(i - row * (D / 8));
+        const I row = i / LANES, lt = row / num_kv_heads, l = lt < num_tokens ? (I)0 : lt / num_tokens;
         h = (int)(row - lt * num_kv_heads);
         layer = (int64_t)l;
         t = (int64_t)(lt - l * num_tokens);

@@ -91,46 +91,68 @@ __global__ void __launch_bounds__(256) kv_append_fp8_kernel(
     }
 }
 
-// INT4 pool: a thread per octet (8 columns, 16 bytes of bf16), so that the four lanes of a
-// 32-column group share its maximum by two shuffles, K and V handled by the same thread: one
-// 32-bit word of K codes, two 16-bit words of V codes and, by the group's first lane, the scale
-// bytes (places and arithmetic: int4.cuh).  A thread takes UNROLL octets a block's width apart, their
-// loads in flight together.  I: the index type, 32 bits where the octets' count allows.  Bound by
-// instruction issue (about 280 an octet of K and of V): 16411 tokens of 8 heads, D 128, 85 MB, take about
-// 23 us of the 39.9 us that append and gather of them take together.
-template <int D, int UNROLL, class I>
-__global__ void __launch_bounds__(256) kv_append_int4_kernel(
+// INT4 pool: four lanes share a 32-column group and its maximum (two shuffles), each with 8 columns
+// (16 bytes of bf16), K and V by the same thread.  A thread takes GP groups of its row: all of them where
+// there are rows enough, so that its codes are 4 NG consecutive bytes of K as of V (int4.cuh) and
+// leave in one store each; one of them for few rows, which leaves a thread less to do in turn.
+// I: the index type, 32 bits where the lanes' count allows.  Bound by DRAM, instruction issue close behind:
+// append and gather of 16411 tokens of 8 heads, D 128, 170 MB, take 27.7 us together, 6.15 TB/s (36.7 with an
+// octet a thread).
+constexpr int ROW_THREADS = 128;
+
+template <int D, int GP, class I>
+__global__ void __launch_bounds__(ROW_THREADS) kv_append_int4_kernel(
     const uint4 *__restrict__ k, const uint4 *__restrict__ v, const int64_t *__restrict__ slots,
     I num_tokens, I total, I num_kv_heads, int64_t num_slots, float inv_k, float inv_v,
     uint8_t *__restrict__ key_cache, uint8_t *__restrict__ value_cache, uint32_t *err)
 {
-    constexpr int TILE = int4::tile_bytes(D);
-    const I i0 = (I)blockIdx.x * (I)(256 * UNROLL) + threadIdx.x;
-    uint4 x[UNROLL][2];
-    int64_t tile[UNROLL];
-    int off[UNROLL];
+    using P = int4::Place<D>;
+    constexpr int NG = P::NG, LANES = 4 * NG / GP;             // lanes of a row
+    static_assert(GP == 1 || GP == NG, "one group or all");
+    const I i = (I)blockIdx.x * (I)ROW_THREADS + threadIdx.x, j = i < total ? i : total - 1;    // (whole warps: the shuffles)
+    const int o = (int)(threadIdx.x % LANES);                  // its octet, or its octet of every group
+    const size_t at = (size_t)(j / LANES) * (D / 8) + o;
+    uint4 x[2 * GP];
+    float inv[2 * GP];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-        // (no branches, so that the loads go out together: past the end the last octet again)
-        const I i = i0 + (I)(256 * u), j = i < total ? i : total - 1;
-        x[u][0] = __ldcs(k + j);
-        x[u][1] = __ldcs(v + j);
-        const int4::Row<D, I> r(j, num_tokens, num_kv_heads);
-        const int64_t slot = __ldg(slots + r.t);
-        if (slot >= num_slots) flag_error(err, PKV_DEVERR_SLOT);
-        const bool in = i < total && slot >= 0 && slot < num_slots;
-        tile[u] = in ? ((r.layer * (num_slots >> 4) + (slot >> 4)) * (int64_t)num_kv_heads + r.h) * TILE : -1;
-        off[u] = (int)(slot & 15);
+    for (int g = 0; g < GP; ++g) {
+        x[g] = __ldcs(k + at + 4 * g);
+        x[GP + g] = __ldcs(v + at + 4 * g);
+        inv[g] = inv_k;
+        inv[GP + g] = inv_v;
     }
-    const float inv[2] = {inv_k, inv_v};
-    const int o = (int)(threadIdx.x % (D / 8));        // (a block's width is whole rows)
+    const int4::Row<LANES, I> r(j, num_tokens, num_kv_heads);
+    const int64_t slot = __ldg(slots + r.t);
+    if (slot >= num_slots) flag_error(err, PKV_DEVERR_SLOT);
+    uint32_t codes[2 * GP], sb[2 * GP];
+    int4::quantise(x, inv, codes, sb);
+    if (i >= total || slot < 0 || slot >= num_slots) return;
+    const int t = (int)(slot & 15);
+    const int64_t tile = ((r.layer * (num_slots >> 4) + (slot >> 4)) * (int64_t)num_kv_heads + r.h) * int4::tile_bytes(D);
+    uint8_t *kt = key_cache + tile, *vt = value_cache + tile;
+    if constexpr (GP == 1) {
+        int4::store_k<D>(kt, t, o, codes[0], sb[0]);
+        int4::store_v<D>(vt, t, o, codes[1], sb[1]);
+    } else {
+        uint32_t kw[NG], vw[NG], ks = 0, vs = 0;
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {                 // (whole warps: the shuffles)
-        uint32_t codes[2], sb[2];
-        int4::quantise(x[u], inv, codes, sb);
-        if (tile[u] < 0) continue;
-        int4::store_k<D>(key_cache + tile[u], off[u], o, codes[0], sb[0]);
-        int4::store_v<D>(value_cache + tile[u], off[u], o, codes[1], sb[1]);
+        for (int g = 0; g < NG; ++g) {
+            kw[g] = codes[g];
+            ks |= sb[g] << (8 * g);
+            vs |= sb[NG + g] << (8 * g);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; g += 2) {
+            vw[g / 2] = __byte_perm(codes[NG + g], codes[NG + g + 1], 0x5410u);
+            vw[(NG + g) / 2] = __byte_perm(codes[NG + g], codes[NG + g + 1], 0x7632u);
+        }
+        int4::store_words(kt + P::k_word(t, o), kw);
+        int4::store_words(vt + P::v_word(t, o), vw);
+        if (o == 0) {
+            if constexpr (NG == 4) *reinterpret_cast<uint32_t *>(kt + P::k_scale(t, 0)) = ks;
+            else *reinterpret_cast<uint16_t *>(kt + P::k_scale(t, 0)) = (uint16_t)ks;
+        }
+        if (o < NG) vt[P::v_scale(t, 4 * o)] = (uint8_t)(vs >> (8 * o));
     }
 }
 
@@ -139,19 +161,20 @@ void append_int4(const pkv_pool *pool, int layers, const void *k, const void *v,
                  void *key_cache, void *value_cache, cudaStream_t s)
 {
     const pkv_pool_desc &d = pool->desc;
-    const int64_t total = (int64_t)layers * num_tokens * d.num_kv_heads * (D / 8);
-    auto run = [&](auto unroll, auto index) {
-        constexpr int U = decltype(unroll)::value;
+    const int64_t rows = (int64_t)layers * num_tokens * d.num_kv_heads;
+    auto run = [&](auto groups, auto index) {
+        constexpr int GP = decltype(groups)::value, LANES = D / 8 / GP;
         using I = decltype(index);
-        kv_append_int4_kernel<D, U, I><<<(unsigned)((total + 256 * U - 1) / (256 * U)), 256, 0, s>>>(
+        const int64_t total = rows * LANES;
+        kv_append_int4_kernel<D, GP, I><<<(unsigned)((total + ROW_THREADS - 1) / ROW_THREADS), ROW_THREADS, 0, s>>>(
             static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), slots, (I)num_tokens, (I)total, (I)d.num_kv_heads,
             (int64_t)d.num_blocks * d.block_size, pool->inv_k_scale, pool->inv_v_scale, static_cast<uint8_t *>(key_cache),
             static_cast<uint8_t *>(value_cache), pool->d_err);
     };
-    // few octets: one a thread, to spread them over the SMs; many: four in flight
-    if (total < (int64_t)1 << 18) run(std::integral_constant<int, 1>{}, uint32_t{});
-    else if (total < (int64_t)1 << 31) run(std::integral_constant<int, 4>{}, uint32_t{});
-    else run(std::integral_constant<int, 4>{}, uint64_t{});
+    constexpr int NG = int4::Place<D>::NG;
+    if (rows <= int4::FEW_ROWS) run(std::integral_constant<int, 1>{}, uint32_t{});
+    else if (rows < (int64_t)1 << 29) run(std::integral_constant<int, NG>{}, uint32_t{});
+    else run(std::integral_constant<int, NG>{}, uint64_t{});
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

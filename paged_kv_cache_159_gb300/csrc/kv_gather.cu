@@ -5,13 +5,11 @@
 // its title's P/D separation is the use: the rows that a prefill instance wrote are handed to
 // a decode instance, or moved into a pool of another type, whatever the pool stores them in.
 //
-// A thread per octet (8 columns of a row), K and V by the same thread, so that every output
-// row is written in 16-byte pieces by consecutive lanes.  An FP8 element becomes bf16(fl32(pool scale *
-// value)), an INT4 one bf16(fl32((n - 8) * fl32(scale * pool scale))): at most two fp32 roundings before
-// the one to bf16, none where the pool scale is a power of two.
-// Bound by DRAM (a row's reads are 17 D / 32 bytes for INT4, D for FP8 or 2 D, its writes 2 D) and, for INT4,
-// nearly by instruction issue: 131072 tokens of 8 heads, D 128, 680.5 MB, take 120 us, 5.66 TB/s;
-// 157 us with 64-bit indexing and one octet a thread.
+// A thread reads octets (8 columns of a row) of K and V and writes 16 bytes of each.  An FP8 element
+// becomes bf16(fl32(pool scale * value)), an INT4 one bf16(fl32((n - 8) * fl32(scale * pool scale))): at most
+// two fp32 roundings before the one to bf16, none where the pool scale is a power of two.
+// Bound by DRAM (a row's reads are 17 D / 32 bytes for INT4, D for FP8 or 2 D, its writes 2 D): INT4,
+// 131072 tokens of 8 heads, D 128, 680.5 MB, take 101 us, 6.71 TB/s; an octet a thread 131 us, four 120.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -24,6 +22,7 @@ namespace pkv {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int ROW_THREADS = 128;              // of the INT4 kernel
 
 __device__ __forceinline__ uint4 pack8(const float (&x)[8])
 {
@@ -32,35 +31,24 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
 }
 
 // Octet o of token t of a tile: its stored words (load), and its 8 bf16 (expand).
-template <int FORMAT, int D, bool IS_K>
+template <int FORMAT, int D>
 struct Octet {
-    uint4 w;                              // bf16: the octet; FP8: codes in x, y; INT4: codes in x, the scale byte in y
+    uint4 w;                              // bf16: the octet; FP8: codes in x, y
     __device__ __forceinline__ void load(const uint8_t *tile, int t, int o)
     {
         if constexpr (FORMAT == PKV_KV_BF16) {
             w = __ldg(reinterpret_cast<const uint4 *>(tile + t * (2 * D)) + o);
-        } else if constexpr (FORMAT == PKV_KV_FP8E4M3) {
+        } else {
             const uint2 c = __ldg(reinterpret_cast<const uint2 *>(tile + t * D) + o);
             w.x = c.x;
             w.y = c.y;
-        } else {
-            using P = int4::Place<D>;
-            if constexpr (IS_K) {
-                w.x = __ldg(reinterpret_cast<const uint32_t *>(tile + P::k_word(t, o)));
-                w.y = __ldg(tile + P::k_scale(t, o));
-            } else {
-                const uint8_t *s = tile + P::v_word(t, o);
-                w.x = __ldg(reinterpret_cast<const uint16_t *>(s));
-                w.z = __ldg(reinterpret_cast<const uint16_t *>(s + P::VSTEP));
-                w.y = __ldg(tile + P::v_scale(t, o));
-            }
         }
     }
     __device__ __forceinline__ uint4 expand(float scale) const
     {
         if constexpr (FORMAT == PKV_KV_BF16) {
             return w;
-        } else if constexpr (FORMAT == PKV_KV_FP8E4M3) {
+        } else {
             float x[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -68,19 +56,6 @@ struct Octet {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
                 x[2 * i] = f.x * scale;
                 x[2 * i + 1] = f.y * scale;
-            }
-            return pack8(x);
-        } else {
-            const uint32_t codes = IS_K ? w.x : (w.x | (w.z << 16));
-            // the nibble at bits 4 i joins 2^23's mantissa in place; less 2^23 + 8 16^i it is (n - 8) 16^i,
-            // exactly, and the multiplier's 16^-i brings it back
-            const float s = int4::scale_value(w.y) * scale;
-            const float m[4] = {s, s * 0x1p-4f, s * 0x1p-8f, s * 0x1p-12f};
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t bits = ((i < 4 ? codes : codes >> 16) & (15u << (4 * (i & 3)))) | 0x4B000000u;
-                x[i] = (__uint_as_float(bits) - (8388608.f + (float)(8 << (4 * (i & 3))))) * m[i & 3];
             }
             return pack8(x);
         }
@@ -95,24 +70,25 @@ __global__ void __launch_bounds__(THREADS) kv_gather_kernel(
     float k_scale, float v_scale, const uint8_t *__restrict__ key_cache, const uint8_t *__restrict__ value_cache,
     uint4 *__restrict__ k, uint4 *__restrict__ v, uint32_t *err)
 {
-    constexpr int64_t TILE = FORMAT == PKV_KV_INT4 ? int4::tile_bytes(D) : 16 * D * (FORMAT == PKV_KV_BF16 ? 2 : 1);
+    constexpr int64_t TILE = 16 * D * (FORMAT == PKV_KV_BF16 ? 2 : 1);
     const I i0 = (I)blockIdx.x * (I)(THREADS * UNROLL) + threadIdx.x;
-    Octet<FORMAT, D, true> ko[UNROLL];
-    Octet<FORMAT, D, false> vo[UNROLL];
+    Octet<FORMAT, D> ko[UNROLL], vo[UNROLL];
     bool in[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
         // (no branches, so that the loads go out together: skipped rows read slot 0)
         const I i = i0 + (I)(THREADS * u);
-        const int4::Row<D, I> r(i < total ? i : total - 1, num_tokens, num_kv_heads);
+        const I j = i < total ? i : total - 1;
+        const int4::Row<D / 8, I> r(j, num_tokens, num_kv_heads);
+        const int o = (int)(j % (D / 8));
         const int64_t slot = __ldg(slots + r.t);
         const bool valid = slot >= 0 && slot < num_slots;
         in[u] = valid && i < total;
         if (slot >= num_slots) dev::flag_error(err, PKV_DEVERR_SLOT);
         const int64_t at = valid ? slot : 0;
         const int64_t tile = ((r.layer * (num_slots >> 4) + (at >> 4)) * (int64_t)num_kv_heads + r.h) * TILE;
-        ko[u].load(key_cache + tile, (int)(at & 15), r.o);
-        vo[u].load(value_cache + tile, (int)(at & 15), r.o);
+        ko[u].load(key_cache + tile, (int)(at & 15), o);
+        vo[u].load(value_cache + tile, (int)(at & 15), o);
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
@@ -120,6 +96,69 @@ __global__ void __launch_bounds__(THREADS) kv_gather_kernel(
         const I i = i0 + (I)(THREADS * u);
         __stcs(k + i, ko[u].expand(k_scale));
         __stcs(v + i, vo[u].expand(v_scale));
+    }
+}
+
+// Octet of codes (column i at bits 4 i), times s: the nibble at bits 4 i joins 2^23's mantissa in
+// place; less 2^23 + 8 16^i it is (n - 8) 16^i, exactly, and the multiplier's 16^-i brings it back.
+__device__ __forceinline__ uint4 expand_octet(uint32_t codes, float s)
+{
+    const float m[4] = {s, s * 0x1p-4f, s * 0x1p-8f, s * 0x1p-12f};
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t bits = ((i < 4 ? codes : codes >> 16) & (15u << (4 * (i & 3)))) | 0x4B000000u;
+        x[i] = (__uint_as_float(bits) - (8388608.f + (float)(8 << (4 * (i & 3))))) * m[i & 3];
+    }
+    return pack8(x);
+}
+
+// INT4: a thread takes 8 columns of GP groups of its row, K and V: of all groups where there are rows enough,
+// so that they are 4 NG consecutive bytes in each (int4.cuh) and come in a few wide loads; of one for few
+// rows, which leaves a thread less to do in turn.
+template <int D, int GP, class I>
+__global__ void __launch_bounds__(ROW_THREADS) kv_gather_int4_kernel(
+    const int64_t *__restrict__ slots, I num_tokens, I total, I num_kv_heads, int64_t num_slots,
+    float k_scale, float v_scale, const uint8_t *__restrict__ key_cache, const uint8_t *__restrict__ value_cache,
+    uint4 *__restrict__ k, uint4 *__restrict__ v, uint32_t *err)
+{
+    using P = int4::Place<D>;
+    constexpr int NG = P::NG, LANES = 4 * NG / GP;             // lanes of a row
+    static_assert(GP == 1 || GP == NG, "one group or all");
+    const I i = (I)blockIdx.x * (I)ROW_THREADS + threadIdx.x;
+    if (i >= total) return;
+    const int o = (int)(threadIdx.x % LANES);                  // its octet, or its octet of every group
+    const int4::Row<LANES, I> r(i, num_tokens, num_kv_heads);
+    const int64_t slot = __ldg(slots + r.t);
+    if (slot >= num_slots) dev::flag_error(err, PKV_DEVERR_SLOT);
+    if (slot < 0 || slot >= num_slots) return;
+    const int t = (int)(slot & 15);
+    const int64_t tile = ((r.layer * (num_slots >> 4) + (slot >> 4)) * (int64_t)num_kv_heads + r.h) * int4::tile_bytes(D);
+    const uint8_t *kt = key_cache + tile, *vt = value_cache + tile;
+    const size_t row = (size_t)(i / LANES) * (D / 8);
+    if constexpr (GP == 1) {
+        const uint32_t kw = __ldg(reinterpret_cast<const uint32_t *>(kt + P::k_word(t, o)));
+        const uint16_t *vp = reinterpret_cast<const uint16_t *>(vt + P::v_word(t, o));
+        const uint32_t vw = __ldg(vp) | ((uint32_t)__ldg(vp + P::VSTEP / 2) << 16);
+        const uint32_t ks = __ldg(kt + P::k_scale(t, o)), vs = __ldg(vt + P::v_scale(t, o));
+        __stcs(k + row + o, expand_octet(kw, int4::scale_value(ks) * k_scale));
+        __stcs(v + row + o, expand_octet(vw, int4::scale_value(vs) * v_scale));
+    } else {
+        uint32_t kw[NG], vw[NG], vs[NG], ks;
+        int4::load_words(kt + P::k_word(t, o), kw);
+        int4::load_words(vt + t * (D / 2) + o * (4 * NG), vw);        // (in storage order)
+        int4::load_words(vt + 8 * D + (t & 3) * (4 * NG), vs);        // (of tokens t & 3, + 4, + 8, + 12)
+        if constexpr (NG == 4) ks = __ldg(reinterpret_cast<const uint32_t *>(kt + P::k_scale(t, 0)));
+        else ks = __ldg(reinterpret_cast<const uint16_t *>(kt + P::k_scale(t, 0)));
+        const int vo = D == 128 ? o ^ (t & 2) : o;                    // the octet that V's words are
+#pragma unroll
+        for (int j = 0; j < NG; ++j)
+            __stcs(k + row + 4 * j + o, expand_octet(kw[j], int4::scale_value((ks >> (8 * j)) & 0xffu) * k_scale));
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            const uint32_t codes = __byte_perm(vw[j >> 1], vw[NG / 2 + (j >> 1)], (j & 1) ? 0x7632u : 0x5410u);
+            __stcs(v + row + 4 * j + vo, expand_octet(codes, int4::scale_value((vs[j] >> (8 * (t >> 2))) & 0xffu) * v_scale));
+        }
     }
 }
 
@@ -157,9 +196,27 @@ int gather_impl(pkv_pool *pool, int layers, const int64_t *slot_mapping, int32_t
         if (d.head_dim == 128) run(format, std::integral_constant<int, 128>{});
         else run(format, std::integral_constant<int, 64>{});
     };
+    auto int4_rows = [&](auto dim, auto groups, auto index) {
+        constexpr int D = decltype(dim)::value, GP = decltype(groups)::value;
+        using I = decltype(index);
+        const int64_t lanes = total / GP;
+        kv_gather_int4_kernel<D, GP, I>
+            <<<(unsigned)((lanes + ROW_THREADS - 1) / ROW_THREADS), ROW_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
+                slot_mapping, (I)num_tokens, (I)lanes, (I)d.num_kv_heads, (int64_t)d.num_blocks * d.block_size, d.k_scale,
+                d.v_scale, static_cast<const uint8_t *>(key_cache), static_cast<const uint8_t *>(value_cache),
+                static_cast<uint4 *>(k), static_cast<uint4 *>(v), pool->d_err);
+    };
+    auto by_int4 = [&](auto dim) {
+        constexpr int NG = decltype(dim)::value / 32;
+        const int64_t rows = total / (d.head_dim / 8);
+        if (rows <= int4::FEW_ROWS) int4_rows(dim, std::integral_constant<int, 1>{}, uint32_t{});
+        else if (rows < (int64_t)1 << 29) int4_rows(dim, std::integral_constant<int, NG>{}, uint32_t{});
+        else int4_rows(dim, std::integral_constant<int, NG>{}, uint64_t{});
+    };
     if (d.kv_dtype == PKV_KV_BF16) by_dim(std::integral_constant<int, PKV_KV_BF16>{});
     else if (d.kv_dtype == PKV_KV_FP8E4M3) by_dim(std::integral_constant<int, PKV_KV_FP8E4M3>{});
-    else by_dim(std::integral_constant<int, PKV_KV_INT4>{});
+    else if (d.head_dim == 128) by_int4(std::integral_constant<int, 128>{});
+    else by_int4(std::integral_constant<int, 64>{});
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -105,8 +105,8 @@ __host__ __device__ inline size_t plan_expand_offset(int grid, size_t units)
 // expands the blocks that the batch's sequences use into bf16 tiles in the workspace, once --
 // exactly: scale * (n - 8) has 4 + 3 significant bits -- with block tables of its own, and the
 // bf16 attention kernel runs over those; the pool's scales go where a bf16 pool's 1 goes.  It
-// moves 17/32 bytes in and 2 out per element, bound by DRAM: 72 us of the 625 us that 16 chunks of
-// 512 behind up to 8192 positions take (32 / 8 heads, D 128; 1079 TFLOP/s in all).
+// moves 17/32 bytes in and 2 out per element, bound by DRAM: 67 us of the 619 us that 16 chunks of
+// 512 behind up to 8192 positions take (32 / 8 heads, D 128; 1089 TFLOP/s in all).
 //
 // Workspace: int32 tables [batch][max_blocks], then K and V [blocks][Hkv][16][D] bf16.
 // ------------------------------------------------------------------------------------
@@ -147,19 +147,6 @@ __device__ __forceinline__ uint4 expand_octet(uint32_t codes, uint32_t scale_byt
                    d = expand_pair(codes >> 12, s);
     return make_uint4(__byte_perm(a, b, 0x5410u), __byte_perm(c, d, 0x5410u), __byte_perm(a, b, 0x7632u),
                       __byte_perm(c, d, 0x7632u));
-}
-
-// NG consecutive words.
-template <int NG>
-__device__ __forceinline__ void load_words(const uint8_t *src, uint32_t (&w)[NG])
-{
-    if constexpr (NG == 4) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src));
-        w[0] = x.x; w[1] = x.y;
-    }
 }
 
 // A CTA per expanded block (a grid stride apart), a warp per KV head.  Lane (r, c) of a pass takes
@@ -204,9 +191,9 @@ __global__ void __launch_bounds__(EXPAND_THREADS) prefill_expand_kernel(const Ex
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int r = 8 * x + (lane >> 2);
-                load_words(kt + r * (D / 2) + c * (4 * NG), kw[x]);
-                load_words(vt + r * (D / 2) + c * (4 * NG), vw[x]);
-                load_words(vt + 8 * D + (r & 3) * (4 * NG), vs[x]);
+                int4::load_words(kt + r * (D / 2) + c * (4 * NG), kw[x]);
+                int4::load_words(vt + r * (D / 2) + c * (4 * NG), vw[x]);
+                int4::load_words(vt + 8 * D + (r & 3) * (4 * NG), vs[x]);
                 if constexpr (NG == 4) ks[x] = __ldg(reinterpret_cast<const uint32_t *>(kt + 8 * D + r * NG));
                 else ks[x] = __ldg(reinterpret_cast<const uint16_t *>(kt + 8 * D + r * NG));
             }
@@ -885,7 +872,8 @@ int expand(const pkv_pool *pool, const void *&key_cache, const void *&value_cach
     p.num_blocks = d.num_blocks;
     p.capacity = (int)capacity;
     p.grid = grid;
-    const unsigned ctas = (unsigned)std::min<int64_t>((int64_t)sms * 8, (int64_t)batch * max_blocks);
+    // (a CTA per block where that is at most 32 an SM: 8 of them, walking, take 6 us longer for 4600 blocks)
+    const unsigned ctas = (unsigned)std::min<int64_t>((int64_t)sms * 32, (int64_t)batch * max_blocks);
     if (d.head_dim == 128) prefill_expand_kernel<128><<<ctas, EXPAND_THREADS, 0, s>>>(p);
     else prefill_expand_kernel<64><<<ctas, EXPAND_THREADS, 0, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;

@@ -114,6 +114,38 @@ def test_gather_of_every_pool_type_and_layer(kv, D):
     assert torch.equal(ko1, ko[1][[0, 0, 5, 3]]) and torch.equal(vo1, vo[1][[0, 0, 5, 3]])
 
 
+@pytest.mark.parametrize("T,Hkv,layers,D", [(4100, 3, 1, 64), (4100, 3, 1, 128), (8193, 1, 1, 128), (1400, 2, 3, 64), (1400, 2, 3, 128)])
+def test_many_rows_of_every_kind_of_value(T, Hkv, layers, D):
+    # enough rows for a quarter of a row a thread; padding, slots beyond the pool, special values
+    rng = np.random.default_rng(T + D)
+    NB = -(-T // 16) + 2
+    slots = rng.permutation(NB * 16)[:T].astype(np.int64)
+    slots[[1, 700, T - 1]] = -1
+    slots[[2, 31, T - 2]] = [NB * 16, 1 << 40, NB * 16 + 5]
+    x = (rng.standard_normal((2, layers, T, Hkv, D)) * np.exp2(rng.integers(-16, 16, (2, layers, T, Hkv, 1)))).astype(np.float32)
+    x = torch.from_numpy(x).bfloat16()
+    b = I.bits(x).copy()
+    at = rng.random(b.shape) < 2e-4
+    b[at] = rng.choice(np.array([0x0000, 0x0001, 0x7F7F, 0x7F80, 0xFF80, 0x7FC0], np.uint16), int(at.sum())).view(b.dtype)
+    k, v = torch.from_numpy(b.view(np.int16)).view(torch.bfloat16)
+    kh, vh = (rng.integers(0, 256, (layers, NB, Hkv, O.tile_bytes(D))).astype(np.uint8) for _ in range(2))
+    pool, kc, vc, sl = _pool(NB, Hkv, D, layers, 0.5, 0.25), I.dev(kh), I.dev(vh), I.dev(slots)
+    pkv.kv_append_layers(pool, k.cuda(), v.cuda(), sl, kc, vc)
+    assert pool.get_device_error() == (pkv.ERR_DEVICE, pkv.DEVERR_SLOT)
+    ok = (slots >= 0) & (slots < NB * 16)
+    for l in range(layers):
+        O.append(b[0, l], b[1, l], np.where(ok, slots, -1), kh[l], vh[l], 0.5, 0.25)
+    assert np.array_equal(kc.cpu().numpy(), kh) and np.array_equal(vc.cpu().numpy(), vh)
+    ko, vo = (torch.full((layers, T, Hkv, D), -5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pkv.kv_gather_layers(pool, sl, kc, vc, ko, vo)
+    assert pool.get_device_error() == (pkv.ERR_DEVICE, pkv.DEVERR_SLOT)
+    for out, cache, is_key, s in ((ko, kh, True, 0.5), (vo, vh, False, 0.25)):
+        got = out.float().cpu().double().numpy()
+        for l in range(layers):                      # (a power-of-two pool scale: no rounding)
+            assert np.array_equal(got[l][ok], O.rows(cache[l], slots[ok], is_key, s))
+        assert (got[:, ~ok] == -5).all()
+
+
 def test_slots_beyond_the_pool_are_flagged_and_skipped():
     pool = _pool(2, 1, 64)
     kc, vc = (torch.zeros(2, 1, 544, dtype=torch.uint8, device="cuda") for _ in range(2))
