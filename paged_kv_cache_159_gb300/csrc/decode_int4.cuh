@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(int4_warps<D, NH>() * 32, 1) decode_int4_kerne
     constexpr int CH = TILE / 16;                  // 16-byte pieces of a tile
     extern __shared__ __align__(128) uint8_t smem[];
     int32_t *prefix = reinterpret_cast<int32_t *>(smem + int4_ring_bytes<D, NH>()), *lens = prefix + p.B + 1;
-    int32_t *wsum = lens + p.B;                    // [I4_NW]
+    int32_t *wsum = lens + p.B;                    // [NW]
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(dev::FULL, tid >> 5, 0);         // (known to be the same in every lane)
     const int Hkv = p.Hkv, group = p.group, HG = int4_team(Hkv), HGN = Hkv / HG;
