@@ -157,6 +157,41 @@ def decode(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_s
     return out, mag, ds
 
 
+def decode_bound(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_scale, blocks):
+    """q [B, Hq, D] -> (out, bound), each [B, Hq, D] in 64 bits: how far the decode may be off, by
+    what the cache holds.  With p_t = exp(s_t - max s), Z = sum p, a = |n - 8|, e the scale of a
+    V element, and `blocks` the most blocks that one partial state gathers:
+      output rounding           2^-8 |out|
+      p and p e in f16          2 * 2^-11 of sum p |v| / Z
+      scores                    off by ds (see decode), which enters p and the normaliser
+      exp2, sums, the merge     2^-16 and 2^-22 a block (the normaliser's additions) of the same
+      products                  two a block into an accumulator, each off by at most 2^-20 of the
+                                magnitudes that it adds, which the codes' offset makes p e (a + 8)
+      f16 underflow             p and p e are held as p 2^8 and p e (the largest p at 2^8 or more) and
+                                off by 2^-25 each where they are subnormal: a (e 2^-8 + 1) 2^-25
+                                a position, of a normaliser of 2^8 Z at least, and 2^8 times larger
+                                once the scale's 2^-8 is taken back."""
+    q = bf16_values(q_bits).astype(np.float64)
+    out, mag, ds = decode(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_scale)
+    Hq, Hkv = q.shape[1], key_cache.shape[1]
+    vs = float(np.float32(v_scale))
+    tol = 2.0 ** -8 * np.abs(out) + mag * (2.0 ** -10 + 2.0 ** -16 + blocks * 2.0 ** -22 + 2 * ds)
+    for b, L in enumerate(np.asarray(seq_lens).tolist()):
+        pos = np.arange(L)
+        slots = np.asarray(tables[b])[pos // BS].astype(np.int64) * BS + pos % BS
+        k = rows(key_cache, slots, True, k_scale)
+        n, e = codes(value_cache, slots, False)
+        a = np.abs(n)
+        for h in range(Hq):
+            hk = h // (Hq // Hkv)
+            s = (k[:, hk] @ q[b, h]) * float(np.float32(scale))
+            p = np.exp(s - s.max())
+            Z = p.sum()
+            tol[b, h] += vs * blocks * 2.0 ** -19 * (p @ (e[:, hk] * (a[:, hk] + 8))) / Z
+            tol[b, h] += vs * 2.0 ** -25 / Z * (a[:, hk] * (e[:, hk] * 2.0 ** -8 + 1)).sum(0)
+    return out, tol
+
+
 def prefill(q_bits, key_cache, value_cache, tables, seq_lens, cu_q, scale, k_scale, v_scale):
     """q [T, Hq, D]: row cu_q[b] + i attends over positions 0 .. L_b - P_b + i of sequence b; (out,
     sum p |v|) in 64 bits."""
