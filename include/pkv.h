@@ -375,7 +375,7 @@ size_t pkv_decode_workspace_bytes(const pkv_pool *pool, int32_t batch, int32_t n
  * 1 <= batch <= 4096, num_q_heads a multiple of Hkv with group <= 16, an attached pool,
  * max_blocks >= 1, batch * max_blocks * Hkv < 2^31.  FP8 pools compute q.K with q rounded
  * to fp16 (|q| must stay below 65504).  INT4 pools take q to fp16 with a power of two per
- * (sequence, KV head) that keeps its largest element in range.  An invalid seq_len sets
+ * (sequence, query head) that keeps its largest element in range.  An invalid seq_len sets
  * PKV_DEVERR_SEQ_LEN and zeroes that sequence's output. */
 int pkv_paged_attention_decode(pkv_pool *pool, const void *q, const void *key_cache,
                                const void *value_cache, const int32_t *block_tables,

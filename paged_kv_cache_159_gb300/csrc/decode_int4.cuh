@@ -10,9 +10,10 @@
 // the f16 tensor cores as they are: a nibble n at the low bits of an f16 is the subnormal n 2^-24,
 // one nibble up it is n 2^-20, so one and makes an operand register of two codes (after one shift
 // by 8 for the other half of a word).
-//   * K: q is scaled by a power of two per unit (exact) to a largest magnitude in [2^14, 2^15), and
-//     the columns at the upper nibbles by 2^-4 of that, which evens out the two factors: exact
-//     for every bf16 element of at least 2^-24 of the largest.  The -8 of every code is the
+//   * K: each query head is scaled by a power of two of its own (exact) to a largest magnitude in
+//     [2^14, 2^15), and the columns at the upper nibbles by 2^-4 of that, which evens out the two
+//     factors: exact for every bf16 element of at least 2^-24 of the head's largest.  Heads are columns
+//     of the product, so an infinity or NaN in one stays there.  The -8 of every code is the
 //     accumulators' start value, -8 2^-24 sum_{d in j} q_d.
 //   * Group j's partial sums are multiplied with scale_tj in fp32 as they join S.
 //   * V: a second product with the constant -8 2^-24 (-8 2^-20) takes the offset out step by step,
@@ -79,7 +80,7 @@ struct Int4Compute {
     float acc[2 * NG][NH][4];
     float m[NH][2], l[NH][2];
     float base_sc = 0.f;          // scale * k_scale * log2(e)
-    float sc = 0.f, rsc = 0.f;    // the unit's score scale (with the queries' power of two), positive, and 1 / it
+    float sc[NH][2];              // score scale of this lane's columns (with the head's power of two), positive
     float thr[NH][2];             // the running max is raised where a score (times sc) passes this (times sc)
     uint32_t ok, oks, ov, ovs;    // byte offsets in a tile of this lane's K words, K scales, V words, V scales
 
@@ -114,8 +115,10 @@ struct Int4Compute {
     __device__ void start(const uint16_t *qs, int group, int lane)
     {
         const int gid = lane >> 2, tid = lane & 3;
-        float amax = 0.f;
+        float amax[NH], up[NH];
         uint4 raw[NG][NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) amax[h] = 0.f;
 #pragma unroll
         for (int j = 0; j < NG; ++j)
 #pragma unroll
@@ -126,17 +129,21 @@ struct Int4Compute {
                 raw[j][h] = x;
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(dev::bf16_lo(w[i])), fabsf(dev::bf16_hi(w[i]))));
+                for (int i = 0; i < 4; ++i) amax[h] = fmaxf(amax[h], fmaxf(fabsf(dev::bf16_lo(w[i])), fabsf(dev::bf16_hi(w[i]))));
             }
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(dev::FULL, amax, o));
-        int e = 0;                                   // amax * 2^e in [2^14, 2^15)
-        if (amax > 0.f) e = 14 - (((int)(__float_as_uint(amax) >> 23) & 0xff) - 127);
-        e = max(-126, min(126, e));
-        const float up = copysignf(__uint_as_float((uint32_t)(127 + e) << 23), base_sc);     // (q takes a negative scale's sign)
-        // (at a scale of zero a masked score still has to come out as -infinity)
-        sc = fmaxf(fabsf(base_sc) * 0x1p24f * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
-        rsc = 1.f / sc;
+        for (int h = 0; h < NH; ++h) {
+            amax[h] = fmaxf(amax[h], __shfl_xor_sync(dev::FULL, amax[h], 1));         // (head 8 h + gid: this quad's lanes)
+            amax[h] = fmaxf(amax[h], __shfl_xor_sync(dev::FULL, amax[h], 2));
+            int e = 0;                               // amax * 2^e in [2^14, 2^15)
+            if (amax[h] > 0.f) e = 14 - (((int)(__float_as_uint(amax[h]) >> 23) & 0xff) - 127);
+            e = max(-126, min(126, e));
+            up[h] = copysignf(__uint_as_float((uint32_t)(127 + e) << 23), base_sc);   // (q takes a negative scale's sign)
+            // (at a scale of zero a masked score still has to come out as -infinity)
+            const float s = fmaxf(fabsf(base_sc) * 0x1p24f * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
+            sc[h][0] = __shfl_sync(dev::FULL, s, 8 * tid);           // (columns 2 tid, + 1: lanes 4 times that)
+            sc[h][1] = __shfl_sync(dev::FULL, s, 8 * tid + 4);
+        }
 #pragma unroll
         for (int j = 0; j < NG; ++j)
 #pragma unroll
@@ -145,8 +152,8 @@ struct Int4Compute {
                 float x[8], sum = 0.f;               // columns 32 j + 8 tid + i of head 8 h + gid
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = dev::bf16_lo(w[i]) * up;
-                    x[2 * i + 1] = dev::bf16_hi(w[i]) * up;
+                    x[2 * i] = dev::bf16_lo(w[i]) * up[h];
+                    x[2 * i + 1] = dev::bf16_hi(w[i]) * up[h];
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {        // pair i of a word: codes i and i + 4, at the upper nibbles for odd i
@@ -309,8 +316,8 @@ struct Int4Compute {
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 16));
-                    const float mn = fmaxf(m[h][r], mx * sc - OFF);
-                    thr[h][r] = (mn + (OFF + TAU)) * rsc;
+                    const float mn = fmaxf(m[h][r], mx * sc[h][r] - OFF);
+                    thr[h][r] = __fdividef(mn + (OFF + TAU), sc[h][r]);
                     const float alpha = dev::fast_exp2(m[h][r] - mn);
                     m[h][r] = mn;
                     l[h][r] *= alpha;
@@ -327,8 +334,8 @@ struct Int4Compute {
         for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                const float p0 = dev::fast_exp2(fmaf(s[x][h][0], sc, -m[h][0])), p1 = dev::fast_exp2(fmaf(s[x][h][1], sc, -m[h][1]));
-                const float p2 = dev::fast_exp2(fmaf(s[x][h][2], sc, -m[h][0])), p3 = dev::fast_exp2(fmaf(s[x][h][3], sc, -m[h][1]));
+                const float p0 = dev::fast_exp2(fmaf(s[x][h][0], sc[h][0], -m[h][0])), p1 = dev::fast_exp2(fmaf(s[x][h][1], sc[h][1], -m[h][1]));
+                const float p2 = dev::fast_exp2(fmaf(s[x][h][2], sc[h][0], -m[h][0])), p3 = dev::fast_exp2(fmaf(s[x][h][3], sc[h][1], -m[h][1]));
                 l[h][0] += p0 + p2;
                 l[h][1] += p1 + p3;
                 pb[x][h][0] = dev::movmatrix_trans(dev::pack_f16x2(p0, p1));
