@@ -19,7 +19,8 @@
 //   * V: a second product with the constant -8 2^-24 (-8 2^-20) takes the offset out step by step,
 //     so that the accumulators stay as small as the sums they stand for.
 //   * p scale is formed per group in f16: p 2^8 <= 2^15 (the running max is raised past 2^7) and
-//     scale 2^-8 (the scale byte moved to f16's fields) <= 1.75; both products round to 11 bits.
+//     scale 2^-8 (the scale byte moved to f16's fields) <= 1.75; both products round to 11 bits, or
+//     to 2^-25 where they are subnormal: a position loses that much of the largest p's 2^8.
 //
 // Schedule.  A 16-token block of one head is 2 x 17 D / 2 bytes, little work to hand between
 // warps, so nothing is: a warp copies its own tiles (cp.async into a ring of its own, two pairs of
@@ -72,16 +73,16 @@ struct Int4Compute {
     static constexpr int ROWB = D / 2;              // bytes of a row's codes
     static constexpr int SCALES = 8 * D;            // byte offset of a tile's scales
     static constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;     // nibbles 0 and 1 of each half
-    static constexpr float OFF = 8.0f;              // m is kept 8 below the max: p is held as p 2^8
-    static constexpr float TAU = 7.0f;              // raise the running max beyond 2^7
+    static constexpr float OFF = 8.0f;              // p is held as p 2^8, p = 2^(score - reference)
+    static constexpr float TAU = 7.0f;              // raise the reference to the max beyond 2^7
 
     uint32_t qb[NG][NH][4];       // Q^T fragments of group j: 2 words of each k-step
     float c0[NG][NH][4];          // -8 2^-24 sum_{d in j} q_d of this lane's columns, for both rows
     float acc[2 * NG][NH][4];
-    float m[NH][2], l[NH][2];
+    float R[NH][2], l[NH][2];     // reference of the scores (before their scale), sum of p 2^8
     float base_sc = 0.f;          // scale * k_scale * log2(e)
     float sc[NH][2];              // score scale of this lane's columns (with the head's power of two), positive
-    float thr[NH][2];             // the running max is raised where a score (times sc) passes this (times sc)
+    float thr[NH][2];             // the reference is raised where a score less it passes this: TAU / sc, -infinity at first
     uint32_t ok, oks, ov, ovs;    // byte offsets in a tile of this lane's K words, K scales, V words, V scales
 
     __device__ __forceinline__ void setup(int lane)
@@ -139,8 +140,9 @@ struct Int4Compute {
             if (amax[h] > 0.f) e = 14 - (((int)(__float_as_uint(amax[h]) >> 23) & 0xff) - 127);
             e = max(-126, min(126, e));
             up[h] = copysignf(__uint_as_float((uint32_t)(127 + e) << 23), base_sc);   // (q takes a negative scale's sign)
-            // (at a scale of zero a masked score still has to come out as -infinity)
-            const float s = fmaxf(fabsf(base_sc) * 0x1p24f * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
+            // (at a scale of zero a masked score still has to come out as -infinity; the upper end keeps
+            // R * sc finite, and from there on any two scores that differ are further apart than f16 reaches)
+            const float s = fminf(fmaxf(fabsf(base_sc) * 0x1p24f * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f), 1e30f);
             sc[h][0] = __shfl_sync(dev::FULL, s, 8 * tid);           // (columns 2 tid, + 1: lanes 4 times that)
             sc[h][1] = __shfl_sync(dev::FULL, s, 8 * tid + 4);
         }
@@ -181,8 +183,7 @@ struct Int4Compute {
                 for (int c = 0; c < 4; ++c) acc[mt][h][c] = 0.f;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            m[h][0] = m[h][1] = -INFINITY;
-            l[h][0] = l[h][1] = 0.f;
+            R[h][0] = R[h][1] = l[h][0] = l[h][1] = 0.f;
             thr[h][0] = thr[h][1] = -INFINITY;
         }
     }
@@ -201,7 +202,9 @@ struct Int4Compute {
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
     }
 
-    // S^T of one tile: stored rows gid, gid + 8 (tokens t0, t0 + 8); columns 8 h + 2 tid, + 1.
+    // S^T - R of one tile: stored rows gid, gid + 8 (tokens t0, t0 + 8); columns 8 h + 2 tid, + 1.
+    // (R joins as the sum's start, which takes no instruction more.  Subtracting a rounded R * sc
+    // later would leave the product's rounding in the exponent, more than f16 holds from scores of 2^28 on.)
     __device__ __forceinline__ void scores(uint32_t tiles, float (&s)[NH][4])
     {
         uint32_t k0[NG], k1[NG], b0, b1;
@@ -239,7 +242,7 @@ struct Int4Compute {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const float f = c < 2 ? ks0[j] : ks1[j];
-                    s[h][c] = j == 0 ? d[c] * f : fmaf(d[c], f, s[h][c]);
+                    s[h][c] = fmaf(d[c], f, j == 0 ? -R[h][c & 1] : s[h][c]);
                 }
             }
         }
@@ -292,7 +295,7 @@ struct Int4Compute {
         float s[2][NH][4];
         scores(tiles, s[0]);
         scores(tiles + 2 * TILE, s[1]);
-        // ---- scale, mask, lazy running max
+        // ---- mask, lazy running max
         const int t0 = (gid >> 1) + 4 * (gid & 1);
         bool need = false;
 #pragma unroll
@@ -316,10 +319,17 @@ struct Int4Compute {
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 16));
-                    const float mn = fmaxf(m[h][r], mx * sc[h][r] - OFF);
-                    thr[h][r] = __fdividef(mn + (OFF + TAU), sc[h][r]);
-                    const float alpha = dev::fast_exp2(m[h][r] - mn);
-                    m[h][r] = mn;
+                    const bool first = thr[h][r] == -INFINITY;
+                    // (no maximum: every score is NaN and so is the sum, which a reference of 0 carries on)
+                    const float raised = mx > -INFINITY ? R[h][r] + (first ? mx : fmaxf(mx, 0.f)) : R[h][r], up = raised - R[h][r];
+                    const float alpha = first ? 0.f : dev::fast_exp2(-up * sc[h][r]);
+                    R[h][r] = raised;
+                    thr[h][r] = __fdividef(TAU, sc[h][r]);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        s[x][h][r] -= up;
+                        s[x][h][r + 2] -= up;
+                    }
                     l[h][r] *= alpha;
 #pragma unroll
                     for (int mt = 0; mt < 2 * NG; ++mt) {
@@ -328,14 +338,14 @@ struct Int4Compute {
                     }
                 }
         }
-        // ---- P 2^8 = exp2(S - m), transposed
+        // ---- P 2^8 = exp2((S - R) sc + 8), transposed
         uint32_t pb[2][NH][2];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                const float p0 = dev::fast_exp2(fmaf(s[x][h][0], sc[h][0], -m[h][0])), p1 = dev::fast_exp2(fmaf(s[x][h][1], sc[h][1], -m[h][1]));
-                const float p2 = dev::fast_exp2(fmaf(s[x][h][2], sc[h][0], -m[h][0])), p3 = dev::fast_exp2(fmaf(s[x][h][3], sc[h][1], -m[h][1]));
+                const float p0 = dev::fast_exp2(fmaf(s[x][h][0], sc[h][0], OFF)), p1 = dev::fast_exp2(fmaf(s[x][h][1], sc[h][1], OFF));
+                const float p2 = dev::fast_exp2(fmaf(s[x][h][2], sc[h][0], OFF)), p3 = dev::fast_exp2(fmaf(s[x][h][3], sc[h][1], OFF));
                 l[h][0] += p0 + p2;
                 l[h][1] += p1 + p3;
                 pb[x][h][0] = dev::movmatrix_trans(dev::pack_f16x2(p0, p1));
@@ -345,7 +355,7 @@ struct Int4Compute {
         outputs<!FULL>(tiles + 2 * TILE, n1, tid, pb[1]);
     }
 
-    // The state's rows (query heads 0 .. group - 1): f(row, max, sum, group j, four consecutive
+    // The state's rows (query heads 0 .. group - 1): f(row, reference, sum, group j, four consecutive
     // columns from 32 j + 4 gid).
     template <class F>
     __device__ __forceinline__ void rows(int group, int lane, F f)
@@ -360,11 +370,12 @@ struct Int4Compute {
                 x += __shfl_xor_sync(dev::FULL, x, 8);
                 x += __shfl_xor_sync(dev::FULL, x, 16);
                 const int row = 8 * h + 2 * tid + r;
+                const float max = x == 0.f ? -INFINITY : R[h][r] * sc[h][r];      // (no sum: nothing valid, any reference)
                 if (row < group) {
 #pragma unroll
                     for (int j = 0; j < NG; ++j)
                         // back from n 2^-24 (n 2^-20), and scale 2^-8 (p 2^8 is in the sum as well)
-                        f(row, m[h][r], x, j, make_float4(acc[2 * j][h][r] * 0x1p32f, acc[2 * j][h][r + 2] * 0x1p28f,
+                        f(row, max, x, j, make_float4(acc[2 * j][h][r] * 0x1p32f, acc[2 * j][h][r + 2] * 0x1p28f,
                                                           acc[2 * j + 1][h][r] * 0x1p32f, acc[2 * j + 1][h][r + 2] * 0x1p28f));
                 }
             }

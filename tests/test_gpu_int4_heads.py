@@ -1,5 +1,5 @@
-"""The query heads of a KV head are independent of each other in the INT4 decode: one that
-holds infinities or NaN leaves the others as they are."""
+"""The query heads of a KV head are independent of each other in the INT4 decode: heads of
+very different magnitude, and one that holds infinities or NaN."""
 import numpy as np
 import pytest
 import torch
@@ -28,6 +28,29 @@ def _grid():
     return torch.cuda.get_device_properties(0).multi_processor_count
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", SHAPES)
+def test_heads_of_very_different_magnitude(Hq, Hkv, D):
+    c = I.Case(LENS, Hq, Hkv, D, seed=Hq + D)
+    gain = torch.tensor([1.0, 2.0 ** 30, 2.0 ** -30, 2.0 ** 100, 2.0 ** -100, 2.0 ** 12, 1.0])
+    c.q = (c.q.float() * gain[torch.arange(Hq) % 7][:, None]).bfloat16()
+    out = c.decode()
+    B.check(out, *B.bound(c, _grid()))
+    # scores of 2^30 and 2^100: the position with the largest, where it stands out by 2^-10 of itself
+    # (scores are off by less than 2^-11 of it), returns its value
+    q, got, seen = O.bf16_values(I.bits(c.q)).astype(np.float64), out.float().cpu().double().numpy(), 0
+    for b, L in enumerate(c.lens.tolist()):
+        k, v = O.sequence(c.kh, c.vh, c.tables[b], L, c.k_scale, c.v_scale)
+        for h in (h for h in range(Hq) if h % 7 in (1, 3)):
+            s = k[:, h // (Hq // Hkv)] @ q[b, h]
+            top = np.argsort(s)[::-1]
+            if s[top[0]] - s[top[1]] > 2.0 ** -10 * s[top[0]]:
+                seen += 1
+                ref = v[top[0], h // (Hq // Hkv)]
+                # (two roundings of p scale to f16, the output's, one of the pool's scale)
+                assert (np.abs(got[b, h] - ref) <= np.abs(ref) * (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -16)).all()
+    assert seen >= Hq // 7
+
+
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
 @pytest.mark.parametrize("Hq,Hkv,D", SHAPES)
 def test_a_head_that_is_not_finite_leaves_the_others(Hq, Hkv, D, bad):
@@ -39,3 +62,16 @@ def test_a_head_that_is_not_finite_leaves_the_others(Hq, Hkv, D, bad):
     hit[0, Hq // Hkv - 1] = hit[1, 0] = True
     got = c.decode().float().cpu().double().numpy()
     assert (np.abs(got - ref) <= tol)[~hit].all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("opts", [None, {"grid_ctas": 1}, {"grid_ctas": 300}], ids=["default", "1", "300"])
+@pytest.mark.parametrize("Hq,Hkv,D", SHAPES)
+def test_a_head_that_is_not_finite_returns_nan(Hq, Hkv, D, opts, bad):
+    # no finite answer of a head without one, whether its unit is cut or whole
+    c = I.Case(LENS, Hq, Hkv, D, seed=Hq)
+    c.q[:, Hq // Hkv - 1, 5] = bad
+    out = c.decode(opts).float()
+    assert bool(out[:, Hq // Hkv - 1].isnan().all())
+    keep = [h for h in range(Hq) if h != Hq // Hkv - 1]
+    assert bool(out[:, keep].isfinite().all())
