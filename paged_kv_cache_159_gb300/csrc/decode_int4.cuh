@@ -31,7 +31,8 @@
 // the teams of a one-wave grid.  A team that holds a whole unit writes its output; a cut unit
 // leaves a partial (max, sum, unnormalised output) per team, and a second launch merges them
 // in team order: placement of the blocks changes no bit.  Both launches may start while the one
-// before them drains (programmatic dependent launch) and wait for it before they read.
+// before them drains (programmatic dependent launch) and wait for it before they read, by loads that
+// are coherent: a non-coherent one takes its data to be the same from the kernel's start on.
 //
 // What it measured (GB300; us a pass in a graph over three states, 32 / 8 heads, D 128, K/V of 64 x
 // 2048 positions, 143.7 MB, and of the ragged batch, 592.9 MB; the measured copy peak gives 21.2
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(int4_warps<D, NH>() * 32, 1) decode_int4_kerne
         const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
         int run = 0;
         for (int b = b0; b < b1; ++b) {
-            const int L = __ldg(p.seq_lens + b);
+            const int L = __ldcg(p.seq_lens + b);
             const bool ok = L >= 1 && L <= p.MB * BS;
             lens[b] = L;
             if (!ok && blockIdx.x == 0) {
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(int4_warps<D, NH>() * 32, 1) decode_int4_kerne
         const int i = chunk * 32 + lane;
         if (i < n) {
             const U u = unit_of(s + i);
-            q.id = __ldg(p.block_tables + (size_t)u.b * p.MB + (int)(s + i - u.U0));
+            q.id = __ldcg(p.block_tables + (size_t)u.b * p.MB + (int)(s + i - u.U0));
             q.base = u.l * p.num_blocks * Hkv + u.h;
         }
         return q;
