@@ -220,7 +220,8 @@ struct Params {
     uint16_t *out;
     uint32_t *err;
     int MB, Hq, Hkv, group, TP, num_blocks, grid;
-    float score_scale;           // scale * k_scale * log2(e)
+    float score_scale;           // |scale| * k_scale * log2(e), at least 1e-37: masked scores stay -infinity
+    uint32_t negate_q;           // instruction descriptor bit of S = -Q K^T where the scale is negative, else 0
     float out_scale;             // v_scale (1 for bf16 pools)
     int test_stall;              // failure-path test: the Q loader waits on a barrier nothing completes
     int expanded;                // sequences of an INT4 call (tables and caches are the workspace's), or 0
@@ -612,7 +613,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             };
             if (is_s) {
                 // S = Q K^T: M 128, N 64 keys (f16 operands for E4M3 pools)
-                constexpr uint32_t IDS = FP8 ? tc::idesc_f16(BM, BN, 0) : tc::idesc_bf16(BM, BN, 0);
+                const uint32_t IDS = (FP8 ? tc::idesc_f16(BM, BN, 0) : tc::idesc_bf16(BM, BN, 0)) | p.negate_q;
                 // The operand descriptors are built once; each MMA adds its offset.
                 const uint64_t dQ = tc::desc_add(tc::smem_desc_sw128(base + L::Q, 16, 1024), (uint32_t)w * 16384);
                 const uint64_t dK = tc::smem_desc_sw128(base + L::K, 16, 1024);
@@ -707,7 +708,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 for (int c = 4; c < BN; c += 8)
 #pragma unroll
                     for (int t = 0; t < 4; ++t) mx4[t] = tc::fmax3(mx4[t], x[c + t], x[c + 4 + t]);
-                const float mx = tc::fmax3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3])) * p.score_scale;   // scale > 0: max commutes
+                const float mx = tc::fmax3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3])) * p.score_scale;   // score_scale > 0: max commutes
                 const bool raise = mx > m + TAU;
                 const bool rescale = raise && m != -INFINITY;
                 const float f = rescale ? dev::fast_exp2(m - mx) : 1.f;
@@ -1134,7 +1135,8 @@ extern "C" int pkv_paged_prefill_ex(pkv_pool *pool, const void *q, const void *k
     p.num_blocks = num_blocks;
     p.grid = grid;
     // (E4M3 pools: q enters the products as q * 2^-8)
-    p.score_scale = scale * d.k_scale * LOG2E * (fp8 ? 1.0f / FP8_Q_SCALE : 1.0f);
+    p.score_scale = std::max(std::fabs(scale * d.k_scale * LOG2E * (fp8 ? 1.0f / FP8_Q_SCALE : 1.0f)), 1e-37f);
+    p.negate_q = scale < 0.f ? pkv::tc::IDESC_NEGATE_A : 0u;
     p.out_scale = d.v_scale;
     p.test_stall = pkv::test_expire() == PKV_TEST_EXPIRE_PREFILL;
     p.expanded = d.kv_dtype == PKV_KV_INT4 ? batch : 0;
