@@ -81,6 +81,7 @@ constexpr float FP8_Q_SCALE = 1.0f / 256.0f;   // E4M3 pools: q is taken to f16 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float TAU = 8.0f;        // raise the running max only beyond 2^8
 constexpr uint32_t PLAN_MAGIC = 0x504b5650u;   // "PVKP"
+constexpr uint32_t NEGATE_A = 1u << 13;         // tcgen05.mma instruction descriptor: A enters the product negated
 constexpr uint32_t TMEM_COLS = 512;            // S (and P over it): 2 buffers x 2 q-tiles x 64, O: 2 x D
 
 // A plan: header, per-CTA unit ranges, units; for INT4 pools (batch > 0) the expanded blocks
@@ -1136,7 +1137,7 @@ extern "C" int pkv_paged_prefill_ex(pkv_pool *pool, const void *q, const void *k
     p.grid = grid;
     // (E4M3 pools: q enters the products as q * 2^-8)
     p.score_scale = std::max(std::fabs(scale * d.k_scale * LOG2E * (fp8 ? 1.0f / FP8_Q_SCALE : 1.0f)), 1e-37f);
-    p.negate_q = scale < 0.f ? pkv::tc::IDESC_NEGATE_A : 0u;
+    p.negate_q = scale < 0.f ? NEGATE_A : 0u;
     p.out_scale = d.v_scale;
     p.test_stall = pkv::test_expire() == PKV_TEST_EXPIRE_PREFILL;
     p.expanded = d.kv_dtype == PKV_KV_INT4 ? batch : 0;

@@ -46,9 +46,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn)
     return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Instruction descriptor bit: A enters the product negated.
-constexpr uint32_t IDESC_NEGATE_A = 1u << 13;
-
 // D[tmem] (+)= A[smem] . B[smem]^T, issued by one thread.
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate)
