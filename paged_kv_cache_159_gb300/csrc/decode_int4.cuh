@@ -322,9 +322,9 @@ struct Int4Compute {
                     mx = fmaxf(mx, __shfl_xor_sync(dev::FULL, mx, 16));
                     const bool first = thr[h][r] == -INFINITY;
                     // (no maximum: every score is NaN and so is the sum, which a reference of 0 carries on)
-                    const float raised = mx > -INFINITY ? R[h][r] + (first ? mx : fmaxf(mx, 0.f)) : R[h][r], up = raised - R[h][r];
+                    const float up = mx > -INFINITY ? (first ? mx : fmaxf(mx, 0.f)) : 0.f;
                     const float alpha = first ? 0.f : dev::fast_exp2(-up * sc[h][r]);
-                    R[h][r] = raised;
+                    R[h][r] += up;                           // (its rounding is one of the later scores', none of the maximum's)
                     thr[h][r] = __fdividef(TAU, sc[h][r]);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {

@@ -75,3 +75,23 @@ def test_a_head_that_is_not_finite_returns_nan(Hq, Hkv, D, opts, bad):
     assert bool(out[:, Hq // Hkv - 1].isnan().all())
     keep = [h for h in range(Hq) if h != Hq // Hkv - 1]
     assert bool(out[:, keep].isfinite().all())
+
+
+@pytest.mark.parametrize("gain", [2.0 ** 12, 2.0 ** 30, 2.0 ** 60, 2.0 ** 120])
+@pytest.mark.parametrize("Hq,Hkv,D", SHAPES)
+def test_large_scores_over_many_pairs(Hq, Hkv, D, gain):
+    # one warp (or a few) takes whole sequences, so that its reference is raised many times; the outputs
+    # are means of rows of V, whatever the positions are that win
+    c = I.Case([3000, 500, 1203], Hq, Hkv, D, seed=D)
+    c.q = (c.q.float() * gain).bfloat16()
+    for o in ({"grid_ctas": 1}, {"grid_ctas": 3}, None):
+        got = c.decode(o).float().cpu().double().numpy()
+        assert np.isfinite(got).all()
+        for b, L in enumerate(c.lens.tolist()):
+            v = O.sequence(c.kh, c.vh, c.tables[b], L, c.k_scale, c.v_scale)[1]
+            for h in range(Hq):
+                x = v[:, h // (Hq // Hkv)]
+                # (the roundings of decode_bound's outputs, of the largest of a column)
+                lo, hi, eps = x.min(0), x.max(0), np.abs(x).max(0) * 2.0 ** -7
+                assert (got[b, h] >= lo - eps).all() and (got[b, h] <= hi + eps).all()
+                assert (np.abs(got[b, h]) > np.abs(x).max() * 2.0 ** -10).any()       # and not zeros
