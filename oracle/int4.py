@@ -134,9 +134,10 @@ def decode(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_s
     and fp32 sums: with ks_tj = k scale * scale of token t and group j,
       |scale| * max_t sum_j ks_tj (7 * 32 * 2^-24 max|q| + 2^-16 sum_{d in j} |q_d|):
     an element of q is off by at most 2^-24 of the largest, times |n - 8| <= 7 for 32 columns; a
-    group's sum starts at -8 sum q and takes two products of codes up to 15, each off by at most
+    group's sum starts at -8 sum q and takes two products of codes up to 15, each taken to be off by
     2^-21 of the largest of these, at most 15 sum |q|, and its joining the score rounds four times
-    by 2^-24: in all below 2^-16 of sum |q|."""
+    by 2^-24: in all about 2^-16 of sum |q|.  (An estimate: decode_bound has what the products can
+    be off by at most.)"""
     q = bf16_values(q_bits).astype(np.float64)
     B, Hq, D = q.shape
     Hkv = key_cache.shape[1]
@@ -158,37 +159,64 @@ def decode(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_s
 
 
 def decode_bound(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_scale, blocks):
-    """q [B, Hq, D] -> (out, bound), each [B, Hq, D] in 64 bits: how far the decode may be off, by
-    what the cache holds.  With p_t = exp(s_t - max s), Z = sum p, a = |n - 8|, e the scale of a
-    V element, and `blocks` the most blocks that one partial state gathers:
+    """q [B, Hq, D] -> (out, bound), each [B, Hq, D] in 64 bits: how far a decode may be off that
+    takes codes to a tensor core as f16 subnormals, by what the cache holds.
+
+    The tensor core aligns a product's 16 terms and its accumulator to the largest exponent among
+    them and cuts each 25 bits below it (17 cuts, so less than 2^-20 of that exponent), and a
+    subnormal counts with the smallest normal's exponent, 2^-14, whatever its value: a code n 2^-24 (the
+    even nibbles) stands 2^10 below it, n 2^-20 (the odd ones) 2^6.
+
+    Scores are off by ds = |scale| max_t sum_j ks_tj (...), with ks_tj = k scale * scale of token t and
+    group j (of 32 columns), of
+      products    two a group of q with the codes, 2 * 2^-20 * 2^10 = 2^-9 of max_{d in j} |q_d| (their
+                  accumulator, at most 15 sum |q| <= 480 max |q| code units, is below 2^10 max |q|)
+      q in f16    2^-24 of the head's largest, times 7, for 32 columns
+      sums        five roundings of 2^-24 as group sums join the reference and each other, each of at
+                  most 2 * 7 sum |q|: below 2^-17 of sum_{d in j} |q_d|.
+    With p_t = exp(s_t - max s), Z = sum p, e the scale of a V element and a = |n - 8|, an output by
       output rounding           2^-8 |out|
       p and p e in f16          2 * 2^-11 of sum p |v| / Z
-      scores                    off by ds (see decode), which enters p and the normaliser
+      scores                    ds in p and in the normaliser, e^(2 ds) - 1 of the same
       exp2, sums, the merge     2^-16 and 2^-22 a block (the normaliser's additions) of the same
-      products                  two a block into an accumulator, each off by at most 2^-20 of the
-                                magnitudes that it adds, which the codes' offset makes p e (a + 8)
+      products                  two a block (the offset's, the codes'), each 2^-20 of the accumulator, at
+                                most sum p e (a + 8) code units, and of 2^10 (2^6 for odd nibbles) times
+                                the block's largest p e; `blocks` the most blocks that a partial state
+                                gathers
       f16 underflow             p and p e are held as p 2^8 and p e (the largest p at 2^8 or more) and
                                 off by 2^-25 each where they are subnormal: a (e 2^-8 + 1) 2^-25
                                 a position, of a normaliser of 2^8 Z at least, and 2^8 times larger
                                 once the scale's 2^-8 is taken back."""
     q = bf16_values(q_bits).astype(np.float64)
-    out, mag, ds = decode(q_bits, key_cache, value_cache, tables, seq_lens, scale, k_scale, v_scale)
-    Hq, Hkv = q.shape[1], key_cache.shape[1]
-    vs = float(np.float32(v_scale))
-    tol = 2.0 ** -8 * np.abs(out) + mag * (2.0 ** -10 + 2.0 ** -16 + blocks * 2.0 ** -22 + 2 * ds)
+    B, Hq, D = q.shape
+    Hkv = key_cache.shape[1]
+    vs, sc = float(np.float32(v_scale)), places(D, True)[2]
+    cut = np.where(np.arange(D) % 2 == 0, 2.0 ** -9, 2.0 ** -13)
+    out, tol = np.zeros_like(q), np.zeros_like(q)
     for b, L in enumerate(np.asarray(seq_lens).tolist()):
         pos = np.arange(L)
         slots = np.asarray(tables[b])[pos // BS].astype(np.int64) * BS + pos % BS
         k = rows(key_cache, slots, True, k_scale)
         n, e = codes(value_cache, slots, False)
-        a = np.abs(n)
+        a, edges = np.abs(n), np.arange(0, L, BS)
         for h in range(Hq):
             hk = h // (Hq // Hkv)
             s = (k[:, hk] @ q[b, h]) * float(np.float32(scale))
             p = np.exp(s - s.max())
             Z = p.sum()
-            tol[b, h] += vs * blocks * 2.0 ** -19 * (p @ (e[:, hk] * (a[:, hk] + 8))) / Z
-            tol[b, h] += vs * 2.0 ** -25 / Z * (a[:, hk] * (e[:, hk] * 2.0 ** -8 + 1)).sum(0)
+            out[b, h] = p @ (n[:, hk] * e[:, hk]) / Z * vs
+            mag = p @ (a[:, hk] * e[:, hk]) / Z * vs
+            ks = e4m3_values()[key_cache[(slots // BS)[:, None], hk, sc[pos % BS][:, ::GROUP]]] * float(np.float32(k_scale))
+            aq = np.abs(q[b, h]).reshape(-1, GROUP)
+            ds = abs(scale) * (ks @ (2.0 ** -9 * aq.max(-1) + 224 * 2.0 ** -24 * aq.max() + 2.0 ** -17 * aq.sum(-1))).max()
+            pe = p[:, None] * e[:, hk]
+            if ds > 30:                                 # scores too large to tell one position from another
+                tol[b, h] = np.inf
+                continue
+            tol[b, h] = (2.0 ** -8 * np.abs(out[b, h]) + mag * (2.0 ** -10 + 2.0 ** -16 + blocks * 2.0 ** -22 + np.expm1(2 * ds))
+                         + vs / Z * (blocks * 2.0 ** -19 * (pe * (a[:, hk] + 8)).sum(0)
+                                     + cut * np.maximum.reduceat(pe, edges, axis=0).sum(0)
+                                     + 2.0 ** -25 * (a[:, hk] * (e[:, hk] * 2.0 ** -8 + 1)).sum(0)))
     return out, tol
 
 
