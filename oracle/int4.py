@@ -239,3 +239,34 @@ def prefill(q_bits, key_cache, value_cache, tables, seq_lens, cu_q, scale, k_sca
             p /= p.sum(-1, keepdims=True)
             out[r0:r1, h], mag[r0:r1, h] = p @ v[:, hk], p @ np.abs(v[:, hk])
     return out, mag
+
+
+def prefill_bound(q_bits, key_cache, value_cache, tables, seq_lens, cu_q, scale, k_scale, v_scale):
+    """q [T, Hq, D] -> (out, bound) in 64 bits: how far a prefill may be off that multiplies exact
+    elements with f16 weights.  With p, Z, mag = sum p |v| / Z and D / 16 (or L / 16) tensor-core products
+    in a sum, each off by at most 2^-20 of the magnitudes that it adds (decode_bound):
+      output rounding    2^-8 |out|
+      p in f16           2^-11 of mag, and 2^-25 |v| / Z a position where p is subnormal (the largest is 1 or more)
+      scores             ds = |scale| D / 16 2^-20 max_t sum |q| |k|, which enters p and Z: e^(2 ds) - 1 of mag
+      products, sums     (L / 16) 2^-20, and 2^-16 for exp2 and the normaliser, of mag."""
+    q = bf16_values(q_bits).astype(np.float64)
+    D, Hq, Hkv = q.shape[2], q.shape[1], key_cache.shape[1]
+    out, tol = np.zeros_like(q), np.zeros_like(q)
+    for b, L in enumerate(np.asarray(seq_lens).tolist()):
+        r0, r1 = int(cu_q[b]), int(cu_q[b + 1])
+        if r1 == r0:
+            continue
+        k, v = sequence(key_cache, value_cache, tables[b], L, k_scale, v_scale)
+        late = np.arange(L)[None, :] > np.arange(L - (r1 - r0), L)[:, None]
+        for h in range(Hq):
+            hk = h // (Hq // Hkv)
+            s = q[r0:r1, h] @ k[:, hk].T * float(np.float32(scale))
+            s[late] = -np.inf
+            p = np.exp(s - s.max(-1, keepdims=True))
+            Z = p.sum(-1, keepdims=True)
+            av = np.abs(v[:, hk])
+            out[r0:r1, h], mag = p @ v[:, hk] / Z, p @ av / Z
+            ds = abs(scale) * D / 16 * 2.0 ** -20 * (np.abs(q[r0:r1, h]) @ np.abs(k[:, hk]).T).max(-1, keepdims=True)
+            tol[r0:r1, h] = (2.0 ** -8 * np.abs(out[r0:r1, h]) + mag * (2.0 ** -11 + L / 16 * 2.0 ** -20 + 2.0 ** -16 + np.expm1(2 * ds))
+                             + 2.0 ** -25 * (~late @ av) / Z)
+    return out, tol

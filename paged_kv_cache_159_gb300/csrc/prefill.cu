@@ -64,6 +64,7 @@
 #include <cstring>
 #include <mutex>
 #include <queue>
+#include <type_traits>
 #include <vector>
 
 #include "int4.cuh"
@@ -103,13 +104,15 @@ __host__ __device__ inline size_t plan_expand_offset(int grid, size_t units)
 // INT4 pools.  Every query tile of 256 rows reads all keys before it, so a chunk of P positions
 // would unpack each K/V element P g / 256 times; converting inside the attention kernel also
 // competes with its softmax (the E4M3 path runs at 0.68 of the bf16 one).  Instead one kernel
-// expands the blocks that the batch's sequences use into bf16 tiles in the workspace, once --
-// exactly: scale * (n - 8) has 4 + 3 significant bits -- with block tables of its own, and the
-// bf16 attention kernel runs over those; the pool's scales go where a bf16 pool's 1 goes.  It
+// expands the blocks that the batch's sequences use into 16-bit tiles in the workspace, once for
+// each sequence (a block that several share, once for each of them) -- exactly: scale * (n - 8) has
+// 4 + 3 significant bits -- with block tables of its own, and the bf16 attention kernel runs over
+// those; the pool's scales go where a bf16 pool's 1 goes.  K is expanded to bf16, like the queries, V
+// to f16, so that P is rounded to 11 bits rather than 8 (off by 2^-25 of the largest where below 2^-14).  It
 // moves 17/32 bytes in and 2 out per element, bound by DRAM: 67 us of the 619 us that 16 chunks of
 // 512 behind up to 8192 positions take (32 / 8 heads, D 128; 1089 TFLOP/s in all).
 //
-// Workspace: int32 tables [batch][max_blocks], then K and V [blocks][Hkv][16][D] bf16.
+// Workspace: int32 tables [batch][max_blocks], then K (bf16) and V (f16) [blocks][Hkv][16][D].
 // ------------------------------------------------------------------------------------
 struct ExpandParams {
     const uint8_t *plan;
@@ -130,19 +133,28 @@ __device__ __forceinline__ bool expanded_ok(const uint8_t *expand, int batch, in
     return off[batch] <= capacity && off[batch + 1] == max_blocks;
 }
 
-// (n - 8) * scale of the codes at bits 0-3 of each half of w, as bf16 pairs: 128 + n by an
-// and-or, then exact arithmetic.
+// (n - 8) * scale of the codes at bits 0-3 of each half of w, as a pair of bf16 (128 + n by an and-or,
+// then exact arithmetic) or of f16 (1024 + n).
 __device__ __forceinline__ uint32_t expand_pair(uint32_t w, __nv_bfloat162 scale)
 {
     const uint32_t x = (w & 0x000F000Fu) | 0x43004300u;
     const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), __float2bfloat162_rn(136.f)), scale);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
+__device__ __forceinline__ uint32_t expand_pair(uint32_t w, __half2 scale)
+{
+    const uint32_t x = (w & 0x000F000Fu) | 0x64006400u;
+    const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&x), __float2half2_rn(1032.f)), scale);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
 
-// Octet of codes (column i at bits 4 i) to 8 bf16.
+// Octet of codes (column i at bits 4 i) to 8 elements, T their pair type.
+template <class T>
 __device__ __forceinline__ uint4 expand_octet(uint32_t codes, uint32_t scale_byte)
 {
-    const __nv_bfloat162 s = __float2bfloat162_rn(int4::scale_value(scale_byte));
+    T s;
+    if constexpr (std::is_same<T, __half2>::value) s = __float2half2_rn(int4::scale_value(scale_byte));
+    else s = __float2bfloat162_rn(int4::scale_value(scale_byte));
     // halves hold columns 0-3 and 4-7: pairs (0, 4), (1, 5), (2, 6), (3, 7)
     const uint32_t a = expand_pair(codes, s), b = expand_pair(codes >> 4, s), c = expand_pair(codes >> 8, s),
                    d = expand_pair(codes >> 12, s);
@@ -206,9 +218,9 @@ __global__ void __launch_bounds__(EXPAND_THREADS) prefill_expand_kernel(const Ex
                 const int t = (r & 8) | ((r >> 1) & 3) | ((r & 1) << 2), oc = D == 128 ? c ^ (r & 2) : c;
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
-                    ko[t * OCTETS + 4 * j + c] = expand_octet(kw[x][j], (ks[x] >> (8 * j)) & 0xffu);
+                    ko[t * OCTETS + 4 * j + c] = expand_octet<__nv_bfloat162>(kw[x][j], (ks[x] >> (8 * j)) & 0xffu);
                     const uint32_t codes = __byte_perm(vw[x][j >> 1], vw[x][NG / 2 + (j >> 1)], (j & 1) ? 0x7632u : 0x5410u);
-                    vo[r * OCTETS + 4 * j + oc] = expand_octet(codes, (vs[x][j] >> (8 * (r >> 2))) & 0xffu);
+                    vo[r * OCTETS + 4 * j + oc] = expand_octet<__half2>(codes, (vs[x][j] >> (8 * (r >> 2))) & 0xffu);
                 }
             }
         }
@@ -252,7 +264,8 @@ struct Smem {
     static_assert(ALLOC <= 227 * 1024, "shared memory");
 };
 
-template <int D, bool FP8>
+// I4: K and V are the expanded tiles of an INT4 pool, K in bf16 and V in f16.
+template <int D, bool FP8, bool I4>
 __global__ void __launch_bounds__(NTHREADS, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap, const Params p)
@@ -642,7 +655,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 }
             } else {
                 // O += P V: M 128, N D, V MN-major
-                constexpr uint32_t IDO = FP8 ? tc::idesc_f16(BM, D, 1) : tc::idesc_bf16(BM, D, 1);
+                constexpr uint32_t IDO = FP8 || I4 ? tc::idesc_f16(BM, D, 1) : tc::idesc_bf16(BM, D, 1);
                 const uint64_t dV = tc::smem_desc_sw128(base + L::V, L::KHALF, 1024);
                 const uint32_t to = tO(w);
                 for (int u = u0; u < u1 && ok; ++u, ++uq) {
@@ -709,23 +722,42 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 for (int c = 4; c < BN; c += 8)
 #pragma unroll
                     for (int t = 0; t < 4; ++t) mx4[t] = tc::fmax3(mx4[t], x[c + t], x[c + 4 + t]);
-                const float mx = tc::fmax3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3])) * p.score_scale;   // score_scale > 0: max commutes
-                const bool raise = mx > m + TAU;
-                const bool rescale = raise && m != -INFINITY;
-                const float f = rescale ? dev::fast_exp2(m - mx) : 1.f;
-                if (raise) m = mx;
-                // P = exp2(x * scale - m) as packed bf16 (the lower key in the low half)
-                const float nm = m == -INFINITY ? 0.f : -m;
-                // (packed pairs: one fma and one add per two keys)
+                const float top = tc::fmax3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
+                bool raise, rescale;
+                float f = 1.f;
                 uint32_t pw[BN / 2];
-                const float2 sc2 = make_float2(p.score_scale, p.score_scale), nm2 = make_float2(nm, nm);
+                const float2 sc2 = make_float2(p.score_scale, p.score_scale);
                 float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int e = 0; e < BN / 2; ++e) {
-                    const float2 t = tc::ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, nm2);
+                // P, two keys at a time, the lower key in the low half
+                auto put = [&](int e, float2 t) {
                     const float2 pe = make_float2(dev::fast_exp2(t.x), dev::fast_exp2(t.y));
                     ps[e & 1] = tc::fadd2(ps[e & 1], pe);
-                    pw[e] = FP8 ? dev::pack_f16x2(pe.x, pe.y) : dev::pack_bf16x2(pe.x, pe.y);
+                    pw[e] = FP8 || I4 ? dev::pack_f16x2(pe.x, pe.y) : dev::pack_bf16x2(pe.x, pe.y);
+                };
+                if constexpr (I4) {
+                    // m before its scale, P = exp2((x - m) * scale): the exponent of f16's P is free of the
+                    // rounding of m * scale, which from scores of 2^28 on is more than f16 holds
+                    const float d = (top - m) * p.score_scale;
+                    raise = d > TAU;
+                    rescale = raise && m != -INFINITY;
+                    if (rescale) f = dev::fast_exp2(-d);
+                    if (raise) m = top;
+                    const float nm = m == -INFINITY ? 0.f : -m;
+                    const float2 nm2 = make_float2(nm, nm);
+#pragma unroll
+                    for (int e = 0; e < BN / 2; ++e) put(e, int4::mul2(tc::fadd2(make_float2(x[2 * e], x[2 * e + 1]), nm2), sc2));
+                } else {
+                    const float mx = top * p.score_scale;        // score_scale > 0: max commutes
+                    raise = mx > m + TAU;
+                    rescale = raise && m != -INFINITY;
+                    if (rescale) f = dev::fast_exp2(m - mx);
+                    if (raise) m = mx;
+                    // P = exp2(x * scale - m)
+                    const float nm = m == -INFINITY ? 0.f : -m;
+                    // (packed pairs: one fma and one add per two keys)
+                    const float2 nm2 = make_float2(nm, nm);
+#pragma unroll
+                    for (int e = 0; e < BN / 2; ++e) put(e, tc::ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, nm2));
                 }
                 const float2 ps2 = tc::fadd2(ps[0], ps[1]);
                 l = l * f + (ps2.x + ps2.y);
@@ -824,18 +856,18 @@ int sm_count()
     return n;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool I4 = false>
 cudaError_t launch(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm, const Params &p,
                    cudaStream_t s)
 {
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(prefill_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr = cudaFuncSetAttribute(prefill_kernel<D, FP8, I4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     Smem<D, FP8>::ALLOC);
     });
     if (attr != cudaSuccess) return attr;
-    prefill_kernel<D, FP8><<<p.grid, NTHREADS, Smem<D, FP8>::ALLOC, s>>>(qm, km, vm, p);
+    prefill_kernel<D, FP8, I4><<<p.grid, NTHREADS, Smem<D, FP8>::ALLOC, s>>>(qm, km, vm, p);
     return cudaGetLastError();
 }
 
@@ -1141,7 +1173,8 @@ extern "C" int pkv_paged_prefill_ex(pkv_pool *pool, const void *q, const void *k
     p.out_scale = d.v_scale;
     p.test_stall = pkv::test_expire() == PKV_TEST_EXPIRE_PREFILL;
     p.expanded = d.kv_dtype == PKV_KV_INT4 ? batch : 0;
-    const cudaError_t e = D == 128 ? (fp8 ? launch<128, true>(qm, km, vm, p, s) : launch<128, false>(qm, km, vm, p, s))
-                                   : (fp8 ? launch<64, true>(qm, km, vm, p, s) : launch<64, false>(qm, km, vm, p, s));
+    const cudaError_t e = p.expanded ? (D == 128 ? launch<128, false, true>(qm, km, vm, p, s) : launch<64, false, true>(qm, km, vm, p, s))
+                          : D == 128 ? (fp8 ? launch<128, true>(qm, km, vm, p, s) : launch<128, false>(qm, km, vm, p, s))
+                                     : (fp8 ? launch<64, true>(qm, km, vm, p, s) : launch<64, false>(qm, km, vm, p, s));
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
