@@ -182,7 +182,7 @@ int pkv_copy_blocks(pkv_pool *pool, void *key_cache, void *value_cache, const in
  * the free list: src_out[i], dst_out[i] (host int32, room for num_forks entries each), and
  * *num_copies of them -- run pkv_copy_blocks on the pairs before the forks append.  Unused
  * entries are -1.  The sequence itself keeps its blocks and may append without a copy of its
- * last block.  INVALID (nothing changed) if seq_len < 1 or needs more than max_blocks entries,
+ * last block, unless that was shared before.  INVALID (nothing changed) if seq_len < 1 or needs more than max_blocks entries,
  * or an entry is not an allocated block; OOM (nothing changed) if the free list is too short.
  * tables_out must not overlap table_row. */
 int pkv_fork_tables(pkv_pool *pool, const int32_t *table_row, int32_t seq_len, int32_t num_forks,
@@ -462,8 +462,9 @@ int pkv_paged_prefill(pkv_pool *pool, const void *q, const void *key_cache, cons
                       int32_t total_q, float scale, const void *plan, int32_t grid, void *out, void *stream);
 
 /* The same with a workspace, which INT4 pools need (pkv_paged_prefill refuses them; other
- * pools ignore it): the blocks that the batch's sequences with rows use are expanded to bf16
- * there by one more launch, exactly, and attended over as a bf16 pool's.  workspace: device
+ * pools ignore it): the blocks that the batch's sequences with rows use are expanded there by one more
+ * launch (once for every sequence that uses a block), exactly, to bf16 (K) and f16 (V), and
+ * attended over as a bf16 pool's.  workspace: device
  * memory, 256-byte aligned, of at least pkv_prefill_workspace_bytes() bytes for the cu_q,
  * seq_lens and max_blocks that the plan was made with (host arrays; 0 for other pools and for
  * invalid shapes); its content before and after is unspecified, and calls sharing it must not

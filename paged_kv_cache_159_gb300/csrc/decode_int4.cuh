@@ -6,7 +6,7 @@
 //   O_d   = sum_t (p_t scale_tj(d)) (n_td - 8)
 // with tokens (S^T = K Q^T) or columns (O^T = V^T P^T) as the 16 rows of a tensor-core product
 // and the group's query heads as its 8 columns, so each code is unpacked once per step whatever
-// the group.  Unpacking sets the pace (the integer pipe issues at half rate), so codes go to
+// the group.  Unpacking is most of the work of the integer pipe (half rate), so codes go to
 // the f16 tensor cores as they are: a nibble n at the low bits of an f16 is the subnormal n 2^-24,
 // one nibble up it is n 2^-20, so one and makes an operand register of two codes (after one shift
 // by 8 for the other half of a word).
@@ -18,6 +18,10 @@
 //   * Group j's partial sums are multiplied with scale_tj in fp32 as they join S.
 //   * V: a second product with the constant -8 2^-24 (-8 2^-20) takes the offset out step by step,
 //     so that the accumulators stay as small as the sums they stand for.
+//   * The tensor core cuts a product's terms 25 bits below the largest exponent among them, and counts
+//     a subnormal's as 2^-14: a term of a code is cut 2^-15 of a code unit (the lower nibble of a byte; the
+//     upper 2^-19), so a group's score is off by at most 2^-9 of its largest |q| in code units, and an
+//     output by 2^-9 (2^-13) of a code unit of the largest p scale of every block.
 //   * p scale is formed per group in f16: p 2^8 <= 2^15 (the running max is raised past 2^7) and
 //     scale 2^-8 (the scale byte moved to f16's fields) <= 1.75; both products round to 11 bits, or
 //     to 2^-25 where they are subnormal: a position loses that much of the largest p's 2^8.
@@ -38,11 +42,15 @@
 // 2048 positions, 143.7 MB, and of the ragged batch, 592.9 MB; the measured copy peak gives 21.2
 // and 87.3): streaming alone 28.0 and 97.3; the first version, on the other pools' schedule with
 // a producer warp and bulk copies of 1088 bytes, 67 and 228; own copies and the merge launch 44 and
-// 148; subnormal operands and pairs of blocks, 43.7 and 139; twelve warps, 41.0 and 132; now 39.6 and
-// 122.7.  Not kept: E4M3 products for K (emulated by conversions on this GPU, 58 and 181), loads
+// 148; subnormal operands and pairs of blocks, 43.7 and 139; twelve warps, 41.0 and 132; now 39.7 and
+// 122.5.  Not kept: E4M3 products for K (emulated by conversions on this GPU, 58 and 181), loads
 // straight to registers (48 and 159: too few bytes in flight), four pairs in the ring (no change),
-// V's codes as whole bytes less their upper nibbles (119, but off by 2^-14 of a step where codes cancel).
-// What bounds it: instruction issue, the integer pipe (two clocks an instruction) first.
+// V's codes as whole bytes less their upper nibbles (119, but the cut of whole bytes grows with the
+// nibble taken out).
+// What bounds it: waits of the three warps that a scheduler has.  No pipe is full on average (64 x 2048: issue
+// slots 52 % busy, integer pipe 49 %, tensor 33 %), but the warps are all unpacking or all multiplying: per issued
+// instruction a warp spends 1.35 waiting for a fixed latency and 0.97 for a pipe, and 0.93 warps are
+// ready a clock.  The merge launch comes on top (7.9 us by itself from cold caches).
 #pragma once
 
 #include "decode_kernels.cuh"

@@ -61,7 +61,8 @@ extern "C" int pkv_paged_attention_decode_noalloc(pkv_pool *pool, const void *q,
     if (batch == 0) return PKV_OK;
     size_t need = pkv_decode_workspace_bytes(pool, batch, num_q_heads, max_blocks, nullptr);
     // An INT4 pool's partials are per warp and grow with the grid: the largest halving of the grid
-    // whose partials fit.
+    // whose partials fit.  (64 x 2048, 8 KV heads, head_dim 128: 44.4 us for a group of 4, 68 to 70 for 5 to 8 and
+    // 188 for 16, against 40, 40 to 42 and 63 us with a workspace.)
     pkv_decode_opts opts{};
     if (pool->desc.kv_dtype == PKV_KV_INT4 && need > (size_t)PKV_NOALLOC_SCRATCH_BYTES) {
         int32_t sms = 0;

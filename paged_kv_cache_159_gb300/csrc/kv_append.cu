@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(256) kv_append_fp8_kernel(
 // there are rows enough, so that its codes are 4 NG consecutive bytes of K as of V (int4.cuh) and
 // leave in one store each; one of them for few rows, which leaves a thread less to do in turn.
 // I: the index type, 32 bits where the lanes' count allows.  Bound by DRAM, instruction issue close behind:
-// append and gather of 16411 tokens of 8 heads, D 128, 170 MB, take 27.7 us together, 6.15 TB/s (36.7 with an
+// append and gather of 16411 tokens of 8 heads, D 128, 170 MB, take 28.8 us together, 5.92 TB/s (36.7 with an
 // octet a thread).
 constexpr int ROW_THREADS = 128;
 
