@@ -359,7 +359,7 @@ size_t pkv_decode_workspace_bytes(const pkv_pool *pool, int32_t batch, int32_t n
 /* Paged decode attention, one query token per sequence [Decode][Attn][GQA][Paged]:
  *   out[b][hq][:] = sum_{j < L_b} softmax_j(scale * q[b][hq] . K_j) V_j,
  *   K_j, V_j = cache[block_tables[b][j / 16]][hq / (Hq/Hkv)][j % 16][:],  L_b = seq_lens[b],
- * scale any finite number (zero and negative ones among them).
+ * scale a finite number, zero and negative ones among them, |scale * k_scale| at most 1e30.
  * Device pointers: q bf16 [batch, num_q_heads, D]; caches as in pkv_pool_desc;
  * block_tables int32 [batch, max_blocks]; seq_lens int32 [batch]; out bf16
  * [batch, num_q_heads, D] (fp32 accumulation, rounded to nearest even); workspace of at
@@ -427,7 +427,7 @@ int pkv_decode_step_layers(pkv_pool *pool, const void *q, const void *k_new, con
  * pkv_slot_mapping_chunks), behind C_b = seq_lens[b] - P_b earlier positions.  Row
  * cu_q[b] + i is position C_b + i and attends causally over positions 0 .. C_b + i of its
  * own sequence:  out[row][hq] = sum_{j <= C_b + i} softmax_j(scale * q[row][hq] . K_j) V_j,
- * scale any finite number (zero and negative ones among them), K_j, V_j gathered through block_tables[b] from KV head hq / (Hq / Hkv).  C_b = 0 is the
+ * scale as for the decode, K_j, V_j gathered through block_tables[b] from KV head hq / (Hq / Hkv).  C_b = 0 is the
  * prefill of a whole prompt; C_b > 0 a later chunk of a long prompt.
  *
  * The work is planned on the host once per batch (every layer of a model can reuse the

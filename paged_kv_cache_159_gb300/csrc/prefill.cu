@@ -723,8 +723,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 #pragma unroll
                     for (int t = 0; t < 4; ++t) mx4[t] = tc::fmax3(mx4[t], x[c + t], x[c + 4 + t]);
                 const float top = tc::fmax3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
-                bool raise, rescale;
-                float f = 1.f;
                 uint32_t pw[BN / 2];
                 const float2 sc2 = make_float2(p.score_scale, p.score_scale);
                 float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -734,37 +732,23 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     ps[e & 1] = tc::fadd2(ps[e & 1], pe);
                     pw[e] = FP8 || I4 ? dev::pack_f16x2(pe.x, pe.y) : dev::pack_bf16x2(pe.x, pe.y);
                 };
-                if constexpr (I4) {
-                    // m before its scale, P = exp2((x - m) * scale).  The rounding of m * scale may join the
-                    // exponents (one fma a pair) while it is below 2^-16; from scores of 2^28 on it is more than
-                    // f16's P holds.  (16 chunks of 512: 616 us, 632 without the short way)
-                    const float d = (top - m) * p.score_scale;
-                    raise = d > TAU;
-                    rescale = raise && m != -INFINITY;
-                    if (rescale) f = dev::fast_exp2(-d);
-                    if (raise) m = top;
-                    const float nm = m == -INFINITY ? 0.f : -m, ns = nm * p.score_scale;
-                    if (!__any_sync(dev::FULL, fabsf(ns) > 256.f)) {
-                        const float2 ns2 = make_float2(ns, ns);
+                // m before its scale (positive, so that the maximum commutes with it), P = exp2((x - m) * scale).  The
+                // rounding of m * scale may join the exponents (one fma a pair) while it is below 2^-16; from
+                // scores of 2^28 on it is more than P holds.  (16 chunks of 512 over INT4: 616 us, 632 without
+                // the short way)
+                const float d = (top - m) * p.score_scale;
+                const bool raise = d > TAU, rescale = raise && m != -INFINITY;
+                const float f = rescale ? dev::fast_exp2(-d) : 1.f;
+                if (raise) m = top;
+                const float nm = m == -INFINITY ? 0.f : -m, ns = nm * p.score_scale;
+                if (!__any_sync(dev::FULL, fabsf(ns) > 256.f)) {
+                    const float2 ns2 = make_float2(ns, ns);
 #pragma unroll
-                        for (int e = 0; e < BN / 2; ++e) put(e, tc::ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, ns2));
-                    } else {
-                        const float2 nm2 = make_float2(nm, nm);
-#pragma unroll
-                        for (int e = 0; e < BN / 2; ++e) put(e, int4::mul2(tc::fadd2(make_float2(x[2 * e], x[2 * e + 1]), nm2), sc2));
-                    }
+                    for (int e = 0; e < BN / 2; ++e) put(e, tc::ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, ns2));
                 } else {
-                    const float mx = top * p.score_scale;        // score_scale > 0: max commutes
-                    raise = mx > m + TAU;
-                    rescale = raise && m != -INFINITY;
-                    if (rescale) f = dev::fast_exp2(m - mx);
-                    if (raise) m = mx;
-                    // P = exp2(x * scale - m)
-                    const float nm = m == -INFINITY ? 0.f : -m;
-                    // (packed pairs: one fma and one add per two keys)
                     const float2 nm2 = make_float2(nm, nm);
 #pragma unroll
-                    for (int e = 0; e < BN / 2; ++e) put(e, tc::ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, nm2));
+                    for (int e = 0; e < BN / 2; ++e) put(e, int4::mul2(tc::fadd2(make_float2(x[2 * e], x[2 * e + 1]), nm2), sc2));
                 }
                 const float2 ps2 = tc::fadd2(ps[0], ps[1]);
                 l = l * f + (ps2.x + ps2.y);
