@@ -42,8 +42,8 @@
 // 2048 positions, 143.7 MB, and of the ragged batch, 592.9 MB; the measured copy peak gives 21.2
 // and 87.3): streaming alone 28.0 and 97.3; the first version, on the other pools' schedule with
 // a producer warp and bulk copies of 1088 bytes, 67 and 228; own copies and the merge launch 44 and
-// 148; subnormal operands and pairs of blocks, 43.7 and 139; twelve warps, 41.0 and 132; now 39.7 and
-// 122.5.  Not kept: E4M3 products for K (emulated by conversions on this GPU, 58 and 181), loads
+// 148; subnormal operands and pairs of blocks, 43.7 and 139; twelve warps, 41.0 and 132; now 39.6 and
+// 122.4.  Not kept: E4M3 products for K (58 and 181), loads
 // straight to registers (48 and 159: too few bytes in flight), four pairs in the ring (no change),
 // V's codes as whole bytes less their upper nibbles (119, but the cut of whole bytes grows with the
 // nibble taken out).

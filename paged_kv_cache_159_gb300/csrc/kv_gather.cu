@@ -9,8 +9,8 @@
 // becomes bf16(fl32(pool scale * value)), an INT4 one bf16(fl32((n - 8) * fl32(scale * pool scale))): at most
 // two fp32 roundings before the one to bf16, none where the pool scale is a power of two.
 // Bound by DRAM (a row's reads are 17 D / 32 bytes for INT4, D for FP8 or 2 D, its writes 2 D): INT4,
-// 131072 tokens of 8 heads, D 128, 680.5 MB, take 102.1 us, 6.66 TB/s (an octet a thread 131 us, four 120); of a bf16 pool 158.7 us, 6.77 TB/s,
-// of an FP8 one 121.6 us, 6.63 TB/s.
+// 131072 tokens of 8 heads, D 128, 680.5 MB, take 102.1 us, 6.66 TB/s (an octet a thread 131 us, four 120); of a bf16 pool 158.8 us, 6.77 TB/s,
+// of an FP8 one 121.4 us, 6.64 TB/s.
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -109,8 +109,8 @@ __host__ __device__ inline size_t plan_expand_offset(int grid, size_t units)
 // 4 + 3 significant bits -- with block tables of its own, and the bf16 attention kernel runs over
 // those; the pool's scales go where a bf16 pool's 1 goes.  K is expanded to bf16, like the queries, V
 // to f16, so that P is rounded to 11 bits rather than 8 (off by 2^-25 of the largest where below 2^-14).  It
-// moves 17/32 bytes in and 2 out per element, bound by DRAM: 67 us of the 617 us that 16 chunks of
-// 512 behind up to 8192 positions take (32 / 8 heads, D 128; 1094 TFLOP/s in all).
+// moves 17/32 bytes in and 2 out per element, bound by DRAM: 67 us of the 616 us that 16 chunks of
+// 512 behind up to 8192 positions take (32 / 8 heads, D 128; 1095 TFLOP/s in all).
 //
 // Workspace: int32 tables [batch][max_blocks], then K (bf16) and V (f16) [blocks][Hkv][16][D].
 // ------------------------------------------------------------------------------------
