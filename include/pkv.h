@@ -61,6 +61,8 @@ typedef enum {
 #define PKV_DEVERR_SEQ_LEN  0x4u   /* decode: seq_len outside [1, max_blocks * block_size] */
 #define PKV_DEVERR_TIMEOUT  0x8u   /* a pipeline wait exceeded its bound (about 1 s) */
 #define PKV_DEVERR_PLAN     0x10u  /* prefill: the plan does not match the call (nothing ran) */
+#define PKV_DEVERR_RESERVE  0x20u  /* extend_tables: the reserve has too few blocks (nothing changed) */
+#define PKV_DEVERR_PATH     0x40u  /* accept_rows: a path is not strictly increasing within its drafts */
 
 typedef enum { PKV_KV_BF16 = 0, PKV_KV_FP8E4M3 = 1, PKV_KV_INT4 = 2 } pkv_kv_dtype;
 
@@ -477,6 +479,88 @@ int pkv_paged_prefill_ex(pkv_pool *pool, const void *q, const void *key_cache, c
                          const int32_t *block_tables, int32_t batch, int32_t num_q_heads, int32_t max_blocks,
                          int32_t total_q, float scale, const void *plan, int32_t grid, void *out,
                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Growing sequences on the GPU [Paged][Life][Slot] ----
+ * One step's bookkeeping from device arrays, without the host (a captured graph may hold it):
+ * sequence b has seq_lens[b] positions and gains P_b = cu_q[b+1] - cu_q[b] rows (device int32
+ * [batch] and [batch+1], cu_q[0] = 0).  The table entries (device int32 [batch, max_blocks]) that
+ * the new positions fall into and that are empty (negative) are filled with the ids of reserve
+ * (device int32, reserve_len entries; blocks that the caller took with pkv_pool_alloc) from
+ * reserve[state[0]] on, in the order of sequences and positions -- the order in which
+ * pkv_build_block_tables hands blocks out -- and state[0] moves past them.  Of those entries the
+ * filled ones must come first.  state: device int32 [2], zeros at first; state[1] is the
+ * library's.  new_lens (device int32 [batch]; may be seq_lens) receives seq_lens[b] + P_b;
+ * slots_out (device int64, total_q entries) the slot of every row, as pkv_slot_mapping_chunks
+ * gives it, for pkv_kv_append; positions_out (device int32 [total_q], or NULL) its position.  Rows
+ * total_q > r >= cu_q[batch] are padding: slot -1, position 0.  A block that receives rows must not
+ * be shared (pkv_cow_prepare).  If cu_q is not ascending from 0 to at most total_q or a length does not
+ * fit its table (PKV_DEVERR_SEQ_LEN), or the reserve has too few ids left (PKV_DEVERR_RESERVE),
+ * nothing changes: tables and state[0] stay, every slot is -1 and new_lens is seq_lens.  An id
+ * outside the pool sets PKV_DEVERR_BLOCK_ID and leaves its entry empty, its rows' slots -1.
+ * Requires batch <= 4096, max_blocks <= 2^26. */
+int pkv_extend_tables(pkv_pool *pool, const int32_t *seq_lens, const int32_t *cu_q, int32_t batch,
+                      int32_t max_blocks, int32_t total_q, int32_t *block_tables, const int32_t *reserve,
+                      int32_t reserve_len, int32_t *state, int32_t *new_lens, int64_t *slots_out,
+                      int32_t *positions_out, void *stream);
+
+/* Keep the accepted path of every sequence's drafts [Slot][Layout]: the last P_b = cu_q[b+1] -
+ * cu_q[b] of sequence b's seq_lens[b] positions hold drafts, whose rows path[b][0 .. n_b - 1]
+ * (device int32 [batch, max_path], strictly increasing from 0 .. P_b - 1; n_b = num_accepted[b],
+ * device int32 [batch]) are accepted.  Row path[b][j] moves to place j, in every layer (caches: the
+ * whole stacked tensors), K and V, bit for bit in any pool type, and lens_out[b] (device int32
+ * [batch]; apart from the inputs) receives seq_lens[b] - P_b + n_b.  The other drafts' positions
+ * hold anything afterwards; the tables stay.  A bad length sets PKV_DEVERR_SEQ_LEN, a bad path
+ * PKV_DEVERR_PATH, an entry of the path's blocks outside the pool PKV_DEVERR_BLOCK_ID; that
+ * sequence is left as it was, its entry of lens_out too.  The blocks of the drafts must not be
+ * shared.  Requires max_blocks <= 2^26. */
+int pkv_accept_rows(pkv_pool *pool, void *key_cache, void *value_cache, const int32_t *block_tables,
+                    const int32_t *seq_lens, const int32_t *cu_q, const int32_t *path,
+                    const int32_t *num_accepted, int32_t batch, int32_t max_blocks, int32_t max_path,
+                    int32_t *lens_out, void *stream);
+
+/* ---- Drafted tokens and sliding windows [Attn][GQA][Paged] ----
+ * Attention of the last P_b = cu_q[b+1] - cu_q[b] positions of every sequence, whose K and V are in
+ * the cache (pkv_extend_tables, pkv_kv_append), behind C_b = seq_lens[b] - P_b cached ones: row
+ * cu_q[b] + i of q and out is position C_b + i, and
+ *   out[row][hq] = sum_j softmax_j(scale * q[row][hq] . K_j) V_j  over the positions j that it sees,
+ *   - tree_mask NULL (a chain): j <= p and (j > p - window or j < sinks), with p = C_b + i;
+ *   - a tree (drafted tokens that branch): position C_b + j where bit j % 64 of
+ *     tree_mask[row][j / 64] is set (device int64 [total_q, ceil(max_q / 64)]; a token's own bit and
+ *     its ancestors'; bits from P_b on are ignored), and j < C_b with j > p - window or j < sinks, where
+ *     p = C_b + (bits set) - 1 is the row's place behind its ancestors.
+ * window 0: no window (every earlier position, sinks ignored); with a tree it is 0 or at least max_q.  A
+ * row that sees nothing is zeros.  Scale as for the decode.  Positions that no row of a sequence sees are
+ * not read, nor the table entries of blocks that hold no other position: they may be negative
+ * (blocks given back once they have left the window).  What the cache holds at a position that a row
+ * does not see never reaches that row's output.
+ * Device pointers: q, out bf16 [total_q, num_q_heads, D]; caches of one layer; block_tables int32
+ * [batch, max_blocks]; seq_lens int32 [batch]; cu_q int32 [batch + 1], ascending from 0.  total_q and max_q are the host's
+ * bounds of cu_q[batch] and of every P_b: rows of out from cu_q[batch] on stay as they were, a sequence without rows does
+ * nothing whatever its length, and one with P_b > max_q, P_b > seq_lens[b] or a length beyond its table sets
+ * PKV_DEVERR_SEQ_LEN and its rows are zeros (a cu_q outside 0 .. total_q: nothing is written for it).  A table
+ * entry outside the pool that is needed sets PKV_DEVERR_BLOCK_ID, and its positions count as not
+ * seen.  workspace: device memory, 256-byte aligned, of at least pkv_tree_workspace_bytes() bytes (0 for
+ * an invalid shape; the bytes depend on max_q and the heads, not on the lengths); its content before and after is unspecified, and
+ * calls sharing it must not overlap on the GPU.  The work is divided from the device's lengths
+ * alone, so that a captured graph serves any lengths; two launches; placement of the blocks changes no bit.  FP8 and
+ * INT4 pools take q to fp16 with a power of two per row and query head that keeps its largest element in range.
+ * Requires batch <= 4096, 1 <= max_q <= 256, num_q_heads a multiple of Hkv with group <= 16,
+ * max_blocks <= 2^26, batch * max_blocks * Hkv < 2^31. */
+size_t pkv_tree_workspace_bytes(const pkv_pool *pool, int32_t batch, int32_t num_q_heads, int32_t max_q);
+int pkv_paged_attention_tree(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
+                             const int32_t *block_tables, const int32_t *seq_lens, const int32_t *cu_q,
+                             const int64_t *tree_mask, int32_t batch, int32_t num_q_heads, int32_t max_blocks,
+                             int32_t total_q, int32_t max_q, float scale, int32_t window, int32_t sinks, void *out,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same with one row per sequence: decode with a sliding window.  The token at position seq_lens[b] - 1
+ * (row b of q and out, bf16 [batch, num_q_heads, D]) sees the last `window` positions, its own among them, and
+ * the first `sinks`.  A seq_len outside [1, max_blocks * block_size] sets PKV_DEVERR_SEQ_LEN and zeroes that
+ * sequence's output.  workspace as above with max_q = 1. */
+int pkv_paged_attention_window(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
+                               const int32_t *block_tables, const int32_t *seq_lens, int32_t batch,
+                               int32_t num_q_heads, int32_t max_blocks, float scale, int32_t window,
+                               int32_t sinks, void *out, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Host side of one decode step, for pkv_decode_step_host: host memory, page-locked (pinned)
  * for the copies to be asynchronous.  block_tables and seq_lens may be NULL when the device

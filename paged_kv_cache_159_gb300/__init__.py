@@ -25,6 +25,10 @@ Names follow the C ABI without the ``pkv_`` prefix:
 * ``Pool.cow_prepare`` and ``copy_blocks`` -- copy-on-write of shared blocks before an append.
 * ``block_hashes``, ``Pool.prefix_lookup / prefix_insert / prefix_evict / prefix_clear`` --
   automatic prefix caching on the host.
+* ``extend_tables`` -- block tables and slots of new rows on the GPU, from device lengths;
+  ``accept_rows`` -- the accepted rows of drafted tokens to where they belong.
+* ``paged_attention_tree`` -- attention of drafted tokens (a tree or a chain) over the cache;
+  ``paged_attention_window`` -- decode with a sliding window and sink tokens.
 * ``slot_mapping_chunks``, ``prefill_plan``, ``paged_prefill`` -- prefill and chunked
   prefill on the tcgen05 tensor cores (plan on the host once per batch, run per layer).
 * ``decode_step_host`` -- one decode step from pinned host memory (upload, one-launch step,
@@ -45,6 +49,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libpkv.so")
 OK, ERR_INVALID, ERR_OOM, ERR_DEVICE, ERR_TIMEOUT, ERR_CUDA = range(6)
 TEST_EXPIRE_NONE, TEST_EXPIRE_DECODE, TEST_EXPIRE_PREFILL = range(3)
 DEVERR_SLOT, DEVERR_BLOCK_ID, DEVERR_SEQ_LEN, DEVERR_TIMEOUT, DEVERR_PLAN = 0x1, 0x2, 0x4, 0x8, 0x10
+DEVERR_RESERVE, DEVERR_PATH = 0x20, 0x40
 KV_BF16, KV_FP8E4M3, KV_INT4 = 0, 1, 2
 BLOCK_SIZE = 16
 
@@ -62,7 +67,8 @@ EXPORTED = (
     "pkv_get_device_error", "pkv_test_expire_waits", "pkv_probe_copy",
     "pkv_device_sm_count", "pkv_status_string", "pkv_pool_tile_bytes", "pkv_kv_gather", "pkv_kv_gather_layers",
     "pkv_fork_tables", "pkv_pool_compact", "pkv_remap_tables", "pkv_move_blocks",
-    "pkv_prefill_workspace_bytes", "pkv_paged_prefill_ex",
+    "pkv_prefill_workspace_bytes", "pkv_paged_prefill_ex", "pkv_extend_tables", "pkv_accept_rows",
+    "pkv_tree_workspace_bytes", "pkv_paged_attention_tree", "pkv_paged_attention_window",
 )
 
 
@@ -149,6 +155,13 @@ def lib():
             "pkv_prefill_workspace_bytes": (ctypes.c_size_t, [_P, _P, _P, _I32, _I32]),
             "pkv_paged_prefill_ex": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, ctypes.c_float, _P,
                                                     _I32, _P, _P, ctypes.c_size_t, _P]),
+            "pkv_extend_tables": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P, _P]),
+            "pkv_accept_rows": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P]),
+            "pkv_tree_workspace_bytes": (ctypes.c_size_t, [_P, _I32, _I32, _I32]),
+            "pkv_paged_attention_tree": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32,
+                                                        ctypes.c_float, _I32, _I32, _P, _P, ctypes.c_size_t, _P]),
+            "pkv_paged_attention_window": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _I32, _I32, ctypes.c_float,
+                                                          _I32, _I32, _P, _P, ctypes.c_size_t, _P]),
             "pkv_paged_prefill": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32,
                                                  ctypes.c_float, _P, _I32, _P, _P]),
             "pkv_decode_step_host": (ctypes.c_int, [_P, ctypes.POINTER(host_step), ctypes.POINTER(device_step),
@@ -208,6 +221,11 @@ def _dev_ptr(t, what: str):
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
     return t.data_ptr()
+
+
+def _sized(t, n: int, what: str, size: int = 4):
+    if t.numel() != n or t.element_size() != size:
+        raise ValueError("%s must have %d entries of %d bytes" % (what, n, size))
 
 
 _current_raw_stream = None
@@ -522,6 +540,77 @@ def move_blocks(pool: Pool, key_cache, value_cache, src, dst, block_tables=None,
     _check(lib().pkv_move_blocks(pool.handle, _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
                                  _dev_ptr(src, "src"), _dev_ptr(dst, "dst"), int(src.numel()),
                                  _dev_ptr(block_tables, "block_tables"), entries, _stream_ptr(stream)), "move_blocks")
+
+
+def extend_tables(pool: Pool, seq_lens, cu_q, block_tables, reserve, state, new_lens, slots, positions=None, stream=None):
+    """Table entries and slots of every sequence's new rows (pkv_extend_tables), all int32 CUDA but
+    slots (int64 [T]): seq_lens, new_lens [B] (may be the same), cu_q [B + 1], block_tables [B, MB]
+    (in place), reserve (blocks from Pool.alloc), state [2] (zeros at first; state[0] counts the ids
+    used), positions [T] or None."""
+    B, MB = block_tables.shape
+    _sized(seq_lens, B, "seq_lens"), _sized(cu_q, B + 1, "cu_q"), _sized(new_lens, B, "new_lens"), _sized(state, 2, "state")
+    if positions is not None:
+        _sized(positions, slots.numel(), "positions")
+    _sized(block_tables, B * MB, "block_tables"), _sized(reserve, reserve.numel(), "reserve"), _sized(slots, slots.numel(), "slots", 8)
+    _check(lib().pkv_extend_tables(pool.handle, _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(cu_q, "cu_q"), B, MB,
+                                   slots.numel(), _dev_ptr(block_tables, "block_tables"), _dev_ptr(reserve, "reserve"),
+                                   reserve.numel(), _dev_ptr(state, "state"), _dev_ptr(new_lens, "new_lens"),
+                                   _dev_ptr(slots, "slots"), _dev_ptr(positions, "positions"), _stream_ptr(stream)),
+           "extend_tables")
+
+
+def accept_rows(pool: Pool, key_cache, value_cache, block_tables, seq_lens, cu_q, path, num_accepted, lens_out, stream=None):
+    """Move the rows of every sequence's accepted drafts to where they belong, in every layer
+    (pkv_accept_rows): int32 CUDA seq_lens (with the drafts), num_accepted, lens_out [B], cu_q
+    [B + 1], path [B, max_path]."""
+    B, MB = block_tables.shape
+    _sized(seq_lens, B, "seq_lens"), _sized(cu_q, B + 1, "cu_q"), _sized(num_accepted, B, "num_accepted"), _sized(lens_out, B, "lens_out")
+    _sized(path, B * path.shape[1], "path"), _sized(block_tables, B * MB, "block_tables")
+    _check(lib().pkv_accept_rows(pool.handle, _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
+                                 _dev_ptr(block_tables, "block_tables"), _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(cu_q, "cu_q"),
+                                 _dev_ptr(path, "path"), _dev_ptr(num_accepted, "num_accepted"), B, MB, path.shape[1],
+                                 _dev_ptr(lens_out, "lens_out"), _stream_ptr(stream)), "accept_rows")
+
+
+def tree_workspace_bytes(pool: Pool, batch: int, num_q_heads: int, max_q: int = 1) -> int:
+    """Device workspace bytes of paged_attention_tree (and, max_q 1, paged_attention_window)."""
+    return int(lib().pkv_tree_workspace_bytes(pool.handle, int(batch), int(num_q_heads), int(max_q)))
+
+
+def paged_attention_tree(pool: Pool, q, key_cache, value_cache, block_tables, seq_lens, cu_q, tree_mask, max_q: int,
+                         scale: float, out, workspace, window: int = 0, sinks: int = 0, stream=None):
+    """Attention of every sequence's last rows, drafted tokens in a tree or (tree_mask None) a chain
+    (pkv_paged_attention_tree).  q/out: bf16 CUDA [T, Hq, D]; seq_lens int32 CUDA [B] with the new
+    tokens; cu_q int32 CUDA [B + 1]; tree_mask int64 CUDA [T, ceil(max_q / 64)], bit j of a row: it sees
+    its sequence's new token j; workspace: CUDA uint8 of >= tree_workspace_bytes() bytes."""
+    T, Hq, _ = q.shape
+    B, MB = block_tables.shape
+    _sized(seq_lens, B, "seq_lens"), _sized(cu_q, B + 1, "cu_q"), _sized(out, q.numel(), "out", 2)
+    if tree_mask is not None:
+        _sized(tree_mask, T * ((int(max_q) + 63) // 64), "tree_mask", 8)
+    _check(lib().pkv_paged_attention_tree(pool.handle, _dev_ptr(q, "q"), _dev_ptr(key_cache, "key_cache"),
+                                          _dev_ptr(value_cache, "value_cache"), _dev_ptr(block_tables, "block_tables"),
+                                          _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(cu_q, "cu_q"), _dev_ptr(tree_mask, "tree_mask"),
+                                          B, Hq, MB, T, int(max_q), float(scale), int(window), int(sinks), _dev_ptr(out, "out"),
+                                          _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                          _stream_ptr(stream)), "paged_attention_tree")
+
+
+def paged_attention_window(pool: Pool, q, key_cache, value_cache, block_tables, seq_lens, scale: float, window: int,
+                           sinks: int, out, workspace, stream=None):
+    """Decode with a sliding window of the last `window` positions and the first `sinks`
+    (pkv_paged_attention_window): q/out bf16 CUDA [B, Hq, D]; workspace: CUDA uint8 of >=
+    tree_workspace_bytes(pool, B, Hq) bytes."""
+    B, Hq, _ = q.shape
+    _sized(seq_lens, B, "seq_lens"), _sized(out, q.numel(), "out", 2)
+    if block_tables.shape[0] != B:
+        raise ValueError("block_tables must have a row for each sequence")
+    _check(lib().pkv_paged_attention_window(pool.handle, _dev_ptr(q, "q"), _dev_ptr(key_cache, "key_cache"),
+                                            _dev_ptr(value_cache, "value_cache"), _dev_ptr(block_tables, "block_tables"),
+                                            _dev_ptr(seq_lens, "seq_lens"), B, Hq, block_tables.shape[1], float(scale),
+                                            int(window), int(sinks), _dev_ptr(out, "out"), _dev_ptr(workspace, "workspace"),
+                                            workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
+           "paged_attention_window")
 
 
 def _opts(opts):

@@ -25,6 +25,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "pkv_device.cuh"
 #include "tc_device.cuh"
@@ -72,6 +73,35 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
+}
+
+// (n - 8) * scale of the codes at bits 0-3 of each half of w, as a pair of bf16 (128 + n by an and-or,
+// then exact arithmetic) or of f16 (1024 + n).
+__device__ __forceinline__ uint32_t expand_pair(uint32_t w, __nv_bfloat162 scale)
+{
+    const uint32_t x = (w & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), __float2bfloat162_rn(136.f)), scale);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t expand_pair(uint32_t w, __half2 scale)
+{
+    const uint32_t x = (w & 0x000F000Fu) | 0x64006400u;
+    const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&x), __float2half2_rn(1032.f)), scale);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Octet of codes (column i at bits 4 i) to 8 elements, T their pair type.
+template <class T>
+__device__ __forceinline__ uint4 expand_octet(uint32_t codes, uint32_t scale_byte)
+{
+    T s;
+    if constexpr (std::is_same<T, __half2>::value) s = __float2half2_rn(scale_value(scale_byte));
+    else s = __float2bfloat162_rn(scale_value(scale_byte));
+    // halves hold columns 0-3 and 4-7: pairs (0, 4), (1, 5), (2, 6), (3, 7)
+    const uint32_t a = expand_pair(codes, s), b = expand_pair(codes >> 4, s), c = expand_pair(codes >> 8, s),
+                   d = expand_pair(codes >> 12, s);
+    return make_uint4(__byte_perm(a, b, 0x5410u), __byte_perm(c, d, 0x5410u), __byte_perm(a, b, 0x7632u),
+                      __byte_perm(c, d, 0x7632u));
 }
 
 // Quantise octets of rows (8 bf16 each; whole warps call it, the 4 consecutive lanes of a group

@@ -46,6 +46,9 @@ inline bool encode_tiled_3d(CUtensorMap *map, const void *ptr, CUtensorMapDataTy
 // Which kernel (PKV_TEST_EXPIRE_*) the failure-path test hook currently targets.
 int test_expire();
 
+// Most entries of a table row that the entry points for drafts and windows take: positions fit an int32.
+constexpr int MOST_TABLE_BLOCKS = 1 << 26;
+
 // Validation shared by the CUDA entry points.
 int check_attached(const pkv_pool *pool);
 inline int elem_bytes(const pkv_pool_desc &d) { return d.kv_dtype == PKV_KV_FP8E4M3 ? 1 : 2; }    // bf16, FP8 pools

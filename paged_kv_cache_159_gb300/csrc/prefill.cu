@@ -133,35 +133,6 @@ __device__ __forceinline__ bool expanded_ok(const uint8_t *expand, int batch, in
     return off[batch] <= capacity && off[batch + 1] == max_blocks;
 }
 
-// (n - 8) * scale of the codes at bits 0-3 of each half of w, as a pair of bf16 (128 + n by an and-or,
-// then exact arithmetic) or of f16 (1024 + n).
-__device__ __forceinline__ uint32_t expand_pair(uint32_t w, __nv_bfloat162 scale)
-{
-    const uint32_t x = (w & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), __float2bfloat162_rn(136.f)), scale);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-__device__ __forceinline__ uint32_t expand_pair(uint32_t w, __half2 scale)
-{
-    const uint32_t x = (w & 0x000F000Fu) | 0x64006400u;
-    const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&x), __float2half2_rn(1032.f)), scale);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-// Octet of codes (column i at bits 4 i) to 8 elements, T their pair type.
-template <class T>
-__device__ __forceinline__ uint4 expand_octet(uint32_t codes, uint32_t scale_byte)
-{
-    T s;
-    if constexpr (std::is_same<T, __half2>::value) s = __float2half2_rn(int4::scale_value(scale_byte));
-    else s = __float2bfloat162_rn(int4::scale_value(scale_byte));
-    // halves hold columns 0-3 and 4-7: pairs (0, 4), (1, 5), (2, 6), (3, 7)
-    const uint32_t a = expand_pair(codes, s), b = expand_pair(codes >> 4, s), c = expand_pair(codes >> 8, s),
-                   d = expand_pair(codes >> 12, s);
-    return make_uint4(__byte_perm(a, b, 0x5410u), __byte_perm(c, d, 0x5410u), __byte_perm(a, b, 0x7632u),
-                      __byte_perm(c, d, 0x7632u));
-}
-
 // A CTA per expanded block (a grid stride apart), a warp per KV head.  Lane (r, c) of a pass takes
 // stored row r of eight and one octet of every group in it: 4 NG consecutive bytes of K (the words of
 // octet c), 4 NG of V (the 16-bit words of two neighbouring columns' quads), and the row's scales.
@@ -218,9 +189,9 @@ __global__ void __launch_bounds__(EXPAND_THREADS) prefill_expand_kernel(const Ex
                 const int t = (r & 8) | ((r >> 1) & 3) | ((r & 1) << 2), oc = D == 128 ? c ^ (r & 2) : c;
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
-                    ko[t * OCTETS + 4 * j + c] = expand_octet<__nv_bfloat162>(kw[x][j], (ks[x] >> (8 * j)) & 0xffu);
+                    ko[t * OCTETS + 4 * j + c] = int4::expand_octet<__nv_bfloat162>(kw[x][j], (ks[x] >> (8 * j)) & 0xffu);
                     const uint32_t codes = __byte_perm(vw[x][j >> 1], vw[x][NG / 2 + (j >> 1)], (j & 1) ? 0x7632u : 0x5410u);
-                    vo[r * OCTETS + 4 * j + oc] = expand_octet<__half2>(codes, (vs[x][j] >> (8 * (r >> 2))) & 0xffu);
+                    vo[r * OCTETS + 4 * j + oc] = int4::expand_octet<__half2>(codes, (vs[x][j] >> (8 * (r >> 2))) & 0xffu);
                 }
             }
         }

@@ -1,0 +1,1026 @@
+// tree_attention.cu -- attention of a few new tokens per sequence over a paged cache: trees (or chains)
+// of drafted tokens, and single tokens with a sliding window and sink tokens.
+//
+// What is computed ("传统 Attention 的 KV Cache 问题" (pyllm.pages.dev) §1.1; the mask: "理解 KV Cache"
+// (steinslab.io) §1.2's M, a row of it per drafted token).  The last P of a sequence's L positions are new,
+// C = L - P cached.  Row i's output is sum_j softmax_j(scale q_i . k_j) v_j over the positions j that it sees:
+//   chain (no mask):  j <= p and (j > p - window or j < sinks), p = C + i;
+//   tree:             new position C + j where bit j of the row's mask is set, and cached j < C with
+//                     j > p - window or j < sinks, p = C + (bits set) - 1: the row's place behind its ancestors.
+// A row that sees nothing is zeros.
+//
+// Schedule.  A unit is (sequence, KV head, up to MR rows): rows are (token, head of the group) pairs, MR = 16,
+// 32, 64 or 128 by the most rows that a sequence may have.  A unit's visible blocks (those of the sinks, then
+// from the window's first on) make tiles of 64 keys, and the tiles of all units, laid end to end, are cut
+// evenly over a one-wave grid.  Every CTA finds its share from the device's lengths.  A unit in one CTA is
+// written there; a cut one leaves a partial (max, sum, output) per CTA, which a second launch merges in order:
+// the placement of blocks changes no bit.
+//
+// A CTA: one warp copies (a tensor copy per bf16 block of K and V, 128-byte swizzle; a bulk copy per FP8 or
+// INT4 block) into a ring of tiles, WR x WK warps multiply (mma.sync m16n8k16, queries as the 16 rows): WR
+// groups of 16 rows, the tile's keys divided over WK warps, whose states meet at a unit's end.  FP8 and INT4
+// tiles are expanded to f16 once a CTA (exactly), q goes to f16 with a power of two per row, P is f16 times 2^8.
+//
+// Masked places.  Scores are masked by select.  A V element that no row of the warp sees is taken as zero (a
+// register mask), since 0 x NaN is NaN; where some rows see a position and others do not, and its V is not
+// finite, its products leave the tensor core and are added row by row.
+//
+// Both launches may start while the one before drains (programmatic dependent launch): they wait before they
+// read, and load coherently.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <cmath>
+
+#include "int4.cuh"
+#include "pkv_internal.h"
+#include "tc_device.cuh"
+
+namespace pkv {
+namespace tree {
+
+constexpr int BS = 16;                 // tokens per block
+constexpr int TB = 4;                  // blocks per tile
+constexpr int MOST_BATCH = 4096;
+constexpr int MOST_NEW = 256;          // new tokens per sequence
+constexpr float LOG2E = 1.4426950408889634f;
+enum { BF16 = 0, FP8 = 1, INT4 = 2 };
+
+struct Params {
+    const uint16_t *q;
+    const uint8_t *key_cache, *value_cache;
+    const int32_t *tables, *lens, *cu;     // cu null: one row per sequence
+    const unsigned long long *mask;        // [total_q][words], or null
+    uint16_t *out;
+    float *part_o, *part_ml;               // [grid][2][MR][D], [grid][2][MR][2]
+    int32_t *meta;                         // [grid][META]: the cut unit that begins in a CTA
+    uint32_t *err;
+    int B, MB, Hq, Hkv, group, num_blocks, total_q, max_q, words, window, sinks, test_stall;
+    float score_scale, out_scale;
+};
+
+constexpr int META = 8;                    // rows (0: none), last CTA, first slot, first row of q, KV head, row tile
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// A sequence: its lengths, its visible blocks (list entry v is block v < sb ? v : v - sb + b1) and its tasks.
+struct Seq {
+    int L, P, C, row0;
+    int sb, b1, nvb;               // blocks of the sinks, first block of the window, entries of the list
+    int nt, rt;                    // tiles and row tiles of a unit (0: nothing to do)
+    int bad;                       // 1: flagged, its rows are zeros; 2: flagged, it has no rows to write
+};
+
+template <int MR>
+__device__ __forceinline__ Seq seq_at(const Params &p, int b)
+{
+    Seq s;
+    s.L = __ldcg(p.lens + b);
+    s.row0 = b;
+    int end = b + 1;
+    if (p.cu) {
+        s.row0 = __ldcg(p.cu + b);
+        end = __ldcg(p.cu + b + 1);
+    }
+    s.nt = s.rt = s.bad = s.sb = s.b1 = s.nvb = 0;
+    s.P = s.C = 0;
+    if (s.row0 < 0 || end < s.row0 || end > p.total_q) {
+        s.bad = 2;
+        return s;
+    }
+    s.P = end - s.row0;
+    if (s.P == 0) return s;
+    if (s.P > p.max_q || s.L < s.P || s.L > p.MB * BS) {
+        s.bad = 1;
+        return s;
+    }
+    s.C = s.L - s.P;
+    const int blocks = (s.L + BS - 1) / BS;
+    if (p.window) {
+        // a tree's row without a bit stands at C - 1
+        const int lo = max(0, s.C - p.window + (p.mask ? 0 : 1));
+        s.sb = min(blocks, (p.sinks + BS - 1) / BS);
+        s.b1 = max(lo / BS, s.sb);
+    }
+    s.nvb = s.sb + max(0, blocks - s.b1);
+    s.nt = (s.nvb + TB - 1) / TB;
+    s.rt = (s.P * p.group + MR - 1) / MR;
+    return s;
+}
+
+__device__ __forceinline__ long long tasks_of(const Seq &s, int Hkv) { return (long long)s.nt * s.rt * Hkv; }
+
+// The even split of W tasks over G CTAs.
+__device__ __forceinline__ long long share(long long W, int G, int c) { return W * c / G; }
+
+template <int D, int KIND, int WR, int WK>
+struct Shape {
+    static constexpr int NC = WR * WK, NT = NC * 32 + 32, MR = 16 * WR;
+    static constexpr int CTAS = NC > 4 ? 1 : 2;                    // per SM
+    static constexpr int BT = BS * D * 2;                          // a block of K or V in 16 bits
+    static constexpr int TILE = KIND == BF16 ? BT : KIND == FP8 ? BS * D : int4::tile_bytes(D);      // as stored
+    static constexpr int STAGE = 2 * TB * TILE;
+    // 16-bit tiles that FP8 and INT4 are expanded to: one where every warp expands its own keys, else two
+    static constexpr int WIDE = 2 * TB * BT;
+    static constexpr int NWIDE = KIND == BF16 ? 0 : WK == TB ? 1 : 2;
+    static constexpr int ROOM = (CTAS == 1 ? 220 : 110) * 1024;
+    static constexpr int NS_ = (ROOM - NWIDE * WIDE) / STAGE;
+    static constexpr int NS = NS_ > 8 ? 8 : NS_;
+    static constexpr int RING = NWIDE * WIDE;                      // (STAGE of a quantised pool is a multiple of 128)
+    static constexpr int ML = RING + NS * STAGE;                   // (max, sum) of the key warps' rows
+    static constexpr int INFO = ML + NC * 16 * 8;                  // loaded blocks of every stage
+    static constexpr int BAR = INFO + 64;
+    static constexpr int ALLOC = BAR + 8 * (2 * NS + 2) + 1024;    // + alignment slack
+    static_assert(NS >= 2 && (CTAS == 1 ? ALLOC <= 227 * 1024 : ALLOC <= 113 * 1024), "shared memory");
+    static_assert(TB % WK == 0 && STAGE % 128 == 0, "");
+};
+
+// Expand one block (16 tokens) of K or V to f16 in the swizzled layout, by a warp.
+template <int D, int KIND>
+__device__ __forceinline__ void widen(const uint8_t *src, uint8_t *dst, bool isk, int lane)
+{
+    auto at = [&](int row, int chunk) {
+        return reinterpret_cast<uint4 *>(dst + (chunk >> 3) * (BS * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+    };
+    if constexpr (KIND == FP8) {
+        constexpr int PR = D / 16;                                 // 16-byte pieces of a row
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const int e = i * 32 + lane, row = e / PR, cc = e % PR;
+            const uint4 x = *reinterpret_cast<const uint4 *>(src + e * 16);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                h[2 * k] = dev::e4m3x2_to_f16x2((uint16_t)w[k]);
+                h[2 * k + 1] = dev::e4m3x2_to_f16x2((uint16_t)(w[k] >> 16));
+            }
+            // (lanes of the upper 64 columns store their second half first: no bank conflict)
+            const bool odd = cc >= 4;
+            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+            *at(row, 2 * cc + (odd ? 1 : 0)) = odd ? hi : lo;
+            *at(row, 2 * cc + (odd ? 0 : 1)) = odd ? lo : hi;
+        }
+    } else if constexpr (KIND == INT4) {
+        constexpr int NG = D / 32;
+        const int c = lane & 3;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = 8 * x + (lane >> 2);
+            const int t = isk ? (r & 8) | ((r >> 1) & 3) | ((r & 1) << 2) : r, oc = !isk && D == 128 ? c ^ (r & 2) : c;
+            uint32_t w[NG], sb = 0, vs[NG];
+            const uint8_t *row = src + r * (D / 2) + c * (4 * NG);
+            if constexpr (NG == 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(row);
+                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2 *>(row);
+                w[0] = v.x; w[1] = v.y;
+            }
+            if (isk) {
+                if constexpr (NG == 4) sb = *reinterpret_cast<const uint32_t *>(src + 8 * D + r * NG);
+                else sb = *reinterpret_cast<const uint16_t *>(src + 8 * D + r * NG);
+            } else {
+#pragma unroll
+                for (int j = 0; j < NG; ++j) vs[j] = *reinterpret_cast<const uint32_t *>(src + 8 * D + (r & 3) * (4 * NG) + 4 * j);
+            }
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const uint32_t codes = isk ? w[j] : __byte_perm(w[j >> 1], w[NG / 2 + (j >> 1)], (j & 1) ? 0x7632u : 0x5410u);
+                const uint32_t scale = isk ? (sb >> (8 * j)) & 0xffu : (vs[j] >> (8 * (r >> 2))) & 0xffu;
+                *at(t, 4 * j + oc) = int4::expand_octet<__half2>(codes, scale);
+            }
+        }
+    }
+}
+
+template <int D, int KIND, int WR, int WK>
+__global__ void __launch_bounds__(Shape<D, KIND, WR, WK>::NT, Shape<D, KIND, WR, WK>::CTAS)
+tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Params p)
+{
+    using S = Shape<D, KIND, WR, WK>;
+    constexpr int NC = S::NC, MR = S::MR, NS = S::NS, BT = S::BT, NB = TB / WK, KS = D / 16, NN = D / 8;
+    constexpr float SHIFT = KIND == BF16 ? 0.f : 8.f;              // P is held as P 2^SHIFT
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ long long wsum[NC + 1], found[2];
+    __shared__ int found_b;
+    uint8_t *sm = smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t base = dev::smem_u32(sm);
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(dev::FULL, tid >> 5, 0);
+    auto full = [&](int s) { return base + S::BAR + 8 * s; };
+    auto empty = [&](int s) { return base + S::BAR + 8 * (NS + s); };
+    const uint32_t meet = base + S::BAR + 8 * (2 * NS), never = meet + 8;
+    int32_t *info = reinterpret_cast<int32_t *>(sm + S::INFO);
+    if (tid == 0) {
+        for (int s = 0; s < NS; ++s) {
+            dev::mbar_init(full(s), 1);
+            dev::mbar_init(empty(s), NC);
+        }
+        dev::mbar_init(meet, NC);
+        dev::mbar_init(never, 1);
+        dev::fence_barrier_init();
+    }
+    pdl_launch();
+    pdl_wait();
+
+    // ---- every CTA's share of the tasks, from the lengths: a thread sums some sequences, the block scans
+    long long first, last, W;
+    Seq sq;
+    int b, G;                                                      // CTAs with work
+    long long U0;                                                  // first task of sequence b
+    {
+        const int per = (p.B + S::NT - 1) / S::NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+        long long run = 0;
+        int bad = 0;
+        for (int x = b0; x < b1; ++x) {
+            const Seq s = seq_at<MR>(p, x);
+            bad |= s.bad;
+            run += tasks_of(s, p.Hkv);
+        }
+        long long incl = run;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(dev::FULL, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) wsum[warp] = incl;
+        const int any_bad = __syncthreads_or(bad);
+        long long at = incl - run;
+        W = 0;
+#pragma unroll
+        for (int w = 0; w < NC + 1; ++w) {
+            if (w < warp) at += wsum[w];
+            W += wsum[w];
+        }
+        G = (int)min((long long)gridDim.x, max(W, 1ll));           // (so that every CTA up to it has a task)
+        first = (int)blockIdx.x < G ? share(W, G, blockIdx.x) : W;
+        last = (int)blockIdx.x < G ? share(W, G, blockIdx.x + 1) : W;
+        if (first >= at && first < at + run) {
+            for (int x = b0; x < b1; ++x) {
+                const long long n = tasks_of(seq_at<MR>(p, x), p.Hkv);
+                if (first < at + n) {
+                    found_b = x;
+                    found[0] = at;
+                    break;
+                }
+                at += n;
+            }
+        }
+        __syncthreads();
+        if (any_bad) {
+            if (tid == 0 && blockIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_SEQ_LEN);
+            for (int x = blockIdx.x; x < p.B; x += gridDim.x) {
+                const Seq s = seq_at<MR>(p, x);
+                uint4 *dst = reinterpret_cast<uint4 *>(p.out + (size_t)s.row0 * p.Hq * D);
+                if (s.bad == 1)
+                    for (size_t e = tid; e < (size_t)s.P * p.Hq * (D / 8); e += S::NT) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        if (tid < META && first >= last) p.meta[(size_t)blockIdx.x * META + tid] = 0;
+        if (first >= last) return;
+        b = found_b;
+        U0 = found[0];
+        sq = seq_at<MR>(p, b);
+    }
+
+    // The segment (run of tiles t0 .. t1 - 1 of one unit) that holds task r; b, sq and U0 move on with it.
+    struct Segment { int h, m, t0, t1; };
+    auto segment_at = [&](long long r) {
+        while (b + 1 < p.B && r >= U0 + tasks_of(sq, p.Hkv)) {
+            U0 += tasks_of(sq, p.Hkv);
+            sq = seq_at<MR>(p, ++b);
+        }
+        const long long rel = r - U0;
+        const int unit = (int)(rel / max(sq.nt, 1));
+        Segment g;
+        g.t0 = (int)(rel - (long long)unit * sq.nt);
+        g.h = unit / max(sq.rt, 1);
+        g.m = unit - g.h * sq.rt;
+        g.t1 = (int)min((long long)sq.nt, g.t0 + (last - r));
+        return g;
+    };
+
+    if (warp == NC) {
+        // ============ the copying warp: lane k < TB takes block k of a tile, K and V
+        int n = 0;                                                 // tiles issued
+        bool ok = true;
+        if (lane == 0) {
+            if constexpr (KIND == BF16) {
+                tc::prefetch_tensormap(&kmap);
+                tc::prefetch_tensormap(&vmap);
+            }
+        }
+        // the table's entries, a tile ahead of their copies
+        long long r = first;
+        Segment g = segment_at(r);
+        int t = g.t0;
+        auto entry = [&]() {
+            const int v = TB * t + lane;
+            if (lane >= TB || v >= sq.nvb) return -2;
+            const int blk = v < sq.sb ? v : v - sq.sb + sq.b1;
+            return __ldcg(p.tables + (size_t)b * p.MB + blk);
+        };
+        int id = entry();
+        while (true) {
+            const int h = g.h, cur = id;
+            ++r;
+            if (r < last) {
+                if (++t == g.t1) {
+                    g = segment_at(r);
+                    t = g.t0;
+                }
+                id = entry();
+            }
+            const int s = n % NS;
+            if (n >= NS) {
+                ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(empty(s), (uint32_t)(((n - NS) / NS) & 1)));
+                if (!ok) break;
+            }
+            const bool want = cur != -2, good = cur >= 0 && cur < p.num_blocks;
+            if (want && !good) dev::flag_error(p.err, PKV_DEVERR_BLOCK_ID);
+            const unsigned got = __ballot_sync(dev::FULL, good);
+            if (lane == 0) {
+                info[s] = (int)got;
+                dev::mbar_arrive_expect_tx(full(s), (uint32_t)(2 * S::TILE * __popc(got)));
+            }
+            __syncwarp();
+            if (good) {
+                const uint32_t dk = base + S::RING + s * S::STAGE + lane * S::TILE, dv = dk + TB * S::TILE;
+                const int tile = cur * p.Hkv + h;
+                if constexpr (KIND != BF16) {
+                    dev::bulk_g2s(dk, p.key_cache + (size_t)tile * S::TILE, S::TILE, full(s));
+                    dev::bulk_g2s(dv, p.value_cache + (size_t)tile * S::TILE, S::TILE, full(s));
+                } else if constexpr (D == 128) {
+                    tc::tma_load_4d(dk, &kmap, 0, 0, 0, tile, full(s));
+                    tc::tma_load_4d(dv, &vmap, 0, 0, 0, tile, full(s));
+                } else {
+                    tc::tma_load_3d(dk, &kmap, 0, 0, tile, full(s));
+                    tc::tma_load_3d(dv, &vmap, 0, 0, tile, full(s));
+                }
+            }
+            ++n;
+            if (r >= last) break;
+        }
+        if (!ok && lane == 0) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
+        // no copy may land after the CTA has left: wait (bounded) for the last one of every stage
+        for (int x = max(0, n - NS); x < n; ++x) (void)dev::mbar_wait_bounded(full(x % NS), (uint32_t)((x / NS) & 1));
+        return;
+    }
+
+    // ============ the multiplying warps: rows 16 wr .. of the unit, blocks NB wk .. of every tile
+    const int wr = warp / WK, wk = warp % WK, gid = lane >> 2, t4 = lane & 3;
+    uint32_t meet_phase = 0;
+    bool ok = true;
+    auto sync_warps = [&]() {                                      // all multiplying warps, bounded
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(meet);
+        ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(meet, meet_phase));
+        meet_phase ^= 1u;
+        return ok;
+    };
+    if (p.test_stall) ok = __all_sync(dev::FULL, dev::mbar_wait_bounded_ns(never, 0, dev::TEST_EXPIRE_NS));
+    int n = 0;                                                     // tiles seen
+    bool cut_begins = false;
+    int cut[META] = {};
+    for (long long r = first; ok && r < last;) {
+        const Segment g = segment_at(r);
+        const int rows = sq.P * p.group - g.m * MR;                // of this unit, at most MR of them here
+        // this lane's two rows
+        int place[2], draft[2];                                    // p of the row; its token
+        bool live[2];
+        const unsigned long long *bits[2];
+        uint32_t qa[KS][4];
+        float sc[2] = {p.score_scale, p.score_scale};
+        size_t qrow[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int x = 16 * wr + gid + 8 * e;
+            live[e] = x < rows;
+            const int y = g.m * MR + (live[e] ? x : 0), i = y / p.group, hh = y - i * p.group;
+            draft[e] = i;
+            qrow[e] = ((size_t)(sq.row0 + i) * p.Hq + (size_t)g.h * p.group + hh) * D;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + qrow[e]);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                qa[k][e] = live[e] ? __ldcg(src + 8 * k + t4) : 0u;
+                qa[k][e + 2] = live[e] ? __ldcg(src + 8 * k + t4 + 4) : 0u;
+            }
+            bits[e] = p.mask ? p.mask + (size_t)(sq.row0 + i) * p.words : nullptr;
+            place[e] = sq.C + i;
+            if (p.mask) {
+                int c = 0;
+                for (int w = 0; w < p.words; ++w) {
+                    const int left = sq.P - 64 * w;
+                    if (left > 0) c += __popcll(__ldcg(bits[e] + w) & (left >= 64 ? ~0ull : (1ull << left) - 1));
+                }
+                place[e] = sq.C + c - 1;
+            }
+        }
+        if constexpr (KIND != BF16) {
+            // q to f16: a power of two per row brings its largest element into [2^14, 2^15), exact for elements
+            // of 2^-24 of it and more; a row with an infinity or NaN gets NaN scores
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const uint32_t m2 = __vmaxu2(qa[k][e] & 0x7fff7fffu, qa[k][e + 2] & 0x7fff7fffu);
+                    top = max(top, max(m2 & 0xffffu, m2 >> 16));
+                }
+                top = max(top, __shfl_xor_sync(dev::FULL, top, 1));
+                top = max(top, __shfl_xor_sync(dev::FULL, top, 2));
+                const int ex = (int)(top >> 7), up = ex == 255 || top == 0 ? 0 : min(126, 141 - max(ex, 1));
+                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+                sc[e] = ex == 255 ? __int_as_float(0x7fffffff) : sc[e] * __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int x = e; x < 4; x += 2) qa[k][x] = dev::pack_f16x2(dev::bf16_lo(qa[k][x]) * f, dev::bf16_hi(qa[k][x]) * f);
+            }
+        }
+        float acc[NN][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < NN; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[x][e] = 0.f;
+        // positions up to which, and from which on, all rows of the unit see the cache
+        const int i0 = g.m * MR / p.group, i1 = min(sq.P - 1, (g.m * MR + min(rows, MR) - 1) / p.group);
+        const int all_to = p.mask ? sq.C : sq.C + i0 + 1;
+        const int all_from = p.window ? sq.C + (p.mask ? sq.P - 1 : i1) - p.window + 1 : INT_MIN;
+
+        for (int t = g.t0; t < g.t1; ++t, ++n) {
+            const int s = n % NS;
+            ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(full(s), (uint32_t)((n / NS) & 1)));
+            if (!ok) break;
+            const unsigned got = (unsigned)info[s];
+            const uint8_t *stage = sm + S::RING + s * S::STAGE;
+            uint32_t kt = base + S::RING + s * S::STAGE;           // the tile in 16 bits: TB blocks of K, TB of V
+            const bool at_end = t == g.t1 - 1;
+            if constexpr (KIND != BF16) {
+                uint8_t *wide = sm + (S::NWIDE == 2 ? (n & 1) * S::WIDE : 0);
+                kt = base + (S::NWIDE == 2 ? (n & 1) * S::WIDE : 0);
+#pragma unroll
+                for (int x = warp; x < 2 * TB; x += NC) {          // (block x % TB, K or V)
+                    const int k = x % TB;
+                    if ((got >> k) & 1u) widen<D, KIND>(stage + x * S::TILE, wide + x * BT, x < TB, lane);
+                }
+                __syncwarp();
+                if (lane == 0) dev::mbar_arrive(empty(s));
+                if (WK != TB && !sync_warps()) break;
+            }
+            const uint32_t vt = kt + TB * BT;
+            int pos[NB];                                           // first position of each of this warp's blocks
+            bool edge = false;
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const int v = TB * t + wk * NB + k, blk = v < sq.sb ? v : v - sq.sb + sq.b1;
+                pos[k] = blk * BS;
+                edge |= !((got >> (wk * NB + k)) & 1u) || pos[k] + BS > all_to || (pos[k] < all_from && pos[k] + BS > p.sinks);
+            }
+            // ---- S = Q K^T
+            float x[2 * NB][4];
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const uint32_t kb = kt + (wk * NB + k) * BT;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[2 * k][e] = x[2 * k + 1][e] = 0.f;
+                const int row = ((lane >> 4) & 1) * 8 + (lane & 7);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const int chunk = 2 * ks + ((lane >> 3) & 1);
+                    uint32_t f[4];
+                    dev::ldsm_x4(kb + (chunk >> 3) * (BS * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), f);
+                    if constexpr (KIND == BF16) {
+                        dev::mma_bf16_16816(x[2 * k], qa[ks], f[0], f[1]);
+                        dev::mma_bf16_16816(x[2 * k + 1], qa[ks], f[2], f[3]);
+                    } else {
+                        dev::mma_f16_16816(x[2 * k], qa[ks], f[0], f[1]);
+                        dev::mma_f16_16816(x[2 * k + 1], qa[ks], f[2], f[3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2 * NB; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[k][e] *= sc[e >> 1];
+            // ---- the mask of each 16 keys: bit j of see[k], row gid in the lower half, gid + 8 in the upper
+            uint32_t see[NB];
+            if (edge) {
+#pragma unroll
+                for (int k = 0; k < NB; ++k) {
+                    see[k] = 0;
+                    const int p0 = pos[k];
+                    auto ones = [](int c) { return (1u << min(max(c, 0), BS)) - 1u; };
+                    const uint32_t valid = (got >> (wk * NB + k)) & 1u ? ones(sq.L - p0) : 0u;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t c = valid & ones((p.mask ? sq.C : sq.C + draft[e] + 1) - p0), d = 0;
+                        if (p.mask && p0 + BS > sq.C) {
+                            const int off = p0 - sq.C;             // bit of the block's first position
+                            unsigned long long w;
+                            if (off < 0) {
+                                w = __ldcg(bits[e]) << -off;
+                            } else {
+                                const int i = off >> 6, sh = off & 63;
+                                w = i < p.words ? __ldcg(bits[e] + i) >> sh : 0ull;
+                                if (sh && i + 1 < p.words) w |= __ldcg(bits[e] + i + 1) << (64 - sh);
+                            }
+                            d = (uint32_t)w & valid & ~ones(sq.C - p0);
+                        }
+                        if (p.window) c &= ~ones(place[e] - p.window + 1 - p0) | ones(p.sinks - p0);
+                        if (live[e]) see[k] |= (c | d) << (16 * e);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (!((see[k] >> (8 * j + 2 * t4 + (e & 1) + 16 * (e >> 1))) & 1u)) x[2 * k + j][e] = -INFINITY;
+                }
+            }
+            // ---- running maximum and sum, P
+            float top[2] = {m[0], m[1]};
+#pragma unroll
+            for (int k = 0; k < 2 * NB; ++k) {
+                top[0] = tc::fmax3(top[0], x[k][0], x[k][1]);
+                top[1] = tc::fmax3(top[1], x[k][2], x[k][3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[e] = fmaxf(top[e], __shfl_xor_sync(dev::FULL, top[e], 1));
+                top[e] = fmaxf(top[e], __shfl_xor_sync(dev::FULL, top[e], 2));
+            }
+            if (__any_sync(dev::FULL, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float f = top[e] > m[e] ? dev::fast_exp2(m[e] - top[e]) : 1.f;
+                    m[e] = top[e];
+                    l[e] *= f;
+#pragma unroll
+                    for (int c = 0; c < NN; ++c) {
+                        acc[c][2 * e] *= f;
+                        acc[c][2 * e + 1] *= f;
+                    }
+                }
+            }
+            const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] - SHIFT, m[1] == -INFINITY ? 0.f : m[1] - SHIFT};
+#pragma unroll
+            for (int k = 0; k < 2 * NB; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[k][e] = dev::fast_exp2(x[k][e] - ref[e >> 1]);
+                    l[e >> 1] += x[k][e];
+                }
+            // ---- O += P V
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                auto pack = [&](float lo, float hi) { return KIND == BF16 ? dev::pack_bf16x2(lo, hi) : dev::pack_f16x2(lo, hi); };
+                const uint32_t pa[4] = {pack(x[2 * k][0], x[2 * k][1]), pack(x[2 * k][2], x[2 * k][3]),
+                                        pack(x[2 * k + 1][0], x[2 * k + 1][1]), pack(x[2 * k + 1][2], x[2 * k + 1][3])};
+                const int row = ((lane >> 3) & 1) * 8 + (lane & 7);
+                const uint32_t vb = vt + (wk * NB + k) * BT;
+                auto load_v = [&](int dd, uint32_t (&f)[4]) {      // 16 columns from 16 dd on
+                    const int chunk = 2 * dd + (lane >> 4);
+                    dev::ldsm_x4_trans(vb + (chunk >> 3) * (BS * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), f);
+                };
+                auto mma = [&](float (&d)[4], uint32_t b0, uint32_t b1) {
+                    if constexpr (KIND == BF16) dev::mma_bf16_16816(d, pa, b0, b1);
+                    else dev::mma_f16_16816(d, pa, b0, b1);
+                };
+                if (!edge) {
+#pragma unroll
+                    for (int dd = 0; dd < NN / 2; ++dd) {
+                        uint32_t f[4];
+                        load_v(dd, f);
+                        mma(acc[2 * dd], f[0], f[1]);
+                        mma(acc[2 * dd + 1], f[2], f[3]);
+                    }
+                    continue;
+                }
+                // V only where a row sees it (a padding row sees nothing, and hides nothing)
+                const uint32_t any2 = __reduce_or_sync(dev::FULL, see[k]);
+                const uint32_t all2 = __reduce_and_sync(dev::FULL, (live[0] ? see[k] : see[k] | 0xffffu) | (live[1] ? 0u : 0xffff0000u));
+                const uint32_t any = (any2 | any2 >> 16) & 0xffffu, all = all2 & (all2 >> 16) & 0xffffu;
+                uint32_t keep = any;
+                if (any & ~all) {
+                    // positions that some rows do not see: those whose V is not finite go row by row
+                    constexpr uint32_t EXP = KIND == BF16 ? 0x7f80u : 0x7c00u;
+                    uint32_t odd = 0;                              // this lane's four keys: 2 t4, + 1, + 8, + 9
+#pragma unroll 1
+                    for (int dd = 0; dd < NN / 2; ++dd) {
+                        uint32_t f[4];
+                        load_v(dd, f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if ((f[e] & EXP) == EXP) odd |= 1u << (2 * t4 + 8 * (e & 1));
+                            if (((f[e] >> 16) & EXP) == EXP) odd |= 2u << (2 * t4 + 8 * (e & 1));
+                        }
+                    }
+                    odd = __reduce_or_sync(dev::FULL, odd) & any & ~all;
+                    keep &= ~odd;
+                    while (odd) {
+                        const int j = __ffs(odd) - 1, from = (lane & ~3) | ((j & 7) >> 1);
+                        odd &= odd - 1;
+                        float pj[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float c = j & 8 ? (j & 1 ? x[2 * k + 1][2 * e + 1] : x[2 * k + 1][2 * e])
+                                                  : (j & 1 ? x[2 * k][2 * e + 1] : x[2 * k][2 * e]);
+                            pj[e] = __shfl_sync(dev::FULL, c, from);
+                        }
+#pragma unroll
+                        for (int c = 0; c < NN; ++c) {
+                            uint32_t w;
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(vb + (c >> 3) * (BS * 128) + j * 128 + (((c & 7) ^ (j & 7)) << 4) + t4 * 4));
+                            float2 v;
+                            if constexpr (KIND == BF16) v = make_float2(dev::bf16_lo(w), dev::bf16_hi(w));
+                            else v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if ((see[k] >> (j + 16 * e)) & 1u) {
+                                    acc[c][2 * e] = fmaf(pj[e], v.x, acc[c][2 * e]);
+                                    acc[c][2 * e + 1] = fmaf(pj[e], v.y, acc[c][2 * e + 1]);
+                                }
+                        }
+                    }
+                }
+                auto halves = [&](int j) { return ((keep >> j) & 1u ? 0xffffu : 0u) | ((keep >> (j + 1)) & 1u ? 0xffff0000u : 0u); };
+                const uint32_t k0 = halves(2 * t4), k1 = halves(2 * t4 + 8);
+#pragma unroll
+                for (int dd = 0; dd < NN / 2; ++dd) {
+                    uint32_t f[4];
+                    load_v(dd, f);
+                    mma(acc[2 * dd], f[0] & k0, f[1] & k1);
+                    mma(acc[2 * dd + 1], f[2] & k0, f[3] & k1);
+                }
+            }
+            // (the last tile of a segment keeps its stage for the key warps' states)
+            if (KIND == BF16 && (WK == 1 || !at_end)) {
+                __syncwarp();
+                if (lane == 0) dev::mbar_arrive(empty(s));
+            }
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(dev::FULL, l[e], 1);
+            l[e] += __shfl_xor_sync(dev::FULL, l[e], 2);
+        }
+        // ---- the key warps' states: each joins all of them for its share of the columns
+        constexpr int NS4 = NN / WK;                               // 8-column groups of a warp's share
+        float o[NS4][4];
+        if constexpr (WK > 1) {
+            const int s = (n - 1) % NS;
+            uint8_t *buf = KIND == BF16 ? sm + S::RING + s * S::STAGE : sm + (S::NWIDE == 2 ? ((n - 1) & 1) * S::WIDE : 0);
+            float4 *all = reinterpret_cast<float4 *>(buf);         // [warp][NN][32]
+            float2 *ml = reinterpret_cast<float2 *>(sm + S::ML);   // [warp][16]
+            if (!sync_warps()) break;                              // the tile is read
+#pragma unroll
+            for (int c = 0; c < NN; ++c)
+                if (c / NS4 != wk) all[(warp * NN + c) * 32 + lane] = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
+            if (t4 == 0) {
+                ml[warp * 16 + gid] = make_float2(m[0], l[0]);
+                ml[warp * 16 + gid + 8] = make_float2(m[1], l[1]);
+            }
+            if (!sync_warps()) break;
+            float2 st[WK][2];
+            float M[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int w = 0; w < WK; ++w)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    st[w][e] = ml[(wr * WK + w) * 16 + gid + 8 * e];
+                    M[e] = fmaxf(M[e], st[w][e].x);
+                }
+#pragma unroll
+            for (int c = 0; c < NS4; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+            l[0] = l[1] = 0.f;
+#pragma unroll
+            for (int w = 0; w < WK; ++w) {
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f[e] = M[e] == -INFINITY ? 1.f : dev::fast_exp2(st[w][e].x - M[e]);
+                    l[e] = fmaf(st[w][e].y, f[e], l[e]);
+                }
+#pragma unroll
+                for (int c = 0; c < NS4; ++c) {
+                    float4 v;
+                    if (w == wk) {
+#pragma unroll
+                        for (int x = 0; x < WK; ++x)               // (a constant index)
+                            if (x == wk) v = make_float4(acc[x * NS4 + c][0], acc[x * NS4 + c][1], acc[x * NS4 + c][2], acc[x * NS4 + c][3]);
+                    } else {
+                        v = all[((wr * WK + w) * NN + wk * NS4 + c) * 32 + lane];
+                    }
+                    o[c][0] = fmaf(v.x, f[0], o[c][0]);
+                    o[c][1] = fmaf(v.y, f[0], o[c][1]);
+                    o[c][2] = fmaf(v.z, f[1], o[c][2]);
+                    o[c][3] = fmaf(v.w, f[1], o[c][3]);
+                }
+            }
+            m[0] = M[0];
+            m[1] = M[1];
+            if constexpr (KIND == BF16) {
+                dev::fence_proxy_async_smem();                     // these accesses before the next copy into the stage
+                __syncwarp();
+                if (lane == 0) dev::mbar_arrive(empty(s));
+            } else if (!sync_warps()) {                            // the buffer is read
+                break;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < NN; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[c][e] = acc[c][e];
+        }
+        const int c0 = wk * NS4;
+        if (g.t0 == 0 && g.t1 == sq.nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (!live[e]) continue;
+                const float inv = l[e] == 0.f ? 0.f : p.out_scale / l[e];
+                uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + qrow[e]) + t4;
+#pragma unroll
+                for (int c = 0; c < NS4; ++c) dst[4 * (c0 + c)] = dev::pack_bf16x2(o[c][2 * e] * inv, o[c][2 * e + 1] * inv);
+            }
+        } else {
+            const int slot = r == first ? 0 : 1;
+            if (g.t0 == 0) {
+                // the unit goes on in the next CTAs, up to the one that holds its last task
+                const long long end = r + sq.nt - 1;
+                cut_begins = true;
+                cut[0] = min(rows, MR);
+                cut[1] = (int)(((end + 1) * G - 1) / W);
+                cut[2] = slot;
+                cut[3] = sq.row0;
+                cut[4] = g.h;
+                cut[5] = g.m;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (!live[e]) continue;
+                const size_t pr = ((size_t)blockIdx.x * 2 + slot) * MR + 16 * wr + gid + 8 * e;
+                float2 *dst = reinterpret_cast<float2 *>(p.part_o + pr * D) + t4;
+#pragma unroll
+                for (int c = 0; c < NS4; ++c) dst[4 * (c0 + c)] = make_float2(o[c][2 * e], o[c][2 * e + 1]);
+                if (wk == 0 && t4 == 0) reinterpret_cast<float2 *>(p.part_ml)[pr] = make_float2(m[e], l[e]);
+            }
+        }
+        r += max(g.t1 - g.t0, 1);
+    }
+    if (!ok && lane == 0) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
+    if (warp == 0 && lane < META) {
+        int v = 0;
+#pragma unroll
+        for (int x = 0; x < META; ++x)
+            if (x == lane) v = cut[x];
+        p.meta[(size_t)blockIdx.x * META + lane] = ok && cut_begins ? v : 0;
+    }
+}
+
+// Merge the partials of cut units: block (c, y) the rows 4 y .. of the unit that begins in CTA c, a warp a row.
+constexpr int MERGE_WARPS = 4;
+template <int D, int MR>
+__global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const Params p)
+{
+    constexpr int DPL = D / 32, BATCH = 8;
+    const int lane = threadIdx.x & 31, row = blockIdx.y * MERGE_WARPS + (threadIdx.x >> 5), c0 = blockIdx.x;
+    pdl_launch();
+    pdl_wait();
+    const ::int4 *meta = reinterpret_cast<const ::int4 *>(p.meta + (size_t)c0 * META);
+    const ::int4 a = __ldcg(meta);
+    if (row >= a.x) return;
+    const ::int4 u = __ldcg(meta + 1);
+    const int c1 = a.y, row0 = a.w, h = u.x, y = u.y * MR + row, i = y / p.group, hh = y - i * p.group;
+    float M = -INFINITY, den = 0.f, num[DPL];
+#pragma unroll
+    for (int x = 0; x < DPL; ++x) num[x] = 0.f;
+    for (int c = c0; c <= c1; c += BATCH) {
+        float2 ml[BATCH];
+        float o[BATCH][DPL];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int x = 0; x < DPL; ++x) o[k][x] = 0.f;
+            if (c + k <= c1) {
+                const size_t pr = ((size_t)(c + k) * 2 + (c + k == c0 ? a.z : 0)) * MR + row;
+                ml[k] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + pr);
+                if constexpr (DPL == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + pr * D) + lane);
+                    o[k][0] = v.x; o[k][1] = v.y; o[k][2] = v.z; o[k][3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.part_o + pr * D) + lane);
+                    o[k][0] = v.x; o[k][1] = v.y;
+                }
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
+        // (a part without a position that the row sees has the maximum -infinity, or a NaN sum, which stays)
+        const float f = M == top ? 1.f : dev::fast_exp2(M - top);
+        den *= f;
+#pragma unroll
+        for (int x = 0; x < DPL; ++x) num[x] *= f;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const float w = ml[k].x == top ? 1.f : dev::fast_exp2(ml[k].x - top);
+            den = fmaf(ml[k].y, w, den);
+#pragma unroll
+            for (int x = 0; x < DPL; ++x) num[x] = fmaf(o[k][x], w, num[x]);
+        }
+        M = top;
+    }
+    const float inv = den == 0.f ? 0.f : p.out_scale / den;
+    uint16_t *dst = p.out + ((size_t)(row0 + i) * p.Hq + (size_t)h * p.group + hh) * D + lane * DPL;
+    if constexpr (DPL == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(dev::pack_bf16x2(num[0] * inv, num[1] * inv), dev::pack_bf16x2(num[2] * inv, num[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = dev::pack_bf16x2(num[0] * inv, num[1] * inv);
+}
+
+// ------------------------------------------------------------------------------------
+// Host side.
+// ------------------------------------------------------------------------------------
+int sm_count()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return n;
+}
+
+// Rows per unit, by the most rows of a sequence.
+int rows_per_unit(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+struct Room { int grid; size_t o, ml, bytes; };
+Room room(int D, int mr)
+{
+    Room r;
+    r.grid = sm_count() * (mr == 128 ? 1 : 2);
+    r.o = ((size_t)r.grid * META * 4 + 255) / 256 * 256;
+    r.ml = r.o + (size_t)r.grid * 2 * mr * D * 4;
+    r.bytes = r.ml + ((size_t)r.grid * 2 * mr * 2 * 4 + 255) / 256 * 256;
+    return r;
+}
+
+template <int D, int KIND, int WR, int WK>
+cudaError_t launch(const CUtensorMap &km, const CUtensorMap &vm, const Params &p, int grid, cudaStream_t s)
+{
+    using S = Shape<D, KIND, WR, WK>;
+    auto kernel = tree_kernel<D, KIND, WR, WK>;
+    // (an attribute of the function on the current device: once for each of them)
+    static std::atomic<uint64_t> asked{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !((asked.load() >> dev) & 1u)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::ALLOC);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) asked.fetch_or(1ull << dev);
+    }
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(S::NT);
+    cfg.dynamicSmemBytes = S::ALLOC;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, km, vm, p);
+    if (e != cudaSuccess || p.MB <= TB) return e;                  // a tile at most: no unit is cut
+    cfg.gridDim = dim3((unsigned)grid, S::MR / MERGE_WARPS);
+    cfg.blockDim = dim3(MERGE_WARPS * 32);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, S::MR>, p);
+}
+
+template <int D, int KIND>
+cudaError_t launch_rows(int mr, const CUtensorMap &km, const CUtensorMap &vm, const Params &p, int grid, cudaStream_t s)
+{
+    if (mr == 16) return launch<D, KIND, 1, 4>(km, vm, p, grid, s);
+    if (mr == 32) return launch<D, KIND, 2, 2>(km, vm, p, grid, s);
+    if (mr == 64) return launch<D, KIND, 4, 1>(km, vm, p, grid, s);
+    return launch<D, KIND, 8, 1>(km, vm, p, grid, s);
+}
+
+bool aligned(const void *ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
+
+// Both entry points; cu_q null: one row per sequence.
+int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache, const int32_t *block_tables,
+        const int32_t *seq_lens, const int32_t *cu_q, const int64_t *tree_mask, int32_t batch, int32_t num_q_heads,
+        int32_t max_blocks, int32_t total_q, int32_t max_q, float scale, int32_t window, int32_t sinks, void *out,
+        void *workspace, size_t workspace_bytes, void *stream)
+{
+    const int st = check_attached(pool);
+    if (st != PKV_OK) return st;
+    const pkv_pool_desc &d = pool->desc;
+    if (batch < 0 || batch > MOST_BATCH || num_q_heads < 1 || max_blocks < 1 || max_blocks > MOST_TABLE_BLOCKS || total_q < 0 ||
+        max_q < 1 || max_q > MOST_NEW || !std::isfinite(scale) || window < 0 || sinks < 0)
+        return PKV_ERR_INVALID;
+    if (num_q_heads % d.num_kv_heads || num_q_heads / d.num_kv_heads > 16) return PKV_ERR_INVALID;
+    if ((int64_t)batch * max_blocks * d.num_kv_heads >= (int64_t)1 << 31) return PKV_ERR_INVALID;
+    if (tree_mask && window > 0 && window < max_q) return PKV_ERR_INVALID;
+    if (batch == 0 || total_q == 0) return PKV_OK;
+    if (!q || !key_cache || !value_cache || !block_tables || !seq_lens || !out || !workspace) return PKV_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(key_cache, 16) || !aligned(value_cache, 16) || !aligned(out, 16) || !aligned(block_tables, 4) ||
+        !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(tree_mask, 8) || !aligned(workspace, 256))
+        return PKV_ERR_INVALID;
+    const int D = d.head_dim, group = num_q_heads / d.num_kv_heads, mr = rows_per_unit(max_q * group);
+    const Room rm = room(D, mr);
+    if (rm.grid < 1) return PKV_ERR_CUDA;
+    if (workspace_bytes < rm.bytes) return PKV_ERR_INVALID;
+    CUtensorMap km{}, vm{};
+    if (d.kv_dtype == PKV_KV_BF16) {
+        const uint64_t tiles = (uint64_t)d.num_blocks * d.num_kv_heads;
+        bool ok;
+        if (D == 128) {
+            const uint64_t dims[4] = {64, BS, 2, tiles}, strides[3] = {256, 128, 256 * BS};
+            const uint32_t box[4] = {64, BS, 2, 1};
+            ok = encode_tiled(&km, key_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                 encode_tiled(&vm, value_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        } else {
+            const uint64_t dims[3] = {64, BS, tiles}, strides[2] = {128, 128 * BS};
+            const uint32_t box[3] = {64, BS, 1};
+            ok = encode_tiled_3d(&km, key_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                 encode_tiled_3d(&vm, value_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        }
+        if (!ok) return PKV_ERR_CUDA;
+    }
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const int most = max_blocks * BS;                              // no position is beyond
+    Params p;
+    p.q = static_cast<const uint16_t *>(q);
+    p.key_cache = static_cast<const uint8_t *>(key_cache);
+    p.value_cache = static_cast<const uint8_t *>(value_cache);
+    p.tables = block_tables;
+    p.lens = seq_lens;
+    p.cu = cu_q;
+    p.mask = reinterpret_cast<const unsigned long long *>(tree_mask);
+    p.out = static_cast<uint16_t *>(out);
+    p.part_o = reinterpret_cast<float *>(ws + rm.o);
+    p.part_ml = reinterpret_cast<float *>(ws + rm.ml);
+    p.meta = reinterpret_cast<int32_t *>(ws);
+    p.err = pool->d_err;
+    p.B = batch;
+    p.MB = max_blocks;
+    p.Hq = num_q_heads;
+    p.Hkv = d.num_kv_heads;
+    p.group = group;
+    p.num_blocks = d.num_blocks;
+    p.total_q = total_q;
+    p.max_q = max_q;
+    p.words = (max_q + 63) / 64;
+    p.window = window >= most ? 0 : window;
+    p.sinks = std::min(sinks, most);
+    p.test_stall = test_expire() == PKV_TEST_EXPIRE_DECODE;
+    p.score_scale = scale * d.k_scale * LOG2E;
+    p.out_scale = d.v_scale;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (d.kv_dtype == PKV_KV_BF16) e = D == 128 ? launch_rows<128, BF16>(mr, km, vm, p, rm.grid, s) : launch_rows<64, BF16>(mr, km, vm, p, rm.grid, s);
+    else if (d.kv_dtype == PKV_KV_FP8E4M3) e = D == 128 ? launch_rows<128, FP8>(mr, km, vm, p, rm.grid, s) : launch_rows<64, FP8>(mr, km, vm, p, rm.grid, s);
+    else e = D == 128 ? launch_rows<128, INT4>(mr, km, vm, p, rm.grid, s) : launch_rows<64, INT4>(mr, km, vm, p, rm.grid, s);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace tree
+}  // namespace pkv
+
+extern "C" size_t pkv_tree_workspace_bytes(const pkv_pool *pool, int32_t batch, int32_t num_q_heads, int32_t max_q)
+{
+    using namespace pkv::tree;
+    if (!pool || batch < 1 || batch > MOST_BATCH || num_q_heads < 1 || num_q_heads % pool->desc.num_kv_heads || max_q < 1 || max_q > MOST_NEW)
+        return 0;
+    const int g = num_q_heads / pool->desc.num_kv_heads;
+    if (g > 16 || sm_count() < 1) return 0;
+    return room(pool->desc.head_dim, rows_per_unit(max_q * g)).bytes;
+}
+
+extern "C" int pkv_paged_attention_tree(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
+                                        const int32_t *block_tables, const int32_t *seq_lens, const int32_t *cu_q,
+                                        const int64_t *tree_mask, int32_t batch, int32_t num_q_heads, int32_t max_blocks,
+                                        int32_t total_q, int32_t max_q, float scale, int32_t window, int32_t sinks, void *out,
+                                        void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (batch > 0 && total_q > 0 && !cu_q) return PKV_ERR_INVALID;
+    return pkv::tree::run(pool, q, key_cache, value_cache, block_tables, seq_lens, cu_q, tree_mask, batch, num_q_heads, max_blocks,
+                          total_q, max_q, scale, window, sinks, out, workspace, workspace_bytes, stream);
+}
+
+extern "C" int pkv_paged_attention_window(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
+                                          const int32_t *block_tables, const int32_t *seq_lens, int32_t batch, int32_t num_q_heads,
+                                          int32_t max_blocks, float scale, int32_t window, int32_t sinks, void *out,
+                                          void *workspace, size_t workspace_bytes, void *stream)
+{
+    return pkv::tree::run(pool, q, key_cache, value_cache, block_tables, seq_lens, nullptr, nullptr, batch, num_q_heads, max_blocks,
+                          batch, 1, scale, window, sinks, out, workspace, workspace_bytes, stream);
+}
