@@ -439,7 +439,7 @@ int pkv_decode_step_layers(pkv_pool *pool, const void *q, const void *k_new, con
  * [batch], each >= its P_b, >= 1, needing at most max_blocks table entries) give the units
  * (sequence, KV head, tile of 256 / g query positions) and their assignment to a one-wave
  * persistent grid, heaviest unit first to the least-loaded CTA; plan_out (host,
- * plan_bytes) receives it and *grid_out the grid.  The caller copies the plan to device
+ * plan_bytes) receives it and *grid_out the grid (pkv_paged_prefill takes it back as it is).  The caller copies the plan to device
  * memory (32-byte aligned) for pkv_paged_prefill.  Requires Hq a multiple of Hkv with
  * g <= 16.  Queries the current device's SM count. */
 size_t pkv_prefill_plan_bytes(const pkv_pool *pool, int32_t batch, int32_t num_q_heads, int32_t total_q);
@@ -561,6 +561,19 @@ int pkv_paged_attention_window(pkv_pool *pool, const void *q, const void *key_ca
                                const int32_t *block_tables, const int32_t *seq_lens, int32_t batch,
                                int32_t num_q_heads, int32_t max_blocks, float scale, int32_t window,
                                int32_t sinks, void *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same with a sliding window [Attn]: position p sees j <= p with j > p - window or j < sinks (window 0:
+ * no window, sinks ignored; a window that every sequence fits into is none).  The plan carries both, and
+ * pkv_paged_prefill(_ex) runs it as any other; the work is that of the visible tiles of 64 keys.  Table entries of
+ * blocks that no row of their sequence sees are not read and may be negative.  V at a position that no row
+ * of a tile of 256 query rows sees is never used, whatever the cache holds there; of a position that some of them
+ * see, V should be finite, as without a window.  INT4 pools: the workspace of pkv_prefill_workspace_bytes_window() for the same
+ * window and sinks. */
+int pkv_prefill_plan_window(const pkv_pool *pool, const int32_t *cu_q, const int32_t *seq_lens, int32_t batch,
+                            int32_t num_q_heads, int32_t max_blocks, int32_t window, int32_t sinks, void *plan_out,
+                            size_t plan_bytes, int32_t *grid_out);
+size_t pkv_prefill_workspace_bytes_window(const pkv_pool *pool, const int32_t *cu_q, const int32_t *seq_lens,
+                                          int32_t batch, int32_t max_blocks, int32_t window, int32_t sinks);
 
 /* Host side of one decode step, for pkv_decode_step_host: host memory, page-locked (pinned)
  * for the copies to be asynchronous.  block_tables and seq_lens may be NULL when the device

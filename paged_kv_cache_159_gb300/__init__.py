@@ -69,6 +69,7 @@ EXPORTED = (
     "pkv_fork_tables", "pkv_pool_compact", "pkv_remap_tables", "pkv_move_blocks",
     "pkv_prefill_workspace_bytes", "pkv_paged_prefill_ex", "pkv_extend_tables", "pkv_accept_rows",
     "pkv_tree_workspace_bytes", "pkv_paged_attention_tree", "pkv_paged_attention_window",
+    "pkv_prefill_plan_window", "pkv_prefill_workspace_bytes_window",
 )
 
 
@@ -157,6 +158,9 @@ def lib():
                                                     _I32, _P, _P, ctypes.c_size_t, _P]),
             "pkv_extend_tables": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P, _P]),
             "pkv_accept_rows": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P]),
+            "pkv_prefill_plan_window": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, ctypes.c_size_t,
+                                                       ctypes.POINTER(_I32)]),
+            "pkv_prefill_workspace_bytes_window": (ctypes.c_size_t, [_P, _P, _P, _I32, _I32, _I32, _I32]),
             "pkv_tree_workspace_bytes": (ctypes.c_size_t, [_P, _I32, _I32, _I32]),
             "pkv_paged_attention_tree": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32,
                                                         ctypes.c_float, _I32, _I32, _P, _P, ctypes.c_size_t, _P]),
@@ -453,9 +457,10 @@ def slot_mapping_chunks(tables, seq_lens, cu_q, block_size: int = BLOCK_SIZE) ->
     return out[:int(cu_q[-1])]
 
 
-def prefill_plan(pool: Pool, cu_q, seq_lens, num_q_heads: int, max_blocks: int):
-    """Host plan of a prefill batch (pkv_prefill_plan): (uint8 plan bytes, grid).  Copy the
-    bytes to the device (e.g. torch.from_numpy(plan).cuda()) for paged_prefill."""
+def prefill_plan(pool: Pool, cu_q, seq_lens, num_q_heads: int, max_blocks: int, window: int = 0, sinks: int = 0):
+    """Host plan of a prefill batch (pkv_prefill_plan; with a sliding window and sinks
+    pkv_prefill_plan_window): (uint8 plan bytes, grid).  Copy the bytes to the device (e.g.
+    torch.from_numpy(plan).cuda()) for paged_prefill."""
     cu_q = np.ascontiguousarray(cu_q, dtype=np.int32)
     seq_lens = np.ascontiguousarray(seq_lens, dtype=np.int32)
     nbytes = int(lib().pkv_prefill_plan_bytes(pool.handle, seq_lens.size, int(num_q_heads), int(cu_q[-1])))
@@ -463,18 +468,19 @@ def prefill_plan(pool: Pool, cu_q, seq_lens, num_q_heads: int, max_blocks: int):
         raise PkvError(ERR_INVALID, "prefill_plan_bytes")
     buf = np.zeros(nbytes, dtype=np.uint8)
     grid = _I32()
-    _check(lib().pkv_prefill_plan(pool.handle, _np_ptr(cu_q), _np_ptr(seq_lens), seq_lens.size,
-                                  int(num_q_heads), int(max_blocks), _np_ptr(buf), nbytes, ctypes.byref(grid)),
-           "prefill_plan")
+    _check(lib().pkv_prefill_plan_window(pool.handle, _np_ptr(cu_q), _np_ptr(seq_lens), seq_lens.size,
+                                         int(num_q_heads), int(max_blocks), int(window), int(sinks), _np_ptr(buf), nbytes,
+                                         ctypes.byref(grid)), "prefill_plan")
     return buf, grid.value
 
 
-def prefill_workspace_bytes(pool: Pool, cu_q, seq_lens, max_blocks: int) -> int:
-    """Device workspace bytes of an INT4 pool's prefill (pkv_prefill_workspace_bytes); 0 for other pools."""
+def prefill_workspace_bytes(pool: Pool, cu_q, seq_lens, max_blocks: int, window: int = 0, sinks: int = 0) -> int:
+    """Device workspace bytes of an INT4 pool's prefill (pkv_prefill_workspace_bytes, with a window
+    pkv_prefill_workspace_bytes_window); 0 for other pools."""
     cu_q = np.ascontiguousarray(cu_q, dtype=np.int32)
     seq_lens = np.ascontiguousarray(seq_lens, dtype=np.int32)
-    return int(lib().pkv_prefill_workspace_bytes(pool.handle, _np_ptr(cu_q), _np_ptr(seq_lens), seq_lens.size,
-                                                 int(max_blocks)))
+    return int(lib().pkv_prefill_workspace_bytes_window(pool.handle, _np_ptr(cu_q), _np_ptr(seq_lens), seq_lens.size,
+                                                        int(max_blocks), int(window), int(sinks)))
 
 
 def paged_prefill(pool: Pool, q, key_cache, value_cache, block_tables, scale: float, plan, grid: int,

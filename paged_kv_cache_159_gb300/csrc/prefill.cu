@@ -12,7 +12,8 @@
 //   q) whose K/V are already in the paged cache (kv_append) behind C_b = L_b - P_b earlier
 //   positions.  Row cu_q[b] + i is position C_b + i and attends over positions 0 .. C_b + i
 //   of its own sequence, gathered through its block table.  C_b = 0 is a whole-prompt
-//   prefill; C_b > 0 a chunk of a longer prompt (chunked prefill).
+//   prefill; C_b > 0 a chunk of a longer prompt (chunked prefill).  With a window of W positions and S
+//   sinks, position p sees j <= p with j > p - W or j < S only.
 //
 // GB300 design:
 //   * Work unit = (sequence, KV head, 256 query rows): TP = 256 / g query positions times the
@@ -53,6 +54,11 @@
 //     are zeroed in shared memory before P.V, so whatever the cache holds there (unused
 //     tail slots, NaN included) never meets the tensor core: P is 0 there, but 0 x NaN is
 //     not.
+//   * A window (WIN) is the plan's: a unit's tiles are those of the sinks, then those from the first that
+//     its first row's window reaches, so that the work is the visible tiles'; a row's own limits join the causal
+//     mask in the tiles that they cross.  Blocks that no row of the unit sees are not loaded (their table
+//     entries may be empty), and V rows that none sees are zeroed as those past the last key are.  The plan's grid
+//     carries the kind (WINDOWED), since the launch picks the instance.
 //   * All waits are bounded (about 1 s, then PKV_DEVERR_TIMEOUT and a bounded drain).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -85,19 +91,27 @@ constexpr uint32_t PLAN_MAGIC = 0x504b5650u;   // "PVKP"
 constexpr uint32_t NEGATE_A = 1u << 13;         // tcgen05.mma instruction descriptor: A enters the product negated
 constexpr uint32_t TMEM_COLS = 512;            // S (and P over it): 2 buffers x 2 q-tiles x 64, O: 2 x D
 
-// A plan: header, per-CTA unit ranges, units; for INT4 pools (batch > 0) the expanded blocks
-// before each sequence as well (batch + 1 entries), and the width of the tables.
-struct PlanHeader { uint32_t magic; int32_t num_units, grid, group, tp, hq, hkv, batch; };
-struct Unit { int32_t b, h, row0, pos0, npos, nkv, kmax, pad; };
+// A plan: header, per-CTA unit ranges, units, and one more where there is a window (Window); for INT4 pools
+// (batch > 0) the expanded blocks before each sequence as well (batch + 1 entries), the width of the tables, and
+// each sequence's first block of the window (batch entries).
+struct PlanHeader { uint32_t magic; int32_t num_units, grid, group, tp, hq, hkv, batch; };       // grid: with WINDOWED
+struct Unit { int32_t b, h, row0, pos0, npos, nkv, kmax, ts; };      // ts: tiles of the sinks before the window's
+constexpr int32_t WINDOWED = 1 << 16;          // in the grid that a plan gives out: it has a window
+constexpr int MOST_GRID = WINDOWED - 1;
+struct Window { int32_t window, sinks, pad[6]; };
+static_assert(sizeof(Window) == sizeof(Unit), "one more unit");
+
+// The first key that a unit's (or chunk's) first row, at position pos0, sees through its window.
+__host__ __device__ inline int window_low(int pos0, int window) { return window > 0 && pos0 >= window ? pos0 - window + 1 : 0; }
 
 __host__ __device__ inline size_t plan_units_offset(int grid)
 {
     return (sizeof(PlanHeader) + sizeof(int32_t) * (size_t)(grid + 1) + 31) / 32 * 32;
 }
 
-__host__ __device__ inline size_t plan_expand_offset(int grid, size_t units)
+__host__ __device__ inline size_t plan_expand_offset(int grid, size_t units, bool windowed)
 {
-    return plan_units_offset(grid) + units * sizeof(Unit);
+    return plan_units_offset(grid) + (units + (windowed ? 1 : 0)) * sizeof(Unit);
 }
 
 // ------------------------------------------------------------------------------------
@@ -122,6 +136,7 @@ struct ExpandParams {
     uint16_t *ws_k, *ws_v;
     uint32_t *err;
     int B, MB, Hkv, num_blocks, capacity, grid;       // capacity: blocks that the workspace holds
+    int windowed;
 };
 
 constexpr int EXPAND_THREADS = 256;
@@ -141,12 +156,13 @@ __global__ void __launch_bounds__(EXPAND_THREADS) prefill_expand_kernel(const Ex
 {
     constexpr int NG = D / 32, OCTETS = D / 8;
     const PlanHeader *hdr = reinterpret_cast<const PlanHeader *>(p.plan);
-    if (hdr->magic != PLAN_MAGIC || hdr->grid != p.grid || hdr->batch != p.B) {
+    if (hdr->magic != PLAN_MAGIC || hdr->grid != (p.grid | (p.windowed ? WINDOWED : 0)) || hdr->batch != p.B) {
         if (blockIdx.x == 0 && threadIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_PLAN);
         return;
     }
-    const int32_t *off = reinterpret_cast<const int32_t *>(p.plan + plan_expand_offset(hdr->grid, (size_t)hdr->num_units));
+    const int32_t *off = reinterpret_cast<const int32_t *>(p.plan + plan_expand_offset(p.grid, (size_t)hdr->num_units, p.windowed));
     const int total = off[p.B];
+    const int sb = p.windowed ? (reinterpret_cast<const Window *>(off)[-1].sinks + BS - 1) / BS : INT_MAX;
     if (!expanded_ok(reinterpret_cast<const uint8_t *>(off), p.B, p.capacity, p.MB)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_PLAN);
         return;
@@ -159,7 +175,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS) prefill_expand_kernel(const Ex
             if (__ldg(off + mid) <= x) lo = mid;
             else hi = mid;
         }
-        const int j = x - __ldg(off + lo);
+        const int e = x - __ldg(off + lo), j = e < sb ? e : e - sb + __ldg(off + p.B + 2 + lo);
         const int id = __ldg(p.tables + (size_t)lo * p.MB + j);
         const bool ok = id >= 0 && id < p.num_blocks;
         if (threadIdx.x == 0) {
@@ -236,7 +252,7 @@ struct Smem {
 };
 
 // I4: K and V are the expanded tiles of an INT4 pool, K in bf16 and V in f16.
-template <int D, bool FP8, bool I4>
+template <int D, bool FP8, bool I4, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap, const Params p)
@@ -276,13 +292,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const PlanHeader *hdr = reinterpret_cast<const PlanHeader *>(p.plan);
     const int32_t *cta_off = reinterpret_cast<const int32_t *>(p.plan + sizeof(PlanHeader));
     const Unit *units = reinterpret_cast<const Unit *>(p.plan + plan_units_offset(p.grid));
-    if (hdr->magic != PLAN_MAGIC || hdr->grid != p.grid || hdr->group != p.group || hdr->hq != p.Hq ||
+    if (hdr->magic != PLAN_MAGIC || hdr->grid != (p.grid | (WIN ? WINDOWED : 0)) || hdr->group != p.group || hdr->hq != p.Hq ||
         hdr->hkv != p.Hkv || hdr->tp != p.TP || hdr->batch != p.expanded ||
-        (p.expanded > 0 && !expanded_ok(p.plan + plan_expand_offset(hdr->grid, (size_t)hdr->num_units), p.expanded, p.num_blocks, p.MB))) {
+        (p.expanded > 0 && !expanded_ok(p.plan + plan_expand_offset(p.grid, (size_t)hdr->num_units, WIN), p.expanded, p.num_blocks, p.MB))) {
         if (tid == 0 && blockIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_PLAN);
         return;
     }
     const int u0 = cta_off[blockIdx.x], u1 = cta_off[blockIdx.x + 1];
+    const Window *win = reinterpret_cast<const Window *>(units + hdr->num_units);
+    const int window = WIN ? win->window : 0, sinks = WIN ? win->sinks : 0;
+    // K/V tile of a unit's j-th: those of the sinks come first, then those from the window's first on
+    auto tile_at = [&](const Unit &un, int j) {
+        if constexpr (!WIN) return j;
+        else return j < un.ts ? j : j - un.ts + window_low(un.pos0, window) / BN;
+    };
 
     if (tid == 0) {
         dev::mbar_init(q_full, 1);
@@ -327,8 +350,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const int nblk = un.kmax / BS + 1;                   // blocks holding keys 0..kmax
 #pragma unroll
         for (int i = 0; i < BN / BS; ++i) {
-            const int blk = j * (BN / BS) + i;
-            raw[i] = (blk < nblk && blk < p.MB) ? __ldg(p.tables + (size_t)un.b * p.MB + blk) : INT_MIN;
+            const int blk = tile_at(un, j) * (BN / BS) + i;
+            bool need = blk < nblk && blk < p.MB;
+            if constexpr (WIN) need = need && (blk * BS < sinks || (blk + 1) * BS > window_low(un.pos0, window));
+            raw[i] = need ? __ldg(p.tables + (size_t)un.b * p.MB + blk) : INT_MIN;
         }
     };
     auto resolve = [&](int id) {
@@ -683,8 +708,16 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         x[32 + i] = __uint_as_float(v1[i]);
                     }
                 }
-                const int kb = j * BN;
-                if (kb + BN - 1 > un.pos0) {                  // the causal diagonal crosses the tile
+                const int kb = tile_at(un, j) * BN;
+                if constexpr (WIN) {
+                    // the causal diagonal crosses the tile, or the first key of some row's window does
+                    if (kb + BN - 1 > un.pos0 || (kb < un.pos0 + un.npos - window && kb + BN > sinks)) {
+                        const int low = qpos - window + 1;
+#pragma unroll
+                        for (int c = 0; c < BN; ++c)
+                            x[c] = valid && kb + c <= qpos && (kb + c >= low || kb + c < sinks) ? x[c] : -INFINITY;
+                    }
+                } else if (kb + BN - 1 > un.pos0) {           // the causal diagonal crosses the tile
 #pragma unroll
                     for (int c = 0; c < BN; ++c) x[c] = (valid && kb + c <= qpos) ? x[c] : -INFINITY;
                 }
@@ -744,7 +777,23 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 tc::tmem_wait_st();
                 // last tile: zero the V rows past the unit's last visible key (both groups do,
                 // each before its own P.V; the stores write the same zeros)
-                if (j == un.nkv - 1) {
+                if constexpr (WIN) {
+                    // (any tile) zero the V rows that no row of the unit sees: past its last key, and between the
+                    // sinks and the first row's window
+                    const int low = window_low(un.pos0, window), h0 = max(sinks - kb, 0), h1 = min(low - kb, BN), h2 = un.kmax + 1 - kb;
+                    if (h0 < h1 || h2 < BN) {
+                        ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(v_full(J % NSTAGE), (J / NSTAGE) & 1));
+                        if (!ok) break;
+                        uint8_t *vst = sm + L::V + (J % NSTAGE) * L::KSTAGE;
+                        for (int c = st; c < BN * 8; c += 128) {
+                            const int row = c >> 3;
+                            if ((row >= h0 && row < h1) || row >= h2)
+                                for (int hf = 0; hf < H; ++hf)
+                                    *reinterpret_cast<uint4 *>(vst + hf * L::KHALF + c * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        dev::fence_proxy_async_smem();           // zeroed rows -> tensor core
+                    }
+                } else if (j == un.nkv - 1) {
                     const int first = un.kmax + 1 - kb;
                     if (first < BN) {
                         ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(v_full(J % NSTAGE), (J / NSTAGE) & 1));
@@ -818,22 +867,42 @@ int sm_count()
     return n;
 }
 
-template <int D, bool FP8, bool I4 = false>
-cudaError_t launch(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm, const Params &p,
+template <int D, bool FP8, bool I4, bool WIN>
+cudaError_t launch_one(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm, const Params &p,
                    cudaStream_t s)
 {
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(prefill_kernel<D, FP8, I4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr = cudaFuncSetAttribute(prefill_kernel<D, FP8, I4, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     Smem<D, FP8>::ALLOC);
     });
     if (attr != cudaSuccess) return attr;
-    prefill_kernel<D, FP8, I4><<<p.grid, NTHREADS, Smem<D, FP8>::ALLOC, s>>>(qm, km, vm, p);
+    prefill_kernel<D, FP8, I4, WIN><<<p.grid, NTHREADS, Smem<D, FP8>::ALLOC, s>>>(qm, km, vm, p);
     return cudaGetLastError();
 }
 
+template <int D, bool FP8, bool I4 = false>
+cudaError_t launch(bool windowed, const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm, const Params &p,
+                   cudaStream_t s)
+{
+    return windowed ? launch_one<D, FP8, I4, true>(qm, km, vm, p, s) : launch_one<D, FP8, I4, false>(qm, km, vm, p, s);
+}
+
 int tile_positions(int group) { return 2 * BM / group; }
+
+// Entries of a plan's part for the expansion of INT4 pools.
+size_t expand_entries(int batch) { return 2 * (size_t)batch + 2; }
+
+// Blocks of a sequence of L positions that the rows from position C on see, and the first of them that is not
+// a sink's.
+int64_t visible_blocks(int64_t C, int64_t L, int window, int sinks, int64_t *first = nullptr)
+{
+    const int64_t all = (L + BS - 1) / BS, sb = std::min(all, ((int64_t)sinks + BS - 1) / BS);
+    const int64_t b1 = std::max<int64_t>(window_low((int)C, window) / BS, sb);
+    if (first) *first = b1;
+    return window > 0 ? sb + std::max<int64_t>(0, all - b1) : all;
+}
 
 // Workspace of an INT4 call: the expanded tables, then K and V of `blocks` blocks.
 size_t ws_tables_bytes(int batch, int max_blocks) { return ((size_t)batch * max_blocks * 4 + 255) / 256 * 256; }
@@ -842,7 +911,8 @@ size_t ws_block_bytes(const pkv_pool_desc &d) { return (size_t)d.num_kv_heads * 
 // Expand the batch's blocks (see ExpandParams); the caches and tables that the attention kernel
 // then reads replace key_cache, value_cache and tables.
 int expand(const pkv_pool *pool, const void *&key_cache, const void *&value_cache, const int32_t *&tables, int batch,
-           int max_blocks, const void *plan, int grid, void *workspace, size_t workspace_bytes, int &num_blocks, cudaStream_t s)
+           int max_blocks, const void *plan, int grid, bool windowed, void *workspace, size_t workspace_bytes, int &num_blocks,
+           cudaStream_t s)
 {
     const pkv_pool_desc &d = pool->desc;
     const size_t head = ws_tables_bytes(batch, max_blocks), block = ws_block_bytes(d);
@@ -868,6 +938,7 @@ int expand(const pkv_pool *pool, const void *&key_cache, const void *&value_cach
     p.num_blocks = d.num_blocks;
     p.capacity = (int)capacity;
     p.grid = grid;
+    p.windowed = windowed;
     // (a CTA per block where that is at most 32 an SM: 8 of them, walking, take 6 us longer for 4600 blocks)
     const unsigned ctas = (unsigned)std::min<int64_t>((int64_t)sms * 32, (int64_t)batch * max_blocks);
     if (d.head_dim == 128) prefill_expand_kernel<128><<<ctas, EXPAND_THREADS, 0, s>>>(p);
@@ -893,20 +964,27 @@ extern "C" size_t pkv_prefill_plan_bytes(const pkv_pool *pool, int32_t batch, in
     const int tp = tile_positions(g);
     const size_t units = (size_t)pool->desc.num_kv_heads * ((size_t)total_q / tp + batch);
     const int grid = std::max(1, sm_count());
-    const size_t more = pool->desc.kv_dtype == PKV_KV_INT4 ? ((size_t)batch + 2) * sizeof(int32_t) : 0;
-    return plan_expand_offset(grid, units) + more;
+    const size_t more = pool->desc.kv_dtype == PKV_KV_INT4 ? expand_entries(batch) * sizeof(int32_t) : 0;
+    return plan_expand_offset(grid, units, true) + more;
 }
 
 extern "C" size_t pkv_prefill_workspace_bytes(const pkv_pool *pool, const int32_t *cu_q, const int32_t *seq_lens,
                                               int32_t batch, int32_t max_blocks)
 {
+    return pkv_prefill_workspace_bytes_window(pool, cu_q, seq_lens, batch, max_blocks, 0, 0);
+}
+
+extern "C" size_t pkv_prefill_workspace_bytes_window(const pkv_pool *pool, const int32_t *cu_q, const int32_t *seq_lens,
+                                                     int32_t batch, int32_t max_blocks, int32_t window, int32_t sinks)
+{
     using namespace pkv::prefill;
-    if (!pool || !cu_q || !seq_lens || batch < 1 || max_blocks < 1 || pool->desc.kv_dtype != PKV_KV_INT4) return 0;
+    if (!pool || !cu_q || !seq_lens || batch < 1 || max_blocks < 1 || window < 0 || sinks < 0 || pool->desc.kv_dtype != PKV_KV_INT4)
+        return 0;
     size_t blocks = 0;
     for (int b = 0; b < batch; ++b) {
         const int64_t P = (int64_t)cu_q[b + 1] - cu_q[b], L = seq_lens[b];
         if (P < 0 || L < P || L < 1 || (L + BS - 1) / BS > max_blocks) return 0;
-        if (P > 0) blocks += (size_t)((L + BS - 1) / BS);
+        if (P > 0) blocks += (size_t)visible_blocks(L - P, L, window, sinks);
     }
     if (blocks == 0) blocks = 1;
     if (blocks >= ((size_t)1 << 31) / (size_t)pool->desc.num_kv_heads) return 0;
@@ -917,8 +995,15 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
                                 int32_t batch, int32_t num_q_heads, int32_t max_blocks, void *plan_out,
                                 size_t plan_bytes, int32_t *grid_out)
 {
+    return pkv_prefill_plan_window(pool, cu_q, seq_lens, batch, num_q_heads, max_blocks, 0, 0, plan_out, plan_bytes, grid_out);
+}
+
+extern "C" int pkv_prefill_plan_window(const pkv_pool *pool, const int32_t *cu_q, const int32_t *seq_lens,
+                                       int32_t batch, int32_t num_q_heads, int32_t max_blocks, int32_t window,
+                                       int32_t sinks, void *plan_out, size_t plan_bytes, int32_t *grid_out)
+{
     using namespace pkv::prefill;
-    if (!pool || !cu_q || !seq_lens || !plan_out || !grid_out || batch < 1 || num_q_heads < 1 || max_blocks < 1)
+    if (!pool || !cu_q || !seq_lens || !plan_out || !grid_out || batch < 1 || num_q_heads < 1 || max_blocks < 1 || window < 0 || sinks < 0)
         return PKV_ERR_INVALID;
     const int Hkv = pool->desc.num_kv_heads;
     if (num_q_heads % Hkv) return PKV_ERR_INVALID;
@@ -927,7 +1012,10 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
     const int tp = tile_positions(g);
     if (cu_q[0] != 0) return PKV_ERR_INVALID;
     const bool i4 = pool->desc.kv_dtype == PKV_KV_INT4;
-    if (i4 && pkv_prefill_workspace_bytes(pool, cu_q, seq_lens, batch, max_blocks) == 0) return PKV_ERR_INVALID;
+    if (i4 && pkv_prefill_workspace_bytes_window(pool, cu_q, seq_lens, batch, max_blocks, window, sinks) == 0) return PKV_ERR_INVALID;
+    // a window that every sequence fits into is none
+    if (window >= *std::max_element(seq_lens, seq_lens + batch)) window = 0;
+    if (window == 0) sinks = 0;
     std::vector<Unit> units;
     for (int b = 0; b < batch; ++b) {
         const int64_t P = (int64_t)cu_q[b + 1] - cu_q[b], L = seq_lens[b];
@@ -940,8 +1028,9 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
             u.pos0 = (int32_t)(C + qt * tp);
             u.npos = (int32_t)std::min<int64_t>(tp, P - qt * tp);
             u.kmax = u.pos0 + u.npos - 1;
-            u.nkv = u.kmax / BN + 1;
-            u.pad = 0;
+            const int t1 = window_low(u.pos0, window) / BN;
+            u.ts = (int32_t)std::min<int64_t>(t1, ((int64_t)sinks + BN - 1) / BN);
+            u.nkv = u.ts + u.kmax / BN + 1 - t1;
             for (int h = 0; h < Hkv; ++h) {
                 u.h = h;
                 units.push_back(u);
@@ -950,8 +1039,8 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
     }
     const int sms = sm_count();
     if (sms < 1) return PKV_ERR_CUDA;
-    const int grid = std::max(1, std::min<int>(sms, (int)units.size()));
-    const size_t need = plan_expand_offset(grid, units.size()) + (i4 ? ((size_t)batch + 2) * sizeof(int32_t) : 0);
+    const int grid = std::max(1, std::min<int>(std::min(sms, MOST_GRID), (int)units.size()));
+    const size_t need = plan_expand_offset(grid, units.size(), window > 0) + (i4 ? expand_entries(batch) * sizeof(int32_t) : 0);
     if (need > plan_bytes) return PKV_ERR_INVALID;
     // A unit costs its K/V tiles plus about three tile-times of its own: waiting for its Q
     // rows, the S -> softmax -> P.V chain filling and draining, and writing its output
@@ -965,10 +1054,11 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
     int l2 = 0, dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev) != cudaSuccess)
         return PKV_ERR_CUDA;
-    std::vector<int64_t> group_kv((size_t)batch * Hkv, 0);      // largest key count of a group's units
+    std::vector<int64_t> group_kv((size_t)batch * Hkv, 0);      // keys that a group's units read
     for (const Unit &u : units) {
         int64_t &gk = group_kv[(size_t)u.b * Hkv + u.h];
-        gk = std::max<int64_t>(gk, (int64_t)u.kmax + 1);
+        const int low = window_low((int)(seq_lens[u.b] - (cu_q[u.b + 1] - cu_q[u.b])), window);
+        gk = std::max<int64_t>(gk, (int64_t)u.kmax + 1 - low + std::min(sinks, low));
     }
     int64_t kv_bytes = 0;
     for (int64_t k : group_kv) kv_bytes += k * pool->desc.head_dim * 2 * 2;
@@ -1038,7 +1128,8 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
     for (auto &v : per)
         std::sort(v.begin(), v.end(), [&](int a, int b) { return rank[(size_t)a] < rank[(size_t)b]; });
     uint8_t *out = static_cast<uint8_t *>(plan_out);
-    PlanHeader hdr{PLAN_MAGIC, (int32_t)units.size(), grid, g, tp, num_q_heads, Hkv, i4 ? batch : 0};
+    const int32_t grid_and_kind = grid | (window > 0 ? WINDOWED : 0);
+    PlanHeader hdr{PLAN_MAGIC, (int32_t)units.size(), grid_and_kind, g, tp, num_q_heads, Hkv, i4 ? batch : 0};
     std::memcpy(out, &hdr, sizeof(hdr));
     int32_t *off = reinterpret_cast<int32_t *>(out + sizeof(PlanHeader));
     Unit *dst = reinterpret_cast<Unit *>(out + plan_units_offset(grid));
@@ -1048,16 +1139,24 @@ extern "C" int pkv_prefill_plan(const pkv_pool *pool, const int32_t *cu_q, const
         for (int i : per[(size_t)c]) dst[n++] = units[(size_t)i];
     }
     off[grid] = n;
+    if (window > 0) {
+        const Window w{window, sinks, {}};
+        std::memcpy(dst + n, &w, sizeof(w));
+    }
     if (i4) {
-        int32_t *ex = reinterpret_cast<int32_t *>(out + plan_expand_offset(grid, units.size())), at = 0;
+        int32_t *ex = reinterpret_cast<int32_t *>(out + plan_expand_offset(grid, units.size(), window > 0)), at = 0;
         for (int b = 0; b < batch; ++b) {
             ex[b] = at;
-            if (cu_q[b + 1] > cu_q[b]) at += (seq_lens[b] - 1) / BS + 1;
+            const int P = cu_q[b + 1] - cu_q[b];
+            int64_t first = 0;
+            const int64_t blocks = visible_blocks(seq_lens[b] - P, seq_lens[b], window, sinks, &first);
+            if (P > 0) at += (int32_t)blocks;
+            ex[batch + 2 + b] = (int32_t)first;
         }
         ex[batch] = at;
         ex[batch + 1] = max_blocks;
     }
-    *grid_out = grid;
+    *grid_out = grid_and_kind;
     return PKV_OK;
 }
 
@@ -1079,6 +1178,8 @@ extern "C" int pkv_paged_prefill_ex(pkv_pool *pool, const void *q, const void *k
     int st = pkv::check_attached(pool);
     if (st != PKV_OK) return st;
     const pkv_pool_desc &d = pool->desc;
+    const bool windowed = grid > 0 && (grid & WINDOWED);
+    if (windowed) grid &= ~WINDOWED;
     if (batch < 1 || num_q_heads < 1 || max_blocks < 1 || total_q < 0 || grid < 1 || !std::isfinite(scale))
         return PKV_ERR_INVALID;
     if (total_q == 0) return PKV_OK;
@@ -1097,7 +1198,7 @@ extern "C" int pkv_paged_prefill_ex(pkv_pool *pool, const void *q, const void *k
     CUtensorMap qm, km, vm;
     int num_blocks = d.num_blocks;
     if (d.kv_dtype == PKV_KV_INT4) {
-        st = expand(pool, key_cache, value_cache, block_tables, batch, max_blocks, plan, grid, workspace, workspace_bytes,
+        st = expand(pool, key_cache, value_cache, block_tables, batch, max_blocks, plan, grid, windowed, workspace, workspace_bytes,
                     num_blocks, s);
         if (st != PKV_OK) return st;
     }
@@ -1135,8 +1236,8 @@ extern "C" int pkv_paged_prefill_ex(pkv_pool *pool, const void *q, const void *k
     p.out_scale = d.v_scale;
     p.test_stall = pkv::test_expire() == PKV_TEST_EXPIRE_PREFILL;
     p.expanded = d.kv_dtype == PKV_KV_INT4 ? batch : 0;
-    const cudaError_t e = p.expanded ? (D == 128 ? launch<128, false, true>(qm, km, vm, p, s) : launch<64, false, true>(qm, km, vm, p, s))
-                          : D == 128 ? (fp8 ? launch<128, true>(qm, km, vm, p, s) : launch<128, false>(qm, km, vm, p, s))
-                                     : (fp8 ? launch<64, true>(qm, km, vm, p, s) : launch<64, false>(qm, km, vm, p, s));
+    const cudaError_t e = p.expanded ? (D == 128 ? launch<128, false, true>(windowed, qm, km, vm, p, s) : launch<64, false, true>(windowed, qm, km, vm, p, s))
+                          : D == 128 ? (fp8 ? launch<128, true>(windowed, qm, km, vm, p, s) : launch<128, false>(windowed, qm, km, vm, p, s))
+                                     : (fp8 ? launch<64, true>(windowed, qm, km, vm, p, s) : launch<64, false>(windowed, qm, km, vm, p, s));
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

@@ -185,8 +185,8 @@ class Case:
                     ds[self.cu[b]:self.cu[b + 1], h] = np.where(see, a, 0).max(-1) * (self.D * 2.0 ** -23 + 2.0 ** -22)
         return out, mag, ds
 
-    def check(self, out, skip=()):
-        """Every output against the arithmetic's bound:
+    def check(self, out, skip=(), p_bits=None):
+        """Every output against the arithmetic's bound (p_bits: significant bits of P, whose largest is then at least 1):
           output rounding   2^-8 |ref|
           P in 8 bits (bf16 pools) or 11 (f16), relative 2^-8 or 2^-11 of sum p |v|; f16 below 2^-14 is off by
                             2^-25, where the largest P is 2^8 and sums are at least that: 2^-33 max |v| a position
@@ -197,10 +197,10 @@ class Case:
         ref, mag, ds = self.reference()
         got = out[:self.T].float().cpu().double().numpy()
         L = np.repeat(self.L, self.P)[:, None, None]
-        p_err = 2.0 ** -8 if self.kind == "bf16" else 2.0 ** -11
+        p_err = 2.0 ** -p_bits if p_bits else 2.0 ** -8 if self.kind == "bf16" else 2.0 ** -11
         tol = 2.0 ** -8 * np.abs(ref) + mag * (p_err + 2 * ds[..., None] + 2.0 ** -20 + L * 2.0 ** -23)
         if self.kind != "bf16":
-            tol = tol + L * 2.0 ** -33 * 7 * 448 * V_SCALE
+            tol = tol + L * (2.0 ** -25 if p_bits else 2.0 ** -33) * 7 * 448 * V_SCALE
         keep = np.ones(self.T, bool)
         for b in skip:
             keep[self.cu[b]:self.cu[b + 1]] = False
