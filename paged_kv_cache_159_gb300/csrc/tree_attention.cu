@@ -27,95 +27,17 @@
 //
 // Both launches may start while the one before drains (programmatic dependent launch): they wait before they
 // read, and load coherently.
-#include <cuda.h>
-#include <cuda_runtime.h>
-
 #include <algorithm>
 #include <atomic>
-#include <climits>
 #include <cmath>
 
-#include "int4.cuh"
-#include "pkv_internal.h"
-#include "tc_device.cuh"
+#include "tree_common.cuh"
 
 namespace pkv {
 namespace tree {
 
-constexpr int BS = 16;                 // tokens per block
-constexpr int TB = 4;                  // blocks per tile
-constexpr int MOST_BATCH = 4096;
-constexpr int MOST_NEW = 256;          // new tokens per sequence
-constexpr float LOG2E = 1.4426950408889634f;
-enum { BF16 = 0, FP8 = 1, INT4 = 2 };
-
-struct Params {
-    const uint16_t *q;
-    const uint8_t *key_cache, *value_cache;
-    const int32_t *tables, *lens, *cu;     // cu null: one row per sequence
-    const unsigned long long *mask;        // [total_q][words], or null
-    uint16_t *out;
-    float *part_o, *part_ml;               // [grid][2][MR][D], [grid][2][MR][2]
-    int32_t *meta;                         // [grid][META]: the cut unit that begins in a CTA
-    uint32_t *err;
-    int B, MB, Hq, Hkv, group, num_blocks, total_q, max_q, words, window, sinks, test_stall;
-    float score_scale, out_scale;
-};
-
-constexpr int META = 8;                    // rows (0: none), last CTA, first slot, first row of q, KV head, row tile
-
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// A sequence: its lengths, its visible blocks (list entry v is block v < sb ? v : v - sb + b1) and its tasks.
-struct Seq {
-    int L, P, C, row0;
-    int sb, b1, nvb;               // blocks of the sinks, first block of the window, entries of the list
-    int nt, rt;                    // tiles and row tiles of a unit (0: nothing to do)
-    int bad;                       // 1: flagged, its rows are zeros; 2: flagged, it has no rows to write
-};
-
-template <int MR>
-__device__ __forceinline__ Seq seq_at(const Params &p, int b)
-{
-    Seq s;
-    s.L = __ldcg(p.lens + b);
-    s.row0 = b;
-    int end = b + 1;
-    if (p.cu) {
-        s.row0 = __ldcg(p.cu + b);
-        end = __ldcg(p.cu + b + 1);
-    }
-    s.nt = s.rt = s.bad = s.sb = s.b1 = s.nvb = 0;
-    s.P = s.C = 0;
-    if (s.row0 < 0 || end < s.row0 || end > p.total_q) {
-        s.bad = 2;
-        return s;
-    }
-    s.P = end - s.row0;
-    if (s.P == 0) return s;
-    if (s.P > p.max_q || s.L < s.P || s.L > p.MB * BS) {
-        s.bad = 1;
-        return s;
-    }
-    s.C = s.L - s.P;
-    const int blocks = (s.L + BS - 1) / BS;
-    if (p.window) {
-        // a tree's row without a bit stands at C - 1
-        const int lo = max(0, s.C - p.window + (p.mask ? 0 : 1));
-        s.sb = min(blocks, (p.sinks + BS - 1) / BS);
-        s.b1 = max(lo / BS, s.sb);
-    }
-    s.nvb = s.sb + max(0, blocks - s.b1);
-    s.nt = (s.nvb + TB - 1) / TB;
-    s.rt = (s.P * p.group + MR - 1) / MR;
-    return s;
-}
-
-__device__ __forceinline__ long long tasks_of(const Seq &s, int Hkv) { return (long long)s.nt * s.rt * Hkv; }
-
-// The even split of W tasks over G CTAs.
-__device__ __forceinline__ long long share(long long W, int G, int c) { return W * c / G; }
 
 template <int D, int KIND, int WR, int WK>
 struct Shape {
@@ -139,65 +61,6 @@ struct Shape {
     static_assert(TB % WK == 0 && STAGE % 128 == 0, "");
 };
 
-// Expand one block (16 tokens) of K or V to f16 in the swizzled layout, by a warp.
-template <int D, int KIND>
-__device__ __forceinline__ void widen(const uint8_t *src, uint8_t *dst, bool isk, int lane)
-{
-    auto at = [&](int row, int chunk) {
-        return reinterpret_cast<uint4 *>(dst + (chunk >> 3) * (BS * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
-    };
-    if constexpr (KIND == FP8) {
-        constexpr int PR = D / 16;                                 // 16-byte pieces of a row
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const int e = i * 32 + lane, row = e / PR, cc = e % PR;
-            const uint4 x = *reinterpret_cast<const uint4 *>(src + e * 16);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t h[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                h[2 * k] = dev::e4m3x2_to_f16x2((uint16_t)w[k]);
-                h[2 * k + 1] = dev::e4m3x2_to_f16x2((uint16_t)(w[k] >> 16));
-            }
-            // (lanes of the upper 64 columns store their second half first: no bank conflict)
-            const bool odd = cc >= 4;
-            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-            *at(row, 2 * cc + (odd ? 1 : 0)) = odd ? hi : lo;
-            *at(row, 2 * cc + (odd ? 0 : 1)) = odd ? lo : hi;
-        }
-    } else if constexpr (KIND == INT4) {
-        constexpr int NG = D / 32;
-        const int c = lane & 3;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int r = 8 * x + (lane >> 2);
-            const int t = isk ? (r & 8) | ((r >> 1) & 3) | ((r & 1) << 2) : r, oc = !isk && D == 128 ? c ^ (r & 2) : c;
-            uint32_t w[NG], sb = 0, vs[NG];
-            const uint8_t *row = src + r * (D / 2) + c * (4 * NG);
-            if constexpr (NG == 4) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(row);
-                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-            } else {
-                const uint2 v = *reinterpret_cast<const uint2 *>(row);
-                w[0] = v.x; w[1] = v.y;
-            }
-            if (isk) {
-                if constexpr (NG == 4) sb = *reinterpret_cast<const uint32_t *>(src + 8 * D + r * NG);
-                else sb = *reinterpret_cast<const uint16_t *>(src + 8 * D + r * NG);
-            } else {
-#pragma unroll
-                for (int j = 0; j < NG; ++j) vs[j] = *reinterpret_cast<const uint32_t *>(src + 8 * D + (r & 3) * (4 * NG) + 4 * j);
-            }
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                const uint32_t codes = isk ? w[j] : __byte_perm(w[j >> 1], w[NG / 2 + (j >> 1)], (j & 1) ? 0x7632u : 0x5410u);
-                const uint32_t scale = isk ? (sb >> (8 * j)) & 0xffu : (vs[j] >> (8 * (r >> 2))) & 0xffu;
-                *at(t, 4 * j + oc) = int4::expand_octet<__half2>(codes, scale);
-            }
-        }
-    }
-}
-
 template <int D, int KIND, int WR, int WK>
 __global__ void __launch_bounds__(Shape<D, KIND, WR, WK>::NT, Shape<D, KIND, WR, WK>::CTAS)
 tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Params p)
@@ -206,8 +69,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     constexpr int NC = S::NC, MR = S::MR, NS = S::NS, BT = S::BT, NB = TB / WK, KS = D / 16, NN = D / 8;
     constexpr float SHIFT = KIND == BF16 ? 0.f : 8.f;              // P is held as P 2^SHIFT
     extern __shared__ uint8_t smem_raw[];
-    __shared__ long long wsum[NC + 1], found[2];
-    __shared__ int found_b;
+    __shared__ ShareScratch<S::NT> scratch;
     uint8_t *sm = smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = dev::smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(dev::FULL, tid >> 5, 0);
@@ -227,82 +89,10 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     pdl_launch();
     pdl_wait();
 
-    // ---- every CTA's share of the tasks, from the lengths: a thread sums some sequences, the block scans
-    long long first, last, W;
-    Seq sq;
-    int b, G;                                                      // CTAs with work
-    long long U0;                                                  // first task of sequence b
-    {
-        const int per = (p.B + S::NT - 1) / S::NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-        long long run = 0;
-        int bad = 0;
-        for (int x = b0; x < b1; ++x) {
-            const Seq s = seq_at<MR>(p, x);
-            bad |= s.bad;
-            run += tasks_of(s, p.Hkv);
-        }
-        long long incl = run;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(dev::FULL, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) wsum[warp] = incl;
-        const int any_bad = __syncthreads_or(bad);
-        long long at = incl - run;
-        W = 0;
-#pragma unroll
-        for (int w = 0; w < NC + 1; ++w) {
-            if (w < warp) at += wsum[w];
-            W += wsum[w];
-        }
-        G = (int)min((long long)gridDim.x, max(W, 1ll));           // (so that every CTA up to it has a task)
-        first = (int)blockIdx.x < G ? share(W, G, blockIdx.x) : W;
-        last = (int)blockIdx.x < G ? share(W, G, blockIdx.x + 1) : W;
-        if (first >= at && first < at + run) {
-            for (int x = b0; x < b1; ++x) {
-                const long long n = tasks_of(seq_at<MR>(p, x), p.Hkv);
-                if (first < at + n) {
-                    found_b = x;
-                    found[0] = at;
-                    break;
-                }
-                at += n;
-            }
-        }
-        __syncthreads();
-        if (any_bad) {
-            if (tid == 0 && blockIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_SEQ_LEN);
-            for (int x = blockIdx.x; x < p.B; x += gridDim.x) {
-                const Seq s = seq_at<MR>(p, x);
-                uint4 *dst = reinterpret_cast<uint4 *>(p.out + (size_t)s.row0 * p.Hq * D);
-                if (s.bad == 1)
-                    for (size_t e = tid; e < (size_t)s.P * p.Hq * (D / 8); e += S::NT) dst[e] = make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
-        if (tid < META && first >= last) p.meta[(size_t)blockIdx.x * META + tid] = 0;
-        if (first >= last) return;
-        b = found_b;
-        U0 = found[0];
-        sq = seq_at<MR>(p, b);
-    }
-
-    // The segment (run of tiles t0 .. t1 - 1 of one unit) that holds task r; b, sq and U0 move on with it.
-    struct Segment { int h, m, t0, t1; };
-    auto segment_at = [&](long long r) {
-        while (b + 1 < p.B && r >= U0 + tasks_of(sq, p.Hkv)) {
-            U0 += tasks_of(sq, p.Hkv);
-            sq = seq_at<MR>(p, ++b);
-        }
-        const long long rel = r - U0;
-        const int unit = (int)(rel / max(sq.nt, 1));
-        Segment g;
-        g.t0 = (int)(rel - (long long)unit * sq.nt);
-        g.h = unit / max(sq.rt, 1);
-        g.m = unit - g.h * sq.rt;
-        g.t1 = (int)min((long long)sq.nt, g.t0 + (last - r));
-        return g;
-    };
+    const Share my = share_of<S::NT, D>(p, scratch);
+    const long long first = my.first, last = my.last;
+    if (first >= last) return;
+    Walk walk(p, my);
 
     if (warp == NC) {
         // ============ the copying warp: lane k < TB takes block k of a tile, K and V
@@ -316,31 +106,35 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
         }
         // the table's entries, a tile ahead of their copies
         long long r = first;
-        Segment g = segment_at(r);
-        int t = g.t0;
-        auto entry = [&]() {
-            const int v = TB * t + lane;
-            if (lane >= TB || v >= sq.nvb) return -2;
-            const int blk = v < sq.sb ? v : v - sq.sb + sq.b1;
-            return __ldcg(p.tables + (size_t)b * p.MB + blk);
+        Segment g = walk.at(p, r);
+        int t = g.t0, chunk = t;
+        // the table's entries of 32 blocks (8 tiles from `chunk` on), and of the 32 after them
+        auto fetch = [&](int t0) {
+            const int v = TB * t0 + lane;
+            return v < walk.sq.nvb && v < TB * g.t1 ? __ldcg(p.tables + (size_t)walk.b * p.MB + walk.block(v)) : -2;
         };
-        int id = entry();
+        int ids = fetch(t), nxt = fetch(t + 8);
         while (true) {
-            const int h = g.h, cur = id;
+            const int h = g.h, cur = __shfl_sync(dev::FULL, ids, TB * (t - chunk) + (lane & (TB - 1)));
             ++r;
             if (r < last) {
                 if (++t == g.t1) {
-                    g = segment_at(r);
-                    t = g.t0;
+                    g = walk.at(p, r);
+                    t = chunk = g.t0;
+                    ids = fetch(t);
+                    nxt = fetch(t + 8);
+                } else if (t - chunk == 8) {
+                    chunk = t;
+                    ids = nxt;
+                    nxt = fetch(t + 8);
                 }
-                id = entry();
             }
             const int s = n % NS;
             if (n >= NS) {
                 ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(empty(s), (uint32_t)(((n - NS) / NS) & 1)));
                 if (!ok) break;
             }
-            const bool want = cur != -2, good = cur >= 0 && cur < p.num_blocks;
+            const bool want = lane < TB && cur != -2, good = lane < TB && cur >= 0 && cur < p.num_blocks;
             if (want && !good) dev::flag_error(p.err, PKV_DEVERR_BLOCK_ID);
             const unsigned got = __ballot_sync(dev::FULL, good);
             if (lane == 0) {
@@ -387,12 +181,12 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     bool cut_begins = false;
     int cut[META] = {};
     for (long long r = first; ok && r < last;) {
-        const Segment g = segment_at(r);
+        const Segment g = walk.at(p, r);
+        const Seq &sq = walk.sq;
         const int rows = sq.P * p.group - g.m * MR;                // of this unit, at most MR of them here
         // this lane's two rows
         int place[2], draft[2];                                    // p of the row; its token
         bool live[2];
-        const unsigned long long *bits[2];
         uint32_t qa[KS][4];
         float sc[2] = {p.score_scale, p.score_scale};
         size_t qrow[2];
@@ -409,20 +203,9 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                 qa[k][e] = live[e] ? __ldcg(src + 8 * k + t4) : 0u;
                 qa[k][e + 2] = live[e] ? __ldcg(src + 8 * k + t4 + 4) : 0u;
             }
-            bits[e] = p.mask ? p.mask + (size_t)(sq.row0 + i) * p.words : nullptr;
-            place[e] = sq.C + i;
-            if (p.mask) {
-                int c = 0;
-                for (int w = 0; w < p.words; ++w) {
-                    const int left = sq.P - 64 * w;
-                    if (left > 0) c += __popcll(__ldcg(bits[e] + w) & (left >= 64 ? ~0ull : (1ull << left) - 1));
-                }
-                place[e] = sq.C + c - 1;
-            }
+            place[e] = p.mask && !p.window ? 0 : place_of(p, sq, i);
         }
         if constexpr (KIND != BF16) {
-            // q to f16: a power of two per row brings its largest element into [2^14, 2^15), exact for elements
-            // of 2^-24 of it and more; a row with an infinity or NaN gets NaN scores
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 uint32_t top = 0;
@@ -433,9 +216,9 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                 }
                 top = max(top, __shfl_xor_sync(dev::FULL, top, 1));
                 top = max(top, __shfl_xor_sync(dev::FULL, top, 2));
-                const int ex = (int)(top >> 7), up = ex == 255 || top == 0 ? 0 : min(126, 141 - max(ex, 1));
-                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-                sc[e] = ex == 255 ? __int_as_float(0x7fffffff) : sc[e] * __uint_as_float((uint32_t)(127 - up) << 23);
+                const int up = q_exponent(top);
+                const float f = q_factor(up);
+                sc[e] = row_scale(sc[e], up);
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -449,8 +232,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
             for (int e = 0; e < 4; ++e) acc[x][e] = 0.f;
         // positions up to which, and from which on, all rows of the unit see the cache
         const int i0 = g.m * MR / p.group, i1 = min(sq.P - 1, (g.m * MR + min(rows, MR) - 1) / p.group);
-        const int all_to = p.mask ? sq.C : sq.C + i0 + 1;
-        const int all_from = p.window ? sq.C + (p.mask ? sq.P - 1 : i1) - p.window + 1 : INT_MIN;
+        const int to = all_to(p, sq, i0), from = all_from(p, sq, i1);
 
         for (int t = g.t0; t < g.t1; ++t, ++n) {
             const int s = n % NS;
@@ -466,7 +248,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
                 for (int x = warp; x < 2 * TB; x += NC) {          // (block x % TB, K or V)
                     const int k = x % TB;
-                    if ((got >> k) & 1u) widen<D, KIND>(stage + x * S::TILE, wide + x * BT, x < TB, lane);
+                    if ((got >> k) & 1u) widen<D, KIND, BS * 128>(stage + x * S::TILE, wide + x * BT, x < TB, lane);
                 }
                 __syncwarp();
                 if (lane == 0) dev::mbar_arrive(empty(s));
@@ -477,9 +259,8 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
             bool edge = false;
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
-                const int v = TB * t + wk * NB + k, blk = v < sq.sb ? v : v - sq.sb + sq.b1;
-                pos[k] = blk * BS;
-                edge |= !((got >> (wk * NB + k)) & 1u) || pos[k] + BS > all_to || (pos[k] < all_from && pos[k] + BS > p.sinks);
+                pos[k] = walk.block(TB * t + wk * NB + k) * BS;
+                edge |= !((got >> (wk * NB + k)) & 1u) || pos[k] + BS > to || (pos[k] < from && pos[k] + BS > p.sinks);
             }
             // ---- S = Q K^T
             float x[2 * NB][4];
@@ -513,27 +294,10 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
                     see[k] = 0;
-                    const int p0 = pos[k];
-                    auto ones = [](int c) { return (1u << min(max(c, 0), BS)) - 1u; };
-                    const uint32_t valid = (got >> (wk * NB + k)) & 1u ? ones(sq.L - p0) : 0u;
+                    const uint32_t valid = (got >> (wk * NB + k)) & 1u ? ones(sq.L - pos[k]) : 0u;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t c = valid & ones((p.mask ? sq.C : sq.C + draft[e] + 1) - p0), d = 0;
-                        if (p.mask && p0 + BS > sq.C) {
-                            const int off = p0 - sq.C;             // bit of the block's first position
-                            unsigned long long w;
-                            if (off < 0) {
-                                w = __ldcg(bits[e]) << -off;
-                            } else {
-                                const int i = off >> 6, sh = off & 63;
-                                w = i < p.words ? __ldcg(bits[e] + i) >> sh : 0ull;
-                                if (sh && i + 1 < p.words) w |= __ldcg(bits[e] + i + 1) << (64 - sh);
-                            }
-                            d = (uint32_t)w & valid & ~ones(sq.C - p0);
-                        }
-                        if (p.window) c &= ~ones(place[e] - p.window + 1 - p0) | ones(p.sinks - p0);
-                        if (live[e]) see[k] |= (c | d) << (16 * e);
-                    }
+                    for (int e = 0; e < 2; ++e)
+                        if (live[e]) see[k] |= seen16(p, sq, draft[e], place[e], pos[k], valid) << (16 * e);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -753,10 +517,9 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
             const int slot = r == first ? 0 : 1;
             if (g.t0 == 0) {
                 // the unit goes on in the next CTAs, up to the one that holds its last task
-                const long long end = r + sq.nt - 1;
                 cut_begins = true;
                 cut[0] = min(rows, MR);
-                cut[1] = (int)(((end + 1) * G - 1) / W);
+                cut[1] = stream_of(r + sq.nt - 1, my.W, my.streams);
                 cut[2] = slot;
                 cut[3] = sq.row0;
                 cut[4] = g.h;
@@ -786,7 +549,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 
 // Merge the partials of cut units: block (c, y) the rows 4 y .. of the unit that begins in CTA c, a warp a row.
 constexpr int MERGE_WARPS = 4;
-template <int D, int MR>
+template <int D>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const Params p)
 {
     constexpr int DPL = D / 32, BATCH = 8;
@@ -797,7 +560,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const Para
     const ::int4 a = __ldcg(meta);
     if (row >= a.x) return;
     const ::int4 u = __ldcg(meta + 1);
-    const int c1 = a.y, row0 = a.w, h = u.x, y = u.y * MR + row, i = y / p.group, hh = y - i * p.group;
+    const int c1 = a.y, row0 = a.w, h = u.x, y = u.y * p.rows_unit + row, i = y / p.group, hh = y - i * p.group;
     float M = -INFINITY, den = 0.f, num[DPL];
 #pragma unroll
     for (int x = 0; x < DPL; ++x) num[x] = 0.f;
@@ -810,7 +573,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const Para
 #pragma unroll
             for (int x = 0; x < DPL; ++x) o[k][x] = 0.f;
             if (c + k <= c1) {
-                const size_t pr = ((size_t)(c + k) * 2 + (c + k == c0 ? a.z : 0)) * MR + row;
+                const size_t pr = ((size_t)(c + k) * 2 + (c + k == c0 ? a.z : 0)) * p.rows_unit + row;
                 ml[k] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + pr);
                 if constexpr (DPL == 4) {
                     const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + pr * D) + lane);
@@ -856,17 +619,23 @@ int sm_count()
     return n;
 }
 
-// Rows per unit, by the most rows of a sequence.
-int rows_per_unit(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Rows per unit by the most rows of a sequence and KV head: 16, 32 or 64 on mma.sync, above that the tcgen05 kernel's.
+constexpr int MOST_MMA_ROWS = 64;
+int rows_per_unit(int max_q, int group)
+{
+    const int rows = max_q * group;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= MOST_MMA_ROWS ? 64 : tcgen05_tokens(group) * group;
+}
 
-struct Room { int grid; size_t o, ml, bytes; };
-Room room(int D, int mr)
+struct Room { int grid, rows; size_t o, ml, bytes; };
+Room room(int D, int max_q, int group)
 {
     Room r;
-    r.grid = sm_count() * (mr == 128 ? 1 : 2);
+    r.rows = rows_per_unit(max_q, group);
+    r.grid = sm_count() * (r.rows <= MOST_MMA_ROWS ? 2 : 1);
     r.o = ((size_t)r.grid * META * 4 + 255) / 256 * 256;
-    r.ml = r.o + (size_t)r.grid * 2 * mr * D * 4;
-    r.bytes = r.ml + ((size_t)r.grid * 2 * mr * 2 * 4 + 255) / 256 * 256;
+    r.ml = r.o + ((size_t)r.grid * 2 * r.rows * D * 4 + 255) / 256 * 256;
+    r.bytes = r.ml + ((size_t)r.grid * 2 * r.rows * 2 * 4 + 255) / 256 * 256;
     return r;
 }
 
@@ -896,11 +665,22 @@ cudaError_t launch(const CUtensorMap &km, const CUtensorMap &vm, const Params &p
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kernel, km, vm, p);
-    if (e != cudaSuccess || p.MB <= TB) return e;                  // a tile at most: no unit is cut
-    cfg.gridDim = dim3((unsigned)grid, S::MR / MERGE_WARPS);
+    return e;
+}
+
+template <int D>
+cudaError_t launch_merge(const Params &p, int grid, cudaStream_t s)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)((p.rows_unit + MERGE_WARPS - 1) / MERGE_WARPS));
     cfg.blockDim = dim3(MERGE_WARPS * 32);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, S::MR>, p);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p);
 }
 
 template <int D, int KIND>
@@ -908,8 +688,7 @@ cudaError_t launch_rows(int mr, const CUtensorMap &km, const CUtensorMap &vm, co
 {
     if (mr == 16) return launch<D, KIND, 1, 4>(km, vm, p, grid, s);
     if (mr == 32) return launch<D, KIND, 2, 2>(km, vm, p, grid, s);
-    if (mr == 64) return launch<D, KIND, 4, 1>(km, vm, p, grid, s);
-    return launch<D, KIND, 8, 1>(km, vm, p, grid, s);
+    return launch<D, KIND, 4, 1>(km, vm, p, grid, s);
 }
 
 bool aligned(const void *ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
@@ -934,26 +713,33 @@ int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_
     if (!aligned(q, 16) || !aligned(key_cache, 16) || !aligned(value_cache, 16) || !aligned(out, 16) || !aligned(block_tables, 4) ||
         !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(tree_mask, 8) || !aligned(workspace, 256))
         return PKV_ERR_INVALID;
-    const int D = d.head_dim, group = num_q_heads / d.num_kv_heads, mr = rows_per_unit(max_q * group);
-    const Room rm = room(D, mr);
+    const int D = d.head_dim, group = num_q_heads / d.num_kv_heads;
+    const Room rm = room(D, max_q, group);
+    const bool many = rm.rows > MOST_MMA_ROWS;
     if (rm.grid < 1) return PKV_ERR_CUDA;
     if (workspace_bytes < rm.bytes) return PKV_ERR_INVALID;
-    CUtensorMap km{}, vm{};
+    CUtensorMap qm{}, km{}, vm{};
     if (d.kv_dtype == PKV_KV_BF16) {
         const uint64_t tiles = (uint64_t)d.num_blocks * d.num_kv_heads;
         bool ok;
-        if (D == 128) {
+        if (D == 128 && !many) {
             const uint64_t dims[4] = {64, BS, 2, tiles}, strides[3] = {256, 128, 256 * BS};
             const uint32_t box[4] = {64, BS, 2, 1};
             ok = encode_tiled(&km, key_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
                  encode_tiled(&vm, value_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
         } else {
-            const uint64_t dims[3] = {64, BS, tiles}, strides[2] = {128, 128 * BS};
+            const uint64_t dims[3] = {(uint64_t)D, BS, tiles}, strides[2] = {(uint64_t)D * 2, (uint64_t)D * 2 * BS};
             const uint32_t box[3] = {64, BS, 1};
             ok = encode_tiled_3d(&km, key_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
                  encode_tiled_3d(&vm, value_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
         }
         if (!ok) return PKV_ERR_CUDA;
+    }
+    if (many) {
+        // eight tokens' rows of a KV head's group
+        const uint64_t dims[3] = {(uint64_t)D, (uint64_t)num_q_heads, (uint64_t)total_q}, strides[2] = {(uint64_t)D * 2, (uint64_t)num_q_heads * D * 2};
+        const uint32_t box[3] = {64, (uint32_t)group, 8};
+        if (!encode_tiled_3d(&qm, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return PKV_ERR_CUDA;
     }
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const int most = max_blocks * BS;                              // no position is beyond
@@ -981,14 +767,18 @@ int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_
     p.words = (max_q + 63) / 64;
     p.window = window >= most ? 0 : window;
     p.sinks = std::min(sinks, most);
+    p.rows_unit = rm.rows;
     p.test_stall = test_expire() == PKV_TEST_EXPIRE_DECODE;
     p.score_scale = scale * d.k_scale * LOG2E;
     p.out_scale = d.v_scale;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (d.kv_dtype == PKV_KV_BF16) e = D == 128 ? launch_rows<128, BF16>(mr, km, vm, p, rm.grid, s) : launch_rows<64, BF16>(mr, km, vm, p, rm.grid, s);
-    else if (d.kv_dtype == PKV_KV_FP8E4M3) e = D == 128 ? launch_rows<128, FP8>(mr, km, vm, p, rm.grid, s) : launch_rows<64, FP8>(mr, km, vm, p, rm.grid, s);
-    else e = D == 128 ? launch_rows<128, INT4>(mr, km, vm, p, rm.grid, s) : launch_rows<64, INT4>(mr, km, vm, p, rm.grid, s);
+    if (many) e = launch_tcgen05(D, d.kv_dtype, qm, km, vm, p, rm.grid, s);
+    else if (d.kv_dtype == PKV_KV_BF16) e = D == 128 ? launch_rows<128, BF16>(rm.rows, km, vm, p, rm.grid, s) : launch_rows<64, BF16>(rm.rows, km, vm, p, rm.grid, s);
+    else if (d.kv_dtype == PKV_KV_FP8E4M3) e = D == 128 ? launch_rows<128, FP8>(rm.rows, km, vm, p, rm.grid, s) : launch_rows<64, FP8>(rm.rows, km, vm, p, rm.grid, s);
+    else e = D == 128 ? launch_rows<128, INT4>(rm.rows, km, vm, p, rm.grid, s) : launch_rows<64, INT4>(rm.rows, km, vm, p, rm.grid, s);
+    if (e == cudaSuccess && max_blocks > TB)                       // (with a tile at most no unit is cut)
+        e = D == 128 ? launch_merge<128>(p, rm.grid, s) : launch_merge<64>(p, rm.grid, s);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -1002,7 +792,7 @@ extern "C" size_t pkv_tree_workspace_bytes(const pkv_pool *pool, int32_t batch, 
         return 0;
     const int g = num_q_heads / pool->desc.num_kv_heads;
     if (g > 16 || sm_count() < 1) return 0;
-    return room(pool->desc.head_dim, rows_per_unit(max_q * g)).bytes;
+    return room(pool->desc.head_dim, max_q, g).bytes;
 }
 
 extern "C" int pkv_paged_attention_tree(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
