@@ -90,7 +90,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     pdl_wait();
 
     const Share my = share_of<S::NT, D>(p, scratch);
-    const long long first = my.first, last = my.last;
+    const int first = my.first, last = my.last;
     if (first >= last) return;
     Walk walk(p, my);
 
@@ -105,7 +105,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
             }
         }
         // the table's entries, a tile ahead of their copies
-        long long r = first;
+        int r = first;
         Segment g = walk.at(p, r);
         int t = g.t0, chunk = t;
         // the table's entries of 32 blocks (8 tiles from `chunk` on), and of the 32 after them
@@ -180,13 +180,14 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     int n = 0;                                                     // tiles seen
     bool cut_begins = false;
     int cut[META] = {};
-    for (long long r = first; ok && r < last;) {
+    for (int r = first; ok && r < last;) {
         const Segment g = walk.at(p, r);
         const Seq &sq = walk.sq;
         const int rows = sq.P * p.group - g.m * MR;                // of this unit, at most MR of them here
         // this lane's two rows
         int place[2], draft[2];                                    // p of the row; its token
         bool live[2];
+        unsigned long long word[2];                                // the first of its mask
         uint32_t qa[KS][4];
         float sc[2] = {p.score_scale, p.score_scale};
         size_t qrow[2];
@@ -204,6 +205,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                 qa[k][e + 2] = live[e] ? __ldcg(src + 8 * k + t4 + 4) : 0u;
             }
             place[e] = p.mask && !p.window ? 0 : place_of(p, sq, i);
+            word[e] = first_word(p, sq, i);
         }
         if constexpr (KIND != BF16) {
 #pragma unroll
@@ -297,7 +299,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                     const uint32_t valid = (got >> (wk * NB + k)) & 1u ? ones(sq.L - pos[k]) : 0u;
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        if (live[e]) see[k] |= seen16(p, sq, draft[e], place[e], pos[k], valid) << (16 * e);
+                        if (live[e]) see[k] |= seen16(p, sq, draft[e], place[e], word[e], pos[k], valid) << (16 * e);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -627,15 +629,19 @@ int rows_per_unit(int max_q, int group)
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= MOST_MMA_ROWS ? 64 : tcgen05_tokens(group) * group;
 }
 
-struct Room { int grid, rows; size_t o, ml, bytes; };
-Room room(int D, int max_q, int group)
+struct Room { int grid, rows; size_t o, ml, q, up, bytes; };
+Room room(const pkv_pool_desc &d, int batch, int max_q, int num_q_heads)
 {
+    const int D = d.head_dim, group = num_q_heads / d.num_kv_heads;
     Room r;
     r.rows = rows_per_unit(max_q, group);
     r.grid = sm_count() * (r.rows <= MOST_MMA_ROWS ? 2 : 1);
     r.o = ((size_t)r.grid * META * 4 + 255) / 256 * 256;
     r.ml = r.o + ((size_t)r.grid * 2 * r.rows * D * 4 + 255) / 256 * 256;
-    r.bytes = r.ml + ((size_t)r.grid * 2 * r.rows * 2 * 4 + 255) / 256 * 256;
+    r.q = r.ml + ((size_t)r.grid * 2 * r.rows * 2 * 4 + 255) / 256 * 256;
+    const size_t q_rows = r.rows > MOST_MMA_ROWS && d.kv_dtype != PKV_KV_BF16 ? (size_t)batch * max_q * num_q_heads : 0;
+    r.up = r.q + (q_rows * D * 2 + 255) / 256 * 256;
+    r.bytes = r.up + (q_rows + 255) / 256 * 256;
     return r;
 }
 
@@ -707,6 +713,9 @@ int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_
         return PKV_ERR_INVALID;
     if (num_q_heads % d.num_kv_heads || num_q_heads / d.num_kv_heads > 16) return PKV_ERR_INVALID;
     if ((int64_t)batch * max_blocks * d.num_kv_heads >= (int64_t)1 << 31) return PKV_ERR_INVALID;
+    // (tiles of all units in 31 bits)
+    if ((int64_t)batch * max_blocks * d.num_kv_heads * std::max<int64_t>(1, (int64_t)max_q * (num_q_heads / d.num_kv_heads) / 128) >= (int64_t)1 << 31)
+        return PKV_ERR_INVALID;
     if (tree_mask && window > 0 && window < max_q) return PKV_ERR_INVALID;
     if (batch == 0 || total_q == 0) return PKV_OK;
     if (!q || !key_cache || !value_cache || !block_tables || !seq_lens || !out || !workspace) return PKV_ERR_INVALID;
@@ -714,7 +723,7 @@ int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_
         !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(tree_mask, 8) || !aligned(workspace, 256))
         return PKV_ERR_INVALID;
     const int D = d.head_dim, group = num_q_heads / d.num_kv_heads;
-    const Room rm = room(D, max_q, group);
+    const Room rm = room(d, batch, max_q, num_q_heads);
     const bool many = rm.rows > MOST_MMA_ROWS;
     if (rm.grid < 1) return PKV_ERR_CUDA;
     if (workspace_bytes < rm.bytes) return PKV_ERR_INVALID;
@@ -735,16 +744,24 @@ int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_
         }
         if (!ok) return PKV_ERR_CUDA;
     }
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const void *q_tiles = q;                                       // what the tcgen05 kernel copies
+    uint64_t q_rows = (uint64_t)total_q;
+    if (many && d.kv_dtype != PKV_KV_BF16) {
+        q_tiles = ws + rm.q;
+        q_rows = (uint64_t)batch * max_q;
+    }
     if (many) {
         // eight tokens' rows of a KV head's group
-        const uint64_t dims[3] = {(uint64_t)D, (uint64_t)num_q_heads, (uint64_t)total_q}, strides[2] = {(uint64_t)D * 2, (uint64_t)num_q_heads * D * 2};
+        const uint64_t dims[3] = {(uint64_t)D, (uint64_t)num_q_heads, q_rows}, strides[2] = {(uint64_t)D * 2, (uint64_t)num_q_heads * D * 2};
         const uint32_t box[3] = {64, (uint32_t)group, 8};
-        if (!encode_tiled_3d(&qm, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return PKV_ERR_CUDA;
+        if (!encode_tiled_3d(&qm, q_tiles, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return PKV_ERR_CUDA;
     }
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
     const int most = max_blocks * BS;                              // no position is beyond
     Params p;
     p.q = static_cast<const uint16_t *>(q);
+    p.q16 = reinterpret_cast<uint16_t *>(ws + rm.q);
+    p.q_up = reinterpret_cast<int8_t *>(ws + rm.up);
     p.key_cache = static_cast<const uint8_t *>(key_cache);
     p.value_cache = static_cast<const uint8_t *>(value_cache);
     p.tables = block_tables;
@@ -792,7 +809,7 @@ extern "C" size_t pkv_tree_workspace_bytes(const pkv_pool *pool, int32_t batch, 
         return 0;
     const int g = num_q_heads / pool->desc.num_kv_heads;
     if (g > 16 || sm_count() < 1) return 0;
-    return room(pool->desc.head_dim, max_q, g).bytes;
+    return room(pool->desc, batch, max_q, num_q_heads).bytes;
 }
 
 extern "C" int pkv_paged_attention_tree(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,

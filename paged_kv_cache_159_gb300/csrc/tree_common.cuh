@@ -24,6 +24,8 @@ enum { BF16 = 0, FP8 = 1, INT4 = 2 };
 
 struct Params {
     const uint16_t *q;
+    uint16_t *q16;                         // tcgen05 over FP8 and INT4 pools: q in f16 [batch][max_q][Hq][D], and its
+    int8_t *q_up;                          // rows' exponents [batch][max_q][Hq]
     const uint8_t *key_cache, *value_cache;
     const int32_t *tables, *lens, *cu;     // cu null: one row per sequence
     const unsigned long long *mask;        // [total_q][words], or null
@@ -81,24 +83,26 @@ __device__ __forceinline__ Seq seq_at(const Params &p, int b)
     return s;
 }
 
-__device__ __forceinline__ long long tasks_of(const Seq &s, int Hkv) { return (long long)s.nt * s.rt * Hkv; }
+// (The host refuses shapes whose tasks could pass 31 bits.)
+__device__ __forceinline__ int tasks_of(const Seq &s, int Hkv) { return s.nt * s.rt * Hkv; }
 
-// The even split of W tasks over G CTAs.
-__device__ __forceinline__ long long share(long long W, int G, int c) { return W * c / G; }
+// floor(W c / G), the even split of W tasks over G CTAs, in 32 bits: a 64-bit division is some hundred instructions.
+__device__ __forceinline__ int share(int W, int G, int c)
+{
+    const int q = W / G;
+    return q * c + (W - q * G) * c / G;
+}
 
 
 // ---- the split of the work
 // Share of one stream of the grid: tasks first .. last - 1 of W, the first of them in sequence b, whose tasks begin
 // at U0.  A stream without work has first >= last.
 struct Share {
-    long long first, last, W, U0;
+    int first, last, W, U0;
     int b, streams;                // streams: those with work
 };
 template <int NT>
-struct ShareScratch {
-    long long wsum[NT / 32], found;
-    int found_b;
-};
+struct ShareScratch { int wsum[NT / 32], found, found_b; };
 
 // By the whole block: a thread sums some sequences, the block scans.  Zeroes the rows of invalid sequences.
 template <int NT, int D>
@@ -106,36 +110,37 @@ __device__ __forceinline__ Share share_of(const Params &p, ShareScratch<NT> &x)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + NT - 1) / NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    long long run = 0;
-    int bad = 0;
+    int run = 0, bad = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         const Seq s = seq_at(p, b);
         bad |= s.bad;
         run += tasks_of(s, p.Hkv);
     }
-    long long incl = run;
+    int incl = run;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(dev::FULL, incl, o);
+        const int v = __shfl_up_sync(dev::FULL, incl, o);
         if (lane >= o) incl += v;
     }
     if (lane == 31) x.wsum[warp] = incl;
     const int any_bad = __syncthreads_or(bad);
-    long long at = incl - run;
+    int at = incl - run;
     Share h;
     h.W = 0;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) at += x.wsum[w];
         h.W += x.wsum[w];
     }
     // (no more streams than tasks, so that each has one: the merge takes consecutive streams' parts)
-    h.streams = (int)min((long long)gridDim.x, max(h.W, 1ll));
+    h.streams = min((int)gridDim.x, max(h.W, 1));
     h.first = (int)blockIdx.x < h.streams ? share(h.W, h.streams, blockIdx.x) : h.W;
     h.last = (int)blockIdx.x < h.streams ? share(h.W, h.streams, blockIdx.x + 1) : h.W;
     if (h.first >= at && h.first < at + run) {
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            const long long n = tasks_of(seq_at(p, b), p.Hkv);
+            const int n = tasks_of(seq_at(p, b), p.Hkv);
             if (h.first < at + n) {
                 x.found_b = b;
                 x.found = at;
@@ -147,10 +152,12 @@ __device__ __forceinline__ Share share_of(const Params &p, ShareScratch<NT> &x)
     __syncthreads();
     if (any_bad) {
         if (tid == 0 && blockIdx.x == 0) dev::flag_error(p.err, PKV_DEVERR_SEQ_LEN);
+#pragma unroll 1
         for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
             const Seq s = seq_at(p, b);
             uint4 *dst = reinterpret_cast<uint4 *>(p.out + (size_t)s.row0 * p.Hq * D);
             if (s.bad == 1)
+#pragma unroll 1
                 for (size_t e = tid; e < (size_t)s.P * p.Hq * (D / 8); e += NT) dst[e] = make_uint4(0u, 0u, 0u, 0u);
         }
     }
@@ -170,30 +177,37 @@ __device__ __forceinline__ Share share_of(const Params &p, ShareScratch<NT> &x)
 struct Segment { int h, m, t0, t1; };
 struct Walk {
     Seq sq;
-    int b;
-    long long U0, last;
+    int b, U0, last;
     __device__ __forceinline__ Walk(const Params &p, const Share &s) : sq(seq_at(p, s.b)), b(s.b), U0(s.U0), last(s.last) {}
-    __device__ __forceinline__ Segment at(const Params &p, long long r)
+    __device__ __forceinline__ Segment at(const Params &p, int r)
     {
+#pragma unroll 1
         while (b + 1 < p.B && r >= U0 + tasks_of(sq, p.Hkv)) {
             U0 += tasks_of(sq, p.Hkv);
             sq = seq_at(p, ++b);
         }
-        const long long rel = r - U0;
-        const int unit = (int)(rel / max(sq.nt, 1));
+        const int rel = r - U0, unit = rel / max(sq.nt, 1);
         Segment g;
-        g.t0 = (int)(rel - (long long)unit * sq.nt);
+        g.t0 = rel - unit * sq.nt;
         g.h = unit / max(sq.rt, 1);
         g.m = unit - g.h * sq.rt;
-        g.t1 = max(g.t0 + 1, (int)min((long long)sq.nt, g.t0 + (last - r)));
+        g.t1 = max(g.t0 + 1, min(sq.nt, g.t0 + (last - r)));
         return g;
     }
     // The logical block of entry v of the list.
     __device__ __forceinline__ int block(int v) const { return v < sq.sb ? v : v - sq.sb + sq.b1; }
 };
 
-// The stream that holds task r of W.
-__device__ __forceinline__ int stream_of(long long r, long long W, int streams) { return (int)(((r + 1) * streams - 1) / W); }
+// The stream that holds task r of W: a guess, off by one at most, put right.
+__device__ __forceinline__ int stream_of(int r, int W, int streams)
+{
+    int c = min(streams - 1, (int)((float)(r + 1) * (float)streams / (float)W));
+#pragma unroll 1
+    while (c > 0 && share(W, streams, c) > r) --c;
+#pragma unroll 1
+    while (c + 1 < streams && share(W, streams, c + 1) <= r) ++c;
+    return c;
+}
 
 // ---- masks
 __device__ __forceinline__ uint32_t ones(int c) { return (1u << min(max(c, 0), BS)) - 1u; }
@@ -204,6 +218,7 @@ __device__ __forceinline__ int place_of(const Params &p, const Seq &s, int token
     if (!p.mask) return s.C + token;
     const unsigned long long *bits = p.mask + (size_t)(s.row0 + token) * p.words;
     int c = 0;
+#pragma unroll 1
     for (int w = 0; w < p.words; ++w) {
         const int left = s.P - 64 * w;
         if (left > 0) c += __popcll(__ldcg(bits + w) & (left >= 64 ? ~0ull : (1ull << left) - 1));
@@ -211,17 +226,25 @@ __device__ __forceinline__ int place_of(const Params &p, const Seq &s, int token
     return s.C + c - 1;
 }
 
-// Which of the 16 positions from p0 on a row sees, `valid` those that are there.
-__device__ __forceinline__ uint32_t seen16(const Params &p, const Seq &s, int token, int place, int p0, uint32_t valid)
+// The first word of a row's mask (0 for a chain), loaded ahead of its use.
+__device__ __forceinline__ unsigned long long first_word(const Params &p, const Seq &s, int token)
+{
+    return p.mask ? __ldcg(p.mask + (size_t)(s.row0 + token) * p.words) : 0ull;
+}
+
+// Which of the 16 positions from p0 on a row sees, `valid` those that are there; w0: its mask's first word.
+__device__ __forceinline__ uint32_t seen16(const Params &p, const Seq &s, int token, int place, unsigned long long w0, int p0, uint32_t valid)
 {
     uint32_t c = valid & ones((p.mask ? s.C : s.C + token + 1) - p0), d = 0;
     if (p.mask && p0 + BS > s.C) {
-        const unsigned long long *bits = p.mask + (size_t)(s.row0 + token) * p.words;
         const int off = p0 - s.C;                              // bit of the first position
         unsigned long long w;
         if (off < 0) {
-            w = __ldcg(bits) << -off;
+            w = w0 << -off;
+        } else if (off < 64 && p.words == 1) {
+            w = w0 >> off;
         } else {
+            const unsigned long long *bits = p.mask + (size_t)(s.row0 + token) * p.words;
             const int i = off >> 6, sh = off & 63;
             w = i < p.words ? __ldcg(bits + i) >> sh : 0ull;
             if (sh && i + 1 < p.words) w |= __ldcg(bits + i + 1) << (64 - sh);

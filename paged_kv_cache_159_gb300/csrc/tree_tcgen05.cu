@@ -7,12 +7,16 @@
 // even share of all tiles, and partial states of cut units are merged by the same second launch.
 //
 // Twenty warps, one CTA per SM.  Warps 0-3 and 4-7: softmax of q-tiles 0 and 1, a row per thread; 8, 9 issue S = Q K^T
-// of the q-tiles (M 128, N 64) and 10, 11 O += P V (M 128, N D, P from tensor memory); 12, 13 bring K, 16, 17 V, 14 Q.
-// S is double-buffered in tensor memory and P overwrites it, O stays there; S of tile J waits for P V of tile J - 2
-// of its q-tile.  One issuing thread per product and q-tile, since a thread issues a tcgen05.mma only every 36 to 60 ns.
+// of the q-tiles (M 128, N 64) and 10, 11 O += P V (M 128, N D, P from tensor memory); 12, 13 (16) bring K, 18, 19 (17) V, 14 Q;
+// 15 goes through the CTA's share ahead of them all and writes down each tile (its blocks, positions, masks and unit) in
+// a ring that the others read.  (Each of them going through it alone cost the two loaders, with a microsecond a
+// tile, twice what the copies take, and the others a microsecond or more a unit.)  S is double-buffered in tensor memory and P
+// overwrites it, O stays there; S of tile J waits for P V of tile J - 2 of its q-tile.  One issuing thread per product and
+// q-tile, since a thread issues a tcgen05.mma only every 36 to 60 ns.
 //   * bf16 pools: tensor copies with 128-byte swizzle straight into the operand rings.
 //   * FP8 and INT4 pools: bulk copies of the blocks as stored into staging rings, expanded (exactly) to f16 operand
-//     tiles by two warps for K and two for V; q to f16 by a power of two per row (warp 14), P in f16 times 2^8.  Four
+//     tiles by three warps for K and three for V, which take half tiles in turn; P in f16 times 2^8.  q goes to f16 by a power of two per row in a launch of its
+//     own (in the kernel, a warp took 8 us a unit for it).  Six
 //     expanding warps beside eight of softmax need registers moved between warpgroups (setmaxnreg: 96 a thread at
 //     launch, 144 for softmax, 64 for the others, which is the same sum).
 //   * V that must not meet the tensor core is zeroed in its operand tile before P V, by the warps that bring V:
@@ -34,7 +38,19 @@ constexpr int REG_LAUNCH = 96, REG_SOFTMAX = 144, REG_OTHER = 64;
 static_assert(256 * REG_SOFTMAX + 384 * REG_OTHER <= TC_THREADS * REG_LAUNCH, "registers that the launch has");
 constexpr uint32_t NEGATE_A = 1u << 13;        // instruction descriptor: A enters the product negated
 constexpr uint32_t TMEM_COLS = 512;            // S (and P over it): 2 buffers x 2 q-tiles x 64, O: 2 x D
-constexpr int LEAD = 16;                       // ring of tiles' masks: more than any warp runs ahead of another
+constexpr int LEAD = 16, STEP = 32 / TB;       // tiles that warp 15 writes down ahead, and at a time
+
+// A tile as warp 15 writes it down.
+struct TileInfo {
+    unsigned long long there, sure;            // bit per key: it is there; every row of the unit sees it
+    int tile[TB], pos[TB];                     // blocks: (block id * Hkv + head), -1 where there is none; first position
+    uint32_t bad[2];                           // bit per key: V kept from the tensor core (written by the V warps)
+    int b, L, P, row0;                         // the sequence
+    int hm, t, left, unit;                     // KV head and (from bit 24) row tile; tile of the unit, tiles left in the segment, in the unit
+    __device__ __forceinline__ int h() const { return hm & 0xffffff; }
+    __device__ __forceinline__ int m() const { return hm >> 24; }
+};
+static_assert(sizeof(TileInfo) == 88, "room");
 
 template <int D, int KIND>
 struct Tc {
@@ -42,17 +58,44 @@ struct Tc {
     static constexpr int NS = KIND == BF16 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 4);       // operand tiles of K and V
     static constexpr int TILE = KIND == BF16 ? BS * D * 2 : KIND == FP8 ? BS * D : int4::tile_bytes(D);
     static constexpr int RAW = TB * TILE;
-    static constexpr int NSG = KIND == BF16 ? 0 : KIND == FP8 && D == 128 ? 4 : D == 128 ? 6 : 8;     // staging tiles
+    static constexpr int NSG = KIND == BF16 ? 0 : KIND == FP8 && D == 128 ? 3 : 6;     // staging tiles
     static constexpr int QHALF = 2 * BM * 128, KHALF = BN * 128, KSTAGE = H * KHALF;
     static constexpr int K = H * QHALF, V = K + NS * KSTAGE, SK = V + NS * KSTAGE, SV = SK + NSG * RAW;
-    static constexpr int QEXP = SV + NSG * RAW;                    // int8 [256]
-    static constexpr int INFO = QEXP + (KIND == BF16 ? 0 : 256);      // u64 sure, live, bad [LEAD], then int got [LEAD]
-    static constexpr int BAR = INFO + LEAD * 28;
-    static constexpr int NRAW = KIND == BF16 ? NS : NSG;
-    static constexpr int BARS = 3 + 4 * NS + 4 + 4 + 4 + 2 + 1 + NRAW + 3 * NSG;
-    static constexpr int ALLOC = BAR + BARS * 8 + 16 + 1024;
-    static_assert(ALLOC <= 227 * 1024 && NS + NSG + 3 < LEAD && RAW % 128 == 0 && BAR % 8 == 0, "shared memory");
+    static constexpr int INFO = SV + NSG * RAW;                    // TileInfo [LEAD]
+    static constexpr int BAR = INFO + LEAD * (int)sizeof(TileInfo);
+    static constexpr int NRAW = KIND == BF16 ? 1 : NSG;            // landings that a V (K) warp looks at, each its own
+    static constexpr int BARS = 2 + 4 * NS + 4 + 4 + 4 + 2 + 1 + 2 * LEAD + (KIND == BF16 ? 2 : 4) * NRAW;
+    static constexpr int ALLOC = BAR + BARS * 8 + 8 + 1024;
+    static_assert(NSG % 3 == 0, "a staging place is one warp's");
+    static_assert(ALLOC <= 227 * 1024 && NS < LEAD && NSG < LEAD && RAW % 128 == 0 && BAR % 8 == 0, "shared memory");
 };
+
+// A bounded wait in few instructions: twenty warps of different code share the instruction cache, and what the unrolled
+// waits of pkv_device.cuh, 64-bit divisions and the like add (100 KB of code, a hit rate of 82 %) made a tile's softmax take
+// 1.2 to 2.9 us instead of 0.5.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity)
+{
+    if (__builtin_expect(dev::mbar_try_wait(bar, parity), 1)) return true;
+    const unsigned long long t0 = dev::globaltimer();
+#pragma unroll 1
+    while (!dev::mbar_try_wait_suspend(bar, parity, dev::WAIT_SUSPEND_NS))
+        if (dev::globaltimer() - t0 > dev::WAIT_NS) return false;
+    return true;
+}
+
+// 8 consecutive columns of this thread's lane (see tmem_ld32).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -86,23 +129,26 @@ __device__ __forceinline__ uint32_t clean_v(uint8_t *dst, uint32_t there16, uint
     constexpr int CHUNKS = D / 16;                                 // half a row a lane
     const int row = lane >> 1, part = lane & 1;
     uint4 *at = reinterpret_cast<uint4 *>(dst + (D == 128 ? part * HALF : 0) + row * 128 + (D == 128 ? 0 : part * 64));
-    bool odd = false;
-#pragma unroll
+    uint32_t lo = 0, hi = 0;                                       // the largest exponents
+#pragma unroll 2
     for (int c = 0; c < CHUNKS; ++c) {
         const uint4 v = at[c];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) odd |= (w[e] & EXP) == EXP || ((w[e] >> 16) & EXP) == EXP;
+        const uint32_t w[4] = {v.x & (EXP | EXP << 16), v.y & (EXP | EXP << 16), v.z & (EXP | EXP << 16), v.w & (EXP | EXP << 16)};
+        const uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+        lo = max(lo, m & 0xffffu);
+        hi = max(hi, m >> 16);
     }
+    bool odd = max(lo, hi) == EXP;
     odd |= __shfl_xor_sync(dev::FULL, (int)odd, 1) != 0;
     const bool is = (there16 >> row) & 1u, keep_out = is && !((sure16 >> row) & 1u) && odd;
     if (!is || keep_out) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < CHUNKS; ++c) at[c] = make_uint4(0u, 0u, 0u, 0u);
     }
     const uint32_t both = __ballot_sync(dev::FULL, keep_out);
     uint32_t rows = 0;
     if (both)
+#pragma unroll 1
         for (int r = 0; r < BS; ++r) rows |= ((both >> (2 * r)) & 1u) << r;
     return rows;
 }
@@ -120,33 +166,29 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     uint8_t *sm = smem_raw + ((1024u - (dev::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = dev::smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(dev::FULL, tid >> 5, 0);
-    unsigned long long *sure = reinterpret_cast<unsigned long long *>(sm + L::INFO), *there = sure + LEAD;
-    uint32_t *bad = reinterpret_cast<uint32_t *>(there + LEAD);    // [LEAD][2]
-    volatile int *got_k = reinterpret_cast<volatile int *>(bad + 2 * LEAD);
-    int8_t *qexp = reinterpret_cast<int8_t *>(sm + L::QEXP);
+    TileInfo *info = reinterpret_cast<TileInfo *>(sm + L::INFO);
     const uint32_t bars = base + L::BAR;
-    const uint32_t q_full = bars, q_ready = bars + 8, q_free = bars + 16;
-    auto k_full = [&](int s) { return bars + 8 * (3 + s); };
-    auto v_full = [&](int s) { return bars + 8 * (3 + NS + s); };
-    auto k_free = [&](int s) { return bars + 8 * (3 + 2 * NS + s); };
-    auto v_free = [&](int s) { return bars + 8 * (3 + 3 * NS + s); };
-    auto s_full = [&](int w, int J) { return bars + 8 * (3 + 4 * NS + 2 * w + (J & 1)); };
-    auto p_full = [&](int w, int J) { return bars + 8 * (7 + 4 * NS + 2 * w + (J & 1)); };
-    auto pv_done = [&](int w, int J) { return bars + 8 * (11 + 4 * NS + 2 * w + (J & 1)); };
-    auto o_free = [&](int w) { return bars + 8 * (15 + 4 * NS + w); };
-    const uint32_t never = bars + 8 * (17 + 4 * NS);
-    auto v_raw = [&](int x) { return bars + 8 * (18 + 4 * NS + x); };
-    auto k_raw = [&](int x) { return bars + 8 * (18 + 4 * NS + L::NRAW + x); };
-    auto raw_free = [&](bool isk, int x) { return bars + 8 * (18 + 4 * NS + L::NRAW + NSG + (isk ? 0 : NSG) + x); };
+    const uint32_t q_full = bars, q_free = bars + 8;
+    auto k_full = [&](int s) { return bars + 8 * (2 + s); };
+    auto v_full = [&](int s) { return bars + 8 * (2 + NS + s); };
+    auto k_free = [&](int s) { return bars + 8 * (2 + 2 * NS + s); };
+    auto v_free = [&](int s) { return bars + 8 * (2 + 3 * NS + s); };
+    auto s_full = [&](int w, int J) { return bars + 8 * (2 + 4 * NS + 2 * w + (J & 1)); };
+    auto p_full = [&](int w, int J) { return bars + 8 * (6 + 4 * NS + 2 * w + (J & 1)); };
+    auto pv_done = [&](int w, int J) { return bars + 8 * (10 + 4 * NS + 2 * w + (J & 1)); };
+    auto o_free = [&](int w) { return bars + 8 * (14 + 4 * NS + w); };
+    const uint32_t never = bars + 8 * (16 + 4 * NS);
+    auto told = [&](int J) { return bars + 8 * (17 + 4 * NS + J % LEAD); };                // tile J is written down
+    auto untold = [&](int J) { return bars + 8 * (17 + 4 * NS + LEAD + J % LEAD); };      // and nobody reads it any more
+    auto raw = [&](int x, int i) { return bars + 8 * (17 + 4 * NS + 2 * LEAD + x * L::NRAW + i); };       // landings of loader x
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::BAR + L::BARS * 8);
 
     if (tid == 0) {
         dev::mbar_init(q_full, 1);
-        dev::mbar_init(q_ready, 1);
-        dev::mbar_init(q_free, WIDE ? 10 : 2);                     // both S issuers (and the softmax warps: exponents)
+        dev::mbar_init(q_free, 2);                                 // both S issuers
         for (int s = 0; s < NS; ++s) {
-            dev::mbar_init(k_full(s), WIDE ? 2 : 1);               // the expanding warps, or the copy
-            dev::mbar_init(v_full(s), 2);                          // the expanding warps; the copy, and warp 17's look
+            dev::mbar_init(k_full(s), 2);                          // two warps each
+            dev::mbar_init(v_full(s), 2);
             dev::mbar_init(k_free(s), 2);                          // both q-tiles' S
             dev::mbar_init(v_free(s), 2);                          // both q-tiles' P V
         }
@@ -159,12 +201,12 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             dev::mbar_init(o_free(w), 4);
         }
         dev::mbar_init(never, 1);
-        for (int x = 0; x < L::NRAW; ++x) dev::mbar_init(v_raw(x), 1);
-        for (int x = 0; x < NSG; ++x) {
-            dev::mbar_init(k_raw(x), 1);
-            dev::mbar_init(raw_free(true, x), 1);
-            dev::mbar_init(raw_free(false, x), 1);
+        for (int J = 0; J < LEAD; ++J) {
+            dev::mbar_init(told(J), 1);
+            dev::mbar_init(untold(J), 2);                          // both P V issuers
         }
+        for (int x = 0; x < (WIDE ? 4 : 2); ++x)
+            for (int i = 0; i < L::NRAW; ++i) dev::mbar_init(raw(x, i), 1);
         dev::fence_barrier_init();
     }
     pdl_launch();
@@ -180,6 +222,8 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     auto tS = [&](int b, int w) { return tmem + (uint32_t)((2 * b + w) * BN); };
     auto tO = [&](int w) { return tmem + 256u + (uint32_t)(w * D); };
     const int nt = (int)(my.last - my.first), tokens = p.rows_unit / p.group;
+    auto wait = [&](uint32_t bar, int phase) { return wait_bar(bar, (uint32_t)phase & 1u); };
+    auto wait_all = [&](uint32_t bar, int phase) { return (bool)__all_sync(dev::FULL, wait_bar(bar, (uint32_t)phase & 1u)); };
 
     // (a warpgroup's registers are moved before its warps part)
     if (warp < 8) {
@@ -187,48 +231,56 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         // ============ softmax and output: a row per thread, all keys of a tile, all columns
         const int w = warp >> 2, q4 = warp & 3, rg = w * BM + 32 * q4 + lane;      // row of the unit
         const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
-        Walk walk(p, my);
-        int J = 0, Jw = 0, uq = 0;
+        int Jw = 0;                                                // this q-tile's tiles (two for a unit that it rests in)
         bool ok = true, cut_begins = false;
         int cut[META] = {};
-        for (long long r = my.first; ok && r < my.last; ++uq) {
-            const Segment g = walk.at(p, r);
-            const Seq &sq = walk.sq;
-            const int i0 = g.m * tokens, i1 = min(sq.P, i0 + tokens) - 1, rows = (i1 + 1 - i0) * p.group;
-            const bool whole = g.t0 == 0 && g.t1 == sq.nt;
-            const int slot = r == my.first ? 0 : 1;
-            if (g.t0 == 0 && !whole) {
+        for (int J = 0; ok && J < nt;) {
+            ok = wait_all(told(J), J / LEAD);
+            if (!ok) break;
+            Seq sq;                                                // (what the masks need of it)
+            const TileInfo &u = info[J % LEAD];
+            sq.L = u.L;
+            sq.P = u.P;
+            sq.C = u.L - u.P;
+            sq.row0 = u.row0;
+            const int b = u.b, h = u.h(), mt = u.m(), left = u.left, unit = u.unit, first_tile = u.t;
+            const int i0 = mt * tokens, i1 = min(sq.P, i0 + tokens) - 1, rows = (i1 + 1 - i0) * p.group;
+            const bool whole = left == unit;
+            const int slot = J == 0 ? 0 : 1;
+            if (first_tile == 0 && !whole) {
                 cut_begins = true;
                 cut[0] = rows;
-                cut[1] = stream_of(r + sq.nt - 1, my.W, my.streams);
+                cut[1] = stream_of(my.first + J + unit - 1, my.W, my.streams);
                 cut[2] = slot;
                 cut[3] = sq.row0;
-                cut[4] = g.h;
-                cut[5] = g.m;
-            }
-            const bool live = rg < rows;
-            float sc = fabsf(p.score_scale);
-            if constexpr (WIDE) {
-                ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(q_ready, (uint32_t)(uq & 1)));
-                if (!ok) break;
-                if (live) sc = row_scale(sc, qexp[rg]);
-                __syncwarp();
-                if (lane == 0) dev::mbar_arrive(q_free);
+                cut[4] = h;
+                cut[5] = mt;
             }
             if (rows <= BM * w) {                                  // this q-tile rests
-                J += g.t1 - g.t0;
-                r += g.t1 - g.t0;
+                // two tiles of nothing: after the first the unit's slot may be written over, and when the second
+                // is done the unit is past, so that of the barriers waited for next none is more than a phase away
+                for (int i = 0; i < 2 && ok; ++i, ++Jw) {
+                    ok = wait_all(s_full(w, Jw), Jw >> 1);
+                    if (ok && lane == 0) dev::mbar_arrive(p_full(w, Jw));
+                }
+                ok = ok && wait_all(pv_done(w, Jw - 1), (Jw - 1) >> 1);
+                J += left;
                 continue;
             }
+            const bool live = rg < rows;
             const int token = i0 + (live ? rg / p.group : 0), hh = live ? rg - (token - i0) * p.group : 0;
             const int place = p.mask && p.window ? place_of(p, sq, token) : sq.C + token;
+            const unsigned long long word = first_word(p, sq, token);
+            float sc = fabsf(p.score_scale);
+            if (WIDE && live) sc = row_scale(sc, __ldcg(p.q_up + ((size_t)b * p.max_q + token) * p.Hq + h * p.group + hh));
             sc = sc == sc ? fmaxf(sc, 1e-37f) : sc;                // (masked scores stay -infinity)
-            const int to = all_to(p, sq, i0), from = all_from(p, sq, i1);
             float m = -INFINITY, l = 0.f;
-            for (int t = g.t0; t < g.t1; ++t, ++J, ++Jw) {
-                ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(s_full(w, Jw), (uint32_t)((Jw >> 1) & 1)));
+            for (const int end = J + left; J < end; ++J, ++Jw) {
+                ok = wait_all(s_full(w, Jw), Jw >> 1);
                 if (!ok) break;
                 tc::fence_after_sync();
+                const volatile TileInfo &ti = info[J % LEAD];
+                const bool edge = ti.sure != ~0ull;
                 float x[BN];
                 {
                     uint32_t v0[32], v1[32];
@@ -241,21 +293,17 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                         x[32 + i] = __uint_as_float(v1[i]);
                     }
                 }
-                const int got = got_k[J % LEAD];
-                bool edge = got != (1 << TB) - 1;
+                if (__builtin_expect(edge, 0)) {
+                    const unsigned long long there = ti.there;
+                    unsigned long long see = 0;
+#pragma unroll 1
+                    for (int k = 0; live && k < TB; ++k)
+                        see |= (unsigned long long)seen16(p, sq, token, place, word, ti.pos[k], (uint32_t)(there >> (BS * k)) & 0xffffu) << (BS * k);
+                    const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
 #pragma unroll
-                for (int k = 0; k < TB; ++k) {
-                    const int p0 = walk.block(TB * t + k) * BS;
-                    edge |= p0 + BS > to || (p0 < from && p0 + BS > p.sinks);
-                }
-                if (edge) {
-#pragma unroll
-                    for (int k = 0; k < TB; ++k) {
-                        const int p0 = walk.block(TB * t + k) * BS;
-                        const uint32_t see = live ? seen16(p, sq, token, place, p0, (got >> k) & 1 ? ones(sq.L - p0) : 0u) : 0u;
-#pragma unroll
-                        for (int c = 0; c < BS; ++c)
-                            if (!((see >> c) & 1u)) x[BS * k + c] = -INFINITY;
+                    for (int c = 0; c < 32; ++c) {
+                        if (!((lo >> c) & 1u)) x[c] = -INFINITY;
+                        if (!((hi >> c) & 1u)) x[32 + c] = -INFINITY;
                     }
                 }
                 float mx4[4] = {x[0], x[1], x[2], x[3]};
@@ -265,33 +313,37 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                     for (int e = 0; e < 4; ++e) mx4[e] = c + 4 + e < BN ? tc::fmax3(mx4[e], x[c + e], x[c + 4 + e]) : fmaxf(mx4[e], x[c + e]);
                 const float top = tc::fmax3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
                 const float d = (top - m) * sc;
-                const bool raise = d > TAU || (m == -INFINITY && top > m), rescale = raise && m != -INFINITY;
+                const bool raise = live && (d > TAU || (m == -INFINITY && top > m)), rescale = raise && m != -INFINITY;
                 const float f = rescale ? dev::fast_exp2(-d) : 1.f;
                 if (raise) m = top;
-                const float nm = m == -INFINITY ? 0.f : -m, ns = nm * sc + SHIFT;
-                uint32_t pw[BN / 2];
-                const float2 sc2 = make_float2(sc, sc);
-                float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                auto put = [&](int e, float2 v) {
-                    const float2 pe = make_float2(dev::fast_exp2(v.x), dev::fast_exp2(v.y));
-                    ps[e & 1] = tc::fadd2(ps[e & 1], pe);
-                    pw[e] = WIDE ? dev::pack_f16x2(pe.x, pe.y) : dev::pack_bf16x2(pe.x, pe.y);
-                };
-                // m's product with the scale may join the exponents while its rounding is below 2^-16
-                if (!__any_sync(dev::FULL, fabsf(ns) > 256.f)) {
-                    const float2 ns2 = make_float2(ns, ns);
+                // m's product with the scale may join the exponents while its rounding is below 2^-16; else m goes first
+                const float nm = m == -INFINITY ? 0.f : -m;
+                float ns = nm * sc + SHIFT;
+                if (__builtin_expect(__any_sync(dev::FULL, live && fabsf(ns) > 256.f), 0)) {        // (what a row beyond the unit holds decides nothing)
+                    const float2 nm2 = make_float2(nm, nm);
 #pragma unroll
-                    for (int e = 0; e < BN / 2; ++e) put(e, tc::ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, ns2));
-                } else {
-                    const float2 nm2 = make_float2(nm, nm), sh2 = make_float2(SHIFT, SHIFT);
-#pragma unroll
-                    for (int e = 0; e < BN / 2; ++e) put(e, tc::ffma2(tc::fadd2(make_float2(x[2 * e], x[2 * e + 1]), nm2), sc2, sh2));
+                    for (int e = 0; e < BN / 2; ++e) {
+                        const float2 v = tc::fadd2(make_float2(x[2 * e], x[2 * e + 1]), nm2);
+                        x[2 * e] = v.x;
+                        x[2 * e + 1] = v.y;
+                    }
+                    ns = SHIFT;
                 }
-                const float2 ps2 = tc::fadd2(ps[0], ps[1]);
-                l = l * f + (ps2.x + ps2.y);
+                uint32_t pw[BN / 2];
+                const float2 sc2 = make_float2(sc, sc), ns2 = make_float2(ns, ns);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int e = 0; e < BN / 2; ++e) {
+                    const float2 v = tc::ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, ns2);
+                    const float2 pe = make_float2(dev::fast_exp2(v.x), dev::fast_exp2(v.y));
+                    sum[e & 1] = tc::fadd2(sum[e & 1], pe);
+                    pw[e] = WIDE ? dev::pack_f16x2(pe.x, pe.y) : dev::pack_bf16x2(pe.x, pe.y);
+                }
+                const float2 sum2 = tc::fadd2(sum[0], sum[1]);
+                l = l * f + (sum2.x + sum2.y);
                 tc::tmem_st32(tS(Jw & 1, w) + lane_off, pw);       // over this tile's S, which is read
-                if (__any_sync(dev::FULL, rescale)) {
-                    ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(pv_done(w, Jw - 1), (uint32_t)(((Jw - 1) >> 1) & 1)));
+                if (__builtin_expect(__any_sync(dev::FULL, rescale), 0)) {
+                    ok = wait_all(pv_done(w, Jw - 1), (Jw - 1) >> 1);
                     if (!ok) break;
                     tc::fence_after_sync();
 #pragma unroll 1
@@ -306,25 +358,38 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 }
                 tc::tmem_wait_st();
                 unsigned long long odd = 0;                        // positions whose V was kept from the tensor core
-                if (edge) {
-                    ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(v_full(J % NS), (uint32_t)((J / NS) & 1)));
+                if (__builtin_expect(edge, 0)) {
+                    ok = wait_all(v_full(J % NS), J / NS);
                     if (!ok) break;
-                    const volatile uint32_t *vb = bad + 2 * (J % LEAD);
-                    odd = vb[0] | (unsigned long long)vb[1] << 32;
+                    odd = ti.bad[0] | (unsigned long long)ti.bad[1] << 32;
+                }
+                int tiles[TB] = {}, ps[TB] = {};                   // (what is read below: the tile may be gone by then)
+                if (__builtin_expect(odd != 0, 0)) {
+#pragma unroll
+                    for (int k = 0; k < TB; ++k) {
+                        tiles[k] = ti.tile[k];
+                        ps[k] = ti.pos[k];
+                    }
                 }
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) dev::mbar_arrive(p_full(w, Jw));
-                if (edge) {
-                    if (odd) {                                     // their products, where this row sees them
-                        ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(pv_done(w, Jw), (uint32_t)((Jw >> 1) & 1)));
+                if (__builtin_expect(odd != 0, 0)) {               // their products, where this row sees them
+                    {
+                        ok = wait_all(pv_done(w, Jw), Jw >> 1);
                         if (!ok) break;
                         tc::fence_after_sync();
-                        for (unsigned long long left = odd; left; left &= left - 1) {
-                            const int j = __ffsll((long long)left) - 1, k = j / BS;
-                            const int blk = walk.block(TB * t + k), id = __ldcg(p.tables + (size_t)walk.b * p.MB + blk);
-                            const uint8_t *tile = p.value_cache + ((size_t)id * p.Hkv + g.h) * L::TILE;
-                            const uint32_t see = live ? seen16(p, sq, token, place, blk * BS, ones(sq.L - blk * BS)) : 0u;
+                        for (unsigned long long rest = odd; rest; rest &= rest - 1) {
+                            const int j = __ffsll((long long)rest) - 1;
+                            int at = 0, p0 = 0;
+#pragma unroll
+                            for (int k = 0; k < TB; ++k)
+                                if (k == j / BS) {
+                                    at = tiles[k];
+                                    p0 = ps[k];
+                                }
+                            const uint8_t *tile = p.value_cache + (size_t)at * L::TILE;
+                            const uint32_t see = live ? seen16(p, sq, token, place, word, p0, ones(sq.L - p0)) : 0u;
                             float pj = 0.f;
 #pragma unroll
                             for (int e = 0; e < BN / 2; ++e)
@@ -338,16 +403,16 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                                 }
                             const bool mine = (see >> (j % BS)) & 1u;
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t v[32];
-                                tc::tmem_ld32(tO(w) + lane_off + c, v);
+                            for (int c = 0; c < D; c += 8) {
+                                uint32_t v[8];
+                                tmem_ld8(tO(w) + lane_off + c, v);
                                 tc::tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
+                                for (int e = 0; e < 8; ++e) {
                                     const float y = v_element<D, KIND>(tile, j % BS, c + e);
                                     if (mine) v[e] = __float_as_uint(fmaf(pj, y, __uint_as_float(v[e])));
                                 }
-                                tc::tmem_st32(tO(w) + lane_off + c, v);
+                                tmem_st8(tO(w) + lane_off + c, v);
                                 tc::tmem_wait_st();
                             }
                         }
@@ -356,11 +421,11 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 }
             }
             if (!ok) break;
-            ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(pv_done(w, Jw - 1), (uint32_t)(((Jw - 1) >> 1) & 1)));
+            ok = wait_all(pv_done(w, Jw - 1), (Jw - 1) >> 1);
             if (!ok) break;
             tc::fence_after_sync();
             const float inv = l == 0.f ? 0.f : p.out_scale / l;
-            uint16_t *dst = p.out + ((size_t)(sq.row0 + token) * p.Hq + (size_t)g.h * p.group + hh) * D;
+            uint16_t *dst = p.out + ((size_t)(sq.row0 + token) * p.Hq + (size_t)h * p.group + hh) * D;
             const size_t pr = ((size_t)blockIdx.x * 2 + slot) * p.rows_unit + rg;
             if (!whole && live) reinterpret_cast<float2 *>(p.part_ml)[pr] = make_float2(m == -INFINITY ? m : m * sc, l);
 #pragma unroll 1
@@ -387,7 +452,6 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) dev::mbar_arrive(o_free(w));
-            r += g.t1 - g.t0;
         }
         if (!ok && lane == 0) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
         if (warp == 0 && lane < META) {
@@ -399,293 +463,236 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         }
     } else {
         fewer_registers<REG_OTHER>();
-    if (warp == 12 || warp == 16) {
-        // ============ K (12) and V (16): the copies, and for FP8 and INT4 half of each tile's expansion
-        const bool isk = warp == 12;
+    if (warp == 15) {
+        // ============ the tiles of the share, written down for the others, up to eight at a time: a block a lane
         Walk walk(p, my);
-        Segment g = walk.at(p, my.first);
-        long long r = my.first;
-        int t = g.t0, chunk = t, n = 0;                            // n: tiles issued
-        // table entries of 32 blocks (8 tiles from `chunk` on), and of the 32 after them
-        auto fetch = [&](int t0) {
-            const int v = TB * t0 + lane;
-            return v < walk.sq.nvb && v < TB * g.t1 ? __ldcg(p.tables + (size_t)walk.b * p.MB + walk.block(v)) : -2;
-        };
-        int cur = fetch(t), nxt = fetch(t + 8);
-        auto issue = [&]() {
-            const int id = __shfl_sync(dev::FULL, cur, TB * (t - chunk) + (lane & 3));
-            const bool good = lane < TB && id >= 0 && id < p.num_blocks;
-            if (isk && lane < TB && id != -2 && !good) dev::flag_error(p.err, PKV_DEVERR_BLOCK_ID);
-            const unsigned got = __ballot_sync(dev::FULL, good);
-            bool edge = false;
-            if (isk) {
-                if (lane == 0) got_k[n % LEAD] = (int)got;
-            } else {
-                // the positions that are there, and those that every row of the unit sees
-                const int p0 = walk.block(TB * t + (lane & 3)) * BS, i0 = g.m * tokens, i1 = min(walk.sq.P, i0 + tokens) - 1;
-                const uint32_t l16 = good ? ones(walk.sq.L - p0) : 0u;
-                uint32_t s16 = l16 & ones(all_to(p, walk.sq, i0) - p0);
-                if (p.window) s16 &= ~ones(all_from(p, walk.sq, i1) - p0) | ones(p.sinks - p0);
-                edge = __any_sync(dev::FULL, lane < TB && s16 != 0xffffu);
-                unsigned long long a = (unsigned long long)l16 << (16 * (lane & 3)), z = (unsigned long long)s16 << (16 * (lane & 3));
-                if (lane >= TB) a = z = 0;
-#pragma unroll
-                for (int o = 1; o < TB; o <<= 1) {
-                    a |= __shfl_xor_sync(dev::FULL, a, o);
-                    z |= __shfl_xor_sync(dev::FULL, z, o);
-                }
-                if (lane == 0) {
-                    there[n % LEAD] = a;
-                    sure[n % LEAD] = z;
-                    if (!WIDE && !edge) bad[2 * (n % LEAD)] = bad[2 * (n % LEAD) + 1] = 0;
-                }
-            }
-            const int tile = id * p.Hkv + g.h;
-            if constexpr (WIDE) {
-                const uint32_t bar = isk ? k_raw(n % NSG) : v_raw(n % NSG);
-                if (lane == 0) dev::mbar_arrive_expect_tx(bar, (uint32_t)(__popc(got) * L::TILE));
-                __syncwarp();
-                if (good) dev::bulk_g2s(base + (isk ? L::SK : L::SV) + (n % NSG) * L::RAW + lane * L::TILE,
-                                        (isk ? p.key_cache : p.value_cache) + (size_t)tile * L::TILE, L::TILE, bar);
-            } else {
-                // (V that needs looking at lands on v_raw, and warp 17 passes it on; it passes every tile, so that it is
-                // never a ring behind)
-                const int s = n % NS;
-                const uint32_t bar = isk ? k_full(s) : edge ? v_raw(s) : v_full(s);
-                if (lane == 0) {
-                    dev::mbar_arrive_expect_tx(bar, (uint32_t)(__popc(got) * L::TILE));
-                    if (!isk) dev::mbar_arrive(edge ? v_full(s) : v_raw(s));
-                }
-                __syncwarp();
-                if (good) {
-                    const uint32_t dst = base + (isk ? L::K : L::V) + s * L::KSTAGE + lane * (BS * 128);
-                    for (int hf = 0; hf < H; ++hf) tc::tma_load_3d(dst + hf * L::KHALF, isk ? &kmap : &vmap, hf * 64, 0, tile, bar);
-                }
-            }
-            ++n;
-            ++r;
-            if (r < my.last) {
-                if (++t == g.t1) {
-                    g = walk.at(p, r);
-                    t = chunk = g.t0;
-                    cur = fetch(t);
-                    nxt = fetch(t + 8);
-                } else if (t - chunk == 8) {
-                    chunk = t;
-                    cur = nxt;
-                    nxt = fetch(t + 8);
-                }
-            }
-        };
         bool ok = true;
         int J = 0;
-        if constexpr (WIDE) {
-            for (; J < nt; ++J) {
-                while (ok && n < nt && n < J + NSG) {
-                    if (n >= NSG) ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(raw_free(isk, n % NSG), (uint32_t)(((n - NSG) / NSG) & 1)));
-                    if (ok) issue();
-                }
-                ok = ok && __all_sync(dev::FULL, dev::mbar_wait_bounded(isk ? k_raw(J % NSG) : v_raw(J % NSG), (uint32_t)((J / NSG) & 1)));
-                if (ok && J >= NS) ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(isk ? k_free(J % NS) : v_free(J % NS), (uint32_t)(((J - NS) / NS) & 1)));
+        while (J < nt) {
+            const Segment g = walk.at(p, my.first + J);
+            // the table's entry of this lane's block, a step ahead of its use
+            auto fetch = [&](int t0) {
+                const int v = TB * t0 + lane;
+                return v < walk.sq.nvb && v < TB * g.t1 ? __ldcg(p.tables + (size_t)walk.b * p.MB + walk.block(v)) : -2;
+            };
+            const int i0 = g.m * tokens, i1 = min(walk.sq.P, i0 + tokens) - 1, to = all_to(p, walk.sq, i0), from = all_from(p, walk.sq, i1);
+            int next = fetch(g.t0);
+            for (int t = g.t0; t < g.t1; t += STEP) {
+                const int id = next, n = min(STEP, g.t1 - t), i = lane / TB, k = lane % TB;
+                next = fetch(t + STEP);
+                ok = __all_sync(dev::FULL, i >= n || J + i < LEAD || wait(untold(J + i), (J + i - LEAD) / LEAD));
                 if (!ok) break;
-                const uint8_t *src = sm + (isk ? L::SK : L::SV) + (J % NSG) * L::RAW;
-                uint8_t *dst = sm + (isk ? L::K : L::V) + (J % NS) * L::KSTAGE;
-                if (isk) {
-                    const int got = got_k[J % LEAD];
-                    for (int k = 0; k < 2; ++k)
-                        if ((got >> k) & 1) widen<D, KIND, L::KHALF>(src + k * L::TILE, dst + k * (BS * 128), true, lane);
-                } else {
-                    const unsigned long long l = there[J % LEAD], z = sure[J % LEAD];
-                    uint32_t b = 0;
-                    for (int k = 0; k < 2; ++k) {
-                        if ((l >> (16 * k)) & 0xffffu) widen<D, KIND, L::KHALF>(src + k * L::TILE, dst + k * (BS * 128), false, lane);
-                        __syncwarp();
-                        b |= clean_v<D, KIND, L::KHALF>(dst + k * (BS * 128), (uint32_t)(l >> (16 * k)) & 0xffffu, (uint32_t)(z >> (16 * k)) & 0xffffu, lane) << (16 * k);
+                const bool good = id >= 0 && id < p.num_blocks;
+                if (id != -2 && !good) dev::flag_error(p.err, PKV_DEVERR_BLOCK_ID);
+                if (i < n) {
+                    const int p0 = walk.block(TB * t + lane) * BS;
+                    const uint32_t l16 = good ? ones(walk.sq.L - p0) : 0u;
+                    uint32_t s16 = l16 & ones(to - p0);
+                    if (p.window) s16 &= ~ones(from - p0) | ones(p.sinks - p0);
+                    TileInfo &u = info[(J + i) % LEAD];
+                    u.tile[k] = good ? id * p.Hkv + g.h : -1;
+                    u.pos[k] = p0;
+                    reinterpret_cast<uint16_t *>(&u.there)[k] = (uint16_t)l16;
+                    reinterpret_cast<uint16_t *>(&u.sure)[k] = (uint16_t)s16;
+                    if (k == 0) {
+                        u.L = walk.sq.L;
+                        u.P = walk.sq.P;
+                        u.row0 = walk.sq.row0;
+                        u.b = walk.b;
+                        u.hm = g.h | g.m << 24;
+                        u.t = t + i;
+                        u.left = g.t1 - t - i;
+                        u.unit = walk.sq.nt;
                     }
-                    if (lane == 0) bad[2 * (J % LEAD)] = b;
                 }
-                dev::fence_proxy_async_smem();                     // expanded rows -> tensor core
                 __syncwarp();
-                if (lane == 0) dev::mbar_arrive(isk ? k_full(J % NS) : v_full(J % NS));
+                if (i < n && k == 0) dev::mbar_arrive(told(J + i));
+                J += n;
             }
-            // no copy may land after the CTA has left
-            for (int x = J; x < n; ++x) (void)dev::mbar_wait_bounded(isk ? k_raw(x % NSG) : v_raw(x % NSG), (uint32_t)((x / NSG) & 1));
-        } else {
-            for (; J < nt; ++J) {
-                if (J >= NS) ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(isk ? k_free(J % NS) : v_free(J % NS), (uint32_t)(((J - NS) / NS) & 1)));
-                if (!ok) break;
-                issue();
-            }
-            for (int x = max(0, n - NS); x < n; ++x) {
-                (void)dev::mbar_wait_bounded(isk ? k_full(x % NS) : v_raw(x % NS), (uint32_t)((x / NS) & 1));
-                if (!isk) (void)dev::mbar_wait_bounded(v_full(x % NS), (uint32_t)((x / NS) & 1));
-            }
+            if (!ok) break;
         }
         if (!ok && lane == 0) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
-    } else if (warp == 13 || warp == 17) {
-        // ============ the other half of K's (13) and V's (17) expansion; bf16: V that needs looking at (17)
-        const bool isk = warp == 13;
+    } else if (warp == 12 || warp == 13 || warp == 18 || warp == 19 || (WIDE && (warp == 16 || warp == 17))) {
+        // ============ K (12, 13, 16) and V (18, 19, 17): a job is two blocks of a tile
+        const bool isk = warp < 14 || warp == 16;
         bool ok = true;
-        for (int J = 0; J < nt && (WIDE || !isk); ++J) {
-            if constexpr (WIDE) {
-                ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(isk ? k_raw(J % NSG) : v_raw(J % NSG), (uint32_t)((J / NSG) & 1)));
-                if (ok && J >= NS) ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(isk ? k_free(J % NS) : v_free(J % NS), (uint32_t)(((J - NS) / NS) & 1)));
-                if (!ok) break;
-                const uint8_t *src = sm + (isk ? L::SK : L::SV) + (J % NSG) * L::RAW;
-                uint8_t *dst = sm + (isk ? L::K : L::V) + (J % NS) * L::KSTAGE;
-                if (isk) {
-                    const int got = got_k[J % LEAD];
-                    for (int k = 2; k < TB; ++k)
-                        if ((got >> k) & 1) widen<D, KIND, L::KHALF>(src + k * L::TILE, dst + k * (BS * 128), true, lane);
+        // the copies of job (J, half) to dst, landing on bar: lane i < 2 the i-th block's
+        auto issue = [&](int J, int half, uint32_t dst, uint32_t bar) {
+            const int tile = lane < 2 ? info[J % LEAD].tile[2 * half + lane] : -1;
+            const int got = __popc(__ballot_sync(dev::FULL, tile >= 0));
+            if (lane == 0) dev::mbar_arrive_expect_tx(bar, (uint32_t)(got * L::TILE));
+            __syncwarp();
+            if (tile >= 0) {
+                if constexpr (WIDE) {
+                    dev::bulk_g2s(dst + (2 * half + lane) * L::TILE, (isk ? p.key_cache : p.value_cache) + (size_t)tile * L::TILE, L::TILE, bar);
                 } else {
-                    const unsigned long long l = there[J % LEAD], z = sure[J % LEAD];
-                    uint32_t b = 0;
-                    for (int k = 2; k < TB; ++k) {
-                        if ((l >> (16 * k)) & 0xffffu) widen<D, KIND, L::KHALF>(src + k * L::TILE, dst + k * (BS * 128), false, lane);
-                        __syncwarp();
-                        b |= clean_v<D, KIND, L::KHALF>(dst + k * (BS * 128), (uint32_t)(l >> (16 * k)) & 0xffffu, (uint32_t)(z >> (16 * k)) & 0xffffu, lane) << (16 * (k - 2));
-                    }
-                    if (lane == 0) bad[2 * (J % LEAD) + 1] = b;
+                    for (int hf = 0; hf < H; ++hf)
+                        tc::tma_load_3d(dst + hf * L::KHALF + (2 * half + lane) * (BS * 128), isk ? &kmap : &vmap, hf * 64, 0, tile, bar);
                 }
-                dev::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    dev::mbar_arrive(isk ? k_full(J % NS) : v_full(J % NS));
-                    dev::mbar_arrive(raw_free(isk, J % NSG));
+            }
+        };
+        auto full = [&](int J) { return isk ? k_full(J % NS) : v_full(J % NS); };
+        auto room = [&](int J) { return J < NS || wait_all(isk ? k_free(J % NS) : v_free(J % NS), (J - NS) / NS); };
+        // what of a job's V must not meet the tensor core (see clean_v)
+        auto look = [&](int J, int half) {
+            TileInfo &u = info[J % LEAD];
+            uint8_t *dst = sm + L::V + (J % NS) * L::KSTAGE;
+            uint32_t b = 0;
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k)
+                b |= clean_v<D, KIND, L::KHALF>(dst + (2 * half + k) * (BS * 128), (uint32_t)(u.there >> (BS * (2 * half + k))) & 0xffffu,
+                                                (uint32_t)(u.sure >> (BS * (2 * half + k))) & 0xffffu, lane) << (BS * k);
+            if (lane == 0) u.bad[half] = b;
+        };
+        auto needs_look = [&](int J, int half) {
+            return !isk && __builtin_expect((uint32_t)(info[J % LEAD].sure >> (32 * half)) != 0xffffffffu, 0);
+        };
+        if constexpr (WIDE) {
+            // three warps take the jobs in turn, each with its own 2 NSG / 3 staging places
+            const int which = warp < 16 ? warp - 12 : warp == 16 || warp == 17 ? 2 : warp - 18, jobs = 2 * nt;
+            auto raw_of = [&](int q) { return raw((isk ? 2 : 0) + (q & 1), (q >> 1) % NSG); };
+            int n = which, q = which;                              // jobs issued, and done with
+            for (; q < jobs; q += 3) {
+                for (; ok && n < jobs && n < q + 2 * NSG; n += 3) {
+                    ok = wait_all(told(n >> 1), (n >> 1) / LEAD);
+                    if (ok) issue(n >> 1, n & 1, base + (isk ? L::SK : L::SV) + ((n >> 1) % NSG) * L::RAW, raw_of(n));
                 }
-            } else {
-                ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(v_raw(J % NS), (uint32_t)((J / NS) & 1)));
+                const int J = q >> 1, half = q & 1;
+                ok = ok && wait_all(raw_of(q), J / NSG) && room(J);
                 if (!ok) break;
-                const unsigned long long l = there[J % LEAD], z = sure[J % LEAD];
-                if (z != ~0ull) {
-                    uint8_t *dst = sm + L::V + (J % NS) * L::KSTAGE;
-                    unsigned long long b = 0;
-                    for (int k = 0; k < TB; ++k)
-                        b |= (unsigned long long)clean_v<D, KIND, L::KHALF>(dst + k * (BS * 128), (uint32_t)(l >> (16 * k)) & 0xffffu,
-                                                                           (uint32_t)(z >> (16 * k)) & 0xffffu, lane) << (16 * k);
-                    if (lane == 0) {
-                        bad[2 * (J % LEAD)] = (uint32_t)b;
-                        bad[2 * (J % LEAD) + 1] = (uint32_t)(b >> 32);
-                    }
+                const uint8_t *src = sm + (isk ? L::SK : L::SV) + (J % NSG) * L::RAW + 2 * half * L::TILE;
+                uint8_t *dst = sm + (isk ? L::K : L::V) + (J % NS) * L::KSTAGE + 2 * half * (BS * 128);
+                // (a block that is not there is expanded as well: whatever it holds is masked, or zeroed below)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) widen<D, KIND, L::KHALF>(src + k * L::TILE, dst + k * (BS * 128), isk, lane);
+                if (needs_look(J, half)) {
+                    __syncwarp();
+                    look(J, half);
+                } else if (!isk && lane == 0) {
+                    info[J % LEAD].bad[half] = 0;
+                }
+                dev::fence_proxy_async_smem();                     // expanded rows -> tensor core (and read before the next copy)
+                __syncwarp();
+                if (lane == 0) dev::mbar_arrive(full(J));
+            }
+            // no copy may land after the CTA has left
+            for (; q < n; q += 3) (void)wait(raw_of(q), (q >> 1) / NSG);
+        } else {
+            const int half = warp & 1;
+            int looks = 0, J = 0;
+            for (; J < nt; ++J) {
+                ok = wait_all(told(J), J / LEAD) && room(J);
+                if (!ok) break;
+                const bool l = needs_look(J, half);
+                if (!isk && lane == 0 && !l) info[J % LEAD].bad[half] = 0;
+                issue(J, half, base + (isk ? L::K : L::V) + (J % NS) * L::KSTAGE, l ? raw(half, 0) : full(J));
+                if (l) {
+                    ok = wait_all(raw(half, 0), looks++);
+                    if (!ok) break;
+                    look(J, half);
                     dev::fence_proxy_async_smem();                 // zeroed rows -> tensor core
                     __syncwarp();
+                    if (lane == 0) dev::mbar_arrive(full(J));
                 }
-                if (lane == 0) dev::mbar_arrive(v_full(J % NS));
             }
+            for (int i = max(0, J - NS); i < J; ++i) (void)wait(full(i), i / NS);
         }
         if (!ok && lane == 0) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 14) {
-        // ============ Q: eight tokens a copy, once the S before is done with its room; FP8 and INT4: to f16 in place
-        Walk walk(p, my);
+        // ============ Q: eight tokens a copy, once the S before is done with its room
         int uq = 0;
         bool pending = false;
         bool ok = __all_sync(dev::FULL, !p.test_stall || lane != 0 || dev::mbar_wait_bounded_ns(never, 0, dev::TEST_EXPIRE_NS));
-        for (long long r = my.first; ok && r < my.last; ++uq) {
-            const Segment g = walk.at(p, r);
-            const int i0 = g.m * tokens, copies = (min(tokens, walk.sq.P - i0) + 7) / 8;
-            if (uq > 0) ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(q_free, (uint32_t)((uq - 1) & 1)));
+        for (int J = 0; ok && J < nt; ++uq) {
+            // (in this order: a tile is waited for only once the one before it has been told, so that its barrier is
+            // not more than a phase away)
+            if (uq > 0) ok = wait_all(q_free, uq - 1);
+            ok = ok && wait_all(told(J), J / LEAD);
             if (!ok) break;
+            const TileInfo &u = info[J % LEAD];
+            const int i0 = u.m() * tokens, copies = (min(tokens, u.P - i0) + 7) / 8, h = u.h(), left = u.left;
+            const int row0 = WIDE ? u.b * p.max_q : u.row0;        // (q16 has room for max_q tokens of each sequence)
             if (lane == 0) dev::mbar_arrive_expect_tx(q_full, (uint32_t)(copies * H * 64 * p.group * 8 * 2));
             __syncwarp();
-            for (int x = lane; x < copies * H; x += 32) {
-                const int hf = x % H, c = x / H;
-                tc::tma_load_3d(base + hf * L::QHALF + c * (8 * p.group * 128), &qmap, hf * 64, g.h * p.group, walk.sq.row0 + i0 + 8 * c, q_full);
+            for (int i = lane; i < copies * H; i += 32) {
+                const int hf = i % H, c = i / H;
+                tc::tma_load_3d(base + hf * L::QHALF + c * (8 * p.group * 128), &qmap, hf * 64, h * p.group, row0 + i0 + 8 * c, q_full);
             }
             pending = true;
-            if constexpr (WIDE) {
-                ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(q_full, (uint32_t)(uq & 1)));
-                if (!ok) break;
-                pending = false;
-                const int rows = copies * 8 * p.group;
-                for (int row = lane; row < rows; row += 32) {
-                    uint4 *src = reinterpret_cast<uint4 *>(sm + row * 128);
-                    uint32_t top = 0;
-                    for (int x = 0; x < 8 * H; ++x) {              // (chunks in the row's swizzled order)
-                        const uint4 v = src[(x >> 3) * (L::QHALF / 16) + ((x ^ row) & 7)];
-                        const uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-                        top = max(top, max(m2 & 0xffffu, m2 >> 16));
-                    }
-                    const int up = q_exponent(top);
-                    const float f = q_factor(up);
-                    for (int x = 0; x < 8 * H; ++x) {
-                        uint4 *at = src + (x >> 3) * (L::QHALF / 16) + ((x ^ row) & 7);
-                        uint4 v = *at;
-                        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] = dev::pack_f16x2(dev::bf16_lo(w[e]) * f, dev::bf16_hi(w[e]) * f);
-                        *at = v;
-                    }
-                    qexp[row] = (int8_t)up;
-                }
-                dev::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) dev::mbar_arrive(q_ready);
-            }
-            r += g.t1 - g.t0;
+            J += left;
         }
         if (!ok && lane == 0) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
         // no copy may land after the CTA has left
-        if (pending) (void)dev::mbar_wait_bounded(q_full, (uint32_t)((ok ? uq - 1 : uq) & 1));
-    } else if (warp >= 8 && warp < 12) {
+        if (pending) (void)wait(q_full, ok ? uq - 1 : uq);
+    } else if (warp < 12 && lane == 0) {
         // ============ the products: warps 8, 9 S and 10, 11 P V of q-tiles 0, 1
-        if (lane == 0) {
-            const bool is_s = warp < 10;
-            const int w = warp & 1;
-            Walk walk(p, my);
-            int J = 0, Jw = 0, uq = 0, uw = 0;                     // tiles and units, and those of this q-tile
-            bool ok = true;
-            auto wait = [&](uint32_t bar, int par) {
-                if (ok && !dev::mbar_wait_bounded(bar, (uint32_t)par & 1u)) ok = false;
-                return ok;
-            };
-            const uint32_t IDS = (WIDE ? tc::idesc_f16(BM, BN, 0) : tc::idesc_bf16(BM, BN, 0)) | (p.score_scale < 0.f ? NEGATE_A : 0u);
-            constexpr uint32_t IDO = WIDE ? tc::idesc_f16(BM, D, 1) : tc::idesc_bf16(BM, D, 1);
-            const uint64_t dQ = tc::desc_add(tc::smem_desc_sw128(base, 16, 1024), (uint32_t)w * 16384);
-            const uint64_t dK = tc::smem_desc_sw128(base + L::K, 16, 1024), dV = tc::smem_desc_sw128(base + L::V, L::KHALF, 1024);
-            for (long long r = my.first; ok && r < my.last; ++uq) {
-                const Segment g = walk.at(p, r);
-                const bool active = min(tokens, walk.sq.P - g.m * tokens) * p.group > BM * w;
-                if (is_s && !wait(WIDE ? q_ready : q_full, uq)) break;
-                for (int t = g.t0; t < g.t1; ++t, ++J) {
-                    const int st = J % NS;
-                    if (!wait(is_s ? k_full(st) : v_full(st), J / NS)) break;
-                    if (!active) {
-                        dev::mbar_arrive(is_s ? k_free(st) : v_free(st));
-                        continue;
-                    }
-                    if (is_s) {
-                        // P V of the tile before last has read P, and the softmax its S
-                        if (Jw >= 2 && !wait(pv_done(w, Jw), (Jw - 2) >> 1)) break;
-                        tc::fence_after_sync();
-                        const uint64_t dk = tc::desc_add(dK, (uint32_t)st * L::KSTAGE);
-#pragma unroll
-                        for (int k = 0; k < 4 * H; ++k) {
-                            const uint32_t hf = k >> 2, kk = (k & 3) * 32;
-                            tc::mma_bf16(tS(Jw & 1, w), tc::desc_add(dQ, hf * L::QHALF + kk), tc::desc_add(dk, hf * L::KHALF + kk), IDS, k > 0);
-                        }
-                        tc::commit(s_full(w, Jw));
-                        tc::commit(k_free(st));
-                        if (t == g.t1 - 1) tc::commit(q_free);
-                    } else {
-                        if (!wait(p_full(w, Jw), Jw >> 1)) break;
-                        if (t == g.t0 && uw > 0 && !wait(o_free(w), uw - 1)) break;      // the unit before has been read
-                        tc::fence_after_sync();
-                        const uint64_t dv = tc::desc_add(dV, (uint32_t)st * L::KSTAGE);
-                        const uint32_t tp = tS(Jw & 1, w);
-#pragma unroll
-                        for (int k = 0; k < BN / 16; ++k)
-                            tc::mma_bf16_ts(tO(w), tp + (uint32_t)(k * 8), tc::desc_add(dv, k * 16 * 128), IDO, t > g.t0 || k > 0);
-                        tc::commit(v_free(st));
-                        tc::commit(pv_done(w, Jw));
-                    }
-                    ++Jw;
+        const bool is_s = warp < 10;
+        const int w = warp & 1;
+        int Jw = 0, uq = 0, uw = 0;                                // this q-tile's tiles; units, and those of this q-tile
+        bool ok = true;
+        const uint32_t IDS = (WIDE ? tc::idesc_f16(BM, BN, 0) : tc::idesc_bf16(BM, BN, 0)) | (p.score_scale < 0.f ? NEGATE_A : 0u);
+        constexpr uint32_t IDO = WIDE ? tc::idesc_f16(BM, D, 1) : tc::idesc_bf16(BM, D, 1);
+        const uint64_t dQ = tc::desc_add(tc::smem_desc_sw128(base, 16, 1024), (uint32_t)w * 16384);
+        const uint64_t dKV = is_s ? tc::smem_desc_sw128(base + L::K, 16, 1024) : tc::smem_desc_sw128(base + L::V, L::KHALF, 1024);
+        // Per tile three waits: the operand tile; S: P V of the tile before last has read P (and the softmax its S), P V:
+        // P is there; P V at a unit's start: the unit before has been read
+        for (int J = 0; ok && J < nt; ++uq) {
+            ok = wait(told(J), J / LEAD) && (!is_s || wait(q_full, uq));
+            if (!ok) break;
+            const TileInfo &u = info[J % LEAD];
+            const int end = J + u.left, J0 = J;
+            const bool active = min(tokens, u.P - u.m() * tokens) * p.group > BM * w;
+            // a unit that this q-tile rests in: a tile of nothing before it, which its softmax passes on when it has
+            // read the unit, and one behind it
+            for (int i = active ? 1 : 0; ok && (i == 0 || J < end || i == 2);) {
+                const bool nothing = !active && (J == end || i == 0);
+                const int st = J % NS;
+                if (!nothing) ok = wait(is_s ? k_full(st) : v_full(st), J / NS);
+                if (nothing || active) {
+                    if (is_s) ok = ok && (Jw < 2 || wait(pv_done(w, Jw), (Jw - 2) >> 1));
+                    else ok = ok && wait(p_full(w, Jw), Jw >> 1) && (!active || J > J0 || uw == 0 || wait(o_free(w), uw - 1));
                 }
-                if (is_s && !active && ok) dev::mbar_arrive(q_free);
-                if (active) ++uw;
-                r += g.t1 - g.t0;
+                if (!ok) break;
+                if (nothing) {
+                    dev::mbar_arrive(is_s ? s_full(w, Jw) : pv_done(w, Jw));
+                    ++Jw;
+                    if (i == 2) break;
+                    i = 1;
+                    continue;
+                }
+                if (!active) {
+                    dev::mbar_arrive(is_s ? k_free(st) : v_free(st));
+                    if (!is_s) dev::mbar_arrive(untold(J));
+                    if (++J == end) i = 2;
+                    continue;
+                }
+                tc::fence_after_sync();
+                const uint64_t d = tc::desc_add(dKV, (uint32_t)st * L::KSTAGE);
+                const uint32_t ts = tS(Jw & 1, w);
+                if (is_s) {
+#pragma unroll
+                    for (int k = 0; k < 4 * H; ++k) {
+                        const uint32_t hf = k >> 2, kk = (k & 3) * 32;
+                        tc::mma_bf16(ts, tc::desc_add(dQ, hf * L::QHALF + kk), tc::desc_add(d, hf * L::KHALF + kk), IDS, k > 0);
+                    }
+                    tc::commit(s_full(w, Jw));
+                    tc::commit(k_free(st));
+                    if (J == end - 1) tc::commit(q_free);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < BN / 16; ++k)
+                        tc::mma_bf16_ts(tO(w), ts + (uint32_t)(k * 8), tc::desc_add(d, k * 16 * 128), IDO, J > J0 || k > 0);
+                    tc::commit(v_free(st));
+                    tc::commit(pv_done(w, Jw));
+                    dev::mbar_arrive(untold(J));
+                }
+                ++Jw;
+                ++J;
             }
-            if (!ok) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
+            if (ok && is_s && !active) dev::mbar_arrive(q_free);
+            if (active) ++uw;
         }
+        if (!ok) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
     }
     }
     tc::fence_before_sync();
@@ -693,6 +700,37 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     if (warp == 15) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// q to f16 [batch][max_q][Hq][D] by a power of two per row and head, a warp each (see q_exponent).  Reads and writes q
+// once.
+constexpr int Q_WARPS = 8;
+template <int D>
+__global__ void __launch_bounds__(Q_WARPS * 32) tree_q_kernel(const Params p)
+{
+    pdl_launch();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    const Seq s = seq_at(p, b);
+    if (s.rt == 0) return;
+    for (int r = blockIdx.x * Q_WARPS + (threadIdx.x >> 5); r < s.P * p.Hq; r += gridDim.x * Q_WARPS) {
+        constexpr int N = D / 64;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + ((size_t)s.row0 * p.Hq + r) * D);
+        const size_t row = (size_t)b * p.max_q * p.Hq + r;
+        uint32_t w[N], top = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            w[i] = __ldcg(src + lane + 32 * i);
+            top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+        }
+        top = __reduce_max_sync(dev::FULL, top);
+        const int up = q_exponent(top);
+        const float f = q_factor(up);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            reinterpret_cast<uint32_t *>(p.q16 + row * D)[lane + 32 * i] = dev::pack_f16x2(dev::bf16_lo(w[i]) * f, dev::bf16_hi(w[i]) * f);
+        if (lane == 0) p.q_up[row] = (int8_t)up;
     }
 }
 
@@ -718,12 +756,19 @@ cudaError_t launch(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorM
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(TC_THREADS);
-    cfg.dynamicSmemBytes = Tc<D, KIND>::ALLOC;
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    if (KIND != BF16) {
+        // (a warp has up to four rows)
+        cfg.gridDim = dim3((unsigned)((p.max_q * p.Hq + 4 * Q_WARPS - 1) / (4 * Q_WARPS)), (unsigned)p.B);
+        cfg.blockDim = dim3(Q_WARPS * 32);
+        e = cudaLaunchKernelEx(&cfg, tree_q_kernel<D>, p);
+        if (e != cudaSuccess) return e;
+    }
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(TC_THREADS);
+    cfg.dynamicSmemBytes = Tc<D, KIND>::ALLOC;
     return cudaLaunchKernelEx(&cfg, kernel, qm, km, vm, p);
 }
 

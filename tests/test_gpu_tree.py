@@ -59,6 +59,17 @@ def test_units_cut_over_many_ctas(kind, new):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("Hq,new,most", [(16, 40, 2500), (32, 50, 700), (8, 18, 2500)])
+def test_many_tiles_and_units_a_cta(kind, Hq, new, most):
+    """Every CTA goes through many units and many times around its rings; units of one and two q-tiles in turn."""
+    rng = np.random.default_rng(new)
+    c = T.Case(rng.integers(0, most, 30), rng.integers(0, new + 1, 30), Hq, 8, 64, kind, seed=new, max_q=new)
+    out = c.run()
+    c.check(out)
+    assert all(torch.equal(c.run()[:c.T], out[:c.T]) for _ in range(10))
+
+
 def test_many_sequences_with_empty_ones_and_padding_rows():
     rng = np.random.default_rng(3)
     new = rng.integers(0, 6, 300)
