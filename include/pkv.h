@@ -545,7 +545,8 @@ int pkv_accept_rows(pkv_pool *pool, void *key_cache, void *value_cache, const in
  * alone, so that a captured graph serves any lengths; two launches; placement of the blocks changes no bit.  FP8 and
  * INT4 pools take q to fp16 with a power of two per row and query head that keeps its largest element in range.
  * Requires batch <= 4096, 1 <= max_q <= 256, num_q_heads a multiple of Hkv with group <= 16,
- * max_blocks <= 2^26, batch * max_blocks * Hkv * max(1, max_q * group / 128) < 2^31. */
+ * max_blocks <= 2^26, batch * max_blocks * Hkv < 2^31, batch * Hkv * ceil(max_q * group / 16) * (max_blocks / 4 + 7)
+ * < 2^31 (less is refused only where the work has more pieces than that). */
 size_t pkv_tree_workspace_bytes(const pkv_pool *pool, int32_t batch, int32_t num_q_heads, int32_t max_q);
 int pkv_paged_attention_tree(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
                              const int32_t *block_tables, const int32_t *seq_lens, const int32_t *cu_q,

@@ -90,8 +90,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     pdl_wait();
 
     const Share my = share_of<S::NT, D>(p, scratch);
-    const int first = my.first, last = my.last;
-    if (first >= last) return;
+    if (my.tiles == 0) return;
     Walk walk(p, my);
 
     if (warp == NC) {
@@ -105,8 +104,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
             }
         }
         // the table's entries, a tile ahead of their copies
-        int r = first;
-        Segment g = walk.at(p, r);
+        Segment g = walk.next(p);
         int t = g.t0, chunk = t;
         // the table's entries of 32 blocks (8 tiles from `chunk` on), and of the 32 after them
         auto fetch = [&](int t0) {
@@ -116,10 +114,9 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
         int ids = fetch(t), nxt = fetch(t + 8);
         while (true) {
             const int h = g.h, cur = __shfl_sync(dev::FULL, ids, TB * (t - chunk) + (lane & (TB - 1)));
-            ++r;
-            if (r < last) {
+            if (n + 1 < my.tiles) {
                 if (++t == g.t1) {
-                    g = walk.at(p, r);
+                    g = walk.next(p);
                     t = chunk = g.t0;
                     ids = fetch(t);
                     nxt = fetch(t + 8);
@@ -157,7 +154,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                 }
             }
             ++n;
-            if (r >= last) break;
+            if (n >= my.tiles) break;
         }
         if (!ok && lane == 0) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
         // no copy may land after the CTA has left: wait (bounded) for the last one of every stage
@@ -180,8 +177,9 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     int n = 0;                                                     // tiles seen
     bool cut_begins = false;
     int cut[META] = {};
-    for (int r = first; ok && r < last;) {
-        const Segment g = walk.at(p, r);
+    while (ok && n < my.tiles) {
+        const bool at_first = n == 0;                              // the share's first segment
+        const Segment g = walk.next(p);
         const Seq &sq = walk.sq;
         const int rows = sq.P * p.group - g.m * MR;                // of this unit, at most MR of them here
         // this lane's two rows
@@ -516,12 +514,12 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                 for (int c = 0; c < NS4; ++c) dst[4 * (c0 + c)] = dev::pack_bf16x2(o[c][2 * e] * inv, o[c][2 * e + 1] * inv);
             }
         } else {
-            const int slot = r == first ? 0 : 1;
+            const int slot = at_first ? 0 : 1;
             if (g.t0 == 0) {
                 // the unit goes on in the next CTAs, up to the one that holds its last task
                 cut_begins = true;
                 cut[0] = min(rows, MR);
-                cut[1] = stream_of(r + sq.nt - 1, my.W, my.streams);
+                cut[1] = stream_of(walk.unit0 + p.unit_cost + sq.nt - 1, my.W, my.streams);
                 cut[2] = slot;
                 cut[3] = sq.row0;
                 cut[4] = g.h;
@@ -531,13 +529,14 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
             for (int e = 0; e < 2; ++e) {
                 if (!live[e]) continue;
                 const size_t pr = ((size_t)blockIdx.x * 2 + slot) * MR + 16 * wr + gid + 8 * e;
-                float2 *dst = reinterpret_cast<float2 *>(p.part_o + pr * D) + t4;
+                const size_t s0 = (size_t)blockIdx.x * 2 + slot;
 #pragma unroll
-                for (int c = 0; c < NS4; ++c) dst[4 * (c0 + c)] = make_float2(o[c][2 * e], o[c][2 * e + 1]);
+                for (int c = 0; c < NS4; ++c)                      // columns 8 (c0 + c) + 2 t4, + 1
+                    *reinterpret_cast<float2 *>(p.part_o + ((s0 * (D / 4) + 2 * (c0 + c) + (t4 >> 1)) * MR + (pr - s0 * MR)) * 4 + 2 * (t4 & 1)) =
+                        make_float2(o[c][2 * e], o[c][2 * e + 1]);
                 if (wk == 0 && t4 == 0) reinterpret_cast<float2 *>(p.part_ml)[pr] = make_float2(m[e], l[e]);
             }
         }
-        r += max(g.t1 - g.t0, 1);
     }
     if (!ok && lane == 0) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
     if (warp == 0 && lane < META) {
@@ -549,13 +548,16 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     }
 }
 
-// Merge the partials of cut units: block (c, y) the rows 4 y .. of the unit that begins in CTA c, a warp a row.
-constexpr int MERGE_WARPS = 4;
+// Merge the partials of cut units: block (c, y) the rows MERGE_ROWS y .. of the unit that begins in stream c.  A warp takes
+// 8 rows and D / 4 columns of them, lane (row, c) columns 4 (c + 4 i) of its quarter ..: every load is four runs of 128
+// bytes.  Bound by reading the partials once (L2).
+constexpr int MERGE_ROWS = 8, MERGE_WARPS = 4;
 template <int D>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const Params p)
 {
-    constexpr int DPL = D / 32, BATCH = 8;
-    const int lane = threadIdx.x & 31, row = blockIdx.y * MERGE_WARPS + (threadIdx.x >> 5), c0 = blockIdx.x;
+    constexpr int NG = D / 4 / 4 / MERGE_WARPS, BATCH = 4;         // groups of 4 columns a lane; parts in flight
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y * MERGE_ROWS + (lane & 7), c0 = blockIdx.x;
+    const int g0 = warp * 4 * NG + (lane >> 3);
     pdl_launch();
     pdl_wait();
     const ::int4 *meta = reinterpret_cast<const ::int4 *>(p.meta + (size_t)c0 * META);
@@ -563,27 +565,25 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const Para
     if (row >= a.x) return;
     const ::int4 u = __ldcg(meta + 1);
     const int c1 = a.y, row0 = a.w, h = u.x, y = u.y * p.rows_unit + row, i = y / p.group, hh = y - i * p.group;
-    float M = -INFINITY, den = 0.f, num[DPL];
+    float M = -INFINITY, den = 0.f;
+    float4 num[NG];
 #pragma unroll
-    for (int x = 0; x < DPL; ++x) num[x] = 0.f;
+    for (int x = 0; x < NG; ++x) num[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int c = c0; c <= c1; c += BATCH) {
         float2 ml[BATCH];
-        float o[BATCH][DPL];
+        float4 o[BATCH][NG];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int x = 0; x < DPL; ++x) o[k][x] = 0.f;
+            for (int x = 0; x < NG; ++x) o[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (c + k <= c1) {
-                const size_t pr = ((size_t)(c + k) * 2 + (c + k == c0 ? a.z : 0)) * p.rows_unit + row;
-                ml[k] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + pr);
-                if constexpr (DPL == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + pr * D) + lane);
-                    o[k][0] = v.x; o[k][1] = v.y; o[k][2] = v.z; o[k][3] = v.w;
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.part_o + pr * D) + lane);
-                    o[k][0] = v.x; o[k][1] = v.y;
-                }
+                const size_t slot = (size_t)(c + k) * 2 + (c + k == c0 ? a.z : 0);
+                ml[k] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + slot * p.rows_unit + row);
+#pragma unroll
+                for (int x = 0; x < NG; ++x)
+                    o[k][x] = __ldcg(reinterpret_cast<const float4 *>(p.part_o) + (slot * (D / 4) + g0 + 4 * x) * p.rows_unit + row);
             }
         }
         float top = M;
@@ -593,22 +593,23 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const Para
         const float f = M == top ? 1.f : dev::fast_exp2(M - top);
         den *= f;
 #pragma unroll
-        for (int x = 0; x < DPL; ++x) num[x] *= f;
+        for (int x = 0; x < NG; ++x) num[x] = make_float4(num[x].x * f, num[x].y * f, num[x].z * f, num[x].w * f);
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             const float w = ml[k].x == top ? 1.f : dev::fast_exp2(ml[k].x - top);
             den = fmaf(ml[k].y, w, den);
 #pragma unroll
-            for (int x = 0; x < DPL; ++x) num[x] = fmaf(o[k][x], w, num[x]);
+            for (int x = 0; x < NG; ++x)
+                num[x] = make_float4(fmaf(o[k][x].x, w, num[x].x), fmaf(o[k][x].y, w, num[x].y), fmaf(o[k][x].z, w, num[x].z),
+                                     fmaf(o[k][x].w, w, num[x].w));
         }
         M = top;
     }
     const float inv = den == 0.f ? 0.f : p.out_scale / den;
-    uint16_t *dst = p.out + ((size_t)(row0 + i) * p.Hq + (size_t)h * p.group + hh) * D + lane * DPL;
-    if constexpr (DPL == 4)
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(dev::pack_bf16x2(num[0] * inv, num[1] * inv), dev::pack_bf16x2(num[2] * inv, num[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(dst) = dev::pack_bf16x2(num[0] * inv, num[1] * inv);
+    uint16_t *dst = p.out + ((size_t)(row0 + i) * p.Hq + (size_t)h * p.group + hh) * D;
+#pragma unroll
+    for (int x = 0; x < NG; ++x)
+        *reinterpret_cast<uint2 *>(dst + 4 * (g0 + 4 * x)) = make_uint2(dev::pack_bf16x2(num[x].x * inv, num[x].y * inv), dev::pack_bf16x2(num[x].z * inv, num[x].w * inv));
 }
 
 // ------------------------------------------------------------------------------------
@@ -628,6 +629,9 @@ int rows_per_unit(int max_q, int group)
     const int rows = max_q * group;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= MOST_MMA_ROWS ? 64 : tcgen05_tokens(group) * group;
 }
+
+// What a unit costs besides its tiles, in tiles (see places_of).
+constexpr int UNIT_COST = 3, UNIT_COST_TCGEN05 = 6;
 
 struct Room { int grid, rows; size_t o, ml, q, up, bytes; };
 Room room(const pkv_pool_desc &d, int batch, int max_q, int num_q_heads)
@@ -681,7 +685,7 @@ cudaError_t launch_merge(const Params &p, int grid, cudaStream_t s)
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)((p.rows_unit + MERGE_WARPS - 1) / MERGE_WARPS));
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)((p.rows_unit + MERGE_ROWS - 1) / MERGE_ROWS));
     cfg.blockDim = dim3(MERGE_WARPS * 32);
     cfg.stream = s;
     cfg.attrs = &attr;
@@ -713,9 +717,6 @@ int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_
         return PKV_ERR_INVALID;
     if (num_q_heads % d.num_kv_heads || num_q_heads / d.num_kv_heads > 16) return PKV_ERR_INVALID;
     if ((int64_t)batch * max_blocks * d.num_kv_heads >= (int64_t)1 << 31) return PKV_ERR_INVALID;
-    // (tiles of all units in 31 bits)
-    if ((int64_t)batch * max_blocks * d.num_kv_heads * std::max<int64_t>(1, (int64_t)max_q * (num_q_heads / d.num_kv_heads) / 128) >= (int64_t)1 << 31)
-        return PKV_ERR_INVALID;
     if (tree_mask && window > 0 && window < max_q) return PKV_ERR_INVALID;
     if (batch == 0 || total_q == 0) return PKV_OK;
     if (!q || !key_cache || !value_cache || !block_tables || !seq_lens || !out || !workspace) return PKV_ERR_INVALID;
@@ -724,6 +725,9 @@ int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_
         return PKV_ERR_INVALID;
     const int D = d.head_dim, group = num_q_heads / d.num_kv_heads;
     const Room rm = room(d, batch, max_q, num_q_heads);
+    // (places of all units, with their cost, in 31 bits)
+    const int64_t units = (int64_t)batch * d.num_kv_heads * (((int64_t)max_q * group + rm.rows - 1) / rm.rows);
+    if (units * ((max_blocks + TB - 1) / TB + std::max(UNIT_COST, UNIT_COST_TCGEN05)) >= (int64_t)1 << 31) return PKV_ERR_INVALID;
     const bool many = rm.rows > MOST_MMA_ROWS;
     if (rm.grid < 1) return PKV_ERR_CUDA;
     if (workspace_bytes < rm.bytes) return PKV_ERR_INVALID;
@@ -785,6 +789,7 @@ int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_
     p.window = window >= most ? 0 : window;
     p.sinks = std::min(sinks, most);
     p.rows_unit = rm.rows;
+    p.unit_cost = many ? UNIT_COST_TCGEN05 : UNIT_COST;
     p.test_stall = test_expire() == PKV_TEST_EXPIRE_DECODE;
     p.score_scale = scale * d.k_scale * LOG2E;
     p.out_scale = d.v_scale;

@@ -30,10 +30,10 @@ struct Params {
     const int32_t *tables, *lens, *cu;     // cu null: one row per sequence
     const unsigned long long *mask;        // [total_q][words], or null
     uint16_t *out;
-    float *part_o, *part_ml;               // [streams][2][rows_unit][D], [streams][2][rows_unit][2]
+    float *part_o, *part_ml;               // [streams][2][D / 4][rows_unit][4], [streams][2][rows_unit][2]
     int32_t *meta;                         // [streams][META]: the cut unit that begins in a stream
     uint32_t *err;
-    int B, MB, Hq, Hkv, group, num_blocks, total_q, max_q, words, window, sinks, rows_unit, test_stall;
+    int B, MB, Hq, Hkv, group, num_blocks, total_q, max_q, words, window, sinks, rows_unit, unit_cost, test_stall;
     float score_scale, out_scale;
 };
 
@@ -83,10 +83,13 @@ __device__ __forceinline__ Seq seq_at(const Params &p, int b)
     return s;
 }
 
-// (The host refuses shapes whose tasks could pass 31 bits.)
-__device__ __forceinline__ int tasks_of(const Seq &s, int Hkv) { return s.nt * s.rt * Hkv; }
+// The work is laid out unit after unit, a unit's unit_cost (what it costs besides its tiles, in tiles: its rows, its
+// edges, its output) and then its tiles; sequence after sequence, KV head after KV head, row tile after row tile.  (The
+// host refuses shapes whose places could pass 31 bits.)
+__device__ __forceinline__ int units_of(const Params &p, const Seq &s) { return s.rt * p.Hkv; }
+__device__ __forceinline__ int places_of(const Params &p, const Seq &s) { return units_of(p, s) * (s.nt + p.unit_cost); }
 
-// floor(W c / G), the even split of W tasks over G CTAs, in 32 bits: a 64-bit division is some hundred instructions.
+// floor(W c / G), the even split of W places over G streams, in 32 bits: a 64-bit division is some hundred instructions.
 __device__ __forceinline__ int share(int W, int G, int c)
 {
     const int q = W / G;
@@ -95,58 +98,71 @@ __device__ __forceinline__ int share(int W, int G, int c)
 
 
 // ---- the split of the work
-// Share of one stream of the grid: tasks first .. last - 1 of W, the first of them in sequence b, whose tasks begin
-// at U0.  A stream without work has first >= last.
+// Share of one stream of the grid: places first .. last - 1 of W, which hold `tiles` tiles; the first of them is in
+// sequence b, whose places begin at U0.
 struct Share {
-    int first, last, W, U0;
-    int b, streams;                // streams: those with work
+    int first, last, W, U0, tiles, b, streams;
 };
 template <int NT>
-struct ShareScratch { int wsum[NT / 32], found, found_b; };
+struct ShareScratch {
+    long long wsum[NT / 32];
+    int U0, b, tiles[2];           // tiles before the share's first and last place
+};
 
-// By the whole block: a thread sums some sequences, the block scans.  Zeroes the rows of invalid sequences.
+// By the whole block: a thread sums some sequences, the block scans (places in the upper half, tiles in the lower).
+// Zeroes the rows of invalid sequences.
 template <int NT, int D>
 __device__ __forceinline__ Share share_of(const Params &p, ShareScratch<NT> &x)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + NT - 1) / NT, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    int run = 0, bad = 0;
+    long long run = 0;
+    int bad = 0;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         const Seq s = seq_at(p, b);
         bad |= s.bad;
-        run += tasks_of(s, p.Hkv);
+        if (s.rt) run += ((long long)places_of(p, s) << 32) + units_of(p, s) * s.nt;
     }
-    int incl = run;
+    long long incl = run;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(dev::FULL, incl, o);
+        const long long v = __shfl_up_sync(dev::FULL, incl, o);
         if (lane >= o) incl += v;
     }
     if (lane == 31) x.wsum[warp] = incl;
     const int any_bad = __syncthreads_or(bad);
-    int at = incl - run;
-    Share h;
-    h.W = 0;
+    long long before = incl - run, all = 0;
 #pragma unroll 1
     for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) at += x.wsum[w];
-        h.W += x.wsum[w];
+        if (w < warp) before += x.wsum[w];
+        all += x.wsum[w];
     }
-    // (no more streams than tasks, so that each has one: the merge takes consecutive streams' parts)
-    h.streams = min((int)gridDim.x, max(h.W, 1));
+    Share h;
+    h.W = (int)(all >> 32);
+    h.streams = min((int)gridDim.x, max((int)all, 1));
     h.first = (int)blockIdx.x < h.streams ? share(h.W, h.streams, blockIdx.x) : h.W;
     h.last = (int)blockIdx.x < h.streams ? share(h.W, h.streams, blockIdx.x + 1) : h.W;
-    if (h.first >= at && h.first < at + run) {
+    int at = (int)(before >> 32), tiles = (int)before;
+    if (h.first < at + (int)(run >> 32) && h.last > at) {
+        // one of the two may fall into this thread's sequences
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            const int n = tasks_of(seq_at(p, b), p.Hkv);
-            if (h.first < at + n) {
-                x.found_b = b;
-                x.found = at;
-                break;
+            const Seq s = seq_at(p, b);
+            if (!s.rt) continue;
+            const int n = places_of(p, s), len = s.nt + p.unit_cost;
+            auto tiles_to = [&](int place) {
+                const int u = (place - at) / len;
+                return tiles + u * s.nt + max(0, place - at - u * len - p.unit_cost);
+            };
+            if (h.first >= at && h.first < at + n) {
+                x.b = b;
+                x.U0 = at;
+                x.tiles[0] = tiles_to(h.first);
             }
+            if (h.last > at && h.last <= at + n) x.tiles[1] = tiles_to(h.last);
             at += n;
+            tiles += units_of(p, s) * s.nt;
         }
     }
     __syncthreads();
@@ -161,44 +177,46 @@ __device__ __forceinline__ Share share_of(const Params &p, ShareScratch<NT> &x)
                 for (size_t e = tid; e < (size_t)s.P * p.Hq * (D / 8); e += NT) dst[e] = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    if (h.first >= h.last) {
-        if (tid < META) p.meta[(size_t)blockIdx.x * META + tid] = 0;
-        h.b = 0;
-        h.U0 = 0;
-    } else {
-        h.b = x.found_b;
-        h.U0 = x.found;
+    h.tiles = h.b = h.U0 = 0;
+    if (h.first < h.last) {
+        h.b = x.b;
+        h.U0 = x.U0;
+        h.tiles = x.tiles[1] - x.tiles[0];
     }
+    if (h.tiles == 0 && tid < META) p.meta[(size_t)blockIdx.x * META + tid] = 0;
     return h;
 }
 
-// The segment (tiles t0 .. t1 - 1 of one unit: KV head h, row tile m of sequence b) that holds task r; successive
-// calls move on from one to the next.
+// The segments of a share: tiles t0 .. t1 - 1 of one unit (KV head h, row tile m of sequence b), one after another.
+// (A share that ends among a unit's cost has no tile of it: its reader counts tiles.)  part0, part1: the streams with
+// the unit's first and last tile.
 struct Segment { int h, m, t0, t1; };
 struct Walk {
     Seq sq;
-    int b, U0, last;
-    __device__ __forceinline__ Walk(const Params &p, const Share &s) : sq(seq_at(p, s.b)), b(s.b), U0(s.U0), last(s.last) {}
-    __device__ __forceinline__ Segment at(const Params &p, int r)
+    int b, U0, place, last, unit0;             // unit0: the current unit's first place
+    __device__ __forceinline__ Walk(const Params &p, const Share &s) : sq(seq_at(p, s.b)), b(s.b), U0(s.U0), place(s.first), last(s.last), unit0(0) {}
+    __device__ __forceinline__ Segment next(const Params &p)
     {
 #pragma unroll 1
-        while (b + 1 < p.B && r >= U0 + tasks_of(sq, p.Hkv)) {
-            U0 += tasks_of(sq, p.Hkv);
+        while (b + 1 < p.B && (!sq.rt || place >= U0 + places_of(p, sq))) {
+            if (sq.rt) U0 += places_of(p, sq);
             sq = seq_at(p, ++b);
         }
-        const int rel = r - U0, unit = rel / max(sq.nt, 1);
+        const int len = max(sq.nt + p.unit_cost, 1), unit = (place - U0) / len;
+        unit0 = U0 + unit * len;
         Segment g;
-        g.t0 = rel - unit * sq.nt;
+        g.t0 = max(0, place - unit0 - p.unit_cost);
+        g.t1 = max(g.t0 + 1, min(sq.nt, last - unit0 - p.unit_cost));
         g.h = unit / max(sq.rt, 1);
         g.m = unit - g.h * sq.rt;
-        g.t1 = max(g.t0 + 1, min(sq.nt, g.t0 + (last - r)));
+        place = unit0 + p.unit_cost + g.t1;
         return g;
     }
     // The logical block of entry v of the list.
     __device__ __forceinline__ int block(int v) const { return v < sq.sb ? v : v - sq.sb + sq.b1; }
 };
 
-// The stream that holds task r of W: a guess, off by one at most, put right.
+// The stream that holds place r of W: a guess, off by one at most, put right.
 __device__ __forceinline__ int stream_of(int r, int W, int streams)
 {
     int c = min(streams - 1, (int)((float)(r + 1) * (float)streams / (float)W));
@@ -252,6 +270,30 @@ __device__ __forceinline__ uint32_t seen16(const Params &p, const Seq &s, int to
         d = (uint32_t)w & valid & ~ones(s.C - p0);
     }
     if (p.window) c &= ~ones(place - p.window + 1 - p0) | ones(p.sinks - p0);
+    return c | d;
+}
+
+// The same for the 64 consecutive positions from p0 on.
+__device__ __forceinline__ unsigned long long ones64(int c) { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; }
+__device__ __forceinline__ unsigned long long seen64(const Params &p, const Seq &s, int token, int place, unsigned long long w0, int p0,
+                                                     unsigned long long valid)
+{
+    unsigned long long c = valid & ones64((p.mask ? s.C : s.C + token + 1) - p0), d = 0;
+    if (p.mask && p0 + 64 > s.C) {
+        const int off = p0 - s.C, sh = off & 63;
+        if (off < 0) {
+            d = w0 << -off;                                        // (off > -64)
+        } else if (p.words == 1) {
+            d = off < 64 ? w0 >> off : 0ull;
+        } else {
+            const unsigned long long *bits = p.mask + (size_t)(s.row0 + token) * p.words;
+            const int i = off >> 6;
+            d = i < p.words ? __ldcg(bits + i) >> sh : 0ull;
+            if (sh && i + 1 < p.words) d |= __ldcg(bits + i + 1) << (64 - sh);
+        }
+        d &= valid & ~ones64(s.C - p0);
+    }
+    if (p.window) c &= ~ones64(place - p.window + 1 - p0) | ones64(p.sinks - p0);
     return c | d;
 }
 

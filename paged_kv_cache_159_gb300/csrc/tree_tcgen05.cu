@@ -46,7 +46,8 @@ struct TileInfo {
     int tile[TB], pos[TB];                     // blocks: (block id * Hkv + head), -1 where there is none; first position
     uint32_t bad[2];                           // bit per key: V kept from the tensor core (written by the V warps)
     int b, L, P, row0;                         // the sequence
-    int hm, t, left, unit;                     // KV head and (from bit 24) row tile; tile of the unit, tiles left in the segment, in the unit
+    int hm, left, unit, t_place;               // KV head and (from bit 24) row tile; tiles left in the segment, in the unit;
+                                               // the unit's place, bit 31: the segment begins after its first tile
     __device__ __forceinline__ int h() const { return hm & 0xffffff; }
     __device__ __forceinline__ int m() const { return hm >> 24; }
 };
@@ -212,7 +213,7 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     pdl_launch();
     pdl_wait();
     const Share my = share_of<TC_THREADS, D>(p, *reinterpret_cast<ShareScratch<TC_THREADS> *>(sm));      // (Q's room, not yet in use)
-    if (my.first >= my.last) return;
+    if (my.tiles == 0) return;
     if (warp == 15) tc::tmem_alloc(dev::smem_u32(tmem_slot), TMEM_COLS);
     tc::fence_before_sync();
     dev::fence_proxy_async_smem();
@@ -221,7 +222,7 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     const uint32_t tmem = *tmem_slot;
     auto tS = [&](int b, int w) { return tmem + (uint32_t)((2 * b + w) * BN); };
     auto tO = [&](int w) { return tmem + 256u + (uint32_t)(w * D); };
-    const int nt = (int)(my.last - my.first), tokens = p.rows_unit / p.group;
+    const int nt = my.tiles, tokens = p.rows_unit / p.group;
     auto wait = [&](uint32_t bar, int phase) { return wait_bar(bar, (uint32_t)phase & 1u); };
     auto wait_all = [&](uint32_t bar, int phase) { return (bool)__all_sync(dev::FULL, wait_bar(bar, (uint32_t)phase & 1u)); };
 
@@ -243,14 +244,14 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             sq.P = u.P;
             sq.C = u.L - u.P;
             sq.row0 = u.row0;
-            const int b = u.b, h = u.h(), mt = u.m(), left = u.left, unit = u.unit, first_tile = u.t;
+            const int b = u.b, h = u.h(), mt = u.m(), left = u.left, unit = u.unit, place0 = u.t_place;
             const int i0 = mt * tokens, i1 = min(sq.P, i0 + tokens) - 1, rows = (i1 + 1 - i0) * p.group;
             const bool whole = left == unit;
             const int slot = J == 0 ? 0 : 1;
-            if (first_tile == 0 && !whole) {
+            if (place0 >= 0 && !whole) {
                 cut_begins = true;
                 cut[0] = rows;
-                cut[1] = stream_of(my.first + J + unit - 1, my.W, my.streams);
+                cut[1] = stream_of(place0 + p.unit_cost + unit - 1, my.W, my.streams);
                 cut[2] = slot;
                 cut[3] = sq.row0;
                 cut[4] = h;
@@ -296,9 +297,14 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 if (__builtin_expect(edge, 0)) {
                     const unsigned long long there = ti.there;
                     unsigned long long see = 0;
+                    const int p0 = ti.pos[0];
+                    if (ti.pos[TB - 1] == p0 + (TB - 1) * BS) {
+                        if (live) see = seen64(p, sq, token, place, word, p0, there);
+                    } else {
 #pragma unroll 1
-                    for (int k = 0; live && k < TB; ++k)
-                        see |= (unsigned long long)seen16(p, sq, token, place, word, ti.pos[k], (uint32_t)(there >> (BS * k)) & 0xffffu) << (BS * k);
+                        for (int k = 0; live && k < TB; ++k)
+                            see |= (unsigned long long)seen16(p, sq, token, place, word, ti.pos[k], (uint32_t)(there >> (BS * k)) & 0xffffu) << (BS * k);
+                    }
                     const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
@@ -443,9 +449,10 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                         *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * e) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
                     }
                 } else if (live) {
-                    uint4 *o = reinterpret_cast<uint4 *>(p.part_o + pr * D + 32 * c);
+                    // (a warp's lanes are consecutive rows: 512 bytes a store)
+                    uint4 *o = reinterpret_cast<uint4 *>(p.part_o) + (((size_t)blockIdx.x * 2 + slot) * (D / 4) + 8 * c) * p.rows_unit + rg;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    for (int e = 0; e < 8; ++e) o[(size_t)e * p.rows_unit] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                 }
                 __syncwarp();
             }
@@ -469,7 +476,7 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         bool ok = true;
         int J = 0;
         while (J < nt) {
-            const Segment g = walk.at(p, my.first + J);
+            const Segment g = walk.next(p);
             // the table's entry of this lane's block, a step ahead of its use
             auto fetch = [&](int t0) {
                 const int v = TB * t0 + lane;
@@ -500,9 +507,9 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                         u.row0 = walk.sq.row0;
                         u.b = walk.b;
                         u.hm = g.h | g.m << 24;
-                        u.t = t + i;
                         u.left = g.t1 - t - i;
                         u.unit = walk.sq.nt;
+                        u.t_place = walk.unit0 | (g.t0 > 0 ? INT_MIN : 0);
                     }
                 }
                 __syncwarp();
@@ -714,23 +721,30 @@ __global__ void __launch_bounds__(Q_WARPS * 32) tree_q_kernel(const Params p)
     const int lane = threadIdx.x & 31, b = blockIdx.y;
     const Seq s = seq_at(p, b);
     if (s.rt == 0) return;
-    for (int r = blockIdx.x * Q_WARPS + (threadIdx.x >> 5); r < s.P * p.Hq; r += gridDim.x * Q_WARPS) {
-        constexpr int N = D / 64;
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + ((size_t)s.row0 * p.Hq + r) * D);
-        const size_t row = (size_t)b * p.max_q * p.Hq + r;
-        uint32_t w[N], top = 0;
+    constexpr int N = D / 64, R = 4;                               // a lane's words of a row; rows in flight
+    const int step = gridDim.x * Q_WARPS, end = s.P * p.Hq;
+    for (int r0 = blockIdx.x * Q_WARPS + (threadIdx.x >> 5); r0 < end; r0 += R * step) {
+        uint32_t w[R][N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            w[i] = __ldcg(src + lane + 32 * i);
-            top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+        for (int x = 0; x < R; ++x)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                w[x][i] = r0 + x * step < end ? __ldcg(reinterpret_cast<const uint32_t *>(p.q + ((size_t)s.row0 * p.Hq + r0 + x * step) * D) + lane + 32 * i) : 0u;
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+            if (r0 + x * step >= end) break;
+            const size_t row = (size_t)b * p.max_q * p.Hq + r0 + x * step;
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) top = max(top, max(w[x][i] & 0x7fffu, (w[x][i] >> 16) & 0x7fffu));
+            top = __reduce_max_sync(dev::FULL, top);
+            const int up = q_exponent(top);
+            const float f = q_factor(up);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                reinterpret_cast<uint32_t *>(p.q16 + row * D)[lane + 32 * i] = dev::pack_f16x2(dev::bf16_lo(w[x][i]) * f, dev::bf16_hi(w[x][i]) * f);
+            if (lane == 0) p.q_up[row] = (int8_t)up;
         }
-        top = __reduce_max_sync(dev::FULL, top);
-        const int up = q_exponent(top);
-        const float f = q_factor(up);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            reinterpret_cast<uint32_t *>(p.q16 + row * D)[lane + 32 * i] = dev::pack_f16x2(dev::bf16_lo(w[i]) * f, dev::bf16_hi(w[i]) * f);
-        if (lane == 0) p.q_up[row] = (int8_t)up;
     }
 }
 
