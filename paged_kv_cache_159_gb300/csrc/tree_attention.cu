@@ -39,30 +39,37 @@ namespace tree {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A tile as the copying warp writes it down; a segment's first tile says what unit it is of.
+struct TileNote {
+    int got, pos[TB];                                              // loaded blocks; first position of each
+    int L, P, row0, h, m, left, unit, place;                       // left: tiles of the segment; place: the unit's, bit 31: not from its first tile
+};
+
 template <int D, int KIND, int WR, int WK>
 struct Shape {
     static constexpr int NC = WR * WK, NT = NC * 32 + 32, MR = 16 * WR;
-    static constexpr int CTAS = NC > 4 ? 1 : 2;                    // per SM
     static constexpr int BT = BS * D * 2;                          // a block of K or V in 16 bits
     static constexpr int TILE = KIND == BF16 ? BT : KIND == FP8 ? BS * D : int4::tile_bytes(D);      // as stored
     static constexpr int STAGE = 2 * TB * TILE;
     // 16-bit tiles that FP8 and INT4 are expanded to: one where every warp expands its own keys, else two
     static constexpr int WIDE = 2 * TB * BT;
     static constexpr int NWIDE = KIND == BF16 ? 0 : WK == TB ? 1 : 2;
-    static constexpr int ROOM = (CTAS == 1 ? 220 : 110) * 1024;
-    static constexpr int NS_ = (ROOM - NWIDE * WIDE) / STAGE;
+    static constexpr int QB = MR * D * 2;                          // a unit's rows of q, the next one's while this one's are in registers
+    static constexpr int ROOM = 110 * 1024;                        // two CTAs per SM
+    static constexpr int NS_ = (ROOM - NWIDE * WIDE - QB) / STAGE;
     static constexpr int NS = NS_ > 8 ? 8 : NS_;
     static constexpr int RING = NWIDE * WIDE;                      // (STAGE of a quantised pool is a multiple of 128)
-    static constexpr int ML = RING + NS * STAGE;                   // (max, sum) of the key warps' rows
-    static constexpr int INFO = ML + NC * 16 * 8;                  // loaded blocks of every stage
-    static constexpr int BAR = INFO + 64;
-    static constexpr int ALLOC = BAR + 8 * (2 * NS + 2) + 1024;    // + alignment slack
-    static_assert(NS >= 2 && (CTAS == 1 ? ALLOC <= 227 * 1024 : ALLOC <= 113 * 1024), "shared memory");
+    static constexpr int Q = RING + NS * STAGE;
+    static constexpr int ML = Q + QB;                              // (max, sum) of the key warps' rows
+    static constexpr int INFO = ML + NC * 16 * 8;                  // TileNote of every stage
+    static constexpr int BAR = INFO + (NS * (int)sizeof(TileNote) + 7) / 8 * 8;
+    static constexpr int ALLOC = BAR + 8 * (2 * NS + 4) + 1024;    // + alignment slack
+    static_assert(NS >= 2 && ALLOC + 256 <= 113 * 1024, "shared memory");
     static_assert(TB % WK == 0 && STAGE % 128 == 0, "");
 };
 
 template <int D, int KIND, int WR, int WK>
-__global__ void __launch_bounds__(Shape<D, KIND, WR, WK>::NT, Shape<D, KIND, WR, WK>::CTAS)
+__global__ void __launch_bounds__(Shape<D, KIND, WR, WK>::NT, 2)
 tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Params p)
 {
     using S = Shape<D, KIND, WR, WK>;
@@ -75,8 +82,9 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(dev::FULL, tid >> 5, 0);
     auto full = [&](int s) { return base + S::BAR + 8 * s; };
     auto empty = [&](int s) { return base + S::BAR + 8 * (NS + s); };
-    const uint32_t meet = base + S::BAR + 8 * (2 * NS), never = meet + 8;
-    int32_t *info = reinterpret_cast<int32_t *>(sm + S::INFO);
+    const uint32_t meet = base + S::BAR + 8 * (2 * NS), never = meet + 8, q_full = meet + 16, q_free = meet + 24;
+    TileNote *info = reinterpret_cast<TileNote *>(sm + S::INFO);
+    auto wait_all = [&](uint32_t bar, int phase) { return (bool)__all_sync(dev::FULL, wait_bar(bar, (uint32_t)phase & 1u)); };
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
             dev::mbar_init(full(s), 1);
@@ -84,6 +92,8 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
         }
         dev::mbar_init(meet, NC);
         dev::mbar_init(never, 1);
+        dev::mbar_init(q_full, 32);                                // the copying warp's lanes
+        dev::mbar_init(q_free, NC);
         dev::fence_barrier_init();
     }
     pdl_launch();
@@ -91,74 +101,92 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 
     const Share my = share_of<S::NT, D>(p, scratch);
     if (my.tiles == 0) return;
-    Walk walk(p, my);
 
     if (warp == NC) {
-        // ============ the copying warp: lane k < TB takes block k of a tile, K and V
-        int n = 0;                                                 // tiles issued
+        // ============ the copying warp: lane k < TB takes block k of a tile, K and V; all of them a unit's rows of q
+        Walk walk(p, my);
         bool ok = true;
-        if (lane == 0) {
-            if constexpr (KIND == BF16) {
-                tc::prefetch_tensormap(&kmap);
-                tc::prefetch_tensormap(&vmap);
+        int n = 0;                                                 // tiles issued
+        for (int u = 0; ok && n < my.tiles; ++u) {
+            const Segment g = walk.next(p);
+            // the table's entries of 32 blocks (8 tiles from `chunk` on), and of the 32 after them
+            auto fetch = [&](int t0) {
+                const int v = TB * t0 + lane;
+                return v < walk.sq.nvb && v < TB * g.t1 ? __ldcg(p.tables + (size_t)walk.b * p.MB + walk.block(v)) : -2;
+            };
+            int chunk = g.t0, ids = fetch(chunk), nxt = fetch(chunk + 8);
+            // rows of q, 16 bytes a lane, chunks swizzled within 64 columns (rows beyond the unit's hold what they held)
+            if (u > 0) ok = wait_all(q_free, u - 1);
+            if (!ok) break;
+            {
+                constexpr int CH = D / 8, STEP = 32 / CH;          // chunks of a row; rows a pass
+                const int rows = min(MR, walk.sq.P * p.group - g.m * MR), c = lane % CH;
+                int x = lane / CH, y = g.m * MR + x, i = y / p.group, hh = y - i * p.group;
+                const uint16_t *src = p.q + ((size_t)walk.sq.row0 * p.Hq + (size_t)g.h * p.group) * D + 8 * c;
+#pragma unroll 1
+                for (; x < rows; x += STEP) {
+                    const uint32_t dst = base + S::Q + (c >> 3) * (MR * 128) + x * 128 + (((c & 7) ^ (x & 7)) << 4);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + ((size_t)i * p.Hq + hh) * D) : "memory");
+                    hh += STEP;
+                    while (hh >= p.group) {
+                        hh -= p.group;
+                        ++i;
+                    }
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(q_full) : "memory");
             }
-        }
-        // the table's entries, a tile ahead of their copies
-        Segment g = walk.next(p);
-        int t = g.t0, chunk = t;
-        // the table's entries of 32 blocks (8 tiles from `chunk` on), and of the 32 after them
-        auto fetch = [&](int t0) {
-            const int v = TB * t0 + lane;
-            return v < walk.sq.nvb && v < TB * g.t1 ? __ldcg(p.tables + (size_t)walk.b * p.MB + walk.block(v)) : -2;
-        };
-        int ids = fetch(t), nxt = fetch(t + 8);
-        while (true) {
-            const int h = g.h, cur = __shfl_sync(dev::FULL, ids, TB * (t - chunk) + (lane & (TB - 1)));
-            if (n + 1 < my.tiles) {
-                if (++t == g.t1) {
-                    g = walk.next(p);
-                    t = chunk = g.t0;
-                    ids = fetch(t);
-                    nxt = fetch(t + 8);
-                } else if (t - chunk == 8) {
+#pragma unroll 1
+            for (int t = g.t0; t < g.t1 && n < my.tiles; ++t, ++n) {
+                if (t - chunk == 8) {
                     chunk = t;
                     ids = nxt;
                     nxt = fetch(t + 8);
                 }
-            }
-            const int s = n % NS;
-            if (n >= NS) {
-                ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(empty(s), (uint32_t)(((n - NS) / NS) & 1)));
+                const int cur = __shfl_sync(dev::FULL, ids, TB * (t - chunk) + (lane & (TB - 1))), s = n % NS;
+                if (n >= NS) ok = wait_all(empty(s), (n - NS) / NS);
                 if (!ok) break;
-            }
-            const bool want = lane < TB && cur != -2, good = lane < TB && cur >= 0 && cur < p.num_blocks;
-            if (want && !good) dev::flag_error(p.err, PKV_DEVERR_BLOCK_ID);
-            const unsigned got = __ballot_sync(dev::FULL, good);
-            if (lane == 0) {
-                info[s] = (int)got;
-                dev::mbar_arrive_expect_tx(full(s), (uint32_t)(2 * S::TILE * __popc(got)));
-            }
-            __syncwarp();
-            if (good) {
-                const uint32_t dk = base + S::RING + s * S::STAGE + lane * S::TILE, dv = dk + TB * S::TILE;
-                const int tile = cur * p.Hkv + h;
-                if constexpr (KIND != BF16) {
-                    dev::bulk_g2s(dk, p.key_cache + (size_t)tile * S::TILE, S::TILE, full(s));
-                    dev::bulk_g2s(dv, p.value_cache + (size_t)tile * S::TILE, S::TILE, full(s));
-                } else if constexpr (D == 128) {
-                    tc::tma_load_4d(dk, &kmap, 0, 0, 0, tile, full(s));
-                    tc::tma_load_4d(dv, &vmap, 0, 0, 0, tile, full(s));
-                } else {
-                    tc::tma_load_3d(dk, &kmap, 0, 0, tile, full(s));
-                    tc::tma_load_3d(dv, &vmap, 0, 0, tile, full(s));
+                const bool want = lane < TB && cur != -2, good = lane < TB && cur >= 0 && cur < p.num_blocks;
+                if (want && !good) dev::flag_error(p.err, PKV_DEVERR_BLOCK_ID);
+                const unsigned got = __ballot_sync(dev::FULL, good);
+                TileNote &note = info[s];
+                if (lane < TB) note.pos[lane] = walk.block(TB * t + lane) * BS;
+                if (lane == 0) {
+                    note.got = (int)got;
+                    if (t == g.t0) {
+                        note.L = walk.sq.L;
+                        note.P = walk.sq.P;
+                        note.row0 = walk.sq.row0;
+                        note.h = g.h;
+                        note.m = g.m;
+                        note.left = g.t1 - t;
+                        note.unit = walk.sq.nt;
+                        note.place = walk.unit0 | (t > 0 ? INT_MIN : 0);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) dev::mbar_arrive_expect_tx(full(s), (uint32_t)(2 * S::TILE * __popc(got)));
+                __syncwarp();
+                if (good) {
+                    const uint32_t dk = base + S::RING + s * S::STAGE + lane * S::TILE, dv = dk + TB * S::TILE;
+                    const int tile = cur * p.Hkv + g.h;
+                    if constexpr (KIND != BF16) {
+                        dev::bulk_g2s(dk, p.key_cache + (size_t)tile * S::TILE, S::TILE, full(s));
+                        dev::bulk_g2s(dv, p.value_cache + (size_t)tile * S::TILE, S::TILE, full(s));
+                    } else if constexpr (D == 128) {
+                        tc::tma_load_4d(dk, &kmap, 0, 0, 0, tile, full(s));
+                        tc::tma_load_4d(dv, &vmap, 0, 0, 0, tile, full(s));
+                    } else {
+                        tc::tma_load_3d(dk, &kmap, 0, 0, tile, full(s));
+                        tc::tma_load_3d(dv, &vmap, 0, 0, tile, full(s));
+                    }
                 }
             }
-            ++n;
-            if (n >= my.tiles) break;
         }
         if (!ok && lane == 0) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
         // no copy may land after the CTA has left: wait (bounded) for the last one of every stage
-        for (int x = max(0, n - NS); x < n; ++x) (void)dev::mbar_wait_bounded(full(x % NS), (uint32_t)((x / NS) & 1));
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+        for (int x = max(0, n - NS); x < n; ++x) (void)wait_bar(full(x % NS), (uint32_t)((x / NS) & 1));
         return;
     }
 
@@ -169,7 +197,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     auto sync_warps = [&]() {                                      // all multiplying warps, bounded
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(meet);
-        ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(meet, meet_phase));
+        ok = wait_all(meet, (int)meet_phase);
         meet_phase ^= 1u;
         return ok;
     };
@@ -177,33 +205,40 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
     int n = 0;                                                     // tiles seen
     bool cut_begins = false;
     int cut[META] = {};
-    while (ok && n < my.tiles) {
+    for (int u = 0; ok && n < my.tiles; ++u) {
         const bool at_first = n == 0;                              // the share's first segment
-        const Segment g = walk.next(p);
-        const Seq &sq = walk.sq;
-        const int rows = sq.P * p.group - g.m * MR;                // of this unit, at most MR of them here
+        ok = wait_all(full(n % NS), n / NS) && wait_all(q_full, u);
+        if (!ok) break;
+        const TileNote &first = info[n % NS];
+        Seq sq;                                                    // (what the masks need of it)
+        sq.L = first.L;
+        sq.P = first.P;
+        sq.C = sq.L - sq.P;
+        sq.row0 = first.row0;
+        const int h = first.h, mt = first.m, left = first.left, unit = first.unit, place0 = first.place;
+        const int rows = sq.P * p.group - mt * MR;                 // of this unit, at most MR of them here
+        uint32_t qa[KS][4];
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int row = 16 * wr + (lane & 15), chunk = 2 * k + (lane >> 4);
+            dev::ldsm_x4(base + S::Q + (chunk >> 3) * (MR * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), qa[k]);
+        }
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(q_free);
         // this lane's two rows
-        int place[2], draft[2];                                    // p of the row; its token
+        int place[2], draft[2], head[2];                           // p of the row; its token; its head in the group
         bool live[2];
         unsigned long long word[2];                                // the first of its mask
-        uint32_t qa[KS][4];
         float sc[2] = {p.score_scale, p.score_scale};
-        size_t qrow[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int x = 16 * wr + gid + 8 * e;
             live[e] = x < rows;
-            const int y = g.m * MR + (live[e] ? x : 0), i = y / p.group, hh = y - i * p.group;
-            draft[e] = i;
-            qrow[e] = ((size_t)(sq.row0 + i) * p.Hq + (size_t)g.h * p.group + hh) * D;
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + qrow[e]);
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                qa[k][e] = live[e] ? __ldcg(src + 8 * k + t4) : 0u;
-                qa[k][e + 2] = live[e] ? __ldcg(src + 8 * k + t4 + 4) : 0u;
-            }
-            place[e] = p.mask && !p.window ? 0 : place_of(p, sq, i);
-            word[e] = first_word(p, sq, i);
+            const int y = mt * MR + (live[e] ? x : 0);
+            draft[e] = y / p.group;
+            head[e] = y - draft[e] * p.group;
+            place[e] = p.mask && !p.window ? 0 : place_of(p, sq, draft[e]);
+            word[e] = first_word(p, sq, draft[e]);
         }
         if constexpr (KIND != BF16) {
 #pragma unroll
@@ -231,35 +266,37 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[x][e] = 0.f;
         // positions up to which, and from which on, all rows of the unit see the cache
-        const int i0 = g.m * MR / p.group, i1 = min(sq.P - 1, (g.m * MR + min(rows, MR) - 1) / p.group);
+        const int i0 = mt * MR / p.group, i1 = min(sq.P - 1, (mt * MR + min(rows, MR) - 1) / p.group);
         const int to = all_to(p, sq, i0), from = all_from(p, sq, i1);
 
-        for (int t = g.t0; t < g.t1; ++t, ++n) {
+#pragma unroll 1
+        for (const int end = n + left; n < end; ++n) {
             const int s = n % NS;
-            ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(full(s), (uint32_t)((n / NS) & 1)));
+            ok = wait_all(full(s), n / NS);
             if (!ok) break;
-            const unsigned got = (unsigned)info[s];
+            const unsigned got = (unsigned)info[s].got;
+            int pos[NB];                                           // first position of each of this warp's blocks
+#pragma unroll
+            for (int k = 0; k < NB; ++k) pos[k] = info[s].pos[wk * NB + k];
             const uint8_t *stage = sm + S::RING + s * S::STAGE;
             uint32_t kt = base + S::RING + s * S::STAGE;           // the tile in 16 bits: TB blocks of K, TB of V
-            const bool at_end = t == g.t1 - 1;
+            const bool at_end = n == end - 1;
             if constexpr (KIND != BF16) {
                 uint8_t *wide = sm + (S::NWIDE == 2 ? (n & 1) * S::WIDE : 0);
                 kt = base + (S::NWIDE == 2 ? (n & 1) * S::WIDE : 0);
 #pragma unroll
                 for (int x = warp; x < 2 * TB; x += NC) {          // (block x % TB, K or V)
                     const int k = x % TB;
-                    if ((got >> k) & 1u) widen<D, KIND, BS * 128>(stage + x * S::TILE, wide + x * BT, x < TB, lane);
+                    if ((got >> k) & 1u) widen<D, KIND>(stage + x * S::TILE, wide + x * BT, BS * 128, x < TB, lane);
                 }
                 __syncwarp();
                 if (lane == 0) dev::mbar_arrive(empty(s));
                 if (WK != TB && !sync_warps()) break;
             }
             const uint32_t vt = kt + TB * BT;
-            int pos[NB];                                           // first position of each of this warp's blocks
             bool edge = false;
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
-                pos[k] = walk.block(TB * t + wk * NB + k) * BS;
                 edge |= !((got >> (wk * NB + k)) & 1u) || pos[k] + BS > to || (pos[k] < from && pos[k] + BS > p.sinks);
             }
             // ---- S = Q K^T
@@ -290,7 +327,7 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                 for (int e = 0; e < 4; ++e) x[k][e] *= sc[e >> 1];
             // ---- the mask of each 16 keys: bit j of see[k], row gid in the lower half, gid + 8 in the upper
             uint32_t see[NB];
-            if (edge) {
+            if (__builtin_expect(edge, 0)) {
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
                     see[k] = 0;
@@ -372,19 +409,20 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                 if (any & ~all) {
                     // positions that some rows do not see: those whose V is not finite go row by row
                     constexpr uint32_t EXP = KIND == BF16 ? 0x7f80u : 0x7c00u;
-                    uint32_t odd = 0;                              // this lane's four keys: 2 t4, + 1, + 8, + 9
-#pragma unroll 1
+                    uint32_t lo = 0, hi = 0;                       // largest exponents of keys 2 t4, + 1; + 8, + 9
+#pragma unroll 2
                     for (int dd = 0; dd < NN / 2; ++dd) {
                         uint32_t f[4];
                         load_v(dd, f);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if ((f[e] & EXP) == EXP) odd |= 1u << (2 * t4 + 8 * (e & 1));
-                            if (((f[e] >> 16) & EXP) == EXP) odd |= 2u << (2 * t4 + 8 * (e & 1));
-                        }
+                        lo = __vmaxu2(lo, __vmaxu2(f[0] & (EXP | EXP << 16), f[2] & (EXP | EXP << 16)));
+                        hi = __vmaxu2(hi, __vmaxu2(f[1] & (EXP | EXP << 16), f[3] & (EXP | EXP << 16)));
                     }
+                    uint32_t odd = ((lo & 0xffffu) == EXP ? 1u : 0u) | ((lo >> 16) == EXP ? 2u : 0u) | ((hi & 0xffffu) == EXP ? 0x100u : 0u) |
+                                   ((hi >> 16) == EXP ? 0x200u : 0u);
+                    odd <<= 2 * t4;
                     odd = __reduce_or_sync(dev::FULL, odd) & any & ~all;
                     keep &= ~odd;
+#pragma unroll 1
                     while (odd) {
                         const int j = __ffs(odd) - 1, from = (lane & ~3) | ((j & 7) >> 1);
                         odd &= odd - 1;
@@ -504,26 +542,26 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
                 for (int e = 0; e < 4; ++e) o[c][e] = acc[c][e];
         }
         const int c0 = wk * NS4;
-        if (g.t0 == 0 && g.t1 == sq.nt) {
+        if (left == unit) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 if (!live[e]) continue;
                 const float inv = l[e] == 0.f ? 0.f : p.out_scale / l[e];
-                uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + qrow[e]) + t4;
+                uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + ((size_t)(sq.row0 + draft[e]) * p.Hq + (size_t)h * p.group + head[e]) * D) + t4;
 #pragma unroll
                 for (int c = 0; c < NS4; ++c) dst[4 * (c0 + c)] = dev::pack_bf16x2(o[c][2 * e] * inv, o[c][2 * e + 1] * inv);
             }
         } else {
             const int slot = at_first ? 0 : 1;
-            if (g.t0 == 0) {
+            if (place0 >= 0) {
                 // the unit goes on in the next CTAs, up to the one that holds its last task
                 cut_begins = true;
                 cut[0] = min(rows, MR);
-                cut[1] = stream_of(walk.unit0 + p.unit_cost + sq.nt - 1, my.W, my.streams);
+                cut[1] = stream_of(place0 + p.unit_cost + unit - 1, my.W, my.streams);
                 cut[2] = slot;
                 cut[3] = sq.row0;
-                cut[4] = g.h;
-                cut[5] = g.m;
+                cut[4] = h;
+                cut[5] = mt;
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -622,12 +660,12 @@ int sm_count()
     return n;
 }
 
-// Rows per unit by the most rows of a sequence and KV head: 16, 32 or 64 on mma.sync, above that the tcgen05 kernel's.
-constexpr int MOST_MMA_ROWS = 64;
+// Rows per unit by the most rows of a sequence and KV head: 16 or 32 on mma.sync, above that the tcgen05 kernel's.
+constexpr int MOST_MMA_ROWS = 32;
 int rows_per_unit(int max_q, int group)
 {
     const int rows = max_q * group;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= MOST_MMA_ROWS ? 64 : tcgen05_tokens(group) * group;
+    return rows <= 16 ? 16 : rows <= MOST_MMA_ROWS ? 32 : tcgen05_tokens(group) * group;
 }
 
 // What a unit costs besides its tiles, in tiles (see places_of).
@@ -697,8 +735,7 @@ template <int D, int KIND>
 cudaError_t launch_rows(int mr, const CUtensorMap &km, const CUtensorMap &vm, const Params &p, int grid, cudaStream_t s)
 {
     if (mr == 16) return launch<D, KIND, 1, 4>(km, vm, p, grid, s);
-    if (mr == 32) return launch<D, KIND, 2, 2>(km, vm, p, grid, s);
-    return launch<D, KIND, 4, 1>(km, vm, p, grid, s);
+    return launch<D, KIND, 2, 2>(km, vm, p, grid, s);
 }
 
 bool aligned(const void *ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
@@ -735,17 +772,16 @@ int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_
     if (d.kv_dtype == PKV_KV_BF16) {
         const uint64_t tiles = (uint64_t)d.num_blocks * d.num_kv_heads;
         bool ok;
-        if (D == 128 && !many) {
-            const uint64_t dims[4] = {64, BS, 2, tiles}, strides[3] = {256, 128, 256 * BS};
-            const uint32_t box[4] = {64, BS, 2, 1};
-            ok = encode_tiled(&km, key_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
-                 encode_tiled(&vm, value_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-        } else {
-            const uint64_t dims[3] = {(uint64_t)D, BS, tiles}, strides[2] = {(uint64_t)D * 2, (uint64_t)D * 2 * BS};
-            const uint32_t box[3] = {64, BS, 1};
-            ok = encode_tiled_3d(&km, key_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
-                 encode_tiled_3d(&vm, value_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-        }
+        // a block in one copy, 64 columns after the other; for the tcgen05 kernel K's halves by themselves
+        const uint64_t dims[3] = {(uint64_t)D, BS, tiles}, strides[2] = {(uint64_t)D * 2, (uint64_t)D * 2 * BS};
+        const uint32_t box[3] = {64, BS, 1};
+        const uint64_t dims4[4] = {64, BS, 2, tiles}, strides4[3] = {256, 128, 256 * BS};
+        const uint32_t box4[4] = {64, BS, 2, 1};
+        auto map = [&](CUtensorMap *m, const void *cache, bool whole) {
+            return whole ? encode_tiled(m, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims4, strides4, box4, CU_TENSOR_MAP_SWIZZLE_128B)
+                         : encode_tiled_3d(m, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        };
+        ok = map(&km, key_cache, D == 128 && !many) && map(&vm, value_cache, D == 128);
         if (!ok) return PKV_ERR_CUDA;
     }
     uint8_t *ws = static_cast<uint8_t *>(workspace);

@@ -61,6 +61,9 @@ struct Tc {
     static constexpr int RAW = TB * TILE;
     static constexpr int NSG = KIND == BF16 ? 0 : KIND == FP8 && D == 128 ? 3 : 6;     // staging tiles
     static constexpr int QHALF = 2 * BM * 128, KHALF = BN * 128, KSTAGE = H * KHALF;
+    // K: [64 columns][64 keys], a copy per block and half row; V: block by block [64 columns][16 keys], as P V takes it,
+    // a copy per block
+    static constexpr int VHALF = BS * 128, VBLOCK = H * VHALF;
     static constexpr int K = H * QHALF, V = K + NS * KSTAGE, SK = V + NS * KSTAGE, SV = SK + NSG * RAW;
     static constexpr int INFO = SV + NSG * RAW;                    // TileInfo [LEAD]
     static constexpr int BAR = INFO + LEAD * (int)sizeof(TileInfo);
@@ -70,19 +73,6 @@ struct Tc {
     static_assert(NSG % 3 == 0, "a staging place is one warp's");
     static_assert(ALLOC <= 227 * 1024 && NS < LEAD && NSG < LEAD && RAW % 128 == 0 && BAR % 8 == 0, "shared memory");
 };
-
-// A bounded wait in few instructions: twenty warps of different code share the instruction cache, and what the unrolled
-// waits of pkv_device.cuh, 64-bit divisions and the like add (100 KB of code, a hit rate of 82 %) made a tile's softmax take
-// 1.2 to 2.9 us instead of 0.5.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity)
-{
-    if (__builtin_expect(dev::mbar_try_wait(bar, parity), 1)) return true;
-    const unsigned long long t0 = dev::globaltimer();
-#pragma unroll 1
-    while (!dev::mbar_try_wait_suspend(bar, parity, dev::WAIT_SUSPEND_NS))
-        if (dev::globaltimer() - t0 > dev::WAIT_NS) return false;
-    return true;
-}
 
 // 8 consecutive columns of this thread's lane (see tmem_ld32).
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
@@ -533,8 +523,12 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 if constexpr (WIDE) {
                     dev::bulk_g2s(dst + (2 * half + lane) * L::TILE, (isk ? p.key_cache : p.value_cache) + (size_t)tile * L::TILE, L::TILE, bar);
                 } else {
-                    for (int hf = 0; hf < H; ++hf)
-                        tc::tma_load_3d(dst + hf * L::KHALF + (2 * half + lane) * (BS * 128), isk ? &kmap : &vmap, hf * 64, 0, tile, bar);
+                    if (isk || H == 1) {
+                        for (int hf = 0; hf < H; ++hf)
+                            tc::tma_load_3d(dst + hf * L::KHALF + (2 * half + lane) * (BS * 128), isk ? &kmap : &vmap, hf * 64, 0, tile, bar);
+                    } else {
+                        tc::tma_load_4d(dst + (2 * half + lane) * L::VBLOCK, &vmap, 0, 0, 0, tile, bar);
+                    }
                 }
             }
         };
@@ -547,7 +541,7 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             uint32_t b = 0;
 #pragma unroll 1
             for (int k = 0; k < 2; ++k)
-                b |= clean_v<D, KIND, L::KHALF>(dst + (2 * half + k) * (BS * 128), (uint32_t)(u.there >> (BS * (2 * half + k))) & 0xffffu,
+                b |= clean_v<D, KIND, L::VHALF>(dst + (2 * half + k) * L::VBLOCK, (uint32_t)(u.there >> (BS * (2 * half + k))) & 0xffffu,
                                                 (uint32_t)(u.sure >> (BS * (2 * half + k))) & 0xffffu, lane) << (BS * k);
             if (lane == 0) u.bad[half] = b;
         };
@@ -568,10 +562,11 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 ok = ok && wait_all(raw_of(q), J / NSG) && room(J);
                 if (!ok) break;
                 const uint8_t *src = sm + (isk ? L::SK : L::SV) + (J % NSG) * L::RAW + 2 * half * L::TILE;
-                uint8_t *dst = sm + (isk ? L::K : L::V) + (J % NS) * L::KSTAGE + 2 * half * (BS * 128);
+                uint8_t *dst = sm + (isk ? L::K : L::V) + (J % NS) * L::KSTAGE + 2 * half * (isk ? BS * 128 : L::VBLOCK);
                 // (a block that is not there is expanded as well: whatever it holds is masked, or zeroed below)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) widen<D, KIND, L::KHALF>(src + k * L::TILE, dst + k * (BS * 128), isk, lane);
+                for (int k = 0; k < 2; ++k)
+                    widen<D, KIND>(src + k * L::TILE, dst + k * (isk ? BS * 128 : L::VBLOCK), isk ? L::KHALF : L::VHALF, isk, lane);
                 if (needs_look(J, half)) {
                     __syncwarp();
                     look(J, half);
@@ -640,7 +635,7 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         const uint32_t IDS = (WIDE ? tc::idesc_f16(BM, BN, 0) : tc::idesc_bf16(BM, BN, 0)) | (p.score_scale < 0.f ? NEGATE_A : 0u);
         constexpr uint32_t IDO = WIDE ? tc::idesc_f16(BM, D, 1) : tc::idesc_bf16(BM, D, 1);
         const uint64_t dQ = tc::desc_add(tc::smem_desc_sw128(base, 16, 1024), (uint32_t)w * 16384);
-        const uint64_t dKV = is_s ? tc::smem_desc_sw128(base + L::K, 16, 1024) : tc::smem_desc_sw128(base + L::V, L::KHALF, 1024);
+        const uint64_t dKV = is_s ? tc::smem_desc_sw128(base + L::K, 16, 1024) : tc::smem_desc_sw128(base + L::V, L::VHALF, 1024);
         // Per tile three waits: the operand tile; S: P V of the tile before last has read P (and the softmax its S), P V:
         // P is there; P V at a unit's start: the unit before has been read
         for (int J = 0; ok && J < nt; ++uq) {
@@ -688,7 +683,7 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 } else {
 #pragma unroll
                     for (int k = 0; k < BN / 16; ++k)
-                        tc::mma_bf16_ts(tO(w), ts + (uint32_t)(k * 8), tc::desc_add(d, k * 16 * 128), IDO, J > J0 || k > 0);
+                        tc::mma_bf16_ts(tO(w), ts + (uint32_t)(k * 8), tc::desc_add(d, (uint32_t)(k * L::VBLOCK)), IDO, J > J0 || k > 0);
                     tc::commit(v_free(st));
                     tc::commit(pv_done(w, Jw));
                     dev::mbar_arrive(untold(J));
