@@ -227,9 +227,11 @@ def _dev_ptr(t, what: str):
     return t.data_ptr()
 
 
-def _sized(t, n: int, what: str, size: int = 4):
-    if t.numel() != n or t.element_size() != size:
-        raise ValueError("%s must have %d entries of %d bytes" % (what, n, size))
+def _ints(t, n: int, what: str, size: int = 4):
+    """Device address of a contiguous CUDA tensor of n entries of `size` bytes."""
+    if not t.is_cuda or not t.is_contiguous() or t.nbytes != n * size:
+        raise ValueError("%s must be a contiguous CUDA tensor of %d entries of %d bytes" % (what, n, size))
+    return t.data_ptr()
 
 
 _current_raw_stream = None
@@ -554,15 +556,13 @@ def extend_tables(pool: Pool, seq_lens, cu_q, block_tables, reserve, state, new_
     (in place), reserve (blocks from Pool.alloc), state [2] (zeros at first; state[0] counts the ids
     used), positions [T] or None."""
     B, MB = block_tables.shape
-    _sized(seq_lens, B, "seq_lens"), _sized(cu_q, B + 1, "cu_q"), _sized(new_lens, B, "new_lens"), _sized(state, 2, "state")
-    if positions is not None:
-        _sized(positions, slots.numel(), "positions")
-    _sized(block_tables, B * MB, "block_tables"), _sized(reserve, reserve.numel(), "reserve"), _sized(slots, slots.numel(), "slots", 8)
-    _check(lib().pkv_extend_tables(pool.handle, _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(cu_q, "cu_q"), B, MB,
-                                   slots.numel(), _dev_ptr(block_tables, "block_tables"), _dev_ptr(reserve, "reserve"),
-                                   reserve.numel(), _dev_ptr(state, "state"), _dev_ptr(new_lens, "new_lens"),
-                                   _dev_ptr(slots, "slots"), _dev_ptr(positions, "positions"), _stream_ptr(stream)),
-           "extend_tables")
+    T, R = slots.shape[0], reserve.shape[0]
+    st = lib().pkv_extend_tables(pool.handle, _ints(seq_lens, B, "seq_lens"), _ints(cu_q, B + 1, "cu_q"), B, MB, T,
+                                 _ints(block_tables, B * MB, "block_tables"), _ints(reserve, R, "reserve"), R,
+                                 _ints(state, 2, "state"), _ints(new_lens, B, "new_lens"), _ints(slots, T, "slots", 8),
+                                 None if positions is None else _ints(positions, T, "positions"), _stream_ptr(stream))
+    if st:
+        _check(st, "extend_tables")
 
 
 def accept_rows(pool: Pool, key_cache, value_cache, block_tables, seq_lens, cu_q, path, num_accepted, lens_out, stream=None):
@@ -570,12 +570,13 @@ def accept_rows(pool: Pool, key_cache, value_cache, block_tables, seq_lens, cu_q
     (pkv_accept_rows): int32 CUDA seq_lens (with the drafts), num_accepted, lens_out [B], cu_q
     [B + 1], path [B, max_path]."""
     B, MB = block_tables.shape
-    _sized(seq_lens, B, "seq_lens"), _sized(cu_q, B + 1, "cu_q"), _sized(num_accepted, B, "num_accepted"), _sized(lens_out, B, "lens_out")
-    _sized(path, B * path.shape[1], "path"), _sized(block_tables, B * MB, "block_tables")
-    _check(lib().pkv_accept_rows(pool.handle, _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
-                                 _dev_ptr(block_tables, "block_tables"), _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(cu_q, "cu_q"),
-                                 _dev_ptr(path, "path"), _dev_ptr(num_accepted, "num_accepted"), B, MB, path.shape[1],
-                                 _dev_ptr(lens_out, "lens_out"), _stream_ptr(stream)), "accept_rows")
+    N = path.shape[1]
+    st = lib().pkv_accept_rows(pool.handle, _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
+                               _ints(block_tables, B * MB, "block_tables"), _ints(seq_lens, B, "seq_lens"), _ints(cu_q, B + 1, "cu_q"),
+                               _ints(path, B * N, "path"), _ints(num_accepted, B, "num_accepted"), B, MB, N,
+                               _ints(lens_out, B, "lens_out"), _stream_ptr(stream))
+    if st:
+        _check(st, "accept_rows")
 
 
 def tree_workspace_bytes(pool: Pool, batch: int, num_q_heads: int, max_q: int = 1) -> int:
@@ -589,17 +590,16 @@ def paged_attention_tree(pool: Pool, q, key_cache, value_cache, block_tables, se
     (pkv_paged_attention_tree).  q/out: bf16 CUDA [T, Hq, D]; seq_lens int32 CUDA [B] with the new
     tokens; cu_q int32 CUDA [B + 1]; tree_mask int64 CUDA [T, ceil(max_q / 64)], bit j of a row: it sees
     its sequence's new token j; workspace: CUDA uint8 of >= tree_workspace_bytes() bytes."""
-    T, Hq, _ = q.shape
+    T, Hq, D = q.shape
     B, MB = block_tables.shape
-    _sized(seq_lens, B, "seq_lens"), _sized(cu_q, B + 1, "cu_q"), _sized(out, q.numel(), "out", 2)
-    if tree_mask is not None:
-        _sized(tree_mask, T * ((int(max_q) + 63) // 64), "tree_mask", 8)
-    _check(lib().pkv_paged_attention_tree(pool.handle, _dev_ptr(q, "q"), _dev_ptr(key_cache, "key_cache"),
-                                          _dev_ptr(value_cache, "value_cache"), _dev_ptr(block_tables, "block_tables"),
-                                          _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(cu_q, "cu_q"), _dev_ptr(tree_mask, "tree_mask"),
-                                          B, Hq, MB, T, int(max_q), float(scale), int(window), int(sinks), _dev_ptr(out, "out"),
-                                          _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                                          _stream_ptr(stream)), "paged_attention_tree")
+    max_q, n = int(max_q), T * Hq * D
+    st = lib().pkv_paged_attention_tree(
+        pool.handle, _ints(q, n, "q", 2), _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
+        _ints(block_tables, B * MB, "block_tables"), _ints(seq_lens, B, "seq_lens"), _ints(cu_q, B + 1, "cu_q"),
+        None if tree_mask is None else _ints(tree_mask, T * ((max_q + 63) // 64), "tree_mask", 8), B, Hq, MB, T, max_q, scale,
+        window, sinks, _ints(out, n, "out", 2), _dev_ptr(workspace, "workspace"), workspace.nbytes, _stream_ptr(stream))
+    if st:
+        _check(st, "paged_attention_tree")
 
 
 def paged_attention_window(pool: Pool, q, key_cache, value_cache, block_tables, seq_lens, scale: float, window: int,
@@ -607,16 +607,14 @@ def paged_attention_window(pool: Pool, q, key_cache, value_cache, block_tables, 
     """Decode with a sliding window of the last `window` positions and the first `sinks`
     (pkv_paged_attention_window): q/out bf16 CUDA [B, Hq, D]; workspace: CUDA uint8 of >=
     tree_workspace_bytes(pool, B, Hq) bytes."""
-    B, Hq, _ = q.shape
-    _sized(seq_lens, B, "seq_lens"), _sized(out, q.numel(), "out", 2)
-    if block_tables.shape[0] != B:
-        raise ValueError("block_tables must have a row for each sequence")
-    _check(lib().pkv_paged_attention_window(pool.handle, _dev_ptr(q, "q"), _dev_ptr(key_cache, "key_cache"),
-                                            _dev_ptr(value_cache, "value_cache"), _dev_ptr(block_tables, "block_tables"),
-                                            _dev_ptr(seq_lens, "seq_lens"), B, Hq, block_tables.shape[1], float(scale),
-                                            int(window), int(sinks), _dev_ptr(out, "out"), _dev_ptr(workspace, "workspace"),
-                                            workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
-           "paged_attention_window")
+    B, Hq, D = q.shape
+    MB, n = block_tables.shape[1], B * Hq * D
+    st = lib().pkv_paged_attention_window(
+        pool.handle, _ints(q, n, "q", 2), _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
+        _ints(block_tables, B * MB, "block_tables"), _ints(seq_lens, B, "seq_lens"), B, Hq, MB, scale, window, sinks,
+        _ints(out, n, "out", 2), _dev_ptr(workspace, "workspace"), workspace.nbytes, _stream_ptr(stream))
+    if st:
+        _check(st, "paged_attention_window")
 
 
 def _opts(opts):

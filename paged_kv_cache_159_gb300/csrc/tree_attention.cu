@@ -653,30 +653,45 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const Para
 // ------------------------------------------------------------------------------------
 // Host side.
 // ------------------------------------------------------------------------------------
+// SMs of the current device, asked for once for each.
 int sm_count()
 {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
 // Rows per unit by the most rows of a sequence and KV head: 16 or 32 on mma.sync, above that the tcgen05 kernel's.
 constexpr int MOST_MMA_ROWS = 32;
-int rows_per_unit(int max_q, int group)
+int rows_per_unit(int max_q, int group, bool few)
 {
     const int rows = max_q * group;
-    return rows <= 16 ? 16 : rows <= MOST_MMA_ROWS ? 32 : tcgen05_tokens(group) * group;
+    return rows <= 16 ? 16 : rows <= MOST_MMA_ROWS || few ? 32 : tcgen05_tokens(group) * group;
 }
 
-// What a unit costs besides its tiles, in tiles (see places_of).
-constexpr int UNIT_COST = 3, UNIT_COST_TCGEN05 = 6;
+// Few tiles: even with the tables full, 32 rows at a time, no CTA of the mma.sync grid gets more than one.  Then a call is
+// the kernels' latency, which is less without tensor memory and twenty warps (13 drafts of 4 heads behind 60 positions,
+// 8 KV heads, in a graph: 12.6 us against 15.4; behind 1500, where CTAs would get more, 16.0 against 14.9).
+bool few_tiles(const pkv_pool_desc &d, int batch, int max_blocks, int max_q, int group)
+{
+    const int64_t tiles = (int64_t)batch * d.num_kv_heads * ((max_blocks + TB - 1) / TB) * (((int64_t)max_q * group + 31) / 32);
+    return tiles <= (int64_t)2 * sm_count();
+}
+
+// What a unit costs besides its tiles, in tiles (see places_of).  64 ragged sequences with 8 drafts: 65 us, 73 with a cost of
+// 1; 37 ragged trees on tcgen05: 70, 73 with 6, 78 with 10.
+constexpr int UNIT_COST = 3, UNIT_COST_TCGEN05 = 3;
 
 struct Room { int grid, rows; size_t o, ml, q, up, bytes; };
-Room room(const pkv_pool_desc &d, int batch, int max_q, int num_q_heads)
+Room room(const pkv_pool_desc &d, int batch, int max_q, int num_q_heads, bool few)
 {
     const int D = d.head_dim, group = num_q_heads / d.num_kv_heads;
     Room r;
-    r.rows = rows_per_unit(max_q, group);
+    r.rows = rows_per_unit(max_q, group, few);
     r.grid = sm_count() * (r.rows <= MOST_MMA_ROWS ? 2 : 1);
     r.o = ((size_t)r.grid * META * 4 + 255) / 256 * 256;
     r.ml = r.o + ((size_t)r.grid * 2 * r.rows * D * 4 + 255) / 256 * 256;
@@ -761,7 +776,7 @@ int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_
         !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(tree_mask, 8) || !aligned(workspace, 256))
         return PKV_ERR_INVALID;
     const int D = d.head_dim, group = num_q_heads / d.num_kv_heads;
-    const Room rm = room(d, batch, max_q, num_q_heads);
+    const Room rm = room(d, batch, max_q, num_q_heads, few_tiles(d, batch, max_blocks, max_q, group));
     // (places of all units, with their cost, in 31 bits)
     const int64_t units = (int64_t)batch * d.num_kv_heads * (((int64_t)max_q * group + rm.rows - 1) / rm.rows);
     if (units * ((max_blocks + TB - 1) / TB + std::max(UNIT_COST, UNIT_COST_TCGEN05)) >= (int64_t)1 << 31) return PKV_ERR_INVALID;
@@ -850,7 +865,8 @@ extern "C" size_t pkv_tree_workspace_bytes(const pkv_pool *pool, int32_t batch, 
         return 0;
     const int g = num_q_heads / pool->desc.num_kv_heads;
     if (g > 16 || sm_count() < 1) return 0;
-    return room(pool->desc, batch, max_q, num_q_heads).bytes;
+    // (which kernel a call takes depends on its max_blocks as well)
+    return std::max(room(pool->desc, batch, max_q, num_q_heads, false).bytes, room(pool->desc, batch, max_q, num_q_heads, true).bytes);
 }
 
 extern "C" int pkv_paged_attention_tree(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,

@@ -8,6 +8,7 @@ from oracle import int4 as O
 
 KINDS = {"bf16": pkv.KV_BF16, "fp8": pkv.KV_FP8E4M3, "int4": pkv.KV_INT4}
 K_SCALE, V_SCALE = 0.0131, 0.0087
+WIDTH = 0                                          # entries that a case's tables have at least: calls with few tiles take another kernel
 
 
 def dev(x) -> torch.Tensor:
@@ -100,7 +101,7 @@ class Case:
         self.drafts = [ancestors(tree_parents(int(p), rng)) if p else np.zeros((0, 0), bool) for p in self.P] if tree else [None] * len(self.P)
         self.see = [visible(int(c), int(p), window, sinks, d) for c, p, d in zip(self.C, self.P, self.drafts)]
         need = [-(-int(n) // 16) for n in self.L]
-        self.NB, self.MB = sum(need) + spare, max(max(need), width, 1)
+        self.NB, self.MB = sum(need) + spare, max(max(need), width, 1, WIDTH)
         order = np.random.default_rng(seed if order_seed is None else order_seed).permutation(self.NB)
         self.tables, at = np.full((len(need), self.MB), -1, np.int32), 0
         for b, n in enumerate(need):

@@ -15,6 +15,12 @@ def lib():
     return pkv.lib()
 
 
+@pytest.fixture(autouse=True, params=["narrow tables", "wide tables"])
+def width(request, monkeypatch):
+    """With narrow tables a small case has few tiles, and takes units of 32 rows whatever its drafts."""
+    monkeypatch.setattr(T, "WIDTH", 1500 if request.param == "wide tables" else 0)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Hq,Hkv,new", [(2, 2, [1, 5, 16]), (8, 2, [3, 4, 1]), (8, 2, [8, 5, 0, 7]), (14, 2, [9, 2, 8]),
@@ -78,7 +84,8 @@ def test_many_sequences_with_empty_ones_and_padding_rows():
     c.check(c.run())
 
 
-def test_every_length_of_a_sequence_without_rows_is_fine():
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_every_length_of_a_sequence_without_rows_is_fine(Hq):
     c = T.Case([20, 30, 40], [2, 0, 3], 4, 2, 64).attach()
     c.sl[1] = -7
     out = c.run()
@@ -88,8 +95,9 @@ def test_every_length_of_a_sequence_without_rows_is_fine():
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
-def test_a_row_that_sees_nothing_is_zero(kind):
-    c = T.Case([0, 40], [6, 5], 8, 2, 128, kind, seed=8)
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_a_row_that_sees_nothing_is_zero(kind, Hq):
+    c = T.Case([0, 40], [6, 5], Hq, 2, 128, kind, seed=8)
     c.drafts[0][:] = False
     c.drafts[0][2, [2]] = True
     c.see[0] = T.visible(0, 6, 0, 0, c.drafts[0])
@@ -132,31 +140,35 @@ def test_nan_and_infinity_stay_with_the_rows_that_see_them(kind, new, keys):
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
 @pytest.mark.parametrize("scale", [-0.09, 0.0, 3.0])
-def test_scales_of_any_sign(kind, scale):
-    c = T.Case([70, 200], [5, 9], 8, 2, 128, kind, scale=float(np.float32(scale)), seed=6)
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_scales_of_any_sign(kind, scale, Hq):
+    c = T.Case([70, 200], [5, 9], Hq, 2, 128, kind, scale=float(np.float32(scale)), seed=6)
     c.check(c.run())
 
 
 @pytest.mark.parametrize("kind", ["fp8", "int4"])
 @pytest.mark.parametrize("gain", [1e-30, 1e-3, 1e4, 1e30])
-def test_queries_of_any_size_over_quantised_pools(kind, gain):
-    c = T.Case([70, 20], [5, 9], 8, 2, 128, kind, q_gain=gain, scale=float(np.float32(0.09 / gain)), seed=6)
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_queries_of_any_size_over_quantised_pools(kind, gain, Hq):
+    c = T.Case([70, 20], [5, 9], Hq, 2, 128, kind, q_gain=gain, scale=float(np.float32(0.09 / gain)), seed=6)
     c.check(c.run())
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
-def test_placement_changes_no_bit_and_calls_repeat(kind):
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_placement_changes_no_bit_and_calls_repeat(kind, Hq):
     outs = []
     for order in (1, 2):
-        c = T.Case([700, 33, 2100], [9, 4, 6], 8, 2, 128, kind, seed=5, order_seed=order)
+        c = T.Case([700, 33, 2100], [9, 4, 6], Hq, 2, 128, kind, seed=5, order_seed=order)
         ws = c.attach().workspace()
         outs += [c.run(ws), c.run(ws)]
     assert all(torch.equal(outs[0][:c.T], o[:c.T]) for o in outs)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "int4"])
-def test_an_entry_outside_the_pool_is_flagged_and_not_seen(kind):
-    c = T.Case([100, 60], [3, 4], 8, 2, 128, kind, seed=7).attach()
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_an_entry_outside_the_pool_is_flagged_and_not_seen(kind, Hq):
+    c = T.Case([100, 60], [3, 4], Hq, 2, 128, kind, seed=7).attach()
     want = c.run()
     bt = c.bt.clone()
     c.bt[0, 2] = c.NB
@@ -169,10 +181,11 @@ def test_an_entry_outside_the_pool_is_flagged_and_not_seen(kind):
     assert torch.equal(c.run()[:c.T], want[:c.T])
 
 
-def test_bad_lengths_are_flagged_and_their_rows_zero():
-    c = T.Case([100, 60, 30, 20], [3, 4, 2, 5], 8, 2, 128, "bf16", seed=7, width=9, max_q=8).attach()
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_bad_lengths_are_flagged_and_their_rows_zero(Hq):
+    c = T.Case([100, 60, 30, 20], [3, 4, 2, 5], Hq, 2, 128, "bf16", seed=7, max_q=8).attach()
     good = c.sl.clone()
-    for b, L in ((1, 3), (1, 0), (1, -4), (2, 9 * 16 + 1), (3, 2 ** 31 - 1)):
+    for b, L in ((1, 3), (1, 0), (1, -4), (2, c.MB * 16 + 1), (3, 2 ** 31 - 1)):
         c.sl.copy_(good)
         c.sl[b] = L
         out = c.run(error=(pkv.ERR_DEVICE, pkv.DEVERR_SEQ_LEN))
@@ -186,8 +199,9 @@ def test_bad_lengths_are_flagged_and_their_rows_zero():
     c.check(out, skip=[3])
 
 
-def test_cu_q_out_of_range_writes_nothing_for_that_sequence():
-    c = T.Case([100, 60, 30], [3, 4, 2], 8, 2, 128, "bf16", seed=7, max_q=8).attach()
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_cu_q_out_of_range_writes_nothing_for_that_sequence(Hq):
+    c = T.Case([100, 60, 30], [3, 4, 2], Hq, 2, 128, "bf16", seed=7, max_q=8).attach()
     for cu in ([0, 3, 7, 10], [0, 3, 2, 9], [-1, 3, 7, 9], [0, 3, 7, 2 ** 31 - 1]):
         c.cq.copy_(torch.tensor(cu, dtype=torch.int32))
         out = c.run(error=(pkv.ERR_DEVICE, pkv.DEVERR_SEQ_LEN))
@@ -218,8 +232,9 @@ def test_refusals():
     assert c.pool.get_device_error() == (pkv.OK, 0)
 
 
-def test_a_captured_call_follows_the_lengths_and_graphs_share_a_workspace():
-    c = T.Case([100, 60, 333], [3, 8, 5], 8, 2, 128, "bf16", seed=1, pad=4, max_q=8).attach()
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_a_captured_call_follows_the_lengths_and_graphs_share_a_workspace(Hq):
+    c = T.Case([100, 60, 333], [3, 8, 5], Hq, 2, 128, "bf16", seed=1, pad=4, max_q=8).attach()
     ws, out = c.workspace(), torch.full_like(c.qd, float("nan"))
     sl, cq, mk, bt = c.sl.clone(), c.cq.clone(), c.mk.clone(), c.bt.clone()
 
@@ -233,7 +248,7 @@ def test_a_captured_call_follows_the_lengths_and_graphs_share_a_workspace():
         with torch.cuda.graph(g):
             call()
         graphs.append(g)
-    d = T.Case([17, 0, 40], [8, 8, 1], 8, 2, 128, "bf16", seed=2, max_q=8, spare=30, width=c.MB)
+    d = T.Case([17, 0, 40], [8, 8, 1], Hq, 2, 128, "bf16", seed=2, max_q=8, spare=30, width=c.MB)
     assert (d.NB, d.MB) == (c.NB, c.MB) and d.T < c.T + 4
     want_c, want_d = c.run(), d.run()
     for g in graphs:
@@ -251,8 +266,9 @@ def test_a_captured_call_follows_the_lengths_and_graphs_share_a_workspace():
     assert c.pool.get_device_error() == (pkv.OK, 0)
 
 
-def test_another_stream():
-    c = T.Case([100, 60, 333], [3, 8, 5], 8, 2, 128, "fp8", seed=1)
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_another_stream(Hq):
+    c = T.Case([100, 60, 333], [3, 8, 5], Hq, 2, 128, "fp8", seed=1)
     want = c.run()
     s, ws = torch.cuda.Stream(), c.workspace()
     out = torch.full_like(c.qd, float("nan"))
@@ -262,10 +278,11 @@ def test_another_stream():
     assert torch.equal(out, want)
 
 
-def test_offsets_past_32_bits():
+@pytest.mark.parametrize("Hq", [16, 128])
+def test_offsets_past_32_bits(Hq):
     """Blocks at the end of a cache of more than 2^32 bytes, and of more than 2^31 elements."""
     NB, Hkv, D = 150_000, 8, 128
-    c = T.Case([100, 60], [3, 4], 16, Hkv, D, "bf16", seed=3).attach()
+    c = T.Case([100, 60], [3, 4], Hq, Hkv, D, "bf16", seed=3).attach()
     far = torch.arange(NB - c.NB, NB, dtype=torch.int32, device="cuda")
     pool = pkv.Pool(NB, Hkv, D)
     pool.attach_device(torch.cuda.current_device())
@@ -279,8 +296,9 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
-def test_a_wait_that_runs_out_is_reported(kind):
-    c = T.Case([500, 60], [3, 9], 8, 2, 128, kind, seed=3)
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_a_wait_that_runs_out_is_reported(kind, Hq):
+    c = T.Case([500, 60], [3, 9], Hq, 2, 128, kind, seed=3)
     want = c.run()
     pkv.test_expire_waits(pkv.TEST_EXPIRE_DECODE)
     try:
