@@ -54,10 +54,12 @@
 //     are zeroed in shared memory before P.V, so whatever the cache holds there (unused
 //     tail slots, NaN included) never meets the tensor core: P is 0 there, but 0 x NaN is
 //     not.
-//   * A window (WIN) is the plan's: a unit's tiles are those of the sinks, then those from the first that
-//     its first row's window reaches, so that the work is the visible tiles'; a row's own limits join the causal
-//     mask in the tiles that they cross.  Blocks that no row of the unit sees are not loaded (their table
-//     entries may be empty), and V rows that none sees are zeroed as those past the last key are.  The plan's grid
+//   * A window (WIN) is the plan's: a unit's blocks are those of the sinks, then those from the first that
+//     its first row's window reaches, four of them in turn to a tile, so that the work is the visible blocks'; a
+//     row's own limits join the causal mask in the tiles that they cross.  Other blocks are not loaded (their table
+//     entries may be empty), and V rows that no row of the unit sees are zeroed as those past the last key are.
+//     16 chunks of 512 behind up to 8192 positions, window 1024, 4 sinks (32 / 8 heads, D 128): WIN_US us, WIN_TF TFLOP/s; bound
+//     as without a window, and by the three tile-times that a unit costs besides its some 18 tiles.  The plan's grid
 //     carries the kind (WINDOWED), since the launch picks the instance.
 //   * All waits are bounded (about 1 s, then PKV_DEVERR_TIMEOUT and a bounded drain).
 #include <cuda.h>
@@ -95,7 +97,7 @@ constexpr uint32_t TMEM_COLS = 512;            // S (and P over it): 2 buffers x
 // (batch > 0) the expanded blocks before each sequence as well (batch + 1 entries), the width of the tables, and
 // each sequence's first block of the window (batch entries).
 struct PlanHeader { uint32_t magic; int32_t num_units, grid, group, tp, hq, hkv, batch; };       // grid: with WINDOWED
-struct Unit { int32_t b, h, row0, pos0, npos, nkv, kmax, ts; };      // ts: tiles of the sinks before the window's
+struct Unit { int32_t b, h, row0, pos0, npos, nkv, kmax, sb; };      // sb: blocks of the sinks before the window's
 constexpr int32_t WINDOWED = 1 << 16;          // in the grid that a plan gives out: it has a window
 constexpr int MOST_GRID = WINDOWED - 1;
 struct Window { int32_t window, sinks, pad[6]; };
@@ -251,6 +253,9 @@ struct Smem {
     static_assert(ALLOC <= 227 * 1024, "shared memory");
 };
 
+// The lowest c bits.
+__device__ __forceinline__ unsigned long long ones64(int c) { return c <= 0 ? 0ull : c >= 64 ? ~0ull : (1ull << c) - 1; }
+
 // I4: K and V are the expanded tiles of an INT4 pool, K in bf16 and V in f16.
 template <int D, bool FP8, bool I4, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 1)
@@ -301,10 +306,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const int u0 = cta_off[blockIdx.x], u1 = cta_off[blockIdx.x + 1];
     const Window *win = reinterpret_cast<const Window *>(units + hdr->num_units);
     const int window = WIN ? win->window : 0, sinks = WIN ? win->sinks : 0;
-    // K/V tile of a unit's j-th: those of the sinks come first, then those from the window's first on
-    auto tile_at = [&](const Unit &un, int j) {
-        if constexpr (!WIN) return j;
-        else return j < un.ts ? j : j - un.ts + window_low(un.pos0, window) / BN;
+    // Block of a unit's v-th: those of the sinks come first, then those from the window's first on.  Four in turn are a tile
+    auto block_at = [&](const Unit &un, int v) {
+        if constexpr (!WIN) return v;
+        else return v < un.sb ? v : v - un.sb + max(window_low(un.pos0, window) / BS, un.sb);
     };
 
     if (tid == 0) {
@@ -350,10 +355,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const int nblk = un.kmax / BS + 1;                   // blocks holding keys 0..kmax
 #pragma unroll
         for (int i = 0; i < BN / BS; ++i) {
-            const int blk = tile_at(un, j) * (BN / BS) + i;
-            bool need = blk < nblk && blk < p.MB;
-            if constexpr (WIN) need = need && (blk * BS < sinks || (blk + 1) * BS > window_low(un.pos0, window));
-            raw[i] = need ? __ldg(p.tables + (size_t)un.b * p.MB + blk) : INT_MIN;
+            const int blk = block_at(un, j * (BN / BS) + i);
+            raw[i] = blk < nblk && blk < p.MB ? __ldg(p.tables + (size_t)un.b * p.MB + blk) : INT_MIN;
         }
     };
     auto resolve = [&](int id) {
@@ -708,14 +711,28 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         x[32 + i] = __uint_as_float(v1[i]);
                     }
                 }
-                const int kb = tile_at(un, j) * BN;
+                const int kb = block_at(un, j * (BN / BS)) * BS;
+                const bool straight = !WIN || block_at(un, (j + 1) * (BN / BS) - 1) * BS == kb + BN - BS;      // 64 keys on end
                 if constexpr (WIN) {
                     // the causal diagonal crosses the tile, or the first key of some row's window does
-                    if (kb + BN - 1 > un.pos0 || (kb < un.pos0 + un.npos - window && kb + BN > sinks)) {
-                        const int low = qpos - window + 1;
+                    if (kb + BN - 1 > un.pos0 || (kb < un.pos0 + un.npos - window && kb + BN > sinks) || !straight) {
+                        // (a bit per key: 64 comparisons of three limits each took the softmax twice its time)
+                        auto seen = [&](int p0) { return ones64(qpos + 1 - p0) & (~ones64(qpos - window + 1 - p0) | ones64(sinks - p0)); };
+                        unsigned long long see = 0;
+                        if (straight) {
+                            see = seen(kb);
+                        } else {
+#pragma unroll 1
+                            for (int k = 0; k < BN / BS; ++k)
+                                see |= (seen(block_at(un, j * (BN / BS) + k) * BS) & 0xffffull) << (BS * k);
+                        }
+                        if (!valid) see = 0;
+                        const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
 #pragma unroll
-                        for (int c = 0; c < BN; ++c)
-                            x[c] = valid && kb + c <= qpos && (kb + c >= low || kb + c < sinks) ? x[c] : -INFINITY;
+                        for (int c = 0; c < 32; ++c) {
+                            if (!((lo >> c) & 1u)) x[c] = -INFINITY;
+                            if (!((hi >> c) & 1u)) x[32 + c] = -INFINITY;
+                        }
                     }
                 } else if (kb + BN - 1 > un.pos0) {           // the causal diagonal crosses the tile
 #pragma unroll
@@ -780,14 +797,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 if constexpr (WIN) {
                     // (any tile) zero the V rows that no row of the unit sees: past its last key, and between the
                     // sinks and the first row's window
-                    const int low = window_low(un.pos0, window), h0 = max(sinks - kb, 0), h1 = min(low - kb, BN), h2 = un.kmax + 1 - kb;
-                    if (h0 < h1 || h2 < BN) {
+                    const int low = window_low(un.pos0, window);
+                    if ((kb < low && kb + BN > sinks) || un.kmax < kb + BN - 1 || !straight) {
                         ok = __all_sync(dev::FULL, dev::mbar_wait_bounded(v_full(J % NSTAGE), (J / NSTAGE) & 1));
                         if (!ok) break;
                         uint8_t *vst = sm + L::V + (J % NSTAGE) * L::KSTAGE;
                         for (int c = st; c < BN * 8; c += 128) {
-                            const int row = c >> 3;
-                            if ((row >= h0 && row < h1) || row >= h2)
+                            const int row = c >> 3, pos = (straight ? kb + row : block_at(un, j * (BN / BS) + row / BS) * BS + row % BS);
+                            if ((pos >= sinks && pos < low) || pos > un.kmax)
                                 for (int hf = 0; hf < H; ++hf)
                                     *reinterpret_cast<uint4 *>(vst + hf * L::KHALF + c * 16) = make_uint4(0, 0, 0, 0);
                         }
@@ -1028,9 +1045,11 @@ extern "C" int pkv_prefill_plan_window(const pkv_pool *pool, const int32_t *cu_q
             u.pos0 = (int32_t)(C + qt * tp);
             u.npos = (int32_t)std::min<int64_t>(tp, P - qt * tp);
             u.kmax = u.pos0 + u.npos - 1;
-            const int t1 = window_low(u.pos0, window) / BN;
-            u.ts = (int32_t)std::min<int64_t>(t1, ((int64_t)sinks + BN - 1) / BN);
-            u.nkv = u.ts + u.kmax / BN + 1 - t1;
+            // blocks that the unit's rows see, in tiles of four
+            int64_t first;
+            const int64_t blocks = visible_blocks(u.pos0, (int64_t)u.kmax + 1, window, sinks, &first);
+            u.sb = window > 0 ? (int32_t)std::min<int64_t>(first, ((int64_t)sinks + BS - 1) / BS) : 0;
+            u.nkv = (int32_t)((blocks + BN / BS - 1) / (BN / BS));
             for (int h = 0; h < Hkv; ++h) {
                 u.h = h;
                 units.push_back(u);
