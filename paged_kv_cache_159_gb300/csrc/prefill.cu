@@ -1031,8 +1031,9 @@ extern "C" int pkv_prefill_plan_window(const pkv_pool *pool, const int32_t *cu_q
     const bool i4 = pool->desc.kv_dtype == PKV_KV_INT4;
     if (i4 && pkv_prefill_workspace_bytes_window(pool, cu_q, seq_lens, batch, max_blocks, window, sinks) == 0) return PKV_ERR_INVALID;
     // a window that every sequence fits into is none
-    if (window >= *std::max_element(seq_lens, seq_lens + batch)) window = 0;
-    if (window == 0) sinks = 0;
+    const int32_t longest = *std::max_element(seq_lens, seq_lens + batch);
+    if (window >= longest) window = 0;
+    sinks = window == 0 ? 0 : std::min(sinks, std::max(longest, 0));
     std::vector<Unit> units;
     for (int b = 0; b < batch; ++b) {
         const int64_t P = (int64_t)cu_q[b + 1] - cu_q[b], L = seq_lens[b];

@@ -36,7 +36,7 @@ def test_heads_and_types(kind, D, Hq, Hkv):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
-@pytest.mark.parametrize("window,sinks", [(1, 0), (2, 1), (15, 16), (16, 0), (17, 15), (63, 2), (64, 64), (65, 100), (128, 1), (5000, 7)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (2, 1), (15, 16), (16, 0), (17, 15), (63, 2), (64, 64), (65, 100), (128, 1), (5000, 7), (9, 2 ** 31 - 1)])
 def test_windows_and_sinks_at_block_and_tile_edges(kind, window, sinks):
     c = case([1, 2, 15, 16, 17, 31, 64, 65, 129, 600], 8, 2, 128, kind, window=window, sinks=sinks, seed=window)
     c.check(decode(c))

@@ -41,7 +41,7 @@ def test_heads_and_types(kind, D, Hq, Hkv):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
-@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (15, 16), (16, 0), (17, 15), (63, 2), (64, 64), (65, 100), (128, 63), (129, 65), (300, 0), (1000, 200), (5000, 7)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (15, 16), (16, 0), (17, 15), (63, 2), (64, 64), (65, 100), (128, 63), (129, 65), (300, 0), (1000, 200), (5000, 7), (50, 2 ** 31 - 1)])
 def test_windows_and_sinks_at_block_and_tile_edges(kind, window, sinks):
     c = case([0, 63, 64, 65, 700], [200, 65, 64, 17, 150], 8, 2, 128, kind, window=window, sinks=sinks, seed=window)
     c.check(prefill(c), p_bits=P_BITS[kind])
