@@ -529,24 +529,24 @@ int pkv_accept_rows(pkv_pool *pool, void *key_cache, void *value_cache, const in
  *     its ancestors'; bits from P_b on are ignored), and j < C_b with j > p - window or j < sinks, where
  *     p = C_b + (bits set) - 1 is the row's place behind its ancestors.
  * window 0: no window (every earlier position, sinks ignored); with a tree it is 0 or at least max_q.  A
- * row that sees nothing is zeros.  Scale as for the decode.  Positions that no row of a sequence sees are
- * not read, nor the table entries of blocks that hold no other position: they may be negative
- * (blocks given back once they have left the window).  What the cache holds at a position that a row
+ * row that sees nothing is zeros.  Scale as for the decode.  Blocks of 16 positions that no row of a
+ * sequence sees are not read, nor their table entries, which may be negative (blocks given back once they have
+ * left the window).  What the cache holds at a position that a row
  * does not see never reaches that row's output.
- * Device pointers: q, out bf16 [total_q, num_q_heads, D]; caches of one layer; block_tables int32
+ * Device pointers: q, out bf16 [total_q, num_q_heads, D], which must not overlap; caches of one layer; block_tables int32
  * [batch, max_blocks]; seq_lens int32 [batch]; cu_q int32 [batch + 1], ascending from 0.  total_q and max_q are the host's
  * bounds of cu_q[batch] and of every P_b: rows of out from cu_q[batch] on stay as they were, a sequence without rows does
  * nothing whatever its length, and one with P_b > max_q, P_b > seq_lens[b] or a length beyond its table sets
  * PKV_DEVERR_SEQ_LEN and its rows are zeros (a cu_q outside 0 .. total_q: nothing is written for it).  A table
  * entry outside the pool that is needed sets PKV_DEVERR_BLOCK_ID, and its positions count as not
  * seen.  workspace: device memory, 256-byte aligned, of at least pkv_tree_workspace_bytes() bytes (0 for
- * an invalid shape; the lengths do not enter); its content before and after is unspecified, and
+ * an invalid shape or without a device; the lengths do not enter); its content before and after is unspecified, and
  * calls sharing it must not overlap on the GPU.  The work is divided from the device's lengths
  * alone, so that a captured graph serves any lengths; two launches; placement of the blocks changes no bit.  FP8 and
  * INT4 pools take q to fp16 with a power of two per row and query head that keeps its largest element in range.
  * Requires batch <= 4096, 1 <= max_q <= 256, num_q_heads a multiple of Hkv with group <= 16,
- * max_blocks <= 2^26, batch * max_blocks * Hkv < 2^31, batch * Hkv * ceil(max_q * group / 16) * (max_blocks / 4 + 7)
- * < 2^31 (less is refused only where the work has more pieces than that). */
+ * max_blocks <= 2^26, batch * max_blocks * Hkv < 2^31, and fewer than 2^31 pieces of work (tiles of 64 positions by
+ * units of rows: batch * Hkv * ceil(max_q * group / 16) * (max_blocks / 4 + 7) < 2^31 suffices). */
 size_t pkv_tree_workspace_bytes(const pkv_pool *pool, int32_t batch, int32_t num_q_heads, int32_t max_q);
 int pkv_paged_attention_tree(pkv_pool *pool, const void *q, const void *key_cache, const void *value_cache,
                              const int32_t *block_tables, const int32_t *seq_lens, const int32_t *cu_q,

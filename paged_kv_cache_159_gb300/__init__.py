@@ -579,6 +579,11 @@ def accept_rows(pool: Pool, key_cache, value_cache, block_tables, seq_lens, cu_q
         _check(st, "accept_rows")
 
 
+def _head_dim(pool: Pool, D: int):
+    if D != pool.desc.head_dim:
+        raise ValueError("q has head_dim %d, the pool %d" % (D, pool.desc.head_dim))
+
+
 def tree_workspace_bytes(pool: Pool, batch: int, num_q_heads: int, max_q: int = 1) -> int:
     """Device workspace bytes of paged_attention_tree (and, max_q 1, paged_attention_window)."""
     return int(lib().pkv_tree_workspace_bytes(pool.handle, int(batch), int(num_q_heads), int(max_q)))
@@ -593,6 +598,7 @@ def paged_attention_tree(pool: Pool, q, key_cache, value_cache, block_tables, se
     T, Hq, D = q.shape
     B, MB = block_tables.shape
     max_q, n = int(max_q), T * Hq * D
+    _head_dim(pool, D)
     st = lib().pkv_paged_attention_tree(
         pool.handle, _ints(q, n, "q", 2), _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
         _ints(block_tables, B * MB, "block_tables"), _ints(seq_lens, B, "seq_lens"), _ints(cu_q, B + 1, "cu_q"),
@@ -609,6 +615,7 @@ def paged_attention_window(pool: Pool, q, key_cache, value_cache, block_tables, 
     tree_workspace_bytes(pool, B, Hq) bytes."""
     B, Hq, D = q.shape
     MB, n = block_tables.shape[1], B * Hq * D
+    _head_dim(pool, D)
     st = lib().pkv_paged_attention_window(
         pool.handle, _ints(q, n, "q", 2), _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
         _ints(block_tables, B * MB, "block_tables"), _ints(seq_lens, B, "seq_lens"), B, Hq, MB, scale, window, sinks,

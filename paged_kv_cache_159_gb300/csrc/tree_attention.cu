@@ -9,12 +9,12 @@
 //                     j > p - window or j < sinks, p = C + (bits set) - 1: the row's place behind its ancestors.
 // A row that sees nothing is zeros.
 //
-// Schedule.  A unit is (sequence, KV head, up to MR rows): rows are (token, head of the group) pairs, MR = 16,
-// 32, 64 or 128 by the most rows that a sequence may have.  A unit's visible blocks (those of the sinks, then
-// from the window's first on) make tiles of 64 keys, and the tiles of all units, laid end to end, are cut
-// evenly over a one-wave grid.  Every CTA finds its share from the device's lengths.  A unit in one CTA is
-// written there; a cut one leaves a partial (max, sum, output) per CTA, which a second launch merges in order:
-// the placement of blocks changes no bit.
+// Schedule.  A unit is (sequence, KV head, up to MR rows): rows are (token, head of the group) pairs, MR = 16 or
+// 32 by the most rows that a sequence may have; more take the kernel of tree_tcgen05.cu (MOST_MMA_ROWS).  A unit's
+// visible blocks (those of the sinks, then from the window's first on) make tiles of 64 keys, and the tiles of all
+// units, laid end to end, are cut evenly over a one-wave grid (a unit counts for UNIT_COST tiles more than it has).
+// Every CTA finds its share from the device's lengths.  A unit in one CTA is written there; a cut one leaves a
+// partial (max, sum, output) per CTA, which a second launch merges in order: the placement of blocks changes no bit.
 //
 // A CTA: one warp copies (a tensor copy per bf16 block of K and V, 128-byte swizzle; a bulk copy per FP8 or
 // INT4 block) into a ring of tiles, WR x WK warps multiply (mma.sync m16n8k16, queries as the 16 rows): WR
@@ -24,6 +24,14 @@
 // Masked places.  Scores are masked by select.  A V element that no row of the warp sees is taken as zero (a
 // register mask), since 0 x NaN is NaN; where some rows see a position and others do not, and its V is not
 // finite, its products leave the tensor core and are added row by row.
+//
+// What bounds it (32 / 8 heads of 128, bf16 pool, in a graph, merge included):
+//   * 256 sequences of up to 16384, window 1024, 4 sinks: 173 us, 6.1 TB/s of the visible keys' bytes, 0.90 of a copy's
+//     rate: the reading.
+//   * 64 sequences of 2048 with 8 drafts (32 rows): 102 us, 5.3 TB/s.  The two CTAs of an SM take 1.28 us a tile, by the
+//     latency of a tile's steps in the two warps that share its keys (issue slots 29 % used, tensor pipe 31 %, DRAM 71 %);
+//     a unit costs three tiles besides (q, the epilogue), and the merge takes 7 us.
+//   * one sequence of 13 drafts: 14 us, latency: lengths, table, tiles, partials, merge one after another.
 //
 // Both launches may start while the one before drains (programmatic dependent launch): they wait before they
 // read, and load coherently.
@@ -588,7 +596,8 @@ tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CU
 
 // Merge the partials of cut units: block (c, y) the rows MERGE_ROWS y .. of the unit that begins in stream c.  A warp takes
 // 8 rows and D / 4 columns of them, lane (row, c) columns 4 (c + 4 i) of its quarter ..: every load is four runs of 128
-// bytes.  Bound by reading the partials once (L2).
+// bytes.  Bound by the latency of the loads (four parts in flight): 6 to 8 us for the 304 parts of 16 or 32 rows, 8 to 13 us
+// for 152 of 256 rows (40 MB at most, of which DRAM sees little).
 constexpr int MERGE_ROWS = 8, MERGE_WARPS = 4;
 template <int D>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_merge_kernel(const Params p)
@@ -772,6 +781,10 @@ int run(pkv_pool *pool, const void *q, const void *key_cache, const void *value_
     if (tree_mask && window > 0 && window < max_q) return PKV_ERR_INVALID;
     if (batch == 0 || total_q == 0) return PKV_OK;
     if (!q || !key_cache || !value_cache || !block_tables || !seq_lens || !out || !workspace) return PKV_ERR_INVALID;
+    // (rows are written while other CTAs still read theirs)
+    const uint64_t q_bytes = (uint64_t)total_q * num_q_heads * d.head_dim * 2;
+    const uint64_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(out);
+    if (qa < oa + q_bytes && oa < qa + q_bytes) return PKV_ERR_INVALID;
     if (!aligned(q, 16) || !aligned(key_cache, 16) || !aligned(value_cache, 16) || !aligned(out, 16) || !aligned(block_tables, 4) ||
         !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(tree_mask, 8) || !aligned(workspace, 256))
         return PKV_ERR_INVALID;

@@ -1,7 +1,7 @@
 // tree_tcgen05.cu -- the attention of tree_attention.cu for many rows per KV head, on the tcgen05 tensor cores.
 //
-// Above some 64 rows (tokens times the group's heads) the products bind, not the reading of K and V: 256 rows on
-// mma.sync ran at a tenth of what the fifth-generation tensor cores give.  A unit is (sequence, KV head, 256 rows)
+// Above 32 rows (tokens times the group's heads) the products and the softmax bind, not the reading of K and V: 16 trees
+// of 61 tokens of 64 / 8 heads (488 rows a KV head, FP8) took 1080 us on mma.sync.  A unit is (sequence, KV head, 256 rows)
 // as two q-tiles of 128, of which the second rests where a unit has no more than 128 rows; a tile is 64 keys of
 // the unit's visible blocks.  The work is divided as in tree_attention.cu: every CTA of a one-wave grid takes an
 // even share of all tiles, and partial states of cut units are merged by the same second launch.
@@ -22,6 +22,13 @@
 //   * V that must not meet the tensor core is zeroed in its operand tile before P V, by the warps that bring V:
 //     what is not there, and, of positions that some rows of the unit do not see, those that are not finite
 //     (0 x NaN is NaN); the softmax threads of rows that do see such a position add its product themselves.
+// What bounds it (head_dim 128, in a graph, all launches):
+//   * those 16 trees behind up to 8192 positions: 220 us, 740 TFLOP/s.  A 64-key tile of both q-tiles takes
+//     1.0 us: the softmax's 0.95 us a row and tile and, next to it, the expansion of E4M3; the tensor pipe is busy 41 %
+//     of the time, the issue slots 53 %.  A unit costs 6 to 7 us besides (edge tiles, epilogue, refill), q to f16 and
+//     the merge 20 us in all.
+//   * 37 trees of up to 25 tokens behind up to 4096, 28 / 4 heads, INT4: 70 us, of which the units' own cost is the larger part (some 10 tiles a unit).
+//   * bf16, one q-tile: 0.85 to 1.2 us a tile, the latency of S, softmax, P V in turn over two S buffers.
 // All waits are bounded (about 1 s, then PKV_DEVERR_TIMEOUT, and the copies in flight are waited for).
 #include <atomic>
 

@@ -320,7 +320,7 @@ def test_accept_leaves_a_bad_sequence_as_it_was(bad):
 def test_accept_refusals():
     a = Accept("fp8", [7, 30], [20, 64], 2, 64)
     d = a.d
-    for kw in (dict(out=d["lens"]), dict(out=d["n"])):
+    for kw in (dict(out=d["lens"]), dict(out=d["n"]), dict(out=d["cu"][1:]), dict(out=d["path"].view(-1)[3:5]), dict(out=d["tables"].view(-1)[1:3])):
         with pytest.raises(pkv.PkvError) as e:
             a.run(**kw)
         assert e.value.status == pkv.ERR_INVALID

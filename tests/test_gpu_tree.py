@@ -227,6 +227,13 @@ def test_refusals():
     for kw in (dict(mask=c.mk[:-1]), dict(mask=c.mk.int()), dict(max_q=65), dict(o=out[:-1]), dict(q=c.qd.transpose(0, 1))):
         with pytest.raises(ValueError):
             call(**kw)
+    with pytest.raises(ValueError):                                     # as many elements, other heads
+        call(q=c.qd.view(7, 16, 64), o=out.view(7, 16, 64))
+    both = torch.empty((8, 8, 128), dtype=torch.bfloat16, device="cuda")
+    for q, o in ((both[:7], both[:7]), (both[:7], both[1:]), (both[1:], both[:7])):
+        with pytest.raises(pkv.PkvError) as e:                          # out over q
+            call(q=q, o=o)
+        assert e.value.status == pkv.ERR_INVALID
     assert pkv.tree_workspace_bytes(c.pool, 0, 8, 4) == 0 and pkv.tree_workspace_bytes(c.pool, 1, 7, 4) == 0
     assert pkv.tree_workspace_bytes(c.pool, 4097, 8, 4) == 0 and pkv.tree_workspace_bytes(c.pool, 1, 66, 4) == 0
     assert c.pool.get_device_error() == (pkv.OK, 0)
@@ -306,3 +313,72 @@ def test_a_wait_that_runs_out_is_reported(kind, Hq):
     finally:
         pkv.test_expire_waits(pkv.TEST_EXPIRE_NONE)
     assert torch.equal(c.run(), want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("Hq,width", [(8, 0), (16, 1000), (32, 1000)])
+def test_a_row_of_nans_stays_by_itself(kind, Hq, width):
+    """A query of NaN: that row of that head is NaN, and the rows that share its unit and its tiles are not."""
+    c = T.Case([700, 333], [30, 9], Hq, 2, 128, kind, seed=5, width=width)
+    c.q[3, 1] = float("nan")
+    c.q[35, 0, 17] = float("nan")
+    out = c.run()
+    c.check(out)
+    assert torch.isnan(out[3, 1].float()).all() and int(torch.isnan(out[:c.T].float()).any(-1).sum()) == 2
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+def test_calls_on_two_streams_at_once(kind):
+    """Two calls in flight, each with its own workspace: each as by itself."""
+    cases = [T.Case([3000, 1200, 40], [20, 7, 64], 32, 4, 128, kind, seed=8).attach(), T.Case([2000] * 6, [3] * 6, 8, 2, 64, kind, seed=9).attach()]
+    alone = [c.run() for c in cases]
+    ws, outs = [c.workspace() for c in cases], [[torch.empty_like(o) for _ in range(20)] for o in alone]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for c, w, o, s in zip(cases, ws, outs, streams):
+            pkv.paged_attention_tree(c.pool, c.qd, c.kc, c.vc, c.bt, c.sl, c.cq, c.mk, c.max_q, c.scale, o[i], w, stream=s)
+    torch.cuda.synchronize()
+    for c, a, o in zip(cases, alone, outs):
+        assert c.pool.get_device_error() == (pkv.OK, 0)
+        for x in o:
+            assert torch.equal(x[:c.T].view(torch.int16), a[:c.T].view(torch.int16))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+def test_blocks_beyond_32_bit_offsets(kind):
+    """The last blocks of a pool whose caches pass 2^32 bytes: attention, a windowed prefill and the accepted rows are
+    those of a small pool, bit for bit."""
+    c = T.Case([500, 90], [30, 5], 16, 2, 128, kind, seed=3, free=False).attach()
+    few = T.Case([500, 90], [1, 2], 16, 2, 128, kind, seed=3, free=False).attach()
+    prompt = T.Case([300, 0], [100, 70], 16, 2, 128, kind, tree=False, window=80, sinks=3, seed=4).attach()
+    for x in (c, few, prompt):
+        bits = torch.uint8 if kind != "bf16" else torch.int16
+        off = 2 ** 32 // x.kc[0].nbytes + 1
+        ks, vs = x.pages.scales
+        pool = pkv.Pool(off + x.NB, x.Hkv, x.D, T.KINDS[kind], ks, vs)
+        pool.attach_device(torch.cuda.current_device())
+        big = [torch.zeros((off + x.NB,) + tuple(y.shape[1:]), dtype=y.dtype, device="cuda") for y in (x.kc, x.vc)]
+        for y, z in zip(big, (x.kc, x.vc)):
+            y.view(bits)[off:] = z.view(bits)
+        bt = torch.where(x.bt >= 0, x.bt + off, x.bt).int()
+        out = torch.empty_like(x.qd)
+        if x is prompt:
+            plan, grid = pkv.prefill_plan(pool, x.cu, x.L, x.Hq, x.MB, window=80, sinks=3)
+            n = pkv.prefill_workspace_bytes(pool, x.cu, x.L, x.MB, window=80, sinks=3)
+            ws = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+            small = torch.empty_like(out)
+            pkv.paged_prefill(x.pool, x.qd, x.kc, x.vc, x.bt, x.scale, T.dev(plan), grid, small, workspace=ws)
+            pkv.paged_prefill(pool, x.qd, *big, bt, x.scale, T.dev(plan), grid, out, workspace=ws)
+        else:
+            small = x.run()
+            pkv.paged_attention_tree(pool, x.qd, *big, bt, x.sl, x.cq, x.mk, x.max_q, x.scale, out, x.workspace())
+            path = torch.tensor([[0, 2, 7], [1, 3, 4]] if x is c else [[0], [1]], dtype=torch.int32, device="cuda")
+            n, lens = torch.full((2,), path.shape[1], dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+            pkv.accept_rows(x.pool, x.kc, x.vc, x.bt, x.sl, x.cq, path, n, lens)
+            pkv.accept_rows(pool, *big, bt, x.sl, x.cq, path, n, lens)
+            for y, z in zip(big, (x.kc, x.vc)):
+                assert torch.equal(y.view(bits)[off:], z.view(bits))
+        assert pool.get_device_error() == (pkv.OK, 0) and x.pool.get_device_error() == (pkv.OK, 0)
+        assert torch.equal(out[:x.T].view(torch.int16), small[:x.T].view(torch.int16))
+        del big

@@ -105,6 +105,10 @@ def test_refusals():
         with pytest.raises(pkv.PkvError) as e:
             call(**kw)
         assert e.value.status == pkv.ERR_INVALID
+    with pytest.raises(ValueError):
+        pkv.paged_attention_window(c.pool, c.qd.view(2, 16, 64), c.kc, c.vc, c.bt, c.sl, c.scale, 20, 2, out.view(2, 16, 64), ws)
+    with pytest.raises(pkv.PkvError):
+        pkv.paged_attention_window(c.pool, c.qd, c.kc, c.vc, c.bt, c.sl, c.scale, 20, 2, c.qd, ws)
     for kw in (dict(sl=c.sl[:1]), dict(sl=c.sl.long()), dict(bt=c.bt[:1])):
         with pytest.raises(ValueError):
             call(**kw)
