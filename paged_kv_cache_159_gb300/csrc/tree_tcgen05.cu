@@ -27,7 +27,8 @@
 //     1.0 us: the softmax's 0.95 us a row and tile and, next to it, the expansion of E4M3; the tensor pipe is busy 41 %
 //     of the time, the issue slots 53 %.  A unit costs 6 to 7 us besides (edge tiles, epilogue, refill), q to f16 and
 //     the merge 20 us in all.
-//   * 37 trees of up to 25 tokens behind up to 4096, 28 / 4 heads, INT4: 70 us, of which the units' own cost is the larger part (some 10 tiles a unit).
+//   * 37 trees of up to 25 tokens behind up to 4096, 28 / 4 heads, INT4: 70 us.  A CTA has 30 tiles
+//     of mostly one q-tile (91 rows a unit on average), at 1.2 us the latency of its chain (below), and two units' own cost.
 //   * bf16, one q-tile: 0.85 to 1.2 us a tile, the latency of S, softmax, P V in turn over two S buffers.
 // All waits are bounded (about 1 s, then PKV_DEVERR_TIMEOUT, and the copies in flight are waited for).
 #include <atomic>
