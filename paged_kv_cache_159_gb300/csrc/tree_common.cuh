@@ -306,20 +306,18 @@ __device__ __forceinline__ int all_from(const Params &p, const Seq &s, int i1)
 }
 
 // q to f16 by a power of two per row that brings its largest element (magnitude bits `top`) into [2^14, 2^15): exact
-// for elements of 2^-24 of it and more.  The exponent; NO_SCALE for a row with an infinity or NaN, whose scores are
-// to be NaN.
+// for elements of 2^-24 of it and more.  The exponent; NO_SCALE for a row with an infinity or NaN, which becomes NaN
+// as a whole: its scores are NaN, and the select of the masked ones takes NaN away where the row sees nothing (a NaN
+// in the row's scale would come back behind that select, where the scale is applied after it).
 constexpr int NO_SCALE = -128;
 __device__ __forceinline__ int q_exponent(uint32_t top)
 {
     const int ex = (int)(top >> 7);
     return ex == 255 ? NO_SCALE : top == 0 ? 0 : min(126, 141 - max(ex, 1));
 }
-__device__ __forceinline__ float q_factor(int up) { return __uint_as_float((uint32_t)(127 + (up == NO_SCALE ? 0 : up)) << 23); }
+__device__ __forceinline__ float q_factor(int up) { return __uint_as_float(up == NO_SCALE ? 0x7fffffffu : (uint32_t)(127 + up) << 23); }
 // The score scale of such a row.
-__device__ __forceinline__ float row_scale(float sc, int up)
-{
-    return up == NO_SCALE ? __int_as_float(0x7fffffff) : sc * __uint_as_float((uint32_t)(127 - up) << 23);
-}
+__device__ __forceinline__ float row_scale(float sc, int up) { return up == NO_SCALE ? sc : sc * __uint_as_float((uint32_t)(127 - up) << 23); }
 
 // Expand one block (16 tokens) of K or V to f16 in the swizzled layout, by a warp; half: bytes from a row's first 64
 // columns to its others.

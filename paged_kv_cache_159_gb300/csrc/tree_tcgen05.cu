@@ -272,7 +272,7 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             const unsigned long long word = first_word(p, sq, token);
             float sc = fabsf(p.score_scale);
             if (WIDE && live) sc = row_scale(sc, __ldcg(p.q_up + ((size_t)b * p.max_q + token) * p.Hq + h * p.group + hh));
-            sc = sc == sc ? fmaxf(sc, 1e-37f) : sc;                // (masked scores stay -infinity)
+            sc = fmaxf(sc, 1e-37f);                                // (masked scores stay -infinity)
             float m = -INFINITY, l = 0.f;
             for (const int end = J + left; J < end; ++J, ++Jw) {
                 ok = wait_all(s_full(w, Jw), Jw >> 1);

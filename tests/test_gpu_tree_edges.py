@@ -1,0 +1,59 @@
+"""Attention of drafted tokens where rows, sequences and waits fail or hold nothing: what the other rows, sequences
+and calls then get."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_159_gb300 as pkv
+from tests import _drafts as T
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    return pkv.lib()
+
+
+def odd_queries(c, rows):
+    """NaN, an infinity in one place and infinities in all places, in turn."""
+    for i, r in enumerate(rows):
+        if i % 3 == 1:
+            c.q[r, :, 5] = float("inf")
+        else:
+            c.q[r] = float("nan") if i % 3 == 0 else -float("inf")
+
+
+# (rows a KV head, and whether the tables make it a call of few tiles: units of 16 and 32 rows, and of 256)
+UNITS = [(2, 3, 0), (8, 7, 0), (8, 30, 0), (8, 30, 1000), (32, 30, 1000), (18, 30, 1000)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("Hq,new,width", UNITS)
+def test_a_query_that_is_not_finite_and_sees_nothing_is_zero(kind, Hq, new, width):
+    """A draft slot that is not in use: an empty mask, no context, and whatever q holds."""
+    c = T.Case([0, 333], [new, 9], Hq, 2, 128, kind, seed=11, width=width)
+    off = [1] if new == 3 else [1, 3, 6]
+    c.drafts[0][off] = False
+    c.see[0] = T.visible(0, new, 0, 0, c.drafts[0])
+    odd_queries(c, off)
+    seeing = new + 4
+    c.q[seeing, 1] = float("nan")                                       # and one that sees its ancestors
+    out = c.run()
+    c.check(out)
+    assert (out[off] == 0).all() and torch.isnan(out[seeing, 1].float()).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("Hq,new,width", UNITS)
+@pytest.mark.parametrize("cached", [0, 40, 3000])
+def test_a_query_that_is_not_finite_without_any_block_is_zero(kind, Hq, new, width, cached):
+    """Every entry of a sequence's table is empty: flagged, and its rows are zeros whatever q holds, also where the
+    unit is cut over several CTAs."""
+    c = T.Case([cached, 100], [new, 4], Hq, 2, 128, kind, seed=12, width=width).attach()
+    want = c.run()[new:c.T]
+    odd_queries(c, range(new))
+    c.qd.copy_(c.q)
+    c.bt[0] = -1
+    out = c.run(error=(pkv.ERR_DEVICE, pkv.DEVERR_BLOCK_ID))
+    assert (out[:new] == 0).all() and torch.equal(out[new:c.T], want)
