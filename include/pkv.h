@@ -650,10 +650,12 @@ int pkv_get_device_error(pkv_pool *pool, void *stream, uint32_t *bits_out);
 
 /* Test hook for the failure path of the kernels' bounded waits (the pages have no
  * counterpart; it exists so that a test can see that path run).  While `which` is
- * PKV_TEST_EXPIRE_DECODE (every decode entry point) or PKV_TEST_EXPIRE_PREFILL
+ * PKV_TEST_EXPIRE_DECODE (every decode entry point, those of drafts and windows among them) or PKV_TEST_EXPIRE_PREFILL
  * (pkv_paged_prefill), every launch of that kernel makes one of its roles -- the decode's
- * streaming warps before their first block, the prefill's Q loader before its first load --
- * wait about 1 ms on an mbarrier that nothing completes.  The wait runs out, the kernel sets
+ * streaming warps before their first block, the prefill's Q loader before its first load, and
+ * for drafts and windows the multiplying warps or (many rows per KV head) the Q loader before a
+ * CTA's last unit -- wait on an mbarrier that nothing completes, for about 1 ms (that last
+ * loader for the normal bound).  The wait runs out, the kernel sets
  * PKV_DEVERR_TIMEOUT, and the roles that depend on the stalled one give up in turn (each
  * after its normal bound of about 1 s at most); copies already in flight are waited for
  * (bounded) before a CTA leaves, so the context stays usable and pkv_get_device_error()

@@ -562,9 +562,10 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             auto raw_of = [&](int q) { return raw((isk ? 2 : 0) + (q & 1), (q >> 1) % NSG); };
             int n = which, q = which;                              // jobs issued, and done with
             for (; q < jobs; q += 3) {
-                for (; ok && n < jobs && n < q + 2 * NSG; n += 3) {
+                for (; n < jobs && n < q + 2 * NSG; n += 3) {
                     ok = wait_all(told(n >> 1), (n >> 1) / LEAD);
-                    if (ok) issue(n >> 1, n & 1, base + (isk ? L::SK : L::SV) + ((n >> 1) % NSG) * L::RAW, raw_of(n));
+                    if (!ok) break;                                // (n stays: only what was issued is waited for below)
+                    issue(n >> 1, n & 1, base + (isk ? L::SK : L::SV) + ((n >> 1) % NSG) * L::RAW, raw_of(n));
                 }
                 const int J = q >> 1, half = q & 1;
                 ok = ok && wait_all(raw_of(q), J / NSG) && room(J);
@@ -590,6 +591,7 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         } else {
             const int half = warp & 1;
             int looks = 0, J = 0;
+            bool looking = false;                                  // the copy that raw() is for may be under way
             for (; J < nt; ++J) {
                 ok = wait_all(told(J), J / LEAD) && room(J);
                 if (!ok) break;
@@ -597,27 +599,32 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 if (!isk && lane == 0 && !l) info[J % LEAD].bad[half] = 0;
                 issue(J, half, base + (isk ? L::K : L::V) + (J % NS) * L::KSTAGE, l ? raw(half, 0) : full(J));
                 if (l) {
-                    ok = wait_all(raw(half, 0), looks++);
+                    looking = true;
+                    ok = wait_all(raw(half, 0), looks);
                     if (!ok) break;
+                    looking = false;
+                    ++looks;
                     look(J, half);
                     dev::fence_proxy_async_smem();                 // zeroed rows -> tensor core
                     __syncwarp();
                     if (lane == 0) dev::mbar_arrive(full(J));
                 }
             }
+            if (looking) (void)wait(raw(half, 0), looks);
             for (int i = max(0, J - NS); i < J; ++i) (void)wait(full(i), i / NS);
         }
         if (!ok && lane == 0) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
     } else if (warp == 14) {
         // ============ Q: eight tokens a copy, once the S before is done with its room
-        int uq = 0;
-        bool pending = false;
-        bool ok = __all_sync(dev::FULL, !p.test_stall || lane != 0 || dev::mbar_wait_bounded_ns(never, 0, dev::TEST_EXPIRE_NS));
-        for (int J = 0; ok && J < nt; ++uq) {
+        int uq = 0;                                                // units whose rows were asked for
+        bool ok = true;
+        for (int J = 0; J < nt; ++uq) {
             // (in this order: a tile is waited for only once the one before it has been told, so that its barrier is
             // not more than a phase away)
             if (uq > 0) ok = wait_all(q_free, uq - 1);
             ok = ok && wait_all(told(J), J / LEAD);
+            // (the failure path's test: the share's last unit does not get its rows, behind units that did)
+            if (ok && p.test_stall && J + info[J % LEAD].left >= nt) ok = wait_all(never, 0);
             if (!ok) break;
             const TileInfo &u = info[J % LEAD];
             const int i0 = u.m() * tokens, copies = (min(tokens, u.P - i0) + 7) / 8, h = u.h(), left = u.left;
@@ -628,12 +635,11 @@ tree_tcgen05_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 const int hf = i % H, c = i / H;
                 tc::tma_load_3d(base + hf * L::QHALF + c * (8 * p.group * 128), &qmap, hf * 64, h * p.group, row0 + i0 + 8 * c, q_full);
             }
-            pending = true;
             J += left;
         }
         if (!ok && lane == 0) dev::flag_error(p.err, PKV_DEVERR_TIMEOUT);
-        // no copy may land after the CTA has left
-        if (pending) (void)wait(q_full, ok ? uq - 1 : uq);
+        // no copy may land after the CTA has left: those of the last unit asked for, however the loop ended
+        if (uq > 0) (void)wait(q_full, uq - 1);
     } else if (warp < 12 && lane == 0) {
         // ============ the products: warps 8, 9 S and 10, 11 P V of q-tiles 0, 1
         const bool is_s = warp < 10;

@@ -1,5 +1,7 @@
 """Attention of drafted tokens where rows, sequences and waits fail or hold nothing: what the other rows, sequences
 and calls then get."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -57,3 +59,28 @@ def test_a_query_that_is_not_finite_without_any_block_is_zero(kind, Hq, new, wid
     c.bt[0] = -1
     out = c.run(error=(pkv.ERR_DEVICE, pkv.DEVERR_BLOCK_ID))
     assert (out[:new] == 0).all() and torch.equal(out[new:c.T], want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [9, 20])
+def test_a_wait_that_runs_out_behind_finished_units_ends_in_time(kind, D, new):
+    """The last unit of every CTA's share gets no q, after units that did: the copies in flight are those that were
+    issued, and the wait for them ends with them.  A wait gives up after 1 s.  All of a CTA's waits begin when it
+    stands, some milliseconds after the launch, so that a warp that waits once more for what never comes would
+    need 2 s."""
+    c = T.Case(np.full(40, 1300), np.full(40, new), 64, 8, D, kind, tree=False, seed=new)       # 320 units, 152 CTAs
+    want = c.run()
+    assert torch.isfinite(want.float()).all()
+    ws, out = c.workspace(), torch.empty_like(c.qd)
+    pkv.test_expire_waits(pkv.TEST_EXPIRE_DECODE)
+    try:
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        pkv.paged_attention_tree(c.pool, c.qd, c.kc, c.vc, c.bt, c.sl, c.cq, c.mk, c.max_q, c.scale, out, ws)
+        assert c.pool.get_device_error() == (pkv.ERR_TIMEOUT, pkv.DEVERR_TIMEOUT)
+        took = time.perf_counter() - t0
+    finally:
+        pkv.test_expire_waits(pkv.TEST_EXPIRE_NONE)
+    assert 0.9 < took < 1.6
+    assert torch.equal(c.run(ws), want)
