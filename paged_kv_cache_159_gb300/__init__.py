@@ -227,10 +227,18 @@ def _dev_ptr(t, what: str):
     return t.data_ptr()
 
 
-def _ints(t, n: int, what: str, size: int = 4):
-    """Device address of a contiguous CUDA tensor of n entries of `size` bytes."""
-    if not t.is_cuda or not t.is_contiguous() or t.nbytes != n * size:
-        raise ValueError("%s must be a contiguous CUDA tensor of %d entries of %d bytes" % (what, n, size))
+_types = {}
+
+
+def _array(t, n: int, what: str, kind: str = "int32"):
+    """Device address of a contiguous CUDA tensor of n entries of the type that torch calls `kind`."""
+    if not _types:
+        import torch
+        _types.update((x, getattr(torch, x)) for x in ("int32", "int64", "bfloat16"))
+    if t.dtype is not _types[kind]:
+        raise ValueError("%s must be of type %s, not %s" % (what, kind, t.dtype))
+    if not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError("%s must be a contiguous CUDA tensor of %d entries" % (what, n))
     return t.data_ptr()
 
 
@@ -557,10 +565,10 @@ def extend_tables(pool: Pool, seq_lens, cu_q, block_tables, reserve, state, new_
     used), positions [T] or None."""
     B, MB = block_tables.shape
     T, R = slots.shape[0], reserve.shape[0]
-    st = lib().pkv_extend_tables(pool.handle, _ints(seq_lens, B, "seq_lens"), _ints(cu_q, B + 1, "cu_q"), B, MB, T,
-                                 _ints(block_tables, B * MB, "block_tables"), _ints(reserve, R, "reserve"), R,
-                                 _ints(state, 2, "state"), _ints(new_lens, B, "new_lens"), _ints(slots, T, "slots", 8),
-                                 None if positions is None else _ints(positions, T, "positions"), _stream_ptr(stream))
+    st = lib().pkv_extend_tables(pool.handle, _array(seq_lens, B, "seq_lens"), _array(cu_q, B + 1, "cu_q"), B, MB, T,
+                                 _array(block_tables, B * MB, "block_tables"), _array(reserve, R, "reserve"), R,
+                                 _array(state, 2, "state"), _array(new_lens, B, "new_lens"), _array(slots, T, "slots", "int64"),
+                                 None if positions is None else _array(positions, T, "positions"), _stream_ptr(stream))
     if st:
         _check(st, "extend_tables")
 
@@ -572,9 +580,9 @@ def accept_rows(pool: Pool, key_cache, value_cache, block_tables, seq_lens, cu_q
     B, MB = block_tables.shape
     N = path.shape[1]
     st = lib().pkv_accept_rows(pool.handle, _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
-                               _ints(block_tables, B * MB, "block_tables"), _ints(seq_lens, B, "seq_lens"), _ints(cu_q, B + 1, "cu_q"),
-                               _ints(path, B * N, "path"), _ints(num_accepted, B, "num_accepted"), B, MB, N,
-                               _ints(lens_out, B, "lens_out"), _stream_ptr(stream))
+                               _array(block_tables, B * MB, "block_tables"), _array(seq_lens, B, "seq_lens"), _array(cu_q, B + 1, "cu_q"),
+                               _array(path, B * N, "path"), _array(num_accepted, B, "num_accepted"), B, MB, N,
+                               _array(lens_out, B, "lens_out"), _stream_ptr(stream))
     if st:
         _check(st, "accept_rows")
 
@@ -600,10 +608,10 @@ def paged_attention_tree(pool: Pool, q, key_cache, value_cache, block_tables, se
     max_q, n = int(max_q), T * Hq * D
     _head_dim(pool, D)
     st = lib().pkv_paged_attention_tree(
-        pool.handle, _ints(q, n, "q", 2), _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
-        _ints(block_tables, B * MB, "block_tables"), _ints(seq_lens, B, "seq_lens"), _ints(cu_q, B + 1, "cu_q"),
-        None if tree_mask is None else _ints(tree_mask, T * ((max_q + 63) // 64), "tree_mask", 8), B, Hq, MB, T, max_q, scale,
-        window, sinks, _ints(out, n, "out", 2), _dev_ptr(workspace, "workspace"), workspace.nbytes, _stream_ptr(stream))
+        pool.handle, _array(q, n, "q", "bfloat16"), _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
+        _array(block_tables, B * MB, "block_tables"), _array(seq_lens, B, "seq_lens"), _array(cu_q, B + 1, "cu_q"),
+        None if tree_mask is None else _array(tree_mask, T * ((max_q + 63) // 64), "tree_mask", "int64"), B, Hq, MB, T, max_q, scale,
+        window, sinks, _array(out, n, "out", "bfloat16"), _dev_ptr(workspace, "workspace"), workspace.nbytes, _stream_ptr(stream))
     if st:
         _check(st, "paged_attention_tree")
 
@@ -617,9 +625,9 @@ def paged_attention_window(pool: Pool, q, key_cache, value_cache, block_tables, 
     MB, n = block_tables.shape[1], B * Hq * D
     _head_dim(pool, D)
     st = lib().pkv_paged_attention_window(
-        pool.handle, _ints(q, n, "q", 2), _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
-        _ints(block_tables, B * MB, "block_tables"), _ints(seq_lens, B, "seq_lens"), B, Hq, MB, scale, window, sinks,
-        _ints(out, n, "out", 2), _dev_ptr(workspace, "workspace"), workspace.nbytes, _stream_ptr(stream))
+        pool.handle, _array(q, n, "q", "bfloat16"), _dev_ptr(key_cache, "key_cache"), _dev_ptr(value_cache, "value_cache"),
+        _array(block_tables, B * MB, "block_tables"), _array(seq_lens, B, "seq_lens"), B, Hq, MB, scale, window, sinks,
+        _array(out, n, "out", "bfloat16"), _dev_ptr(workspace, "workspace"), workspace.nbytes, _stream_ptr(stream))
     if st:
         _check(st, "paged_attention_window")
 

@@ -41,6 +41,52 @@ def test_host_tensors_are_refused():
         pkv.accept_rows(p, q, q, i(1, 4), i(1), i(2), i(1, 3), i(1), i(1))
 
 
+class OnDevice:
+    """What the binding asks of a CUDA tensor, of a host one: the refusals below come before any address is used."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t, self.dtype, self.shape, self.nbytes = t, t.dtype, t.shape, t.nbytes
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def halves(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+CALLS = {
+    "paged_attention_tree": (dict(q=halves(3, 8, 64), key_cache=halves(8, 2, 16, 64), value_cache=halves(8, 2, 16, 64), block_tables=i32(1, 4),
+                                  seq_lens=i32(1), cu_q=i32(2), tree_mask=torch.zeros(3, 1, dtype=torch.int64), max_q=3, scale=0.1,
+                                  out=halves(3, 8, 64), workspace=i32(64)), ["q", "block_tables", "seq_lens", "cu_q", "tree_mask", "out"]),
+    "paged_attention_window": (dict(q=halves(3, 8, 64), key_cache=halves(8, 2, 16, 64), value_cache=halves(8, 2, 16, 64), block_tables=i32(3, 4),
+                                    seq_lens=i32(3), scale=0.1, window=4, sinks=1, out=halves(3, 8, 64), workspace=i32(64)),
+                               ["q", "block_tables", "seq_lens", "out"]),
+    "extend_tables": (dict(seq_lens=i32(1), cu_q=i32(2), block_tables=i32(1, 4), reserve=i32(4), state=i32(2), new_lens=i32(1),
+                           slots=torch.zeros(3, dtype=torch.int64), positions=i32(3)),
+                      ["seq_lens", "cu_q", "block_tables", "reserve", "state", "new_lens", "slots", "positions"]),
+    "accept_rows": (dict(key_cache=halves(8, 2, 16, 64), value_cache=halves(8, 2, 16, 64), block_tables=i32(1, 4), seq_lens=i32(1), cu_q=i32(2),
+                         path=i32(1, 3), num_accepted=i32(1), lens_out=i32(1)),
+                    ["block_tables", "seq_lens", "cu_q", "path", "num_accepted", "lens_out"]),
+}
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, (_, names) in CALLS.items() for n in names])
+def test_a_tensor_of_another_type_is_refused(call, name):
+    """A float16 q has the size of a bfloat16 one and would be read as it: types are those documented."""
+    args = dict(CALLS[call][0])
+    other = {2: torch.float16, 4: torch.float32, 8: torch.float64}[args[name].element_size()]
+    args[name] = args[name].to(other)
+    args = {k: OnDevice(x) if torch.is_tensor(x) else x for k, x in args.items()}
+    with pytest.raises(ValueError, match="%s must be of type" % name):
+        getattr(pkv, call)(pkv.Pool(8, 2, 64), **args)
+
+
 def test_windowed_plan_refusals():
     p = pkv.Pool(8, 2, 64)
     for kw in (dict(window=-1), dict(window=8, sinks=-1)):
