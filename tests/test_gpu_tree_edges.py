@@ -84,3 +84,45 @@ def test_a_wait_that_runs_out_behind_finished_units_ends_in_time(kind, D, new):
         pkv.test_expire_waits(pkv.TEST_EXPIRE_NONE)
     assert 0.9 < took < 1.6
     assert torch.equal(c.run(ws), want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("Hq,new,width", UNITS)
+@pytest.mark.parametrize("cu,bad", [(lambda a, b, t: [0, a, b, t + 1], [2]), (lambda a, b, t: [-1, a, b, t], [0]),
+                                    (lambda a, b, t: [0, a, b, 2 ** 31 - 1], [2]), (lambda a, b, t: [0, a, a - 1, a - 1], [1, 2]),
+                                    (lambda a, b, t: [-2 ** 31, a, b, 2 ** 31 - 1], [0, 2])])
+def test_a_sequence_whose_rows_are_out_of_range_is_left_alone(kind, Hq, new, width, cu, bad):
+    """Rows of a sequence whose cu_q leaves 0 .. total_q, or descends, stay as they were; the others are right."""
+    c = T.Case([100, 60, 700], [new, 4, 2], Hq, 2, 128, kind, seed=7, max_q=new + 4, width=width).attach()
+    c.cq.copy_(torch.tensor(cu(int(c.cu[1]), int(c.cu[2]), c.T), dtype=torch.int32))
+    out = c.run(error=(pkv.ERR_DEVICE, pkv.DEVERR_SEQ_LEN))
+    c.check(out, skip=bad)
+    for b in bad:
+        assert torch.isnan(out[c.cu[b]:c.cu[b + 1]].float()).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("Hq,Hkv,most", [(2, 1, 6), (4, 2, 3), (8, 1, 21)])
+@pytest.mark.parametrize("batch,active", [(4096, 1.0), (4096, 0.01), (2500, 0.5), (4095, 0.0)])
+def test_batches_of_thousands(kind, Hq, Hkv, most, batch, active):
+    """Several sequences a thread in the split of the work, and long runs of slots without rows, whose lengths mean
+    nothing."""
+    rng = np.random.default_rng(batch + most)
+    new = np.where(rng.random(batch) < active, rng.integers(1, most + 1, batch), 0)
+    cached = rng.integers(0, 40, batch) * (rng.random(batch) < 0.5)
+    new[[7, batch - 1]], cached[[7, batch - 1]] = [most, 1], [900, 333]         # one long, and the last slot
+    c = T.Case(cached, new, Hq, Hkv, 64, kind, seed=13, pad=5, max_q=most).attach()
+    c.sl[torch.from_numpy(new == 0).cuda()] = -3
+    out = c.run()
+    c.check(out)
+    assert torch.equal(c.run()[:c.T], out[:c.T])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group", [3, 5, 6, 7, 9, 10, 11, 12, 13, 14, 15])
+def test_groups_whose_units_are_not_256_rows(kind, D, group):
+    """Several units a KV head, with q-tiles that end inside a token's heads."""
+    tokens = 256 // group // 8 * 8
+    c = T.Case([130, 5, 40], [2 * tokens + 3, 128 // group + 1, tokens], 2 * group, 2, D, kind, seed=group, width=400, max_q=2 * tokens + 3)
+    c.check(c.run())
