@@ -227,19 +227,20 @@ def _dev_ptr(t, what: str):
     return t.data_ptr()
 
 
-_types = {}
+_types = {}                                    # torch's types by name, once they are asked for
 
 
 def _array(t, n: int, what: str, kind: str = "int32"):
     """Device address of a contiguous CUDA tensor of n entries of the type that torch calls `kind`."""
+    if t.dtype is _types.get(kind) and t.is_cuda and t.is_contiguous() and t.numel() == n:
+        return t.data_ptr()
     if not _types:
         import torch
         _types.update((x, getattr(torch, x)) for x in ("int32", "int64", "bfloat16"))
+        return _array(t, n, what, kind)
     if t.dtype is not _types[kind]:
         raise ValueError("%s must be of type %s, not %s" % (what, kind, t.dtype))
-    if not t.is_cuda or not t.is_contiguous() or t.numel() != n:
-        raise ValueError("%s must be a contiguous CUDA tensor of %d entries" % (what, n))
-    return t.data_ptr()
+    raise ValueError("%s must be a contiguous CUDA tensor of %d entries" % (what, n))
 
 
 _current_raw_stream = None
