@@ -542,8 +542,11 @@ int pkv_accept_rows(pkv_pool *pool, void *key_cache, void *value_cache, const in
  * seen.  workspace: device memory, 256-byte aligned, of at least pkv_tree_workspace_bytes() bytes (0 for
  * an invalid shape or without a device; the lengths do not enter); its content before and after is unspecified, and
  * calls sharing it must not overlap on the GPU.  The work is divided from the device's lengths
- * alone, so that a captured graph serves any lengths; two launches; placement of the blocks changes no bit.  FP8 and
- * INT4 pools take q to fp16 with a power of two per row and query head that keeps its largest element in range.
+ * alone, so that a captured graph serves any lengths; placement of the blocks changes no bit.  There are two kernels: up to
+ * 32 rows per KV head (max_q * group), or with tables so narrow that there are few tiles, one on mma.sync, above that one on
+ * tcgen05; a call with other max_blocks may take the other one and differ in the last bits.  A second launch merges cut units
+ * (max_blocks above 4).  FP8 and INT4 pools take q to fp16 with a power of two per row and query head that keeps its largest
+ * element in range, for the tcgen05 kernel in a launch in front of it, into room for batch * max_q rows in the workspace.
  * Requires batch <= 4096, 1 <= max_q <= 256, num_q_heads a multiple of Hkv with group <= 16,
  * max_blocks <= 2^26, batch * max_blocks * Hkv < 2^31, and fewer than 2^31 pieces of work (tiles of 64 positions by
  * units of rows: batch * Hkv * ceil(max_q * group / 16) * (max_blocks / 4 + 7) < 2^31 suffices). */

@@ -24,8 +24,8 @@ constexpr int BS = 16;
 // tables, so no CTA can see an entry half a step old.  Then the rows' slots: by the same CTA up to
 // FEW_SLOTS, by a launch over all SMs above.
 // Bound by latency: lengths, two entries a sequence, the reserve and the slots' entries are four dependent
-// trips to L2: 3.7 us (64 sequences, 8 rows each, in a graph).  512 prompts of 1 to 1500 rows: 8.0 us in two launches,
-// 4.5 MB of slots and positions (one SM stores 64 bytes a cycle, which would be 35 us).
+// trips to L2: 3.9 us (64 sequences, 8 rows each, in a graph).  512 prompts of 1 to 2000 rows, 501483 in all: 8.6 us in
+// two launches, 6.0 MB of slots and positions (one SM stores 64 bytes a cycle, which would be 47 us at 2 GHz).
 // ------------------------------------------------------------------------------------
 constexpr int EXT_THREADS = 1024;
 constexpr int EXT_MOST = 4096;                  // sequences
@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(ROW_THREADS) extend_rows_kernel(const ExtendPa
 // chunk read before any of it is written, no row is overwritten that a later one comes from.  A row is
 // bytes of its own in every pool type, so stored bits move as they are; in INT4 tiles a row's place and the
 // order of V's halves follow from its token.
-// Bound by latency (path, table entries, rows) up to some hundred rows: 2.2 us (5 trees, FP8, one layer, in a graph);
-// then by DRAM: 7.2 us for 64 trees in 8 layers.
+// Bound by latency (path, table entries, rows) up to some hundred rows: 2.4 us (5 trees, FP8, one layer, in a graph);
+// then by DRAM: 7.5 us for 64 trees in 8 layers.
 // ------------------------------------------------------------------------------------
 constexpr int ACC_WARPS = 8, ACC_ROWS = 8;
 

@@ -58,7 +58,7 @@
 //     its first row's window reaches, four of them in turn to a tile, so that the work is the visible blocks'; a
 //     row's own limits join the causal mask in the tiles that they cross.  Other blocks are not loaded (their table
 //     entries may be empty), and V rows that no row of the unit sees are zeroed as those past the last key are.
-//     16 chunks of 512 behind up to 8192 positions, window 1024, 4 sinks (32 / 8 heads, D 128): 163 us, 830 TFLOP/s (484 us
+//     16 chunks of 512 behind up to 8192 positions, window 1024, 4 sinks (32 / 8 heads, D 128): 163 us, 826 TFLOP/s (484 us
 //     without the window); bound as without a window, and by the three tile-times that a unit costs besides its some 18 tiles.  The plan's grid
 //     carries the kind (WINDOWED), since the launch picks the instance.
 //   * All waits are bounded (about 1 s, then PKV_DEVERR_TIMEOUT and a bounded drain).

@@ -19,18 +19,22 @@
 // A CTA: one warp copies (a tensor copy per bf16 block of K and V, 128-byte swizzle; a bulk copy per FP8 or
 // INT4 block) into a ring of tiles, WR x WK warps multiply (mma.sync m16n8k16, queries as the 16 rows): WR
 // groups of 16 rows, the tile's keys divided over WK warps, whose states meet at a unit's end.  FP8 and INT4
-// tiles are expanded to f16 once a CTA (exactly), q goes to f16 with a power of two per row, P is f16 times 2^8.
+// tiles are expanded to f16 once a CTA (exactly), q goes to f16 with a power of two per row, P is f16 times 2^8.  Over
+// bf16 pools P is bf16, 8 bits, since both factors of a product have one type and V is bf16 (the plain decode does the same;
+// P in two bf16 terms would be twice the products): outputs are 0.0020 to 0.0023 off in norm, where their own rounding
+// alone is 0.0017.
 //
 // Masked places.  Scores are masked by select.  A V element that no row of the warp sees is taken as zero (a
 // register mask), since 0 x NaN is NaN; where some rows see a position and others do not, and its V is not
 // finite, its products leave the tensor core and are added row by row.
 //
 // What bounds it (32 / 8 heads of 128, bf16 pool, in a graph, merge included):
-//   * 256 sequences of up to 16384, window 1024, 4 sinks: 173 us, 6.1 TB/s of the visible keys' bytes, 0.90 of a copy's
+//   * 256 sequences of up to 16384, window 1024, 4 sinks: 175 us, 6.05 TB/s of the visible keys' bytes, 0.89 of a copy's
 //     rate: the reading.
-//   * 64 sequences of 2048 with 8 drafts (32 rows): 102 us, 5.3 TB/s.  The two CTAs of an SM take 1.28 us a tile, by the
-//     latency of a tile's steps in the two warps that share its keys (issue slots 29 % used, tensor pipe 31 %, DRAM 71 %);
-//     a unit costs three tiles besides (q, the epilogue), and the merge takes 7 us.
+//   * 64 sequences of 2048 with 8 drafts (32 rows): 103 us, 5.3 TB/s.  The two CTAs of an SM take 1.28 us a tile, by the
+//     latency of a tile's steps in the two warps that share its keys (issue slots 29 % used, tensor pipe 31 %, DRAM 71 %;
+//     some four spilled registers a warp and tile, at 168 a thread, are part of it); a unit costs three tiles besides (q, the
+//     epilogue), and the merge takes 7 us.
 //   * one sequence of 13 drafts: 14 us, latency: lengths, table, tiles, partials, merge one after another.
 //
 // Both launches may start while the one before drains (programmatic dependent launch): they wait before they
@@ -682,9 +686,11 @@ int rows_per_unit(int max_q, int group, bool few)
     return rows <= 16 ? 16 : rows <= MOST_MMA_ROWS || few ? 32 : tcgen05_tokens(group) * group;
 }
 
-// Few tiles: even with the tables full, 32 rows at a time, no CTA of the mma.sync grid gets more than one.  Then a call is
+// Few tiles: even with the tables full, 32 rows at a time, no more of them than the mma.sync grid has CTAs.  Then a call is
 // the kernels' latency, which is less without tensor memory and twenty warps (13 drafts of 4 heads behind 60 positions,
-// 8 KV heads, in a graph: 12.6 us against 15.4; behind 1500, where CTAs would get more, 16.0 against 14.9).
+// 8 KV heads, in a graph: 12.6 us against 15.4; behind 1500, where there are more, 16.0 against 14.9).  Not every CTA gets
+// one of them, since the units' cost is dealt out with the tiles: of 96 tiles on 96 CTAs (16 units of 6) a third have none
+// and a third two; where short units stand beside a long one a CTA may get three.
 bool few_tiles(const pkv_pool_desc &d, int batch, int max_blocks, int max_q, int group)
 {
     const int64_t tiles = (int64_t)batch * d.num_kv_heads * ((max_blocks + TB - 1) / TB) * (((int64_t)max_q * group + 31) / 32);

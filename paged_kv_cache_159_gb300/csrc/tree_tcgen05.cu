@@ -23,11 +23,14 @@
 //     what is not there, and, of positions that some rows of the unit do not see, those that are not finite
 //     (0 x NaN is NaN); the softmax threads of rows that do see such a position add its product themselves.
 // What bounds it (head_dim 128, in a graph, all launches):
-//   * those 16 trees behind up to 8192 positions: 220 us, 740 TFLOP/s.  A 64-key tile of both q-tiles takes
-//     1.0 us: the softmax's 0.95 us a row and tile and, next to it, the expansion of E4M3; the tensor pipe is busy 41 %
-//     of the time, the issue slots 53 %.  A unit costs 6 to 7 us besides (edge tiles, epilogue, refill), q to f16 and
-//     the merge 20 us in all.
-//   * 37 trees of up to 25 tokens behind up to 4096, 28 / 4 heads, INT4: 70 us.  A CTA has 30 tiles
+//   * those 16 trees behind up to 8192 positions: 221 us, 738 TFLOP/s.  A CTA has 136 tiles of 64 keys and both q-tiles at
+//     1.28 us (the slope of the time over contexts of 4096 to 16384): 174 us.  Besides, 2.7 pieces of units a CTA at 6 to 7 us
+//     (edge tiles, epilogue, refill), and q to f16 and the merge, 14 and 13 us by themselves.  Of a tile, 0.95 us are the
+//     softmax's, the rest is S and P handed over; the expansion of E4M3 does not set the pace, since over a bf16 pool a tile
+//     takes 1.42 us and the call, without a launch for q, 203.  The tensor pipe is busy 41 % of the time, the issue slots
+//     53 %.  The softmax threads also store P to local memory, a tile's 32 words a thread, for the rare path that picks
+//     one of them by its number.
+//   * 37 trees of up to 25 tokens behind up to 4096, 28 / 4 heads, INT4: 72 us.  A CTA has 30 tiles
 //     of mostly one q-tile (91 rows a unit on average), at 1.2 us the latency of its chain (below), and two units' own cost.
 //   * bf16, one q-tile: 0.85 to 1.2 us a tile, the latency of S, softmax, P V in turn over two S buffers.
 // All waits are bounded (about 1 s, then PKV_DEVERR_TIMEOUT, and the copies in flight are waited for).
